@@ -14,7 +14,8 @@ import sys
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
-SOURCES = [os.path.join(PKG, "csrc", "gemm_f32.hip")]
+SOURCES = [os.path.join(PKG, "csrc", f) for f in
+           ("gemm_f32.hip", "rows_route.hip", "rows_grouped.hip", "rows_adapters.hip")]
 INCLUDE = os.path.join(ROOT, "include")
 LIBRARY = os.path.join(PKG, "libgemm_f32.so")
 ARCH = "gfx950"
@@ -35,26 +36,49 @@ HIPFLAGS = [
 POISON_LDS = "-DGEMM_F32_POISON_LDS"
 
 
-def command(out: str, extra: list[str] | None = None, poison_lds: bool = False) -> list[str]:
-    """The hipcc command line that builds the library into `out`."""
+def command(out: str, extra: list[str] | None = None, poison_lds: bool = False,
+            sources: list[str] | None = None) -> list[str]:
+    """The hipcc command line that builds `sources` (all of them: the library) into `out`."""
     flags = [*HIPFLAGS, *([POISON_LDS] if poison_lds else []), *(extra or [])]
-    return ["hipcc", *flags, "-I", INCLUDE, *SOURCES, "-o", out]
+    return ["hipcc", *flags, "-I", INCLUDE, *(sources or SOURCES), "-o", out]
 
 
 def build(verbose: bool = False, extra: list[str] | None = None, poison_lds: bool = False) -> str:
-    """Compile the library; returns its path.  Always recompiles."""
+    """Compile the library; returns its path.  Always recompiles.
+
+    The sources compile side by side (they share nothing but host symbols),
+    then link.
+    """
     tmp = LIBRARY + ".tmp%d" % os.getpid()
-    cmd = command(tmp, extra, poison_lds)
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    res = subprocess.run(cmd, capture_output=True, text=True)
+    objects = ["%s.%s.o" % (tmp, os.path.basename(src)) for src in SOURCES]
+    jobs = []
     noise = "'-packed-fp32-ops' is not a recognized feature for this target"
-    msgs = [l for l in (res.stdout + res.stderr).splitlines() if noise not in l and l.strip()]
-    if res.returncode != 0:
-        raise RuntimeError("hipcc failed:\n" + "\n".join(msgs))
-    if verbose and msgs:
-        print("\n".join(msgs), flush=True)
-    os.replace(tmp, LIBRARY)
+
+    def finish(proc):
+        out, _ = proc.communicate()
+        msgs = [l for l in out.splitlines() if noise not in l and l.strip()]
+        if verbose and msgs and proc.returncode == 0:
+            print("\n".join(msgs), flush=True)
+        return "" if proc.returncode == 0 else "\n".join(msgs)
+
+    def start(cmd):
+        if verbose:
+            print(" ".join(cmd), flush=True)
+        return subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
+
+    try:
+        for src, obj in zip(SOURCES, objects):
+            jobs.append(start([*command(obj, extra, poison_lds, [src]), "-c"]))
+        errors = [e for e in [finish(j) for j in jobs] if e]
+        if not errors:
+            errors = [e for e in [finish(start(["hipcc", "-shared", f"--offload-arch={ARCH}", *objects, "-o", tmp]))] if e]
+        if errors:
+            raise RuntimeError("hipcc failed:\n" + "\n".join(errors))
+        os.replace(tmp, LIBRARY)
+    finally:
+        for obj in objects:
+            if os.path.exists(obj):
+                os.remove(obj)
     return LIBRARY
 
 

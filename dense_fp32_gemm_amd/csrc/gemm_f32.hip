@@ -41,6 +41,7 @@
 #include <string.h>
 
 #include "gemm_f32.h"
+#include "internal.h"
 
 namespace {
 
@@ -2370,6 +2371,16 @@ int run_noalloc(int M, int N, int K, const float *A, int lda, const float *B, in
 
 }  // namespace
 
+namespace gemm_f32_internal {
+
+Device current_device()
+{
+    const Machine m = machine();
+    return {m.cus, m.xcds};
+}
+
+}  // namespace gemm_f32_internal
+
 extern "C" {
 
 int gemm_f32_ws_noalloc(int M, int N, int K, const float *A, int lda, const float *B, int ldb,
@@ -2486,8 +2497,11 @@ const char *gemm_f32_status_string(int status)
     case GEMM_F32_ERR_NULL: return "a required pointer is NULL";
     case GEMM_F32_ERR_LAUNCH: return "kernel launch failed";
     case GEMM_F32_ERR_CONFIG: return "unknown kernel configuration";
-    case GEMM_F32_ERR_ALIGN: return "a pointer is not 4-byte aligned";
+    case GEMM_F32_ERR_ALIGN: return "a pointer is not aligned to its elements (4 bytes for binary32)";
     case GEMM_F32_ERR_SCRATCH: return "the split plan needs more than the library's static scratch holds";
+    case GEMM_F32_ERR_TYPE: return "unknown element type";
+    case GEMM_F32_ERR_OPTION: return "an option is outside its range";
+    case GEMM_F32_ERR_WORKSPACE: return "the workspace is NULL, too small or not 16-byte aligned";
     default: return "unknown status";
     }
 }

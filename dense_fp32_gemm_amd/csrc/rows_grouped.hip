@@ -1,0 +1,452 @@
+// Products per group of rows, their gradients, and the weighted sum of a
+// token's results (include/gemm_f32_rows.h).
+//
+//  * grouped_kernel<E, OP, ...>: one workgroup per output tile.  Which group a
+//    workgroup's tile belongs to is found on the device, from the offsets.
+//  * combine_kernel, combine_grad_kernel: one workgroup per token.
+
+#include "rows_tile.h"
+
+namespace rows {
+namespace {
+
+enum Op { kForward, kGradX, kGradW };
+
+struct GroupedArgs {
+    const int *offsets;
+    const int *order;        // forward, grad_w: rows of A; NULL: the place itself
+    const void *A;           // X (forward, grad_w), dY (grad_x)
+    const void *B;           // W (forward, grad_x), dY (grad_w)
+    void *C;                 // Y, dX, dW
+    int64_t lda, ldb, ldc;
+    int64_t stride;          // of W (of dW for grad_w)
+    int G, P, per_row, rows; // rows: of X
+    int M, N, K;             // grad_w: M x N of dW; else columns N of C, summed K
+    int tiles_n;
+    int xcds;
+};
+
+// Workgroups are dealt to the dies round-robin; renumbered so that each die
+// gets a contiguous range of tiles, whose operands its L2 then shares.
+__device__ inline int die_contiguous(int w, int total, int xcds)
+{
+    const int per = total / xcds, rem = total % xcds, xcd = w % xcds;
+    return xcd * per + (xcd < rem ? xcd : rem) + w / xcds;
+}
+
+// Group g's range of places, clamped to 0..P.
+__device__ inline void group_range(const int *offsets, int g, int P, int &lo, int &hi)
+{
+    lo = min(max(offsets[g], 0), P);
+    hi = min(max(offsets[g + 1], lo), P);
+}
+
+// Tile number -> group and row tile within it, by counting the row tiles of
+// every group (64 groups at a time, a lane each).  Every wave of the
+// workgroup computes it for itself.  Returns false past the last tile.
+__device__ inline bool find_tile(const GroupedArgs &g, int bm, int &group, int &lo, int &hi, int &tm, int &tn)
+{
+    const int lane = threadIdx.x % kWave;
+    int total = 0;
+    for (int g0 = 0; g0 < g.G; g0 += kWave) {
+        int a = 0, b = 0;
+        if (g0 + lane < g.G)
+            group_range(g.offsets, g0 + lane, g.P, a, b);
+        int n = (b - a + bm - 1) / bm;
+#pragma unroll
+        for (int d = kWave / 2; d > 0; d /= 2)
+            n += __shfl_xor(n, d);
+        total += n;
+    }
+    // Rising offsets never have more tiles than workgroups; others are cut there.
+    total = min(total, (int)(gridDim.x / g.tiles_n)) * g.tiles_n;
+    if ((int)blockIdx.x >= total)
+        return false;
+    const int t = die_contiguous(blockIdx.x, total, g.xcds);
+    int before = 0;                                  // row tiles of the groups before
+    for (int g0 = 0; g0 < g.G; g0 += kWave) {
+        int a = 0, b = 0;
+        if (g0 + lane < g.G)
+            group_range(g.offsets, g0 + lane, g.P, a, b);
+        const int n = (b - a + bm - 1) / bm;
+        int scan = n;
+#pragma unroll
+        for (int d = 1; d < kWave; d *= 2) {
+            const int x = __shfl_up(scan, d);
+            scan += lane >= d ? x : 0;
+        }
+        const uint64_t past = __ballot(before + scan > t / g.tiles_n);
+        if (past) {
+            const int at = (int)__builtin_ctzll(past);
+            group = g0 + at;
+            lo = __builtin_amdgcn_readlane(a, at);
+            hi = __builtin_amdgcn_readlane(b, at);
+            const int mine = __builtin_amdgcn_readlane(n, at);
+            const int first = before + __builtin_amdgcn_readlane(scan, at) - mine;
+            const int r = t - first * g.tiles_n;     // column by column: W's panels are shared
+            tm = r % mine;
+            tn = r / mine;
+            return true;
+        }
+        before += __builtin_amdgcn_readlane(scan, kWave - 1);
+    }
+    return false;
+}
+
+// Row of X at place p, NULL if there is none.
+template <class T>
+__device__ inline const T *row_at(const GroupedArgs &g, const T *X, int p)
+{
+    int64_t r = p;
+    if (g.order != nullptr) {
+        const int s = g.order[p];
+        r = s < 0 ? -1 : s / g.per_row;
+    }
+    return r >= 0 && r < g.rows ? X + r * g.lda : nullptr;
+}
+
+template <class E, Op OP, int BM, int BN, int WM, int WN, bool VEC>
+__global__ __launch_bounds__(WM *WN *kWave) void grouped_kernel(GroupedArgs g)
+{
+    constexpr bool kAlongA = OP != kGradW, kAlongB = OP == kGradX;
+    using Ti = Tile<E, kAlongA, kAlongB, BM, BN, WM, WN>;
+    using T = typename E::T;
+    constexpr int NT = Ti::kThreads;
+    __shared__ __attribute__((aligned(16))) T lds[2 * (Ti::kLdsA + Ti::kLdsB)];
+    const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
+    const int wm = wave / WN, wn = wave % WN;
+
+    int group, lo, hi, tm, tn;
+    if constexpr (OP == kGradW) {
+        const int tiles_m = (g.M + BM - 1) / BM, per = tiles_m * g.tiles_n;
+        const int t = die_contiguous(blockIdx.x, gridDim.x, g.xcds);
+        group = t / per;
+        tm = t % per % tiles_m;
+        tn = t % per / tiles_m;
+        group_range(g.offsets, group, g.P, lo, hi);
+    } else if (!find_tile(g, BM, group, lo, hi, tm, tn)) {
+        return;                                      // the whole workgroup
+    }
+    const int m0 = OP == kGradW ? tm * BM : lo + tm * BM;
+    const int m_end = OP == kGradW ? g.M : hi;
+    const int n0 = tn * BN;
+    const T *A = (const T *)g.A, *B = (const T *)g.B;
+
+    Ti tile;
+    tile.clear();
+    if constexpr (OP == kForward) {
+        const T *W = B + group * g.stride;
+        const Along<E, BM, NT> a(tid, g.K, [&](int r) { return m0 + r < m_end ? row_at(g, A, m0 + r) : nullptr; });
+        const auto b = across<E, BN, NT>(tid, g.K, n0, g.N, [&](int k) { return W + k * g.ldb; });
+        sum_panels<E, VEC>(tile, g.K, a, b, lds, tid, wm, wn);
+    } else if constexpr (OP == kGradX) {
+        const T *W = B + group * g.stride;
+        const Along<E, BM, NT> a(tid, g.K, [&](int r) { return m0 + r < m_end ? A + (m0 + r) * g.lda : nullptr; });
+        const Along<E, BN, NT> b(tid, g.K, [&](int r) { return n0 + r < g.N ? W + (n0 + r) * g.ldb : nullptr; });
+        sum_panels<E, VEC>(tile, g.K, a, b, lds, tid, wm, wn);
+    } else {
+        const auto a = across<E, BM, NT>(tid, hi - lo, m0, g.M, [&](int k) { return row_at(g, A, lo + k); });
+        const auto b = across<E, BN, NT>(tid, hi - lo, n0, g.N, [&](int k) { return B + (lo + k) * g.ldb; });
+        sum_panels<E, VEC>(tile, hi - lo, a, b, lds, tid, wm, wn);
+    }
+
+    T *C = (T *)g.C + (OP == kGradW ? group * g.stride : 0);
+    tile.each(wm, wn, lane, [&](int r, int c, f32x4 v) {
+        const int m = m0 + r, n = n0 + c;
+        if (m < m_end && n < g.N)
+            store4<E, VEC>(C + (int64_t)m * g.ldc + n, v, g.N - n);
+    });
+}
+
+// ---------------------------------------------------------------------------
+// Weighted sum of a token's results
+// ---------------------------------------------------------------------------
+constexpr int kCombineThreads = 256;
+
+struct CombineArgs {
+    const int *position;
+    const float *weight;
+    const void *Y;
+    const void *dout;
+    void *out;
+    void *dY;
+    float *dweight;
+    int64_t ldy, ldo, lddo, lddy;
+    int T, k, N, P;
+};
+
+template <class E, bool VEC>
+__global__ __launch_bounds__(kCombineThreads) void combine_kernel(CombineArgs g)
+{
+    using T = typename E::T;
+    for (int64_t t = blockIdx.x; t < g.T; t += gridDim.x)
+    for (int n = threadIdx.x * E::kChunk; n < g.N; n += kCombineThreads * E::kChunk) {
+        const int *position = g.position + t * g.k;
+        float sum[E::kChunk] = {};
+        for (int j = 0; j < g.k; ++j) {
+            const int p = position[j];
+            if (p < 0 || p >= g.P)
+                continue;
+            const float w = g.weight != nullptr ? g.weight[t * g.k + j] : 1.f;
+            Chunk<E> y;
+            y.raw = load_chunk<E, VEC>((const T *)g.Y + p * g.ldy + n, g.N - n);
+#pragma unroll
+            for (int i = 0; i < E::kChunk; ++i)
+                sum[i] = fmaf(w, (float)y.e[i], sum[i]);
+        }
+        Chunk<E> o;
+#pragma unroll
+        for (int i = 0; i < E::kChunk; ++i)
+            o.e[i] = (T)sum[i];
+        store_chunk<E, VEC>((T *)g.out + t * g.ldo + n, o, g.N - n);
+    }
+}
+
+template <class E, bool VEC>
+__global__ __launch_bounds__(kCombineThreads) void combine_grad_kernel(CombineArgs g)
+{
+    using T = typename E::T;
+    __shared__ float part[kCombineThreads / kWave];
+    const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+    for (int64_t t = blockIdx.x; t < g.T; t += gridDim.x)
+    for (int j = 0; j < g.k; ++j) {
+        const int p = g.position[t * g.k + j];
+        const bool there = p >= 0 && p < g.P;
+        const float w = g.weight != nullptr ? g.weight[t * g.k + j] : 1.f;
+        float sum = 0.f;
+        if (there) {
+            for (int n = threadIdx.x * E::kChunk; n < g.N; n += kCombineThreads * E::kChunk) {
+                Chunk<E> d;
+                d.raw = load_chunk<E, VEC>((const T *)g.dout + t * g.lddo + n, g.N - n);
+                if (g.dweight != nullptr) {
+                    Chunk<E> y;
+                    y.raw = load_chunk<E, VEC>((const T *)g.Y + p * g.ldy + n, g.N - n);
+#pragma unroll
+                    for (int i = 0; i < E::kChunk; ++i)
+                        sum = fmaf((float)y.e[i], (float)d.e[i], sum);
+                }
+                if (g.dY != nullptr) {
+                    Chunk<E> o;
+#pragma unroll
+                    for (int i = 0; i < E::kChunk; ++i)
+                        o.e[i] = (T)(w * (float)d.e[i]);
+                    store_chunk<E, VEC>((T *)g.dY + p * g.lddy + n, o, g.N - n);
+                }
+            }
+        }
+        if (g.dweight == nullptr)
+            continue;
+#pragma unroll
+        for (int d = kWave / 2; d > 0; d /= 2)
+            sum += __shfl_xor(sum, d);
+        if (lane == 0)
+            part[wave] = sum;
+        __syncthreads();
+        if (threadIdx.x == 0)
+            g.dweight[t * g.k + j] = (part[0] + part[1]) + (part[2] + part[3]);
+        __syncthreads();
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Host side
+// ---------------------------------------------------------------------------
+bool vector_rows(int type, const void *p, int64_t ld, int64_t cols)
+{
+    const int chunk = 16 / type_bytes(type);
+    return aligned_to(p, 16) && ld % chunk == 0 && cols % chunk == 0;
+}
+
+// Workgroups of a launch: a grid has fewer than 2^32 threads.
+constexpr int64_t kMaxTiles = UINT32_MAX / 256;
+static_assert(kCombineThreads <= 256, "grid limit");
+int token_grid(int T) { return T < kMaxTiles ? T : (int)kMaxTiles; }
+
+template <class E, Op OP, int BM, int BN, int WM, int WN>
+int launch_tile(GroupedArgs g, bool vec, hipStream_t stream)
+{
+    g.tiles_n = (int)ceil_div(g.N, BN);
+    // Every group ends in at most one partial tile.
+    const int64_t tiles_m = OP == kGradW ? g.G * ceil_div(g.M, BM) : g.P / BM + (g.G < g.P ? g.G : g.P);
+    const int64_t grid = tiles_m * g.tiles_n;
+    if (grid > kMaxTiles)
+        return GEMM_F32_ERR_DIM;
+    if (grid == 0)
+        return GEMM_F32_OK;
+    if (vec)
+        grouped_kernel<E, OP, BM, BN, WM, WN, true><<<(int)grid, WM * WN * kWave, 0, stream>>>(g);
+    else
+        grouped_kernel<E, OP, BM, BN, WM, WN, false><<<(int)grid, WM * WN * kWave, 0, stream>>>(g);
+    return launched();
+}
+
+template <Op OP>
+int launch_grouped(int type, const GroupedArgs &g, bool vec, hipStream_t stream)
+{
+    int rc = GEMM_F32_OK;
+    with_type(type, [&](auto e) {
+        using E = decltype(e);
+        // Few rows a group: tiles of 16 rows read each weight once without
+        // spending matrix instructions on rows that are not there.
+        if (OP != kGradW && g.P <= 32 * (int64_t)g.G)
+            rc = launch_tile<E, OP, 16, 128, 1, 4>(g, vec, stream);
+        else
+            rc = launch_tile<E, OP, 128, 128, 2, 2>(g, vec, stream);
+    });
+    return rc;
+}
+
+int check_grouped(int type, int G, int P, int N, int K)
+{
+    if (!known_type(type))
+        return GEMM_F32_ERR_TYPE;
+    return G < 0 || P < 0 || N < 0 || K < 0 ? GEMM_F32_ERR_DIM : GEMM_F32_OK;
+}
+
+bool short_ld(int64_t ld, int cols) { return ld < at_least_one(cols); }
+// K * ldw elements between groups at least (the last row may end at N).
+bool short_stride(int64_t stride, int G, int K, int64_t ldw) { return G > 1 && stride < K * ldw; }
+
+}  // namespace
+}  // namespace rows
+
+using namespace rows;
+
+extern "C" {
+
+int gemm_f32_grouped(int type, int G, int P, int N, int K, const int *offsets, const int *order, int per_row, int rows,
+                     const void *X, int ldx, const void *W, int ldw, int64_t stride_w, void *Y, int ldy,
+                     hipStream_t stream)
+{
+    const int rc = check_grouped(type, G, P, N, K);
+    if (rc != GEMM_F32_OK)
+        return rc;
+    if (rows < 0 || (order == nullptr && rows < P))
+        return GEMM_F32_ERR_DIM;
+    if (short_ld(ldx, K) || short_ld(ldw, N) || short_ld(ldy, N) || short_stride(stride_w, G, K, ldw))
+        return GEMM_F32_ERR_LD;
+    if (order != nullptr && per_row < 1)
+        return GEMM_F32_ERR_OPTION;
+    if (G == 0 || P == 0 || N == 0)
+        return GEMM_F32_OK;
+    if (offsets == nullptr || Y == nullptr || (K > 0 && ((X == nullptr && rows > 0) || W == nullptr)))
+        return GEMM_F32_ERR_NULL;
+    const int b = type_bytes(type);
+    if (!aligned_to(offsets, 4) || !aligned_to(order, 4) || !aligned_to(X, b) || !aligned_to(W, b) || !aligned_to(Y, b))
+        return GEMM_F32_ERR_ALIGN;
+    const bool vec = vector_rows(type, X, ldx, K) && vector_rows(type, W, ldw, N) && vector_rows(type, Y, ldy, N) &&
+                     stride_w % (16 / b) == 0;
+    const GroupedArgs g{offsets, order, X, W, Y, ldx, ldw, ldy, stride_w, G, P, per_row, rows, 0, N, K, 0,
+                        gemm_f32_internal::current_device().xcds};
+    return launch_grouped<kForward>(type, g, vec, stream);
+}
+
+int gemm_f32_grouped_grad_x(int type, int G, int P, int N, int K, const int *offsets, const void *dY, int lddy,
+                            const void *W, int ldw, int64_t stride_w, void *dX, int lddx, hipStream_t stream)
+{
+    const int rc = check_grouped(type, G, P, N, K);
+    if (rc != GEMM_F32_OK)
+        return rc;
+    if (short_ld(lddy, N) || short_ld(ldw, N) || short_ld(lddx, K) || short_stride(stride_w, G, K, ldw))
+        return GEMM_F32_ERR_LD;
+    if (G == 0 || P == 0 || K == 0)
+        return GEMM_F32_OK;
+    if (offsets == nullptr || dX == nullptr || (N > 0 && (dY == nullptr || W == nullptr)))
+        return GEMM_F32_ERR_NULL;
+    const int b = type_bytes(type);
+    if (!aligned_to(offsets, 4) || !aligned_to(dY, b) || !aligned_to(W, b) || !aligned_to(dX, b))
+        return GEMM_F32_ERR_ALIGN;
+    const bool vec = vector_rows(type, dY, lddy, N) && vector_rows(type, W, ldw, N) && vector_rows(type, dX, lddx, K) &&
+                     stride_w % (16 / b) == 0;
+    const GroupedArgs g{offsets, nullptr, dY, W, dX, lddy, ldw, lddx, stride_w, G, P, 1, P, 0, K, N, 0,
+                        gemm_f32_internal::current_device().xcds};
+    return launch_grouped<kGradX>(type, g, vec, stream);
+}
+
+int gemm_f32_grouped_grad_w(int type, int G, int P, int N, int K, const int *offsets, const int *order, int per_row,
+                            int rows, const void *X, int ldx, const void *dY, int lddy, void *dW, int lddw,
+                            int64_t stride_dw, hipStream_t stream)
+{
+    const int rc = check_grouped(type, G, P, N, K);
+    if (rc != GEMM_F32_OK)
+        return rc;
+    if (rows < 0 || (order == nullptr && rows < P))
+        return GEMM_F32_ERR_DIM;
+    if (short_ld(ldx, K) || short_ld(lddy, N) || short_ld(lddw, N) || short_stride(stride_dw, G, K, lddw))
+        return GEMM_F32_ERR_LD;
+    if (order != nullptr && per_row < 1)
+        return GEMM_F32_ERR_OPTION;
+    if (G == 0 || K == 0 || N == 0)
+        return GEMM_F32_OK;
+    if (offsets == nullptr || dW == nullptr || (P > 0 && ((X == nullptr && rows > 0) || dY == nullptr)))
+        return GEMM_F32_ERR_NULL;
+    const int b = type_bytes(type);
+    if (!aligned_to(offsets, 4) || !aligned_to(order, 4) || !aligned_to(X, b) || !aligned_to(dY, b) || !aligned_to(dW, b))
+        return GEMM_F32_ERR_ALIGN;
+    const bool vec = vector_rows(type, X, ldx, K) && vector_rows(type, dY, lddy, N) && vector_rows(type, dW, lddw, N) &&
+                     stride_dw % (16 / b) == 0;
+    const GroupedArgs g{offsets, order, X, dY, dW, ldx, lddy, lddw, stride_dw, G, P, per_row, rows, K, N, 0, 0,
+                        gemm_f32_internal::current_device().xcds};
+    return launch_grouped<kGradW>(type, g, vec, stream);
+}
+
+int gemm_f32_combine(int type, int T, int k, int N, int P, const int *position, const float *weight, const void *Y,
+                     int ldy, void *out, int ldo, hipStream_t stream)
+{
+    if (!known_type(type))
+        return GEMM_F32_ERR_TYPE;
+    if (T < 0 || k < 0 || N < 0 || P < 0)
+        return GEMM_F32_ERR_DIM;
+    if (short_ld(ldy, N) || short_ld(ldo, N))
+        return GEMM_F32_ERR_LD;
+    if (T == 0 || N == 0)
+        return GEMM_F32_OK;
+    if (out == nullptr || (k > 0 && (position == nullptr || (P > 0 && Y == nullptr))))
+        return GEMM_F32_ERR_NULL;
+    const int b = type_bytes(type);
+    if (!aligned_to(position, 4) || !aligned_to(weight, 4) || !aligned_to(Y, b) || !aligned_to(out, b))
+        return GEMM_F32_ERR_ALIGN;
+    const CombineArgs g{position, weight, Y, nullptr, out, nullptr, nullptr, ldy, ldo, 0, 0, T, k, N, P};
+    const bool vec = vector_rows(type, Y, ldy, N) && vector_rows(type, out, ldo, N);
+    with_type(type, [&](auto e) {
+        using E = decltype(e);
+        if (vec)
+            combine_kernel<E, true><<<token_grid(T), kCombineThreads, 0, stream>>>(g);
+        else
+            combine_kernel<E, false><<<token_grid(T), kCombineThreads, 0, stream>>>(g);
+    });
+    return launched();
+}
+
+int gemm_f32_combine_grad(int type, int T, int k, int N, int P, const int *position, const float *weight,
+                          const void *Y, int ldy, const void *dout, int lddo, void *dY, int lddy, float *dweight,
+                          hipStream_t stream)
+{
+    if (!known_type(type))
+        return GEMM_F32_ERR_TYPE;
+    if (T < 0 || k < 0 || N < 0 || P < 0)
+        return GEMM_F32_ERR_DIM;
+    if ((dweight != nullptr && short_ld(ldy, N)) || short_ld(lddo, N) || (dY != nullptr && short_ld(lddy, N)))
+        return GEMM_F32_ERR_LD;
+    if (T == 0 || k == 0 || (dY == nullptr && dweight == nullptr))
+        return GEMM_F32_OK;
+    if (position == nullptr || (N > 0 && (dout == nullptr || (dweight != nullptr && P > 0 && Y == nullptr))))
+        return GEMM_F32_ERR_NULL;
+    const int b = type_bytes(type);
+    if (!aligned_to(position, 4) || !aligned_to(weight, 4) || !aligned_to(Y, b) || !aligned_to(dout, b) ||
+        !aligned_to(dY, b) || !aligned_to(dweight, 4))
+        return GEMM_F32_ERR_ALIGN;
+    const CombineArgs g{position, weight, Y, dout, nullptr, dY, dweight, ldy, 0, lddo, lddy, T, k, N, P};
+    const bool vec = (dweight == nullptr || vector_rows(type, Y, ldy, N)) && vector_rows(type, dout, lddo, N) &&
+                     (dY == nullptr || vector_rows(type, dY, lddy, N));
+    with_type(type, [&](auto e) {
+        using E = decltype(e);
+        if (vec)
+            combine_grad_kernel<E, true><<<token_grid(T), kCombineThreads, 0, stream>>>(g);
+        else
+            combine_grad_kernel<E, false><<<token_grid(T), kCombineThreads, 0, stream>>>(g);
+    });
+    return launched();
+}
+
+}  // extern "C"

@@ -78,9 +78,15 @@ extern "C" {
 #define GEMM_F32_ERR_NULL    3  /* a pointer the shape needs is NULL            */
 #define GEMM_F32_ERR_LAUNCH  4  /* the HIP runtime refused the kernel launch    */
 #define GEMM_F32_ERR_CONFIG  5  /* unknown configuration index                 */
-#define GEMM_F32_ERR_ALIGN   6  /* a pointer is not 4-byte aligned              */
+#define GEMM_F32_ERR_ALIGN   6  /* a pointer is not aligned to its elements
+                                   (4 bytes for binary32)                      */
 #define GEMM_F32_ERR_SCRATCH 7  /* gemm_f32_ws_noalloc: the split plan needs
                                    more than GEMM_F32_SCRATCH_BYTES            */
+/* Of the entry points in gemm_f32_rows.h only: */
+#define GEMM_F32_ERR_TYPE    8  /* unknown element type                       */
+#define GEMM_F32_ERR_OPTION  9  /* an option outside its range                */
+#define GEMM_F32_ERR_WORKSPACE 10 /* the workspace is NULL, too small or not
+                                   16-byte aligned                             */
 
 /*
  * C := A . B on `stream`, with the kernel configuration chosen for the shape

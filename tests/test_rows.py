@@ -1,0 +1,541 @@
+"""The row-chosen products on the GPU against plain 64-bit implementations
+(rows_oracle.py).  Whole numbers are equal; sums are within the bound of binary32 summation plus
+one rounding to the output's type (rows_oracle.product_bound)."""
+import math
+import sys
+import zlib
+
+import pytest
+
+from dense_fp32_gemm_amd import binding as gb
+import rows_oracle as oracle
+
+torch = pytest.importorskip("torch")
+
+pytestmark = pytest.mark.gpu
+
+INF, NAN = math.inf, math.nan
+TYPES = [torch.float32, torch.bfloat16, torch.float16]
+IDS = ["f32", "bf16", "f16"]
+
+
+@pytest.fixture(scope="module")
+def dev():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    return torch.device("cuda:0")
+
+
+def say(*msg):
+    print("[rows]", *msg, file=sys.__stderr__, flush=True)
+
+
+def seeded(*key):
+    return torch.Generator().manual_seed(zlib.crc32(repr(key).encode()))
+
+
+def normal(g, *shape, dtype=torch.float32, scale=1.0):
+    return (torch.randn(*shape, generator=g) * scale).to(dtype)
+
+
+def strided(t, pad, dev, fill=NAN):
+    """A copy on the GPU whose rows are `pad` elements further apart, filled around."""
+    wide = torch.full((*t.shape[:-1], t.shape[-1] + pad), fill, dtype=t.dtype)
+    wide[..., :t.shape[-1]] = t
+    return wide.to(dev)[..., :t.shape[-1]]
+
+
+# --- routing ---------------------------------------------------------------------
+ROUTES = [
+    # T, E, k, options
+    (1, 1, 1, dict()), (1, 2, 2, dict(normalize=True)), (7, 8, 2, dict(score="sigmoid")), (33, 64, 4, dict(normalize=True, scale=2.5)),
+    (5, 65, 8, dict()), (9, 128, 6, dict(score="sigmoid", normalize=True, bias=True)), (6, 100, 64, dict(normalize=True)),
+    (11, 256, 8, dict(score="sigmoid", normalize=True, bias=True, groups=8, keep_groups=4, group_top=2, scale=2.5)),
+    (10, 160, 6, dict(groups=8, keep_groups=3, group_top=1)), (4, 512, 8, dict(bias=True)), (3, 1024, 10, dict(normalize=True)),
+    (3, 1000, 5, dict(score="sigmoid", bias=True, groups=40, keep_groups=7, group_top=2)),
+    (12, 64, 3, dict(groups=64, keep_groups=5, group_top=2, score="sigmoid", normalize=True)),
+    (8, 12, 12, dict(groups=4, keep_groups=2, group_top=2, bias=True, normalize=True)),
+]
+
+
+def masked_logits(g, T, E, dtype):
+    """Rows of each kind: ordinary, ties, masked in part, wholly, at the type's lowest value, +inf, NaN."""
+    l = normal(g, T, E, scale=1.5)
+    for t in range(T):
+        kind = t % 7
+        if kind == 1:
+            l[t] = torch.round(l[t])                            # ties
+        elif kind == 2:
+            l[t, torch.rand(E, generator=g) < 0.6] = -INF
+        elif kind == 3:
+            l[t] = -INF
+        elif kind == 4:
+            l[t, torch.rand(E, generator=g) < 0.7] = torch.finfo(dtype).min
+        elif kind == 5:
+            l[t, E // 2] = INF
+            l[t, 0] = -INF if E > 1 else 0.0
+        elif kind == 6:
+            l[t, E // 3] = NAN
+    return l.to(dtype)
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=IDS)
+@pytest.mark.parametrize("case", range(len(ROUTES)))
+def test_route(dev, dtype, case):
+    T, E, k, opt = ROUTES[case]
+    opt = dict(opt)
+    g = seeded("route", case)
+    l = masked_logits(g, T, E, dtype)
+    bias = normal(g, E, scale=0.1) if opt.pop("bias", False) else None
+    if bias is not None and E > 4:
+        bias[E // 4] = -INF
+    say("route", T, E, k, opt, dtype)
+    want_w, want_i, _ = oracle.route(l, k, bias=bias, **opt)
+    w, i = gb.route(strided(l, 3, dev), k, bias=None if bias is None else bias.to(dev), **opt)
+    assert torch.equal(i.cpu(), want_i)
+    # binary64 throughout (a few 2^-52 over at most 1024 terms), one rounding to binary32
+    oracle.close(w, want_w, want_w.abs() * (2.0 ** -24 + 2.0 ** -40) + 2.0 ** -150, "weight")
+
+
+GRADS = [(1, 1, 1), (9, 8, 2), (14, 65, 8), (7, 256, 8), (7, 1000, 64)]
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=IDS)
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("normalize", [False, True])
+@pytest.mark.parametrize("T,E,k", GRADS)
+def test_route_grad(dev, dtype, score, normalize, T, E, k):
+    g = seeded("grad", T, E, k)
+    l = normal(g, T, E, scale=1.5)
+    if T > 4 and E > 2:
+        l[1, torch.rand(E, generator=g) < 0.5] = -INF
+        l[2] = -INF
+        l[3, ::2] = torch.finfo(dtype).min
+    l = l.to(dtype)
+    dw = normal(g, T, k)
+    say("route_grad", T, E, k, score, normalize, dtype)
+    _, index, _ = oracle.route(l, k, score=score, normalize=normalize, scale=1.5)
+    want = oracle.route_grad(l, index, dw, score, normalize, 1.5)
+    full = torch.full((T, E + 5), 7.0, dtype=dtype, device=dev)
+    gb.route_grad(strided(l, 2, dev), index.to(dev), dw.to(dev), score=score, normalize=normalize, scale=1.5, out=full[:, :E])
+    assert (full[:, E:] == 7.0).all()
+    # both sides in binary64; their terms cancel to within 2^-52 of the row's largest dweight
+    room = 2.0 ** -44 * 1.5 * dw.double().abs().sum(1, keepdim=True)
+    oracle.close(full[:, :E], want, want.abs() * (oracle.STEP[dtype] + 2.0 ** -23) + room + oracle.TINY[dtype], "dlogits")
+
+
+def test_route_grad_adds_what_an_index_named_twice_gets(dev):
+    l = normal(seeded("twice"), 2, 6).to(dev)
+    dw = torch.tensor([[1.0, 2.0], [3.0, 4.0]], device=dev)
+    once = gb.route_grad(l, torch.tensor([[3, -1], [9, 2]], dtype=torch.int32, device=dev), dw, score="sigmoid")
+    s = torch.sigmoid(l.double())
+    want = torch.zeros(2, 6, dtype=torch.float64, device=dev)
+    want[0, 3] = (s * (1 - s))[0, 3]
+    want[1, 2] = 4 * (s * (1 - s))[1, 2]
+    oracle.close(once, want.cpu(), want.cpu().abs() * 2.0 ** -23, "skipped")
+    both = gb.route_grad(l, torch.tensor([[3, 3], [1, 1]], dtype=torch.int32, device=dev), dw, score="sigmoid")
+    want.zero_()
+    want[0, 3] = 3 * (s * (1 - s))[0, 3]
+    want[1, 1] = 7 * (s * (1 - s))[1, 1]
+    oracle.close(both, want.cpu(), want.cpu().abs() * 2.0 ** -23, "twice")
+
+
+@pytest.mark.parametrize("S,E", [(0, 3), (1, 1), (5, 4), (64, 64), (2047, 7), (2048, 1024), (2049, 3), (6000, 130), (20001, 1000)])
+def test_expert_map(dev, S, E):
+    g = seeded("map", S, E)
+    index = torch.randint(-1, E + 1, (S,), generator=g, dtype=torch.int32)      # -1 and E: left out
+    index[S // 2:] = torch.where(torch.rand(S - S // 2, generator=g) < 0.5, torch.zeros((), dtype=torch.int32), index[S // 2:])
+    say("expert_map", S, E)
+    for got, want in zip(gb.expert_map(index.to(dev), E), oracle.expert_map(index, E)):
+        assert torch.equal(got.cpu(), want)
+
+
+# --- products per group ------------------------------------------------------------
+def places(g, T, k, E, drop=0.0):
+    """offsets, order, position of a random choice, some slots left out, some experts without any."""
+    score = torch.rand(T, E, generator=g)
+    score[:, E // 2] = -1.0
+    index = torch.topk(score, k, dim=1).indices.int()
+    index[torch.rand(T, k, generator=g) < drop] = -1
+    return oracle.expert_map(index, E)
+
+
+SHAPES = [
+    # T, E, k, K, N
+    (1, 1, 1, 1, 1), (1, 4, 2, 8, 8), (5, 3, 1, 17, 33), (3, 8, 4, 64, 128), (40, 4, 2, 65, 63), (33, 70, 2, 96, 136),
+    (200, 3, 2, 129, 200), (300, 2, 2, 72, 256), (260, 5, 3, 256, 24), (9, 2, 1, 0, 5), (513, 2, 1, 128, 130), (700, 130, 2, 64, 64),
+]
+
+
+def grouped_want(X, W, offsets, order, k):
+    rows = oracle.rows_of(X, order, k)
+    want = torch.zeros(len(order), W.shape[2], dtype=torch.float64)
+    size = torch.zeros_like(want)
+    for e in range(W.shape[0]):
+        lo, hi = int(offsets[e]), int(offsets[e + 1])
+        want[lo:hi] = rows[lo:hi] @ W[e].double()
+        size[lo:hi] = rows[lo:hi].abs() @ W[e].double().abs()
+    return want, size
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=IDS)
+@pytest.mark.parametrize("pad", [0, 1, 8])
+@pytest.mark.parametrize("T,E,k,K,N", SHAPES)
+def test_grouped_and_its_gradients(dev, dtype, pad, T, E, k, K, N):
+    g = seeded("grouped", T, E, k, K, N)
+    offsets, order, position = places(g, T, k, E, drop=0.1)
+    P, used = len(order), int(offsets[-1])
+    X, W = normal(g, T, K, dtype=dtype), normal(g, E, K, N, dtype=dtype, scale=max(K, 1) ** -0.5)
+    dY = normal(g, P, N, dtype=dtype)
+    say("grouped", T, E, k, K, N, pad, dtype)
+    dX, dW_, dYd = strided(X, pad, dev), strided(W, pad, dev), strided(dY, pad, dev)
+    off, ord_ = offsets.to(dev), order.to(dev)
+
+    full = torch.full((P, N + pad), 7.0, dtype=dtype, device=dev)
+    gb.grouped_matmul(dX, dW_, off, order=ord_, per_row=k, out=full[:, :N])
+    want, size = grouped_want(X, W, offsets, order, k)
+    oracle.close(full[:used, :N], want[:used], oracle.product_bound(want, size, K + 1, dtype)[:used], "Y")
+    assert (full[used:] == 7.0).all() and (full[:, N:] == 7.0).all()
+
+    full = torch.full((P, K + pad), 7.0, dtype=dtype, device=dev)
+    gb.grouped_grad_x(dYd, dW_, off, out=full[:, :K])
+    want, size = torch.zeros(P, K, dtype=torch.float64), torch.zeros(P, K, dtype=torch.float64)
+    for e in range(E):
+        lo, hi = int(offsets[e]), int(offsets[e + 1])
+        want[lo:hi] = dY[lo:hi].double() @ W[e].double().t()
+        size[lo:hi] = dY[lo:hi].double().abs() @ W[e].double().abs().t()
+    oracle.close(full[:used, :K], want[:used], oracle.product_bound(want, size, N + 1, dtype)[:used], "dX")
+    assert (full[used:] == 7.0).all() and (full[:, K:] == 7.0).all()
+
+    full = torch.full((E, K, N + pad), 7.0, dtype=dtype, device=dev)
+    gb.grouped_grad_w(dX, dYd, off, order=ord_, per_row=k, out=full[:, :, :N])
+    rows = oracle.rows_of(X, order, k)
+    want, size = torch.zeros(E, K, N, dtype=torch.float64), torch.zeros(E, K, N, dtype=torch.float64)
+    for e in range(E):
+        lo, hi = int(offsets[e]), int(offsets[e + 1])
+        want[e] = rows[lo:hi].t() @ dY[lo:hi].double()
+        size[e] = rows[lo:hi].t().abs() @ dY[lo:hi].double().abs()
+    oracle.close(full[:, :, :N], want, oracle.product_bound(want, size, P + 1, dtype), "dW")
+    assert (full[:, :, N:] == 7.0).all()
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=IDS)
+@pytest.mark.parametrize("K,N", [(64, 136), (77, 61)])
+def test_grouped_without_order_and_rows_out_of_range(dev, dtype, K, N):
+    g = seeded("plain groups", K, N)
+    sizes = [0, 150, 1, 0, 17, 129, 0]
+    offsets = torch.tensor([0] + list(torch.tensor(sizes).cumsum(0)), dtype=torch.int32)
+    P = int(offsets[-1])
+    X, W = normal(g, P, K, dtype=dtype), normal(g, len(sizes), K, N, dtype=dtype)
+    identity = torch.arange(P, dtype=torch.int32)
+    want, size = grouped_want(X, W, offsets, identity, 1)
+    say("grouped without order", dtype, K, N)
+    got = gb.grouped_matmul(X.to(dev), W.to(dev), offsets.to(dev))
+    oracle.close(got, want, oracle.product_bound(want, size, K + 1, dtype), "Y")
+    wild = identity.clone()
+    wild[3], wild[60], wild[-1] = -5, P, 2 ** 31 - 1            # zero rows
+    want, size = grouped_want(X, W, offsets, wild, 1)
+    got = gb.grouped_matmul(X.to(dev), W.to(dev), offsets.to(dev), order=wild.to(dev))
+    oracle.close(got, want, oracle.product_bound(want, size, K + 1, dtype), "zero rows")
+    # offsets outside 0..P are clamped: nothing outside the operands is touched
+    far = torch.tensor([-7, 0, 150, 151, 151, 168, 297 + 1000, 9 * P], dtype=torch.int32)
+    got = gb.grouped_matmul(X.to(dev), W.to(dev), far.to(dev))
+    want, size = grouped_want(X, W, offsets, identity, 1)
+    oracle.close(got, want, oracle.product_bound(want, size, K + 1, dtype), "clamped")
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=IDS)
+def test_grouped_infinities_stay_in_their_group(dev, dtype):
+    g = seeded("inf groups")
+    offsets = torch.tensor([0, 20, 45], dtype=torch.int32)
+    X, W = normal(g, 45, 40, dtype=dtype), normal(g, 2, 40, 48, dtype=dtype)
+    X[44, 39] = NAN
+    W[0, 39, 47] = INF
+    say("inf groups", dtype)
+    got = gb.grouped_matmul(X.to(dev), W.to(dev), offsets.to(dev)).cpu()
+    assert got[44].isnan().all() and got[20:44].isfinite().all() and got[:20, :47].isfinite().all()
+    assert not got[:20, 47].isfinite().any()
+
+
+# --- weighted sums -------------------------------------------------------------------
+@pytest.mark.parametrize("dtype", TYPES, ids=IDS)
+@pytest.mark.parametrize("pad", [0, 1, 8])
+@pytest.mark.parametrize("T,k,N", [(1, 1, 1), (3, 2, 8), (5, 8, 1000), (17, 4, 2048), (2, 3, 5001), (70, 1, 72), (4, 0, 9), (300, 6, 130)])
+def test_combine_and_its_gradients(dev, dtype, pad, T, k, N):
+    g = seeded("combine", T, k, N)
+    P = T * k + 3
+    position = torch.randperm(P, generator=g)[:T * k].int().reshape(T, k)
+    if T * k > 2:
+        position[0, 0], position[-1, -1] = -1, P + 9
+    weight = normal(g, T, k)
+    Y, dout = normal(g, P, N, dtype=dtype), normal(g, T, N, dtype=dtype)
+    say("combine", T, k, N, pad, dtype)
+    for w in (weight, None):
+        ws = torch.ones(T, k, dtype=torch.float64) if w is None else weight.double()
+        want, size = torch.zeros(T, N, dtype=torch.float64), torch.zeros(T, N, dtype=torch.float64)
+        dY_want, dw_want, dw_size = torch.full((P, N), 7.0, dtype=torch.float64), torch.zeros(T, k, dtype=torch.float64), torch.zeros(T, k, dtype=torch.float64)
+        for t in range(T):
+            for j in range(k):
+                p = int(position[t, j])
+                if 0 <= p < P:
+                    want[t] += ws[t, j] * Y[p].double()
+                    size[t] += (ws[t, j] * Y[p].double()).abs()
+                    dY_want[p] = ws[t, j] * dout[t].double()
+                    dw_want[t, j] = (Y[p].double() * dout[t].double()).sum()
+                    dw_size[t, j] = (Y[p].double() * dout[t].double()).abs().sum()
+        wd = None if w is None else w.to(dev)
+        full = torch.full((T, N + pad), 7.0, dtype=dtype, device=dev)
+        gb.combine(strided(Y, pad, dev), position.to(dev), wd, out=full[:, :N])
+        oracle.close(full[:, :N], want, oracle.product_bound(want, size, k + 1, dtype), "out")
+        assert (full[:, N:] == 7.0).all()
+        full = torch.full((P, N + pad), 7.0, dtype=dtype, device=dev)
+        dY, dw = gb.combine_grad(strided(dout, pad, dev), strided(Y, pad, dev), position.to(dev), wd, out=full[:, :N])
+        # one product in binary32, rounded again to the type
+        oracle.close(dY, dY_want, dY_want.abs() * (oracle.STEP[dtype] + 2.0 ** -23) + oracle.TINY[dtype], "dY")
+        assert (full[:, N:] == 7.0).all()
+        oracle.close(dw, dw_want, oracle.product_bound(dw_want, dw_size, N + 1, torch.float32), "dweight")
+
+
+# --- adapters -----------------------------------------------------------------------
+ADAPTERS = [
+    # T, K, N, R, n
+    (1, 1, 1, 1, 1), (1, 64, 128, 16, 3), (3, 130, 70, 5, 2), (16, 256, 264, 8, 40), (17, 200, 72, 24, 4), (64, 512, 256, 32, 64),
+    (130, 96, 136, 33, 3), (300, 128, 200, 64, 5), (20, 64, 64, 200, 2), (50, 1000, 63, 4, 50), (5, 0, 8, 4, 2), (9, 40, 40, 0, 3),
+    (33, 4096, 256, 16, 30),
+]
+
+
+def adapters_want(X, W, A, B, adapter, scale):
+    want = X.double() @ W.double()
+    size = X.double().abs() @ W.double().abs()
+    for t, a in enumerate(adapter.tolist()):
+        if 0 <= a < A.shape[0]:
+            low = X[t].double() @ A[a].double()
+            want[t] += float(scale[a]) * (low @ B[a].double())
+            size[t] += abs(float(scale[a])) * ((X[t].double().abs() @ A[a].double().abs()) @ B[a].double().abs())
+    return want, size
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=IDS)
+@pytest.mark.parametrize("pad", [0, 1, 8])
+@pytest.mark.parametrize("runs", [False, True], ids=["mixed", "runs"])
+@pytest.mark.parametrize("T,K,N,R,n", ADAPTERS)
+def test_adapters(dev, dtype, pad, runs, T, K, N, R, n):
+    g = seeded("adapters", T, K, N, R, n)
+    X, W = normal(g, T, K, dtype=dtype), normal(g, K, N, dtype=dtype, scale=max(K, 1) ** -0.5)
+    A, B = normal(g, n, K, R, dtype=dtype, scale=max(K, 1) ** -0.5), normal(g, n, R, N, dtype=dtype)
+    adapter = torch.randint(-1, n + 1, (T,), generator=g, dtype=torch.int32)          # -1 and n: none
+    if runs:
+        adapter = adapter.sort().values
+    scale = 0.5 + torch.rand(n, generator=g)
+    say("adapters", T, K, N, R, n, pad, runs, dtype)
+    want, size = adapters_want(X, W, A, B, adapter, scale)
+    full = torch.full((T, N + pad), 7.0, dtype=dtype, device=dev)
+    gb.adapter_matmul(strided(X, pad, dev), strided(W, pad, dev), strided(A, pad, dev), strided(B, pad, dev), adapter.to(dev),
+                      scale.to(dev), out=full[:, :N])
+    # the two low-rank sums follow one another; U is kept to 2^-16 (bf16: high + low parts) of its row's largest at least
+    bound = oracle.product_bound(want, size, K + 2 * R + 4, dtype)
+    low_top = torch.zeros(T, 1, dtype=torch.float64)
+    for t, a in enumerate(adapter.tolist()):
+        if 0 <= a < n and R:
+            low_top[t] = float(scale[a]) * (X[t].double() @ A[a].double()).abs().max() * B[a].double().abs().sum(0).max()
+    oracle.close(full[:, :N], want, bound + (0 if dtype == torch.float32 else 2.0 ** -16) * low_top, "Y")
+    assert (full[:, N:] == 7.0).all()
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=IDS)
+@pytest.mark.parametrize("T", [3, 40, 150])
+def test_adapters_infinities_stay_with_their_requests(dev, dtype, T):
+    g = seeded("inf adapters", T)
+    X, W = normal(g, T, 64, dtype=dtype), normal(g, 64, 72, dtype=dtype)
+    A, B = normal(g, 3, 64, 8, dtype=dtype), normal(g, 3, 8, 72, dtype=dtype)
+    A[1, 5, 2], B[1, 3, 4] = INF, NAN
+    adapter = (torch.arange(T) % 4 - 1).int()
+    say("inf adapters", T, dtype)
+    got = gb.adapter_matmul(X.to(dev), W.to(dev), A.to(dev), B.to(dev), adapter.to(dev)).cpu()
+    assert got[adapter != 1].isfinite().all()
+    assert not got[adapter == 1][:, 4].isfinite().any()
+    want, size = adapters_want(X, W, A, B, torch.where(adapter == 1, -1, adapter), torch.ones(3))
+    keep = adapter != 1
+    oracle.close(got[keep], want[keep], (oracle.product_bound(want, size, 64 + 20, dtype) + 2.0 ** -12 * size)[keep], "others")
+
+
+@pytest.mark.parametrize("factor", [2.0 ** -30, 2.0 ** 14])
+def test_adapters_half_precision_range(dev, factor):
+    """The low-rank intermediate may lie outside the 16-bit type's range."""
+    g = seeded("range")
+    X, W = normal(g, 20, 64, dtype=torch.float16, scale=2.0 ** -3), normal(g, 64, 40, dtype=torch.float16)
+    A, B = normal(g, 2, 64, 8, dtype=torch.float16), normal(g, 2, 8, 40, dtype=torch.float16, scale=2.0 ** -8)
+    adapter = (torch.arange(20) % 2).int()
+    scale = torch.tensor([factor, factor])
+    say("half range", factor)
+    W *= 0
+    want, size = adapters_want(X, W, A, B, adapter, scale)
+    got = gb.adapter_matmul(X.to(dev), W.to(dev), A.to(dev), B.to(dev), adapter.to(dev), scale.to(dev))
+    oracle.close(got, want, oracle.product_bound(want, size, 64 + 20, torch.float16) + 2.0 ** -16 * size, "Y")
+
+
+# --- together, as a layer uses them ----------------------------------------------------
+def test_expert_layer_forward_and_backward(dev):
+    """Router, map, two expert products with silu between, weighted sum; all gradients against 64-bit autograd."""
+    T, E, k, K, N = 150, 6, 2, 64, 96
+    g = seeded("layer")
+    X, Wr = normal(g, T, K), normal(g, K, E, scale=K ** -0.5)
+    W1, W2 = normal(g, E, K, N, scale=K ** -0.5), normal(g, E, N, K, scale=N ** -0.5)
+    up = normal(g, T, K)
+    Xd, Wrd, W1d, W2d, upd = (t.to(dev) for t in (X, Wr, W1, W2, up))
+
+    logits = gb.matmul(Xd, Wrd)
+    weight, index = gb.route(logits, k, normalize=True)
+    offsets, order, position = gb.expert_map(index, E)
+    h = gb.grouped_matmul(Xd, W1d, offsets, order=order, per_row=k)
+    a = torch.nn.functional.silu(h)
+    y = gb.grouped_matmul(a, W2d, offsets)
+    out = gb.combine(y, position, weight)
+
+    dy, dweight = gb.combine_grad(upd, y, position, weight)
+    da = gb.grouped_grad_x(dy, W2d, offsets)
+    dW2 = gb.grouped_grad_w(a, dy, offsets)
+    s = torch.sigmoid(h)
+    dh = da * s * (1 + h * (1 - s))
+    dW1 = gb.grouped_grad_w(Xd, dh, offsets, order=order, per_row=k)
+    dX = gb.combine(gb.grouped_grad_x(dh, W1d, offsets), position)
+    dlogits = gb.route_grad(logits, index, dweight, normalize=True)
+    dX = dX + gb.matmul(dlogits, Wrd.t().contiguous())
+    dWr = gb.matmul(Xd.t().contiguous(), dlogits)
+
+    leaves = [t.double().requires_grad_(True) for t in (X, Wr, W1, W2)]
+    x, wr, w1, w2 = leaves
+    at = index.cpu().long()
+    w = oracle.route_weight_of(x @ wr, index.cpu(), "softmax", True, 1.0)
+    rows = []
+    for j in range(k):
+        hj = torch.bmm(x.unsqueeze(1), w1[at[:, j]])
+        rows.append(w[:, j:j + 1] * torch.bmm(torch.nn.functional.silu(hj), w2[at[:, j]]).squeeze(1))
+    ref = rows[0] + rows[1]
+    (ref * up.double()).sum().backward()
+    # a chain of binary32 sums of some hundred terms of size about 1: relative to the largest element
+    for name, got, want in (("out", out, ref.detach()), ("dX", dX, x.grad), ("dWr", dWr, wr.grad), ("dW1", dW1, w1.grad),
+                            ("dW2", dW2, w2.grad)):
+        oracle.close(got, want, 2.0 ** -23 * 1000 * want.abs().max(), name)
+
+
+def test_layer_gradient_against_differences(dev):
+    """The kernels' own forward pass, differenced along random directions of the expert weights."""
+    T, E, k, K, N = 40, 4, 2, 32, 32
+    g = seeded("differences")
+    X, W, up = normal(g, T, K).to(dev), normal(g, E, K, N).to(dev), normal(g, T, N).to(dev)
+    weight, index = gb.route(normal(g, T, E).to(dev), k, normalize=True)
+    offsets, order, position = gb.expert_map(index, E)
+
+    def value(w):
+        y = gb.grouped_matmul(X, w, offsets, order=order, per_row=k)
+        return float((gb.combine(y, position, weight).double() * up.double()).sum())
+    y = gb.grouped_matmul(X, W, offsets, order=order, per_row=k)
+    dy, _ = gb.combine_grad(up, y, position, weight)
+    dW = gb.grouped_grad_w(X, dy, offsets, order=order, per_row=k)
+    for trial in range(4):
+        d = normal(g, E, K, N).to(dev)
+        step = 0.5                                   # the value is linear in W: no truncation error
+        diff = (value(W + step * d) - value(W - step * d)) / (2 * step)
+        want = float((dW.double() * d.double()).sum())
+        # T*N outputs of size under K, each off by under 2^-23 * 2K relative to sqrt(K): well under 1e-2 in all
+        assert abs(diff - want) < 1e-2 + 1e-4 * abs(want)
+
+
+def test_calls_on_another_stream_and_in_a_graph(dev):
+    T, E, k, K, N, R = 70, 8, 2, 64, 72, 8
+    g = seeded("stream")
+    X, W = normal(g, T, K, dtype=torch.bfloat16).to(dev), normal(g, E, K, N, dtype=torch.bfloat16).to(dev)
+    A, B = normal(g, 3, K, R, dtype=torch.bfloat16).to(dev), normal(g, 3, R, N, dtype=torch.bfloat16).to(dev)
+    adapter = (torch.arange(T) % 4 - 1).int().to(dev)
+    l = normal(g, T, E).to(dev)
+
+    def everything(stream=None):
+        weight, index = gb.route(l, k, normalize=True, stream=stream)
+        offsets, order, position = gb.expert_map(index, E, stream=stream)
+        y = gb.grouped_matmul(X, W, offsets, order=order, per_row=k, stream=stream)
+        out = gb.combine(y, position, weight, stream=stream)
+        dy, dw = gb.combine_grad(out, y, position, weight, stream=stream)
+        dx = gb.grouped_grad_x(dy, W, offsets, stream=stream)
+        dW = gb.grouped_grad_w(X, dy, offsets, order=order, per_row=k, stream=stream)
+        dl = gb.route_grad(l, index, dw, normalize=True, stream=stream)
+        z = gb.adapter_matmul(X, W[0], A, B, adapter, stream=stream)
+        return [weight, index, offsets, order, position, y, out, dy, dw, dx, dW, dl, z]
+
+    say("eager")
+    want = [t.clone() for t in everything()]
+    torch.cuda.synchronize()
+    say("another stream")
+    side = torch.cuda.Stream()
+    for a, b in zip(want, everything(side)):
+        side.synchronize()
+        assert torch.equal(a, b)
+    say("captured")
+    graph = torch.cuda.CUDAGraph()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        everything()
+    torch.cuda.current_stream().wait_stream(side)
+    with torch.cuda.graph(graph):
+        got = everything()
+    for replay in range(3):
+        l.copy_(normal(seeded("replay", replay), T, E).to(dev))
+        graph.replay()
+        torch.cuda.synchronize()
+        mine = everything()
+        torch.cuda.synchronize()
+        for a, b in zip(mine, got):
+            assert torch.equal(a, b)
+
+
+def test_far_rows(dev):
+    """Offsets past 2^32 bytes: rows far apart in one buffer."""
+    ld = (1 << 31) // 64 + 8                                     # 33 rows span over 2^31 elements
+    buf = torch.empty(66 * ld, dtype=torch.bfloat16, device=dev)
+    X = buf.as_strided((66, 24), (ld, 1))
+    g = seeded("far")
+    x, W = normal(g, 66, 24, dtype=torch.bfloat16), normal(g, 2, 24, 40, dtype=torch.bfloat16)
+    X.copy_(x.to(dev))
+    offsets = torch.tensor([0, 5, 66], dtype=torch.int32)
+    say("far rows")
+    want, size = grouped_want(x, W, offsets, torch.arange(66, dtype=torch.int32), 1)
+    got = gb.grouped_matmul(X, W.to(dev), offsets.to(dev))
+    oracle.close(got, want, oracle.product_bound(want, size, 25, torch.bfloat16), "Y")
+    got = gb.adapter_matmul(X, W[0].to(dev), torch.zeros(1, 24, 8, dtype=torch.bfloat16, device=dev),
+                            torch.zeros(1, 8, 40, dtype=torch.bfloat16, device=dev), torch.zeros(66, dtype=torch.int32, device=dev))
+    want, size = grouped_want(x, W[:1], torch.tensor([0, 66], dtype=torch.int32), torch.arange(66, dtype=torch.int32), 1)
+    oracle.close(got, want, oracle.product_bound(want, size, 25, torch.bfloat16), "adapters")
+
+
+def test_refusals_with_gpu_tensors(dev):
+    x = torch.zeros(4, 8, device=dev)
+    o = torch.zeros(3, dtype=torch.int32, device=dev)
+    W = torch.zeros(2, 8, 5, device=dev)
+    with pytest.raises(gb.GemmError) as e:
+        gb.route(x, 9)
+    assert e.value.status == gb.GEMM_F32_ERR_DIM
+    with pytest.raises(ValueError):
+        gb.route(x, 2, score="tanh")
+    with pytest.raises(TypeError):
+        gb.route(x, 2, bias=torch.zeros(8, dtype=torch.float64, device=dev))
+    with pytest.raises(ValueError):
+        gb.route(x, 2, bias=torch.zeros(7, device=dev))
+    with pytest.raises(TypeError):
+        gb.expert_map(torch.zeros(4, dtype=torch.int64, device=dev), 3)
+    with pytest.raises(TypeError):
+        gb.grouped_matmul(x, W.half(), o)
+    with pytest.raises(ValueError):
+        gb.grouped_matmul(x, W[:, :7], o)
+    with pytest.raises(ValueError):
+        gb.grouped_matmul(x, W.transpose(1, 2).contiguous().transpose(1, 2), o)
+    with pytest.raises(ValueError):
+        gb.grouped_matmul(x, W[:1].expand(2, 8, 5), o)
+    with pytest.raises(TypeError):
+        gb.grouped_matmul(x, W, o.cpu())
+    with pytest.raises(ValueError):
+        gb.combine(x, torch.zeros(4, 3, dtype=torch.int32, device=dev)[:, :2])
+    with pytest.raises(gb.GemmError) as e:
+        gb.adapter_matmul(x, W[0], torch.zeros(1, 8, 4, device=dev), torch.zeros(1, 4, 5, device=dev), o[:1].expand(4).contiguous(),
+                          workspace=torch.zeros(8, dtype=torch.uint8, device=dev))
+    assert e.value.status == gb.GEMM_F32_ERR_WORKSPACE

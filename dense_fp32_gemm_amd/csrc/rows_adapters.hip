@@ -39,9 +39,29 @@ struct AdapterArgs {
 // Rank indices a panel of the up-projection holds: 16-bit panels are 64 deep,
 // 32 high parts and then the 32 low parts of the same ranks.
 template <class E>
-constexpr int ranks_deep() { return 32; }
+constexpr int panel_deep() { return 128 / E::kBytes; }
 template <class E>
-int factor_depth(int R) { return (int)ceil_div(R, 32) * deep<E>(); }
+int factor_depth(int R) { return (int)ceil_div(R, 32) * panel_deep<E>(); }
+
+// B_a's rows as the second operand of the up-projection: twice per panel for
+// the 16-bit types.
+template <class E, int RN, int NT>
+struct UpRows : Across<E, RN, NT> {
+    using Base = Across<E, RN, NT>;
+    int R;
+    __device__ inline UpRows(const typename E::T *base_, int tid_, int depth, int64_t ld_, int first_, int cols_, int R_)
+        : Base(base_, tid_, depth, ld_, first_, cols_), R(R_)
+    {
+    }
+    __device__ inline int rank(int i, int k0) const { return k0 / panel_deep<E>() * 32 + this->krow(i) % 32; }
+    __device__ inline int64_t step() const { return 32 * this->ld; }
+    __device__ inline bool partial(int k0) const { return (k0 / panel_deep<E>() + 1) * 32 > R; }
+    __device__ inline int left(int i, int k0) const { return rank(i, k0) < R ? Base::left(i, k0) : 0; }
+    __device__ inline int64_t offset(int i, int) const
+    {
+        return this->krow(i) % 32 * this->ld + (int64_t)this->col(i) * E::kBytes;
+    }
+};
 
 // Calls f(a, members) for each adapter a among up to 128 rows, members being
 // bit masks of its rows.  which: the adapter of row `lane` and of row 64 + lane, -1:
@@ -67,7 +87,7 @@ __device__ inline int adapter_of(const AdapterArgs &g, int64_t t, bool there)
 }
 
 // One wave: U of 16 rows over split_k of K.  RN: rank rounded up.
-template <class E, int RN, bool VEC>
+template <class E, int RN, bool DMA>
 __global__ __launch_bounds__(kWave) void down_kernel(AdapterArgs g)
 {
     using Ti = Tile<E, true, false, 16, RN, 1, 1>;
@@ -77,14 +97,13 @@ __global__ __launch_bounds__(kWave) void down_kernel(AdapterArgs g)
     const int t0 = blockIdx.x * 16, k0 = blockIdx.y * g.split_k, K = min(g.split_k, g.K - k0);
     const int which = adapter_of(g, t0 + lane, lane < 16 && t0 + lane < g.T);
     each_adapter<16>(which, -1, [&](int a, uint64_t members, uint64_t) {
-        const T *X = (const T *)g.X + t0 * g.ldx + k0;
-        const T *A = (const T *)g.A + a * g.stride_a + k0 * g.lda;
         Ti tile;
         tile.clear();
-        const Along<E, 16, kWave> x(lane, K, [&](int r) { return members >> r & 1 ? X + r * g.ldx : nullptr; });
-        const auto w = across<E, RN, kWave>(lane, K, 0, g.R, [&](int k) { return A + k * g.lda; });
+        const Along<E, 16, kWave> x((const T *)g.X + t0 * g.ldx + k0, lane, K,
+                                    [&](int, int r) { return members >> r & 1 ? r * g.ldx * E::kBytes : -1; });
+        const Across<E, RN, kWave> w((const T *)g.A + a * g.stride_a + k0 * g.lda, lane, K, g.lda, 0, g.R);
         __syncthreads();
-        sum_panels<E, VEC>(tile, K, x, w, lds, lane, 0, 0);
+        sum_panels<E, DMA>(tile, K, x, w, lds, lane, 0, 0);
         tile.each(0, 0, lane, [&](int r, int c, f32x4 v) {
             if (members >> r & 1) {
                 float *u = g.partial + ((int64_t)blockIdx.y * g.T + t0 + r) * g.R + c;
@@ -153,7 +172,7 @@ __global__ __launch_bounds__(kFactorThreads) void factor_kernel(AdapterArgs g)
     }
 }
 
-template <class E, int BM, int BN, int WM, int WN, bool VEC>
+template <class E, int BM, int BN, int WM, int WN, bool DMA>
 __global__ __launch_bounds__(WM *WN *kWave) void adapters_kernel(AdapterArgs g)
 {
     using Ti = Tile<E, true, false, BM, BN, WM, WN>;
@@ -168,27 +187,24 @@ __global__ __launch_bounds__(WM *WN *kWave) void adapters_kernel(AdapterArgs g)
 
     Ti tile;
     tile.clear();
-    const T *X = (const T *)g.X, *W = (const T *)g.W;
     {
-        const Along<E, BM, NT> x(tid, g.K, [&](int r) { return m0 + r < g.T ? X + (m0 + r) * g.ldx : nullptr; });
-        const auto w = across<E, BN, NT>(tid, g.K, n0, g.N, [&](int k) { return W + k * g.ldw; });
-        sum_panels<E, VEC>(tile, g.K, x, w, lds, tid, wm, wn);
+        const Along<E, BM, NT> x((const T *)g.X + m0 * g.ldx, tid, g.K,
+                                 [&](int, int r) { return m0 + r < g.T ? r * g.ldx * E::kBytes : -1; });
+        const Across<E, BN, NT> w((const T *)g.W, tid, g.K, g.ldw, n0, g.N);
+        sum_panels<E, DMA>(tile, g.K, x, w, lds, tid, wm, wn);
     }
     if (g.R > 0 && g.n > 0) {
         const int which0 = adapter_of(g, m0 + lane, lane < BM && m0 + lane < g.T);
         const int which1 = adapter_of(g, m0 + 64 + lane, 64 + lane < BM && m0 + 64 + lane < g.T);
         each_adapter<BM>(which0, which1, [&](int a, uint64_t members0, uint64_t members1) {
             auto member = [&](int r) { return (r < 64 ? members0 >> r : members1 >> (r - 64)) & 1; };
-            const T *U = (const T *)g.factor, *B = (const T *)g.B + a * g.stride_b;
-            const Along<E, BM, NT> u(tid, g.depth, [&](int r) { return member(r) ? U + (int64_t)(m0 + r) * g.depth : nullptr; });
-            const auto b = across<E, BN, NT>(tid, g.depth, n0, g.N, [&](int k) {
-                const int r = E::kBytes == 4 ? k : k / 64 * 32 + k % 32;
-                return r < g.R ? B + r * g.ldb : nullptr;
-            });
+            const Along<E, BM, NT> u((const T *)g.factor + (int64_t)m0 * g.depth, tid, g.depth,
+                                     [&](int, int r) { return member(r) ? (int64_t)r * g.depth * E::kBytes : -1; });
+            const UpRows<E, BN, NT> b((const T *)g.B + a * g.stride_b, tid, g.depth, g.ldb, n0, g.N, g.R);
             Ti add;
             add.clear();
             __syncthreads();
-            sum_panels<E, VEC>(add, g.depth, u, b, lds, tid, wm, wn);
+            sum_panels<E, DMA>(add, g.depth, u, b, lds, tid, wm, wn);
 #pragma unroll
             for (int m = 0; m < Ti::kFm; ++m) {
                 const int r = wm * (BM / WM) + Ti::Fa::row_of(m, lane % 16);
@@ -207,7 +223,7 @@ __global__ __launch_bounds__(WM *WN *kWave) void adapters_kernel(AdapterArgs g)
     tile.each(wm, wn, lane, [&](int r, int c, f32x4 v) {
         const int m = m0 + r, n = n0 + c;
         if (m < g.T && n < g.N)
-            store4<E, VEC>(Y + m * g.ldy + n, v, g.N - n);
+            store4<E, DMA>(Y + m * g.ldy + n, v, g.N - n);
     });
 }
 
@@ -235,31 +251,31 @@ Workspace workspace(int T, int K, int R)
 {
     Workspace w;
     w.partial = 0;
-    w.factor = round16((size_t)down_splits(T, K, deep<E>()) * (size_t)T * (size_t)R * 4);
+    w.factor = round16((size_t)down_splits(T, K, panel_deep<E>()) * (size_t)T * (size_t)R * 4);
     w.unscale = w.factor + round16((size_t)T * (size_t)factor_depth<E>(R) * E::kBytes);
     w.bytes = w.unscale + round16((size_t)T * 4);
     return w;
 }
 
 template <class E, int RN>
-void launch_down(const AdapterArgs &g, bool vec, hipStream_t stream)
+void launch_down(const AdapterArgs &g, bool dma, hipStream_t stream)
 {
     const dim3 grid((unsigned)ceil_div(g.T, 16), (unsigned)g.splits);
-    if (vec)
+    if (dma)
         down_kernel<E, RN, true><<<grid, kWave, 0, stream>>>(g);
     else
         down_kernel<E, RN, false><<<grid, kWave, 0, stream>>>(g);
 }
 
 template <class E, int BM, int BN, int WM, int WN>
-int launch_tiles(AdapterArgs g, bool vec, hipStream_t stream)
+int launch_tiles(AdapterArgs g, bool dma, hipStream_t stream)
 {
     const int64_t tm = ceil_div(g.T, BM), tn = ceil_div(g.N, BN);
     if (tm * tn > (int64_t)UINT32_MAX / 256)
         return GEMM_F32_ERR_DIM;
     g.tiles_m = (int)tm;
     g.tiles_n = (int)tn;
-    if (vec)
+    if (dma)
         adapters_kernel<E, BM, BN, WM, WN, true><<<(int)(tm * tn), WM * WN * kWave, 0, stream>>>(g);
     else
         adapters_kernel<E, BM, BN, WM, WN, false><<<(int)(tm * tn), WM * WN * kWave, 0, stream>>>(g);
@@ -270,11 +286,6 @@ int launch_tiles(AdapterArgs g, bool vec, hipStream_t stream)
 constexpr int kMaxTokens = 1 << 25;
 
 bool short_ld(int64_t ld, int cols) { return ld < at_least_one(cols); }
-bool vector_rows(int type, const void *p, int64_t ld, int64_t cols)
-{
-    const int chunk = 16 / type_bytes(type);
-    return aligned_to(p, 16) && ld % chunk == 0 && cols % chunk == 0;
-}
 
 }  // namespace
 }  // namespace rows
@@ -319,9 +330,10 @@ int gemm_f32_adapters(int type, int T, int N, int K, int R, int n, const void *X
         return GEMM_F32_ERR_WORKSPACE;
 
     const int chunk = 16 / b;
-    const bool vec_main = vector_rows(type, X, ldx, K) && vector_rows(type, W, ldw, N) && vector_rows(type, Y, ldy, N) &&
-                          (!low || (vector_rows(type, B, ldb, N) && (n == 1 || stride_b % chunk == 0)));
-    const bool vec_down = vector_rows(type, X, ldx, K) && vector_rows(type, A, lda, R) && (n == 1 || stride_a % chunk == 0);
+    const bool dma_x = dma_rows(type, X, ldx, K, 256);
+    const bool dma_main = dma_x && dma_rows(type, W, ldw, N, 256) && dma_rows(type, Y, ldy, N, 0) &&
+                          (!low || (dma_rows(type, B, ldb, N, 256) && (n == 1 || stride_b % chunk == 0)));
+    const bool dma_down = dma_x && dma_rows(type, A, lda, R, 256) && (n == 1 || stride_a % chunk == 0);
     int rc = GEMM_F32_OK;
     with_type(type, [&](auto e) {
         using E = decltype(e);
@@ -338,21 +350,21 @@ int gemm_f32_adapters(int type, int T, int N, int K, int R, int n, const void *X
             g.factor = (char *)ws + w.factor;
             g.unscale = (float *)((char *)ws + w.unscale);
             g.depth = factor_depth<E>(R);
-            g.splits = down_splits(T, K, deep<E>());
+            g.splits = down_splits(T, K, panel_deep<E>());
             // whole panels, so that every split starts on a 16-byte boundary
-            g.split_k = (int)(ceil_div(ceil_div(K, g.splits), deep<E>()) * deep<E>());
+            g.split_k = (int)(ceil_div(ceil_div(K, g.splits), panel_deep<E>()) * panel_deep<E>());
             if (g.split_k > 0)
                 g.splits = (int)ceil_div(K, g.split_k);
             if (R <= 16)
-                launch_down<E, 16>(g, vec_down, stream);
+                launch_down<E, 16>(g, dma_down, stream);
             else if (R <= 32)
-                launch_down<E, 32>(g, vec_down, stream);
+                launch_down<E, 32>(g, dma_down, stream);
             else if (R <= 64)
-                launch_down<E, 64>(g, vec_down, stream);
+                launch_down<E, 64>(g, dma_down, stream);
             else if (R <= 128)
-                launch_down<E, 128>(g, vec_down, stream);
+                launch_down<E, 128>(g, dma_down, stream);
             else
-                launch_down<E, 256>(g, vec_down, stream);
+                launch_down<E, 256>(g, dma_down, stream);
             factor_kernel<E><<<(unsigned)ceil_div(T, kFactorThreads / kWave), kFactorThreads, 0, stream>>>(g);
             rc = launched();
             if (rc != GEMM_F32_OK)
@@ -360,7 +372,7 @@ int gemm_f32_adapters(int type, int T, int N, int K, int R, int n, const void *X
         }
         // Up to 16 rows: tiles of 16, which read W once without spending
         // matrix instructions on rows that are not there.
-        rc = T <= 16 ? launch_tiles<E, 16, 128, 1, 4>(g, vec_main, stream) : launch_tiles<E, 128, 128, 2, 2>(g, vec_main, stream);
+        rc = T <= 16 ? launch_tiles<E, 16, 128, 1, 4>(g, dma_main, stream) : launch_tiles<E, 128, 128, 2, 2>(g, dma_main, stream);
     });
     return rc;
 }

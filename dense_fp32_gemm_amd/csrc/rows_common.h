@@ -62,6 +62,23 @@ inline int at_least_one(int n) { return n > 1 ? n : 1; }
 
 inline int launched() { return hipGetLastError() == hipSuccess ? GEMM_F32_OK : GEMM_F32_ERR_LAUNCH; }
 
+// Division of 0 .. 2^31 - 1 by a number 1 .. 2^31 - 1 known on the host:
+// n / d = n * m >> 31 + L with L = ceil(log2 d), m = ceil(2^(31+L) / d).  m d exceeds
+// 2^(31+L) by less than d <= 2^L, so the quotient by less than n / 2^31 < 1 /d's share of it.
+struct Divisor {
+    uint32_t m;
+    int shift;
+    explicit Divisor(int d)
+    {
+        int L = 0;
+        while (((int64_t)1 << L) < d)
+            ++L;
+        shift = 31 + L;
+        m = (uint32_t)(((((uint64_t)1 << shift) + (uint64_t)d - 1)) / (uint64_t)d);
+    }
+    __device__ inline int of(int n) const { return (int)((uint64_t)(uint32_t)n * m >> shift); }
+};
+
 // 16 bytes of a row that has `left` elements from p on, +0 behind them.
 // Global loads of 16 bytes may start at any element of the types here; rows
 // that are 16-byte aligned and a whole number of chunks long (VEC) need no

@@ -20,7 +20,8 @@ struct GroupedArgs {
     void *C;                 // Y, dX, dW
     int64_t lda, ldb, ldc;
     int64_t stride;          // of W (of dW for grad_w)
-    int G, P, per_row, rows; // rows: of X
+    int G, P, rows;          // rows: of X
+    Divisor per_row;
     int M, N, K;             // grad_w: M x N of dW; else columns N of C, summed K
     int tiles_n;
     int xcds;
@@ -59,7 +60,7 @@ __device__ inline bool find_tile(const GroupedArgs &g, int bm, int &group, int &
         total += n;
     }
     // Rising offsets never have more tiles than workgroups; others are cut there.
-    total = min(total, (int)(gridDim.x / g.tiles_n)) * g.tiles_n;
+    total = __builtin_amdgcn_readfirstlane(min(total, (int)(gridDim.x / g.tiles_n)) * g.tiles_n);
     if ((int)blockIdx.x >= total)
         return false;
     const int t = die_contiguous(blockIdx.x, total, g.xcds);
@@ -93,19 +94,7 @@ __device__ inline bool find_tile(const GroupedArgs &g, int bm, int &group, int &
     return false;
 }
 
-// Row of X at place p, NULL if there is none.
-template <class T>
-__device__ inline const T *row_at(const GroupedArgs &g, const T *X, int p)
-{
-    int64_t r = p;
-    if (g.order != nullptr) {
-        const int s = g.order[p];
-        r = s < 0 ? -1 : s / g.per_row;
-    }
-    return r >= 0 && r < g.rows ? X + r * g.lda : nullptr;
-}
-
-template <class E, Op OP, int BM, int BN, int WM, int WN, bool VEC>
+template <class E, Op OP, int BM, int BN, int WM, int WN, bool DMA>
 __global__ __launch_bounds__(WM *WN *kWave) void grouped_kernel(GroupedArgs g)
 {
     constexpr bool kAlongA = OP != kGradW, kAlongB = OP == kGradX;
@@ -127,6 +116,11 @@ __global__ __launch_bounds__(WM *WN *kWave) void grouped_kernel(GroupedArgs g)
     } else if (!find_tile(g, BM, group, lo, hi, tm, tn)) {
         return;                                      // the whole workgroup
     }
+    group = __builtin_amdgcn_readfirstlane(group);
+    lo = __builtin_amdgcn_readfirstlane(lo);
+    hi = __builtin_amdgcn_readfirstlane(hi);
+    tm = __builtin_amdgcn_readfirstlane(tm);
+    tn = __builtin_amdgcn_readfirstlane(tn);
     const int m0 = OP == kGradW ? tm * BM : lo + tm * BM;
     const int m_end = OP == kGradW ? g.M : hi;
     const int n0 = tn * BN;
@@ -135,26 +129,43 @@ __global__ __launch_bounds__(WM *WN *kWave) void grouped_kernel(GroupedArgs g)
     Ti tile;
     tile.clear();
     if constexpr (OP == kForward) {
-        const T *W = B + group * g.stride;
-        const Along<E, BM, NT> a(tid, g.K, [&](int r) { return m0 + r < m_end ? row_at(g, A, m0 + r) : nullptr; });
-        const auto b = across<E, BN, NT>(tid, g.K, n0, g.N, [&](int k) { return W + k * g.ldb; });
-        sum_panels<E, VEC>(tile, g.K, a, b, lds, tid, wm, wn);
+        using Src = Along<E, BM, NT>;
+        int row[Src::kCount];                        // of X; the loads side by side, then the rest
+        if (g.order != nullptr) {
+#pragma unroll
+            for (int i = 0; i < Src::kCount; ++i)
+                row[i] = g.order[min(m0 + Src::row_of(i, tid), m_end - 1)];
+#pragma unroll
+            for (int i = 0; i < Src::kCount; ++i)
+                row[i] = row[i] < 0 ? INT32_MAX : g.per_row.of(row[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < Src::kCount; ++i)
+                row[i] = m0 + Src::row_of(i, tid);
+        }
+        const Src a(A, tid, g.K,
+                    [&](int i, int r) { return m0 + r < m_end && row[i] < g.rows ? row[i] * g.lda * E::kBytes : -1; });
+        const Across<E, BN, NT> b(B + group * g.stride, tid, g.K, g.ldb, n0, g.N);
+        sum_panels<E, DMA>(tile, g.K, a, b, lds, tid, wm, wn);
     } else if constexpr (OP == kGradX) {
-        const T *W = B + group * g.stride;
-        const Along<E, BM, NT> a(tid, g.K, [&](int r) { return m0 + r < m_end ? A + (m0 + r) * g.lda : nullptr; });
-        const Along<E, BN, NT> b(tid, g.K, [&](int r) { return n0 + r < g.N ? W + (n0 + r) * g.ldb : nullptr; });
-        sum_panels<E, VEC>(tile, g.K, a, b, lds, tid, wm, wn);
+        const Along<E, BM, NT> a(A + m0 * g.lda, tid, g.K,
+                                 [&](int, int r) { return m0 + r < m_end ? r * g.lda * E::kBytes : -1; });
+        const Along<E, BN, NT> b(B + group * g.stride + n0 * g.ldb, tid, g.K,
+                                 [&](int, int r) { return n0 + r < g.N ? r * g.ldb * E::kBytes : -1; });
+        sum_panels<E, DMA>(tile, g.K, a, b, lds, tid, wm, wn);
     } else {
-        const auto a = across<E, BM, NT>(tid, hi - lo, m0, g.M, [&](int k) { return row_at(g, A, lo + k); });
-        const auto b = across<E, BN, NT>(tid, hi - lo, n0, g.N, [&](int k) { return B + (lo + k) * g.ldb; });
-        sum_panels<E, VEC>(tile, hi - lo, a, b, lds, tid, wm, wn);
+        const int *list = g.order != nullptr ? g.order + lo : nullptr;
+        const T *X = g.order != nullptr ? A : A + lo * g.lda;
+        const Gathered<E, BM, NT> a(X, tid, hi - lo, g.lda, m0, g.M, list, g.per_row, g.rows);
+        const Across<E, BN, NT> b(B + lo * g.ldb, tid, hi - lo, g.ldb, n0, g.N);
+        sum_panels<E, DMA>(tile, hi - lo, a, b, lds, tid, wm, wn);
     }
 
     T *C = (T *)g.C + (OP == kGradW ? group * g.stride : 0);
     tile.each(wm, wn, lane, [&](int r, int c, f32x4 v) {
         const int m = m0 + r, n = n0 + c;
         if (m < m_end && n < g.N)
-            store4<E, VEC>(C + (int64_t)m * g.ldc + n, v, g.N - n);
+            store4<E, DMA>(C + (int64_t)m * g.ldc + n, v, g.N - n);
     });
 }
 
@@ -257,13 +268,16 @@ bool vector_rows(int type, const void *p, int64_t ld, int64_t cols)
     return aligned_to(p, 16) && ld % chunk == 0 && cols % chunk == 0;
 }
 
+// Most rows of an operand that one panel's offsets span (BM, BN or a panel's depth).
+constexpr int kPanelRows = 256;
+
 // Workgroups of a launch: a grid has fewer than 2^32 threads.
 constexpr int64_t kMaxTiles = UINT32_MAX / 256;
 static_assert(kCombineThreads <= 256, "grid limit");
 int token_grid(int T) { return T < kMaxTiles ? T : (int)kMaxTiles; }
 
 template <class E, Op OP, int BM, int BN, int WM, int WN>
-int launch_tile(GroupedArgs g, bool vec, hipStream_t stream)
+int launch_tile(GroupedArgs g, bool dma, hipStream_t stream)
 {
     g.tiles_n = (int)ceil_div(g.N, BN);
     // Every group ends in at most one partial tile.
@@ -273,7 +287,7 @@ int launch_tile(GroupedArgs g, bool vec, hipStream_t stream)
         return GEMM_F32_ERR_DIM;
     if (grid == 0)
         return GEMM_F32_OK;
-    if (vec)
+    if (dma)
         grouped_kernel<E, OP, BM, BN, WM, WN, true><<<(int)grid, WM * WN * kWave, 0, stream>>>(g);
     else
         grouped_kernel<E, OP, BM, BN, WM, WN, false><<<(int)grid, WM * WN * kWave, 0, stream>>>(g);
@@ -281,7 +295,7 @@ int launch_tile(GroupedArgs g, bool vec, hipStream_t stream)
 }
 
 template <Op OP>
-int launch_grouped(int type, const GroupedArgs &g, bool vec, hipStream_t stream)
+int launch_grouped(int type, const GroupedArgs &g, bool dma, hipStream_t stream)
 {
     int rc = GEMM_F32_OK;
     with_type(type, [&](auto e) {
@@ -289,9 +303,9 @@ int launch_grouped(int type, const GroupedArgs &g, bool vec, hipStream_t stream)
         // Few rows a group: tiles of 16 rows read each weight once without
         // spending matrix instructions on rows that are not there.
         if (OP != kGradW && g.P <= 32 * (int64_t)g.G)
-            rc = launch_tile<E, OP, 16, 128, 1, 4>(g, vec, stream);
+            rc = launch_tile<E, OP, 16, 128, 1, 4>(g, dma, stream);
         else
-            rc = launch_tile<E, OP, 128, 128, 2, 2>(g, vec, stream);
+            rc = launch_tile<E, OP, 128, 128, 2, 2>(g, dma, stream);
     });
     return rc;
 }
@@ -334,11 +348,11 @@ int gemm_f32_grouped(int type, int G, int P, int N, int K, const int *offsets, c
     const int b = type_bytes(type);
     if (!aligned_to(offsets, 4) || !aligned_to(order, 4) || !aligned_to(X, b) || !aligned_to(W, b) || !aligned_to(Y, b))
         return GEMM_F32_ERR_ALIGN;
-    const bool vec = vector_rows(type, X, ldx, K) && vector_rows(type, W, ldw, N) && vector_rows(type, Y, ldy, N) &&
-                     stride_w % (16 / b) == 0;
-    const GroupedArgs g{offsets, order, X, W, Y, ldx, ldw, ldy, stride_w, G, P, per_row, rows, 0, N, K, 0,
+    const bool dma = dma_rows(type, X, ldx, K, rows) && dma_rows(type, W, ldw, N, kPanelRows) &&
+                     dma_rows(type, Y, ldy, N, 0) && stride_w % (16 / b) == 0;
+    const GroupedArgs g{offsets, order, X, W, Y, ldx, ldw, ldy, stride_w, G, P, rows, Divisor(order != nullptr ? per_row : 1), 0, N, K, 0,
                         gemm_f32_internal::current_device().xcds};
-    return launch_grouped<kForward>(type, g, vec, stream);
+    return launch_grouped<kForward>(type, g, dma, stream);
 }
 
 int gemm_f32_grouped_grad_x(int type, int G, int P, int N, int K, const int *offsets, const void *dY, int lddy,
@@ -356,11 +370,11 @@ int gemm_f32_grouped_grad_x(int type, int G, int P, int N, int K, const int *off
     const int b = type_bytes(type);
     if (!aligned_to(offsets, 4) || !aligned_to(dY, b) || !aligned_to(W, b) || !aligned_to(dX, b))
         return GEMM_F32_ERR_ALIGN;
-    const bool vec = vector_rows(type, dY, lddy, N) && vector_rows(type, W, ldw, N) && vector_rows(type, dX, lddx, K) &&
-                     stride_w % (16 / b) == 0;
-    const GroupedArgs g{offsets, nullptr, dY, W, dX, lddy, ldw, lddx, stride_w, G, P, 1, P, 0, K, N, 0,
+    const bool dma = dma_rows(type, dY, lddy, N, kPanelRows) && dma_rows(type, W, ldw, N, kPanelRows) &&
+                     dma_rows(type, dX, lddx, K, 0) && stride_w % (16 / b) == 0;
+    const GroupedArgs g{offsets, nullptr, dY, W, dX, lddy, ldw, lddx, stride_w, G, P, P, Divisor(1), 0, K, N, 0,
                         gemm_f32_internal::current_device().xcds};
-    return launch_grouped<kGradX>(type, g, vec, stream);
+    return launch_grouped<kGradX>(type, g, dma, stream);
 }
 
 int gemm_f32_grouped_grad_w(int type, int G, int P, int N, int K, const int *offsets, const int *order, int per_row,
@@ -383,11 +397,11 @@ int gemm_f32_grouped_grad_w(int type, int G, int P, int N, int K, const int *off
     const int b = type_bytes(type);
     if (!aligned_to(offsets, 4) || !aligned_to(order, 4) || !aligned_to(X, b) || !aligned_to(dY, b) || !aligned_to(dW, b))
         return GEMM_F32_ERR_ALIGN;
-    const bool vec = vector_rows(type, X, ldx, K) && vector_rows(type, dY, lddy, N) && vector_rows(type, dW, lddw, N) &&
-                     stride_dw % (16 / b) == 0;
-    const GroupedArgs g{offsets, order, X, dY, dW, ldx, lddy, lddw, stride_dw, G, P, per_row, rows, K, N, 0, 0,
+    const bool dma = dma_rows(type, X, ldx, K, rows) && dma_rows(type, dY, lddy, N, kPanelRows) &&
+                     dma_rows(type, dW, lddw, N, 0) && stride_dw % (16 / b) == 0;
+    const GroupedArgs g{offsets, order, X, dY, dW, ldx, lddy, lddw, stride_dw, G, P, rows, Divisor(order != nullptr ? per_row : 1), K, N, 0, 0,
                         gemm_f32_internal::current_device().xcds};
-    return launch_grouped<kGradW>(type, g, vec, stream);
+    return launch_grouped<kGradW>(type, g, dma, stream);
 }
 
 int gemm_f32_combine(int type, int T, int k, int N, int P, const int *position, const float *weight, const void *Y,

@@ -1,9 +1,9 @@
 // One output tile of a product on the matrix cores, from panels in LDS.
 //
-// Panels are kDeep (128 bytes of) elements deep in the summed index.  An operand
-// lies in LDS as it lies in memory, in 16-byte chunks:
+// Panels are CH 16-byte chunks (8: 128 bytes, 4: 64 bytes) deep in the summed
+// index, kDeep elements.  An operand lies in LDS as it lies in memory:
 //
-//  * summed index contiguous ("along"): [row][kDeep], 8 chunks per row; chunk
+//  * summed index contiguous ("along"): [row][kDeep], CH chunks per row; chunk
 //    c of row r stands at c ^ swz(r), so that 16 rows read at one chunk
 //    column fall on distinct banks;
 //  * row index contiguous ("across"): [kDeep][rows].  The 16-bit types read
@@ -25,10 +25,13 @@
 
 namespace rows {
 
-template <class E>
-constexpr int deep() { return 128 / E::kBytes; }
-
-__device__ inline int swz_along(int r) { return (r ^ (r >> 3)) & 7; }
+// Chunk permutation of row r of an "along" panel of CH chunks per row.
+template <int CH>
+__device__ inline int swz_along(int r)
+{
+    static_assert(CH == 8 || CH == 4, "panels are 128 or 64 bytes deep");
+    return CH == 8 ? (r ^ (r >> 3)) & 7 : (r >> 2) & 3;
+}
 
 // Chunk permutation of k row k of an "across" panel of RN rows (16-bit types).
 template <int RN>
@@ -43,11 +46,11 @@ __device__ inline int swz_across(int k)
 }
 
 // LDS element offset of chunk c of row r (along) or of k row r (across).
-template <class E, bool ALONG, int RN>
+template <class E, bool ALONG, int RN, int CH>
 __device__ inline int lds_chunk(int r, int c)
 {
     if constexpr (ALONG)
-        return r * deep<E>() + (c ^ swz_along(r)) * E::kChunk;
+        return (r * CH + (c ^ swz_along<CH>(r))) * E::kChunk;
     else if constexpr (E::kBytes == 2)
         return r * RN + (c ^ swz_across<RN>(r)) * E::kChunk;
     else
@@ -61,8 +64,8 @@ template <class T>
 using lds_ptr = __attribute__((address_space(3))) T *;
 
 // Fragments of F consecutive 16-row blocks from row `row0` of a panel, one
-// k step (a step: 32 k of a 16-bit type, 16 of binary32; panels hold two).
-template <class E, bool ALONG, int RN, int F>
+// k step (32 k of a 16-bit type, 16 of binary32: four chunks).
+template <class E, bool ALONG, int RN, int CH, int F>
 struct Fragments {
     using T = typename E::T;
     // rows a group of fragments read together covers, /16
@@ -75,14 +78,14 @@ struct Fragments {
         if constexpr (ALONG) {
 #pragma unroll
             for (int f = 0; f < F; ++f)
-                q[f] = *reinterpret_cast<const u32x4 *>(panel + lds_chunk<E, true, RN>(row0 + 16 * f + i, 4 * step + h));
+                q[f] = *reinterpret_cast<const u32x4 *>(panel + lds_chunk<E, true, RN, CH>(row0 + 16 * f + i, 4 * step + h));
         } else if constexpr (E::kBytes == 2) {
             const int k = 32 * step + 8 * h + i / 4;     // this lane's row of the 4 x 16 block
 #pragma unroll
             for (int f = 0; f < F; ++f) {
                 const int col = row0 + 16 * f + 4 * (i % 4);
-                const T *p0 = panel + lds_chunk<E, false, RN>(k, col / 8) + col % 8;
-                const T *p1 = panel + lds_chunk<E, false, RN>(k + 4, col / 8) + col % 8;
+                const T *p0 = panel + lds_chunk<E, false, RN, CH>(k, col / 8) + col % 8;
+                const T *p1 = panel + lds_chunk<E, false, RN, CH>(k + 4, col / 8) + col % 8;
                 const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr<s16x4>)p0);
                 const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr<s16x4>)p1);
                 q[f] = __builtin_bit_cast(u32x4, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
@@ -123,16 +126,18 @@ __device__ inline f32x4 mfma_step(u32x4 b, u32x4 a, f32x4 d)
     }
 }
 
-// A workgroup's BM x BN tile, WM x WN waves of (BM/WM) x (BN/WN).
-template <class E, bool A_ALONG, bool B_ALONG, int BM_, int BN_, int WM_, int WN_>
+// A workgroup's BM x BN tile, WM x WN waves of (BM/WM) x (BN/WN), panels of CH chunks
+// of the summed index.
+template <class E, bool A_ALONG, bool B_ALONG, int BM_, int BN_, int WM_, int WN_, int CH_ = 8>
 struct Tile {
     using T = typename E::T;
     static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_;
     static constexpr int kThreads = WM * WN * kWave;
     static constexpr int kFm = BM / WM / 16, kFn = BN / WN / 16;
-    static constexpr int kLdsA = BM * deep<E>(), kLdsB = BN * deep<E>();   // elements of a panel
-    using Fa = Fragments<E, A_ALONG, BM, kFm>;
-    using Fb = Fragments<E, B_ALONG, BN, kFn>;
+    static constexpr int CH = CH_, kDeep = CH * E::kChunk, kSteps = CH / 4;
+    static constexpr int kLdsA = BM * kDeep, kLdsB = BN * kDeep;           // elements of a panel
+    using Fa = Fragments<E, A_ALONG, BM, CH, kFm>;
+    using Fb = Fragments<E, B_ALONG, BN, CH, kFn>;
     static_assert(BM % (16 * WM) == 0 && BN % (16 * WN) == 0, "wave tile");
 
     f32x4 acc[kFm][kFn];
@@ -146,20 +151,29 @@ struct Tile {
                 acc[m][n] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
 
-    __device__ inline void panel(const T *la, const T *lb, int wm, int wn, int lane)
+    // The panel's fragments, all steps.
+    struct Panel {
+        Fa a[kSteps];
+        Fb b[kSteps];
+        __device__ inline void read(const T *la, const T *lb, int wm, int wn, int lane)
+        {
+#pragma unroll
+            for (int step = 0; step < kSteps; ++step) {
+                a[step].read(la, wm * (BM / WM), step, lane);
+                b[step].read(lb, wn * (BN / WN), step, lane);
+            }
+        }
+    };
+
+    __device__ inline void multiply(const Panel &p)
     {
 #pragma unroll
-        for (int step = 0; step < 2; ++step) {
-            Fa a;
-            Fb b;
-            a.read(la, wm * (BM / WM), step, lane);
-            b.read(lb, wn * (BN / WN), step, lane);
+        for (int step = 0; step < kSteps; ++step)
 #pragma unroll
             for (int m = 0; m < kFm; ++m)
 #pragma unroll
                 for (int n = 0; n < kFn; ++n)
-                    acc[m][n] = mfma_step<E>(b.q[n], a.q[m], acc[m][n]);
-        }
+                    acc[m][n] = mfma_step<E>(p.b[step].q[n], p.a[step].q[m], acc[m][n]);
     }
 
     // f(row, column, 4 neighbouring columns' sums) over the lane's results,
@@ -214,94 +228,147 @@ __device__ inline void store4(typename E::T *p, f32x4 v, int64_t left)
 
 // ---------------------------------------------------------------------------
 // Where a thread's chunks of a panel come from.  Chunk i of thread tid is the
-// panel's 16-byte LDS slot tid + i * threads; at() gives its address for
-// the panel that starts at k0 and how many elements of its row there are from there on
-// (none: the chunk is zero).
+// panel's 16-byte LDS slot tid + i * threads.  base is a uniform address, p[i]
+// (Along) or row(k) (Across) lies a byte offset off it, kNowhere: zeros.
 // ---------------------------------------------------------------------------
-template <class E, int RN, int NT>
+constexpr uint32_t kNowhere = 0x80000000u;           // a buffer offset that reads as 0
+constexpr int kRawBufferFlags = 0x00020000;          // dword 3 of a raw buffer resource
+
+// A pointer that is the same in all lanes, in scalar registers (the compiler
+// does not always see it, and loops over lanes around every load then).
+__device__ inline const char *uniform(const void *p)
+{
+    const uint64_t u = (uint64_t)p;
+    const uint32_t lo = __builtin_amdgcn_readfirstlane((int)(uint32_t)u), hi = __builtin_amdgcn_readfirstlane((int)(u >> 32));
+    return (const char *)((uint64_t)hi << 32 | lo);
+}
+
+// Operand rows contiguous in the summed index.  row(i, r): byte offset from base of the
+// panel's row r (of chunk i), negative if there is none; rows are K elements long.
+template <class E, int RN, int NT, int CH = 8>
 struct Along {
     using T = typename E::T;
-    static constexpr bool kAlong = true;
-    static constexpr int kSlots = RN * 8, kCount = (kSlots + NT - 1) / NT;
-    const T *p[kCount];                              // chunk's address at k0 = 0
-    int left[kCount];                                // elements from there on
+    static constexpr int kSlots = RN * CH, kDeep = CH * E::kChunk, kCount = (kSlots + NT - 1) / NT;
+    const char *base;
+    int64_t off[kCount];
+    int k[kCount], K;                                // the chunk's first k in panel 0
 
-    // row(r): the panel's row r, NULL if there is none; K elements long.
+    // Panel row of chunk i.
+    static __device__ inline int row_of(int i, int tid) { return (tid + i * NT) / CH; }
+
     template <class Row>
-    __device__ inline Along(int tid, int K, Row &&row)
+    __device__ inline Along(const T *base_, int tid, int K_, Row &&row) : base(uniform(base_)), K(__builtin_amdgcn_readfirstlane(K_))
     {
 #pragma unroll
         for (int i = 0; i < kCount; ++i) {
-            const int slot = tid + i * NT, r = slot / 8;
-            const int k = (slot % 8 ^ swz_along(r)) * E::kChunk;
-            const T *base = kSlots % NT == 0 || slot < kSlots ? row(r) : nullptr;
-            p[i] = base != nullptr ? base + k : nullptr;
-            left[i] = base != nullptr ? K - k : 0;
+            const int slot = tid + i * NT, r = slot / CH;
+            k[i] = (slot % CH ^ swz_along<CH>(r)) * E::kChunk;
+            const int64_t o = kSlots % NT == 0 || slot < kSlots ? row(i, r) : -1;
+            off[i] = o < 0 ? -1 : o + k[i] * E::kBytes;
         }
     }
-    __device__ inline const T *at(int i, int k0, int &n) const
-    {
-        n = left[i] - k0;
-        return p[i] + k0;
-    }
+    __device__ inline int64_t step() const { return kDeep * E::kBytes; }   // bytes from panel to panel
+    // Whether chunks that panel 0 has may be missing from the panel at k0.
+    __device__ inline bool partial(int k0) const { return K - k0 < kDeep; }
+    // Elements from chunk i of the panel at k0 to its row's end (none: zeros), and its offset.
+    __device__ inline int left(int i, int k0) const { return off[i] < 0 ? 0 : K - k0 - k[i]; }
+    __device__ inline int64_t offset(int i, int) const { return off[i]; }
 };
 
-template <class E, int RN, int NT, class Row>
+// Operand rows contiguous across the summed index: row(k) is the byte offset of k row k
+// from panel to panel step_ bytes further, columns first .. of cols.
+template <class E, int RN, int NT, int CH = 8>
 struct Across {
     using T = typename E::T;
-    static constexpr bool kAlong = false;
-    static constexpr int kSlots = RN * 8, kCount = (kSlots + NT - 1) / NT;
+    static constexpr int kSlots = RN * CH, kDeep = CH * E::kChunk, kCount = (kSlots + NT - 1) / NT;
     static constexpr int kPer = RN / E::kChunk;      // chunks of a k row
-    Row row;                                         // row(k): k row k, NULL if there is none
-    int tid, K, first, cols;                         // columns first .. of cols
+    const char *base;
+    int64_t ld;                                      // bytes between k rows
+    int tid, K, first, cols;
 
-    __device__ inline Across(int tid_, int K_, int first_, int cols_, Row row_)
-        : row(row_), tid(tid_), K(K_), first(first_), cols(cols_)
+    __device__ inline Across(const T *base_, int tid_, int K_, int64_t ld_, int first_, int cols_)
+        : base(uniform(base_)), ld(ld_ * E::kBytes), tid(tid_), K(__builtin_amdgcn_readfirstlane(K_)), first(first_),
+          cols(cols_)
     {
     }
-    __device__ inline const T *at(int i, int k0, int &n) const
+    __device__ inline int krow(int i) const { return (tid + i * NT) / kPer; }
+    __device__ inline int col(int i) const
     {
-        const int slot = tid + i * NT, r = slot / kPer;
-        int c = slot % kPer;
+        int c = (tid + i * NT) % kPer;
         if constexpr (E::kBytes == 2)
-            c ^= swz_across<RN>(r);
-        const int col = first + c * E::kChunk;
-        const bool there = (kSlots % NT == 0 || slot < kSlots) && k0 + r < K;
-        const T *base = there ? row(k0 + r) : nullptr;
-        n = base != nullptr ? cols - col : 0;
-        return base + col;
+            c ^= swz_across<RN>(krow(i));
+        return first + c * E::kChunk;
+    }
+    __device__ inline int64_t step() const { return kDeep * ld; }
+    __device__ inline bool partial(int k0) const { return K - k0 < kDeep; }
+    __device__ inline int left(int i, int k0) const
+    {
+        return (kSlots % NT == 0 || tid + i * NT < kSlots) && k0 + krow(i) < K ? cols - col(i) : 0;
+    }
+    __device__ inline int64_t offset(int i, int) const { return krow(i) * ld + (int64_t)col(i) * E::kBytes; }
+};
+
+// The same with k rows in any order: list[k] names k row k, a row of `rows`
+// (negative or past them: zeros) after division by per_row; list NULL: k itself.
+template <class E, int RN, int NT, int CH = 8>
+struct Gathered : Across<E, RN, NT, CH> {
+    using Base = Across<E, RN, NT, CH>;
+    const int *list;
+    Divisor per_row;
+    int rows;
+    __device__ inline Gathered(const typename E::T *base_, int tid_, int K_, int64_t ld_, int first_, int cols_,
+                               const int *list_, Divisor per_row_, int rows_)
+        : Base(base_, tid_, K_, ld_, first_, cols_), list(list_), per_row(per_row_), rows(rows_)
+    {
+    }
+    __device__ inline int row(int k) const
+    {
+        if (list == nullptr)
+            return k;
+        const int s = list[k], r = per_row.of(s);
+        return s < 0 || r >= rows ? -1 : r;
+    }
+    __device__ inline int64_t step() const { return 0; }
+    __device__ inline int left(int i, int k0) const
+    {
+        const int n = Base::left(i, k0);
+        return n > 0 && row(k0 + this->krow(i)) >= 0 ? n : 0;
+    }
+    __device__ inline int64_t offset(int i, int k0) const
+    {
+        return row(k0 + this->krow(i)) * this->ld + (int64_t)this->col(i) * E::kBytes;
     }
 };
 
-template <class E, int RN, int NT, class Row>
-__device__ inline Across<E, RN, NT, Row> across(int tid, int K, int first, int cols, Row row)
-{
-    return Across<E, RN, NT, Row>(tid, K, first, cols, row);
-}
-
-// Adds the K-long sums of the tile from panels staged through registers: two
-// LDS buffers, one barrier per panel, the next panel's loads in flight
-// during a panel's matrix instructions.  lds: 2 * (kLdsA + kLdsB) elements.
-template <class E, bool VEC, class Ti, class SrcA, class SrcB>
-__device__ inline void sum_panels(Ti &tile, int K, const SrcA &a, const SrcB &b, typename E::T *lds, int tid, int wm,
-                                  int wn)
+// ---------------------------------------------------------------------------
+// The K loop.  Adds the K-long sums to the tile from two LDS buffers of one
+// panel each (2 * (kLdsA + kLdsB) elements), one barrier per panel.
+//
+// DMA: buffer loads write the panels straight into LDS, the next panel's
+// while the matrix cores work on this one.  Rows that are 16-byte
+// aligned, whole chunks long and less than 2^31 bytes from their base.  Else the
+// chunks are staged through registers, element by element at a row's end.
+// ---------------------------------------------------------------------------
+template <class E, class Ti, class SrcA, class SrcB>
+__device__ inline void sum_panels_staged(Ti &tile, int K, const SrcA &a, const SrcB &b, typename E::T *lds, int tid,
+                                         int wm, int wn)
 {
     using T = typename E::T;
-    constexpr int BK = deep<E>(), NT = Ti::kThreads;
+    constexpr int BK = Ti::kDeep, NT = Ti::kThreads;
     const int lane = tid % kWave;
     u32x4 ra[SrcA::kCount], rb[SrcB::kCount];
+    auto load = [&](const auto &src, int i, int k0) {
+        const int n = src.left(i, k0);
+        const char *p = src.base + (int64_t)(k0 / BK) * src.step();
+        return load_chunk<E, false>((const T *)(p + (n > 0 ? src.offset(i, k0) : 0)), n);
+    };
     auto fetch = [&](int k0) {
-        int n;
 #pragma unroll
-        for (int i = 0; i < SrcA::kCount; ++i) {
-            const T *p = a.at(i, k0, n);
-            ra[i] = load_chunk<E, VEC>(p, n);
-        }
+        for (int i = 0; i < SrcA::kCount; ++i)
+            ra[i] = load(a, i, k0);
 #pragma unroll
-        for (int i = 0; i < SrcB::kCount; ++i) {
-            const T *p = b.at(i, k0, n);
-            rb[i] = load_chunk<E, VEC>(p, n);
-        }
+        for (int i = 0; i < SrcB::kCount; ++i)
+            rb[i] = load(b, i, k0);
     };
     auto put = [&](T *panel, int slots, int i, u32x4 v) {
         if (slots % NT == 0 || tid + i * NT < slots)
@@ -321,8 +388,115 @@ __device__ inline void sum_panels(Ti &tile, int K, const SrcA &a, const SrcB &b,
         __syncthreads();         // the other buffer's readers passed the last one
         if (k0 + BK < K)
             fetch(k0 + BK);
-        tile.panel(la, lb, wm, wn, lane);
+        typename Ti::Panel p;
+        p.read(la, lb, wm, wn, lane);
+        tile.multiply(p);
     }
+}
+
+// The panel loads of one operand by one wave: lane l's 16 bytes land at the
+// wave's LDS base + 16 * l.
+template <class E, class Src, int NT>
+struct PanelLoads {
+    using T = typename E::T;
+    uint32_t off[Src::kCount];
+    __device__ inline PanelLoads(const Src &src)
+    {
+#pragma unroll
+        for (int i = 0; i < Src::kCount; ++i)
+            off[i] = src.left(i, 0) > 0 ? (uint32_t)src.offset(i, 0) : kNowhere;
+    }
+    __device__ inline void fire(const Src &src, int k0, T *panel, int wave) const
+    {
+        const char *base = src.base + (int64_t)(k0 / Src::kDeep) * src.step();
+        const auto rsrc = __builtin_amdgcn_make_buffer_rsrc((void *)base, 0, (int)kNowhere, kRawBufferFlags);
+        auto load = [&](int i, uint32_t o) {
+            if (Src::kSlots % NT != 0 && (i * NT + wave * kWave) >= Src::kSlots)
+                return;                              // whole waves: kSlots is a multiple of 64
+            auto *dst = (lds_ptr<void>)(panel + (i * NT + wave * kWave) * E::kChunk);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, dst, 16, o, 0, 0, 0);
+        };
+        if (src.partial(k0)) {
+#pragma unroll
+            for (int i = 0; i < Src::kCount; ++i)
+                load(i, src.left(i, k0) > 0 ? off[i] : kNowhere);
+        } else {
+#pragma unroll
+            for (int i = 0; i < Src::kCount; ++i)
+                load(i, off[i]);
+        }
+    }
+};
+
+template <class E, int RN, int NT, int CH>
+struct PanelLoads<E, Gathered<E, RN, NT, CH>, NT> {
+    using Src = Gathered<E, RN, NT, CH>;
+    using T = typename E::T;
+    __device__ inline PanelLoads(const Src &) {}
+    __device__ inline void fire(const Src &src, int k0, T *panel, int wave) const
+    {
+        const auto rsrc = __builtin_amdgcn_make_buffer_rsrc((void *)src.base, 0, (int)kNowhere, kRawBufferFlags);
+#pragma unroll
+        for (int i = 0; i < Src::kCount; ++i) {
+            const uint32_t o = src.left(i, k0) > 0 ? (uint32_t)src.offset(i, k0) : kNowhere;
+            auto *dst = (lds_ptr<void>)(panel + (i * NT + wave * kWave) * E::kChunk);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, dst, 16, o, 0, 0, 0);
+        }
+    }
+};
+
+template <class E, class Ti, class SrcA, class SrcB>
+__device__ inline void sum_panels_dma(Ti &tile, int K, const SrcA &a, const SrcB &b, typename E::T *lds, int tid,
+                                      int wm, int wn)
+{
+    using T = typename E::T;
+    constexpr int BK = Ti::kDeep, NT = Ti::kThreads;
+    const int lane = tid % kWave, wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+    const PanelLoads<E, SrcA, NT> pa(a);
+    const PanelLoads<E, SrcB, NT> pb(b);
+    auto fire = [&](int k0, int buf) {
+        T *la = lds + buf * (Ti::kLdsA + Ti::kLdsB);
+        pa.fire(a, k0, la, wave);
+        pb.fire(b, k0, la + Ti::kLdsA, wave);
+    };
+    if (K > 0)
+        fire(0, 0);
+    int buf = 0;
+    for (int k0 = 0; k0 < K; k0 += BK, buf ^= 1) {
+        // This panel has landed, and the other buffer's reads are complete in
+        // every wave: it may be filled again.
+        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        // This panel's LDS reads go first: the compiler waits for every load
+        // in flight before a transposing read that follows it.
+        const T *la = lds + buf * (Ti::kLdsA + Ti::kLdsB);
+        typename Ti::Panel p;
+        p.read(la, la + Ti::kLdsA, wm, wn, lane);
+        __builtin_amdgcn_sched_barrier(0);
+        if (k0 + BK < K)
+            fire(k0 + BK, buf ^ 1);
+        __builtin_amdgcn_sched_barrier(0);
+        tile.multiply(p);
+    }
+}
+
+template <class E, bool DMA, class Ti, class SrcA, class SrcB>
+__device__ inline void sum_panels(Ti &tile, int K, const SrcA &a, const SrcB &b, typename E::T *lds, int tid, int wm,
+                                  int wn)
+{
+    if constexpr (DMA)
+        sum_panels_dma<E>(tile, K, a, b, lds, tid, wm, wn);
+    else
+        sum_panels_staged<E>(tile, K, a, b, lds, tid, wm, wn);
+}
+
+// Rows that the direct loads can address: 16-byte aligned, a whole number of
+// chunks long, `span` rows of ld elements within 2^31 bytes.
+inline bool dma_rows(int type, const void *p, int64_t ld, int64_t cols, int64_t span)
+{
+    const int b = type_bytes(type), chunk = 16 / b;
+    return aligned_to(p, 16) && ld % chunk == 0 && cols % chunk == 0 && span * ld < (int64_t)kNowhere / b;
 }
 
 }  // namespace rows

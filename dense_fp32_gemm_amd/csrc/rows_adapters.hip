@@ -34,6 +34,7 @@ struct AdapterArgs {
     int depth;           // of factor's rows
     int tiles_m, tiles_n;
     int xcds;
+    bool vector_y;       // Y's rows take stores of four elements
 };
 
 // Rank indices a panel of the up-projection holds: 16-bit panels are 64 deep,
@@ -50,7 +51,7 @@ struct UpRows : Across<E, RN, NT> {
     using Base = Across<E, RN, NT>;
     int R;
     __device__ inline UpRows(const typename E::T *base_, int tid_, int depth, int64_t ld_, int first_, int cols_, int R_)
-        : Base(base_, tid_, depth, ld_, first_, cols_), R(R_)
+        : Base(base_, tid_, depth, ld_, first_, cols_, R_), R(R_)
     {
     }
     __device__ inline int rank(int i, int k0) const { return k0 / panel_deep<E>() * 32 + this->krow(i) % 32; }
@@ -103,7 +104,7 @@ __global__ __launch_bounds__(kWave) void down_kernel(AdapterArgs g)
                                     [&](int, int r) { return members >> r & 1 ? r * g.ldx * E::kBytes : -1; });
         const Across<E, RN, kWave> w((const T *)g.A + a * g.stride_a + k0 * g.lda, lane, K, g.lda, 0, g.R);
         __syncthreads();
-        sum_panels<E, DMA>(tile, K, x, w, lds, lane, 0, 0);
+        sum_panels<E, DMA, 2>(tile, K, x, w, lds, lane, 0, 0);
         tile.each(0, 0, lane, [&](int r, int c, f32x4 v) {
             if (members >> r & 1) {
                 float *u = g.partial + ((int64_t)blockIdx.y * g.T + t0 + r) * g.R + c;
@@ -191,7 +192,7 @@ __global__ __launch_bounds__(WM *WN *kWave) void adapters_kernel(AdapterArgs g)
         const Along<E, BM, NT> x((const T *)g.X + m0 * g.ldx, tid, g.K,
                                  [&](int, int r) { return m0 + r < g.T ? r * g.ldx * E::kBytes : -1; });
         const Across<E, BN, NT> w((const T *)g.W, tid, g.K, g.ldw, n0, g.N);
-        sum_panels<E, DMA>(tile, g.K, x, w, lds, tid, wm, wn);
+        sum_panels<E, DMA, 2>(tile, g.K, x, w, lds, tid, wm, wn);
     }
     if (g.R > 0 && g.n > 0) {
         const int which0 = adapter_of(g, m0 + lane, lane < BM && m0 + lane < g.T);
@@ -204,7 +205,7 @@ __global__ __launch_bounds__(WM *WN *kWave) void adapters_kernel(AdapterArgs g)
             Ti add;
             add.clear();
             __syncthreads();
-            sum_panels<E, DMA>(add, g.depth, u, b, lds, tid, wm, wn);
+            sum_panels<E, DMA, 2>(add, g.depth, u, b, lds, tid, wm, wn);
 #pragma unroll
             for (int m = 0; m < Ti::kFm; ++m) {
                 const int r = wm * (BM / WM) + Ti::Fa::row_of(m, lane % 16);
@@ -220,11 +221,17 @@ __global__ __launch_bounds__(WM *WN *kWave) void adapters_kernel(AdapterArgs g)
         });
     }
     T *Y = (T *)g.Y;
-    tile.each(wm, wn, lane, [&](int r, int c, f32x4 v) {
-        const int m = m0 + r, n = n0 + c;
-        if (m < g.T && n < g.N)
-            store4<E, DMA>(Y + m * g.ldy + n, v, g.N - n);
-    });
+    auto store = [&](auto vec) {
+        tile.each(wm, wn, lane, [&](int r, int c, f32x4 v) {
+            const int m = m0 + r, n = n0 + c;
+            if (m < g.T && n < g.N)
+                store4<E, decltype(vec)::value>(Y + m * g.ldy + n, v, g.N - n);
+        });
+    };
+    if (g.vector_y)
+        store(std::true_type{});
+    else
+        store(std::false_type{});
 }
 
 // ---------------------------------------------------------------------------
@@ -285,6 +292,9 @@ int launch_tiles(AdapterArgs g, bool dma, hipStream_t stream)
 // A grid has fewer than 2^32 threads, and there is a wave per token.
 constexpr int kMaxTokens = 1 << 25;
 
+// Most rows of an operand that one panel's offsets span (a tile's, or a panel's depth).
+constexpr int kPanelRows = 256;
+
 bool short_ld(int64_t ld, int cols) { return ld < at_least_one(cols); }
 
 }  // namespace
@@ -329,11 +339,10 @@ int gemm_f32_adapters(int type, int T, int N, int K, int R, int n, const void *X
     if (need > 0 && (ws == nullptr || ws_bytes < need || !aligned_to(ws, 16)))
         return GEMM_F32_ERR_WORKSPACE;
 
-    const int chunk = 16 / b;
-    const bool dma_x = dma_rows(type, X, ldx, K, 256);
-    const bool dma_main = dma_x && dma_rows(type, W, ldw, N, 256) && dma_rows(type, Y, ldy, N, 0) &&
-                          (!low || (dma_rows(type, B, ldb, N, 256) && (n == 1 || stride_b % chunk == 0)));
-    const bool dma_down = dma_x && dma_rows(type, A, lda, R, 256) && (n == 1 || stride_a % chunk == 0);
+    const bool dma_x = dma_rows(type, X, ldx, kPanelRows);
+    const bool dma_main = dma_x && dma_rows(type, W, ldw, kPanelRows) &&
+                          (!low || (dma_rows(type, B, ldb, kPanelRows) && (n == 1 || stride_b * b % 4 == 0)));
+    const bool dma_down = dma_x && low && dma_rows(type, A, lda, kPanelRows) && (n == 1 || stride_a * b % 4 == 0);
     int rc = GEMM_F32_OK;
     with_type(type, [&](auto e) {
         using E = decltype(e);
@@ -344,6 +353,7 @@ int gemm_f32_adapters(int type, int T, int N, int K, int R, int n, const void *X
         g.stride_a = stride_a, g.stride_b = stride_b;
         g.T = T, g.N = N, g.K = K, g.R = R, g.n = n;
         g.xcds = gemm_f32_internal::current_device().xcds;
+        g.vector_y = vector_rows(type, Y, ldy, 0, N);
         if (low) {
             const Workspace w = workspace<E>(T, K, R);
             g.partial = (float *)((char *)ws + w.partial);

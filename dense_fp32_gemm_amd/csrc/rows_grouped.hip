@@ -25,6 +25,7 @@ struct GroupedArgs {
     int M, N, K;             // grad_w: M x N of dW; else columns N of C, summed K
     int tiles_n;
     int xcds;
+    bool vector_c;           // C's rows take stores of four elements
 };
 
 // Workgroups are dealt to the dies round-robin; renumbered so that each die
@@ -94,14 +95,15 @@ __device__ inline bool find_tile(const GroupedArgs &g, int bm, int &group, int &
     return false;
 }
 
-template <class E, Op OP, int BM, int BN, int WM, int WN, bool DMA>
+template <class E, Op OP, int BM, int BN, int WM, int WN, int CH, int S, bool DMA>
 __global__ __launch_bounds__(WM *WN *kWave) void grouped_kernel(GroupedArgs g)
 {
     constexpr bool kAlongA = OP != kGradW, kAlongB = OP == kGradX;
-    using Ti = Tile<E, kAlongA, kAlongB, BM, BN, WM, WN>;
+    using Ti = Tile<E, kAlongA, kAlongB, BM, BN, WM, WN, CH>;
     using T = typename E::T;
     constexpr int NT = Ti::kThreads;
-    __shared__ __attribute__((aligned(16))) T lds[2 * (Ti::kLdsA + Ti::kLdsB)];
+    __shared__ __attribute__((aligned(16))) T lds[(DMA ? S : 2) * (Ti::kLdsA + Ti::kLdsB)];
+    __shared__ uint32_t ahead[OP == kGradW && DMA ? 1024 : 1];
     const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
     const int wm = wave / WN, wn = wave % WN;
 
@@ -129,7 +131,7 @@ __global__ __launch_bounds__(WM *WN *kWave) void grouped_kernel(GroupedArgs g)
     Ti tile;
     tile.clear();
     if constexpr (OP == kForward) {
-        using Src = Along<E, BM, NT>;
+        using Src = Along<E, BM, NT, CH>;
         int row[Src::kCount];                        // of X; the loads side by side, then the rest
         if (g.order != nullptr) {
 #pragma unroll
@@ -145,28 +147,35 @@ __global__ __launch_bounds__(WM *WN *kWave) void grouped_kernel(GroupedArgs g)
         }
         const Src a(A, tid, g.K,
                     [&](int i, int r) { return m0 + r < m_end && row[i] < g.rows ? row[i] * g.lda * E::kBytes : -1; });
-        const Across<E, BN, NT> b(B + group * g.stride, tid, g.K, g.ldb, n0, g.N);
-        sum_panels<E, DMA>(tile, g.K, a, b, lds, tid, wm, wn);
+        const Across<E, BN, NT, CH> b(B + group * g.stride, tid, g.K, g.ldb, n0, g.N);
+        sum_panels<E, DMA, S>(tile, g.K, a, b, lds, tid, wm, wn);
     } else if constexpr (OP == kGradX) {
-        const Along<E, BM, NT> a(A + m0 * g.lda, tid, g.K,
+        const Along<E, BM, NT, CH> a(A + m0 * g.lda, tid, g.K,
                                  [&](int, int r) { return m0 + r < m_end ? r * g.lda * E::kBytes : -1; });
-        const Along<E, BN, NT> b(B + group * g.stride + n0 * g.ldb, tid, g.K,
+        const Along<E, BN, NT, CH> b(B + group * g.stride + n0 * g.ldb, tid, g.K,
                                  [&](int, int r) { return n0 + r < g.N ? r * g.ldb * E::kBytes : -1; });
-        sum_panels<E, DMA>(tile, g.K, a, b, lds, tid, wm, wn);
+        sum_panels<E, DMA, S>(tile, g.K, a, b, lds, tid, wm, wn);
     } else {
         const int *list = g.order != nullptr ? g.order + lo : nullptr;
         const T *X = g.order != nullptr ? A : A + lo * g.lda;
-        const Gathered<E, BM, NT> a(X, tid, hi - lo, g.lda, m0, g.M, list, g.per_row, g.rows);
-        const Across<E, BN, NT> b(B + lo * g.ldb, tid, hi - lo, g.ldb, n0, g.N);
-        sum_panels<E, DMA>(tile, hi - lo, a, b, lds, tid, wm, wn);
+        const int rows = g.order != nullptr ? g.rows : hi - lo;
+        const Gathered<E, BM, NT, CH> a(X, tid, hi - lo, g.lda, m0, g.M, list, g.per_row, rows, ahead);
+        const Across<E, BN, NT, CH> b(B + lo * g.ldb, tid, hi - lo, g.ldb, n0, g.N);
+        sum_panels<E, DMA, S>(tile, hi - lo, a, b, lds, tid, wm, wn);
     }
 
     T *C = (T *)g.C + (OP == kGradW ? group * g.stride : 0);
-    tile.each(wm, wn, lane, [&](int r, int c, f32x4 v) {
-        const int m = m0 + r, n = n0 + c;
-        if (m < m_end && n < g.N)
-            store4<E, DMA>(C + (int64_t)m * g.ldc + n, v, g.N - n);
-    });
+    auto store = [&](auto vec) {
+        tile.each(wm, wn, lane, [&](int r, int c, f32x4 v) {
+            const int m = m0 + r, n = n0 + c;
+            if (m < m_end && n < g.N)
+                store4<E, decltype(vec)::value>(C + (int64_t)m * g.ldc + n, v, g.N - n);
+        });
+    };
+    if (g.vector_c)
+        store(std::true_type{});
+    else
+        store(std::false_type{});
 }
 
 // ---------------------------------------------------------------------------
@@ -262,7 +271,8 @@ __global__ __launch_bounds__(kCombineThreads) void combine_grad_kernel(CombineAr
 // ---------------------------------------------------------------------------
 // Host side
 // ---------------------------------------------------------------------------
-bool vector_rows(int type, const void *p, int64_t ld, int64_t cols)
+// Rows whose chunks are whole and aligned.
+bool chunk_rows(int type, const void *p, int64_t ld, int64_t cols)
 {
     const int chunk = 16 / type_bytes(type);
     return aligned_to(p, 16) && ld % chunk == 0 && cols % chunk == 0;
@@ -272,11 +282,11 @@ bool vector_rows(int type, const void *p, int64_t ld, int64_t cols)
 constexpr int kPanelRows = 256;
 
 // Workgroups of a launch: a grid has fewer than 2^32 threads.
-constexpr int64_t kMaxTiles = UINT32_MAX / 256;
-static_assert(kCombineThreads <= 256, "grid limit");
+constexpr int64_t kMaxTiles = UINT32_MAX / 512;
+static_assert(kCombineThreads <= 512, "grid limit");
 int token_grid(int T) { return T < kMaxTiles ? T : (int)kMaxTiles; }
 
-template <class E, Op OP, int BM, int BN, int WM, int WN>
+template <class E, Op OP, int BM, int BN, int WM, int WN, int CH, int S>
 int launch_tile(GroupedArgs g, bool dma, hipStream_t stream)
 {
     g.tiles_n = (int)ceil_div(g.N, BN);
@@ -288,9 +298,9 @@ int launch_tile(GroupedArgs g, bool dma, hipStream_t stream)
     if (grid == 0)
         return GEMM_F32_OK;
     if (dma)
-        grouped_kernel<E, OP, BM, BN, WM, WN, true><<<(int)grid, WM * WN * kWave, 0, stream>>>(g);
+        grouped_kernel<E, OP, BM, BN, WM, WN, CH, S, true><<<(int)grid, WM * WN * kWave, 0, stream>>>(g);
     else
-        grouped_kernel<E, OP, BM, BN, WM, WN, false><<<(int)grid, WM * WN * kWave, 0, stream>>>(g);
+        grouped_kernel<E, OP, BM, BN, WM, WN, CH, S, false><<<(int)grid, WM * WN * kWave, 0, stream>>>(g);
     return launched();
 }
 
@@ -300,12 +310,18 @@ int launch_grouped(int type, const GroupedArgs &g, bool dma, hipStream_t stream)
     int rc = GEMM_F32_OK;
     with_type(type, [&](auto e) {
         using E = decltype(e);
-        // Few rows a group: tiles of 16 rows read each weight once without
-        // spending matrix instructions on rows that are not there.
-        if (OP != kGradW && g.P <= 32 * (int64_t)g.G)
-            rc = launch_tile<E, OP, 16, 128, 1, 4>(g, dma, stream);
+        if constexpr (OP != kGradW) {
+            // Few rows a group: tiles of 16 rows read each weight once without
+            // spending matrix instructions on rows that are not there.
+            if (g.P <= 32 * (int64_t)g.G) {
+                rc = launch_tile<E, OP, 16, 128, 1, 4, 8, 3>(g, dma, stream);
+                return;
+            }
+        }
+        if constexpr (E::kBytes == 4)
+            rc = launch_tile<E, OP, 64, 64, 2, 2, 8, 2>(g, dma, stream);
         else
-            rc = launch_tile<E, OP, 128, 128, 2, 2>(g, dma, stream);
+            rc = launch_tile<E, OP, 128, 256, 2, 4, 4, 3>(g, dma, stream);
     });
     return rc;
 }
@@ -348,10 +364,9 @@ int gemm_f32_grouped(int type, int G, int P, int N, int K, const int *offsets, c
     const int b = type_bytes(type);
     if (!aligned_to(offsets, 4) || !aligned_to(order, 4) || !aligned_to(X, b) || !aligned_to(W, b) || !aligned_to(Y, b))
         return GEMM_F32_ERR_ALIGN;
-    const bool dma = dma_rows(type, X, ldx, K, rows) && dma_rows(type, W, ldw, N, kPanelRows) &&
-                     dma_rows(type, Y, ldy, N, 0) && stride_w % (16 / b) == 0;
+    const bool dma = dma_rows(type, X, ldx, rows) && dma_rows(type, W, ldw, kPanelRows) && stride_w * b % 4 == 0;
     const GroupedArgs g{offsets, order, X, W, Y, ldx, ldw, ldy, stride_w, G, P, rows, Divisor(order != nullptr ? per_row : 1), 0, N, K, 0,
-                        gemm_f32_internal::current_device().xcds};
+                        gemm_f32_internal::current_device().xcds, vector_rows(type, Y, ldy, 0, N)};
     return launch_grouped<kForward>(type, g, dma, stream);
 }
 
@@ -370,10 +385,9 @@ int gemm_f32_grouped_grad_x(int type, int G, int P, int N, int K, const int *off
     const int b = type_bytes(type);
     if (!aligned_to(offsets, 4) || !aligned_to(dY, b) || !aligned_to(W, b) || !aligned_to(dX, b))
         return GEMM_F32_ERR_ALIGN;
-    const bool dma = dma_rows(type, dY, lddy, N, kPanelRows) && dma_rows(type, W, ldw, N, kPanelRows) &&
-                     dma_rows(type, dX, lddx, K, 0) && stride_w % (16 / b) == 0;
+    const bool dma = dma_rows(type, dY, lddy, kPanelRows) && dma_rows(type, W, ldw, kPanelRows) && stride_w * b % 4 == 0;
     const GroupedArgs g{offsets, nullptr, dY, W, dX, lddy, ldw, lddx, stride_w, G, P, P, Divisor(1), 0, K, N, 0,
-                        gemm_f32_internal::current_device().xcds};
+                        gemm_f32_internal::current_device().xcds, vector_rows(type, dX, lddx, 0, K)};
     return launch_grouped<kGradX>(type, g, dma, stream);
 }
 
@@ -397,10 +411,9 @@ int gemm_f32_grouped_grad_w(int type, int G, int P, int N, int K, const int *off
     const int b = type_bytes(type);
     if (!aligned_to(offsets, 4) || !aligned_to(order, 4) || !aligned_to(X, b) || !aligned_to(dY, b) || !aligned_to(dW, b))
         return GEMM_F32_ERR_ALIGN;
-    const bool dma = dma_rows(type, X, ldx, K, rows) && dma_rows(type, dY, lddy, N, kPanelRows) &&
-                     dma_rows(type, dW, lddw, N, 0) && stride_dw % (16 / b) == 0;
+    const bool dma = dma_rows(type, X, ldx, rows) && dma_rows(type, dY, lddy, kPanelRows);
     const GroupedArgs g{offsets, order, X, dY, dW, ldx, lddy, lddw, stride_dw, G, P, rows, Divisor(order != nullptr ? per_row : 1), K, N, 0, 0,
-                        gemm_f32_internal::current_device().xcds};
+                        gemm_f32_internal::current_device().xcds, vector_rows(type, dW, lddw, stride_dw, N)};
     return launch_grouped<kGradW>(type, g, dma, stream);
 }
 
@@ -421,7 +434,7 @@ int gemm_f32_combine(int type, int T, int k, int N, int P, const int *position, 
     if (!aligned_to(position, 4) || !aligned_to(weight, 4) || !aligned_to(Y, b) || !aligned_to(out, b))
         return GEMM_F32_ERR_ALIGN;
     const CombineArgs g{position, weight, Y, nullptr, out, nullptr, nullptr, ldy, ldo, 0, 0, T, k, N, P};
-    const bool vec = vector_rows(type, Y, ldy, N) && vector_rows(type, out, ldo, N);
+    const bool vec = chunk_rows(type, Y, ldy, N) && chunk_rows(type, out, ldo, N);
     with_type(type, [&](auto e) {
         using E = decltype(e);
         if (vec)
@@ -451,8 +464,8 @@ int gemm_f32_combine_grad(int type, int T, int k, int N, int P, const int *posit
         !aligned_to(dY, b) || !aligned_to(dweight, 4))
         return GEMM_F32_ERR_ALIGN;
     const CombineArgs g{position, weight, Y, dout, nullptr, dY, dweight, ldy, 0, lddo, lddy, T, k, N, P};
-    const bool vec = (dweight == nullptr || vector_rows(type, Y, ldy, N)) && vector_rows(type, dout, lddo, N) &&
-                     (dY == nullptr || vector_rows(type, dY, lddy, N));
+    const bool vec = (dweight == nullptr || chunk_rows(type, Y, ldy, N)) && chunk_rows(type, dout, lddo, N) &&
+                     (dY == nullptr || chunk_rows(type, dY, lddy, N));
     with_type(type, [&](auto e) {
         using E = decltype(e);
         if (vec)

@@ -21,16 +21,26 @@
 #ifndef GEMM_F32_ROWS_TILE_H
 #define GEMM_F32_ROWS_TILE_H
 
+#include <type_traits>
+
 #include "rows_common.h"
 
 namespace rows {
 
-// Chunk permutation of row r of an "along" panel of CH chunks per row.
+// Chunk permutation of row r of an "along" panel of CH chunks per row.  A
+// 128-bit LDS read serves lanes {0-3, 12-15, 20-27} together, then {4-11, 16-19,
+// 28-31}, and the same 32 further: rows 0-3 and 12-15 of one chunk column with
+// rows 4-11 of the next.  Both permutations put those 16 chunks on
+// the 16 distinct quarters of the 256 bytes that the banks span (128-byte rows:
+// r>>1, 64-byte rows: r>>2 times 2 in the field of four elements).
 template <int CH>
 __device__ inline int swz_along(int r)
 {
     static_assert(CH == 8 || CH == 4, "panels are 128 or 64 bytes deep");
-    return CH == 8 ? (r ^ (r >> 3)) & 7 : (r >> 2) & 3;
+    if constexpr (CH == 8)
+        return (r >> 1) & 7;
+    const int q = (r >> 2) & 3;
+    return ((q << 1) & 3) ^ ((q & 2) ? 3 : 0);
 }
 
 // Chunk permutation of k row k of an "across" panel of RN rows (16-bit types).
@@ -139,6 +149,7 @@ struct Tile {
     using Fa = Fragments<E, A_ALONG, BM, CH, kFm>;
     using Fb = Fragments<E, B_ALONG, BN, CH, kFn>;
     static_assert(BM % (16 * WM) == 0 && BN % (16 * WN) == 0, "wave tile");
+    static_assert((BM & (BM - 1)) == 0 && (BN & (BN - 1)) == 0, "the chunk permutations are made for powers of two");
 
     f32x4 acc[kFm][kFn];
 
@@ -206,7 +217,7 @@ struct Tile {
     }
 };
 
-// Four sums to four neighbouring elements of a row with `left` of them.
+// Four sums to four neighbouring elements of a row with `left` of them (VEC: at least four).
 template <class E, bool VEC>
 __device__ inline void store4(typename E::T *p, f32x4 v, int64_t left)
 {
@@ -216,7 +227,7 @@ __device__ inline void store4(typename E::T *p, f32x4 v, int64_t left)
 #pragma unroll
     for (int i = 0; i < 4; ++i)
         o.e[i] = (typename E::T)v[i];
-    if (left >= 4) {
+    if (VEC || left >= 4) {
         __builtin_memcpy(__builtin_assume_aligned(p, alignof(Four)), &o, sizeof o);
     } else {
 #pragma unroll
@@ -248,16 +259,19 @@ __device__ inline const char *uniform(const void *p)
 template <class E, int RN, int NT, int CH = 8>
 struct Along {
     using T = typename E::T;
+    static constexpr bool kListed = false;
     static constexpr int kSlots = RN * CH, kDeep = CH * E::kChunk, kCount = (kSlots + NT - 1) / NT;
     const char *base;
     int64_t off[kCount];
-    int k[kCount], K;                                // the chunk's first k in panel 0
+    int k[kCount], K, tid;                           // k: the chunk's first in panel 0
 
+    static constexpr bool kGuardTail = true;
+    __device__ inline uint32_t extent(int64_t) const { return kNowhere; }
     // Panel row of chunk i.
     static __device__ inline int row_of(int i, int tid) { return (tid + i * NT) / CH; }
 
     template <class Row>
-    __device__ inline Along(const T *base_, int tid, int K_, Row &&row) : base(uniform(base_)), K(__builtin_amdgcn_readfirstlane(K_))
+    __device__ inline Along(const T *base_, int tid, int K_, Row &&row) : base(uniform(base_)), K(__builtin_amdgcn_readfirstlane(K_)), tid(tid)
     {
 #pragma unroll
         for (int i = 0; i < kCount; ++i) {
@@ -280,16 +294,31 @@ struct Along {
 template <class E, int RN, int NT, int CH = 8>
 struct Across {
     using T = typename E::T;
+    static constexpr bool kListed = false;
     static constexpr int kSlots = RN * CH, kDeep = CH * E::kChunk, kCount = (kSlots + NT - 1) / NT;
     static constexpr int kPer = RN / E::kChunk;      // chunks of a k row
     const char *base;
     int64_t ld;                                      // bytes between k rows
     int tid, K, first, cols;
+    int rows;                                        // from base on
 
-    __device__ inline Across(const T *base_, int tid_, int K_, int64_t ld_, int first_, int cols_)
+    __device__ inline Across(const T *base_, int tid_, int K_, int64_t ld_, int first_, int cols_, int rows_)
         : base(uniform(base_)), ld(ld_ * E::kBytes), tid(tid_), K(__builtin_amdgcn_readfirstlane(K_)), first(first_),
-          cols(cols_)
+          cols(cols_), rows(rows_)
     {
+    }
+    __device__ inline Across(const T *base_, int tid_, int K_, int64_t ld_, int first_, int cols_)
+        : Across(base_, tid_, K_, ld_, first_, cols_, K_)
+    {
+    }
+    static constexpr bool kGuardTail = false;
+    // Bytes from the panel's base to the operand's end: a chunk that crosses the last
+    // row's end reads zeros there (one that crosses another row's end reads the
+    // next row's start, for columns that are not stored).  Whole dwords.
+    __device__ inline uint32_t extent(int64_t done) const
+    {
+        const int64_t n = ((rows - 1) * ld + (int64_t)cols * E::kBytes + 3) / 4 * 4 - done;
+        return (uint32_t)(n < (int64_t)kNowhere ? n : (int64_t)kNowhere);
     }
     __device__ inline int krow(int i) const { return (tid + i * NT) / kPer; }
     __device__ inline int col(int i) const
@@ -308,25 +337,26 @@ struct Across {
     __device__ inline int64_t offset(int i, int) const { return krow(i) * ld + (int64_t)col(i) * E::kBytes; }
 };
 
-// The same with k rows in any order: list[k] names k row k, a row of `rows`
-// (negative or past them: zeros) after division by per_row; list NULL: k itself.
+// The same with k rows in any order: k row k is row list[k] / per_row of
+// `rows` (negative or past them: zeros).  The direct loads take the rows' offsets
+// from LDS, where refill() puts kBlock of them at a time.
 template <class E, int RN, int NT, int CH = 8>
 struct Gathered : Across<E, RN, NT, CH> {
     using Base = Across<E, RN, NT, CH>;
-    const int *list;
+    static constexpr int kBlock = 512;
+    static constexpr bool kListed = true;
+    const int *list;                                 // NULL: k itself
+    uint32_t *ahead;                                 // LDS: 2 * kBlock offsets
     Divisor per_row;
-    int rows;
     __device__ inline Gathered(const typename E::T *base_, int tid_, int K_, int64_t ld_, int first_, int cols_,
-                               const int *list_, Divisor per_row_, int rows_)
-        : Base(base_, tid_, K_, ld_, first_, cols_), list(list_), per_row(per_row_), rows(rows_)
+                               const int *list_, Divisor per_row_, int rows_, uint32_t *ahead_)
+        : Base(base_, tid_, K_, ld_, first_, cols_, rows_), list(list_), ahead(ahead_), per_row(per_row_)
     {
     }
     __device__ inline int row(int k) const
     {
-        if (list == nullptr)
-            return k;
-        const int s = list[k], r = per_row.of(s);
-        return s < 0 || r >= rows ? -1 : r;
+        const int s = list != nullptr ? list[k] : k, r = per_row.of(s);
+        return s < 0 || r >= this->rows ? -1 : r;
     }
     __device__ inline int64_t step() const { return 0; }
     __device__ inline int left(int i, int k0) const
@@ -338,16 +368,26 @@ struct Gathered : Across<E, RN, NT, CH> {
     {
         return row(k0 + this->krow(i)) * this->ld + (int64_t)this->col(i) * E::kBytes;
     }
+    // Called by every thread before the barrier ahead of the panel at k0's loads.
+    __device__ inline void refill(int k0) const
+    {
+        if (k0 % kBlock != 0)
+            return;
+        for (int j = this->tid; j < kBlock; j += NT) {
+            const int k = k0 + j, r = k < this->K ? row(k) : -1;
+            ahead[(k0 / kBlock % 2) * kBlock + j] = r < 0 ? kNowhere : (uint32_t)(r * this->ld);
+        }
+    }
 };
 
 // ---------------------------------------------------------------------------
-// The K loop.  Adds the K-long sums to the tile from two LDS buffers of one
-// panel each (2 * (kLdsA + kLdsB) elements), one barrier per panel.
+// The K loop: adds the K-long sums to the tile.
 //
-// DMA: buffer loads write the panels straight into LDS, the next panel's
-// while the matrix cores work on this one.  Rows that are 16-byte
-// aligned, whole chunks long and less than 2^31 bytes from their base.  Else the
-// chunks are staged through registers, element by element at a row's end.
+// DMA: buffer loads write panels straight into a ring of S LDS buffers of
+// kLdsA + kLdsB elements, S - 1 panels ahead of the matrix cores, one
+// barrier per panel.  For rows on 4-byte boundaries less than 2^31 bytes from
+// their base.  Else the chunks are staged through registers into two
+// buffers, element by element at a row's end.
 // ---------------------------------------------------------------------------
 template <class E, class Ti, class SrcA, class SrcB>
 __device__ inline void sum_panels_staged(Ti &tile, int K, const SrcA &a, const SrcB &b, typename E::T *lds, int tid,
@@ -408,22 +448,32 @@ struct PanelLoads {
     }
     __device__ inline void fire(const Src &src, int k0, T *panel, int wave) const
     {
-        const char *base = src.base + (int64_t)(k0 / Src::kDeep) * src.step();
-        const auto rsrc = __builtin_amdgcn_make_buffer_rsrc((void *)base, 0, (int)kNowhere, kRawBufferFlags);
+        const int64_t done = (int64_t)(k0 / Src::kDeep) * src.step();
+        const auto rsrc = __builtin_amdgcn_make_buffer_rsrc((void *)(src.base + done), 0, (int)src.extent(done), kRawBufferFlags);
         auto load = [&](int i, uint32_t o) {
             if (Src::kSlots % NT != 0 && (i * NT + wave * kWave) >= Src::kSlots)
                 return;                              // whole waves: kSlots is a multiple of 64
             auto *dst = (lds_ptr<void>)(panel + (i * NT + wave * kWave) * E::kChunk);
             __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, dst, 16, o, 0, 0, 0);
         };
-        if (src.partial(k0)) {
+        if (!src.partial(k0)) {
+#pragma unroll
+            for (int i = 0; i < Src::kCount; ++i)
+                load(i, off[i]);
+        } else if (!Src::kGuardTail || src.K % E::kChunk == 0) {
 #pragma unroll
             for (int i = 0; i < Src::kCount; ++i)
                 load(i, src.left(i, k0) > 0 ? off[i] : kNowhere);
         } else {
+            // The last chunk of a row that is no whole number of chunks long:
+            // element by element, what lies behind the row must not be summed.
 #pragma unroll
-            for (int i = 0; i < Src::kCount; ++i)
-                load(i, off[i]);
+            for (int i = 0; i < Src::kCount; ++i) {
+                const int slot = src.tid + i * NT, n = src.left(i, k0);
+                if (Src::kSlots % NT == 0 || slot < Src::kSlots)
+                    *reinterpret_cast<u32x4 *>(panel + slot * E::kChunk) =
+                        load_chunk<E, false>((const T *)(src.base + done + (n > 0 ? src.offset(i, k0) : 0)), n);
+            }
         }
     }
 };
@@ -435,68 +485,103 @@ struct PanelLoads<E, Gathered<E, RN, NT, CH>, NT> {
     __device__ inline PanelLoads(const Src &) {}
     __device__ inline void fire(const Src &src, int k0, T *panel, int wave) const
     {
-        const auto rsrc = __builtin_amdgcn_make_buffer_rsrc((void *)src.base, 0, (int)kNowhere, kRawBufferFlags);
+        static_assert(Src::kSlots % NT == 0 && Src::kBlock % Src::kDeep == 0, "whole panels");
+        const auto rsrc = __builtin_amdgcn_make_buffer_rsrc((void *)src.base, 0, (int)src.extent(0), kRawBufferFlags);
+        const uint32_t *block = src.ahead + (k0 / Src::kBlock % 2) * Src::kBlock + k0 % Src::kBlock;
 #pragma unroll
         for (int i = 0; i < Src::kCount; ++i) {
-            const uint32_t o = src.left(i, k0) > 0 ? (uint32_t)src.offset(i, k0) : kNowhere;
+            const uint32_t row = block[src.krow(i)];
+            const uint32_t o = row == kNowhere || src.col(i) >= src.cols ? kNowhere : row + src.col(i) * E::kBytes;
             auto *dst = (lds_ptr<void>)(panel + (i * NT + wave * kWave) * E::kChunk);
             __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, dst, 16, o, 0, 0, 0);
         }
     }
 };
 
-template <class E, class Ti, class SrcA, class SrcB>
+// One panel: the next one's loads into `next`, this one's sums from `now`.  The
+// two do not overlap; saying so keeps the compiler from waiting for
+// the loads before it reads.
+template <class E, class Ti, class Fire>
+__device__ __forceinline__ void panel_step(Ti &tile, const typename E::T *__restrict__ now, typename E::T *__restrict__ next,
+                                           Fire &&fire, int wm, int wn, int lane)
+{
+    fire(next);
+    typename Ti::Panel p;
+    p.read(now, now + Ti::kLdsA, wm, wn, lane);
+    tile.multiply(p);
+}
+
+template <class E, int S, class Ti, class SrcA, class SrcB>
 __device__ inline void sum_panels_dma(Ti &tile, int K, const SrcA &a, const SrcB &b, typename E::T *lds, int tid,
                                       int wm, int wn)
 {
     using T = typename E::T;
-    constexpr int BK = Ti::kDeep, NT = Ti::kThreads;
+    constexpr int BK = Ti::kDeep, NT = Ti::kThreads, kPanel = Ti::kLdsA + Ti::kLdsB;
+    // A wave's loads per panel (where the slots are no multiple of the threads the last
+    // waves have fewer, and wait for more than they must).
+    constexpr int kLoads = SrcA::kSlots / NT + SrcB::kSlots / NT;
     const int lane = tid % kWave, wave = __builtin_amdgcn_readfirstlane(tid / kWave);
     const PanelLoads<E, SrcA, NT> pa(a);
     const PanelLoads<E, SrcB, NT> pb(b);
-    auto fire = [&](int k0, int buf) {
-        T *la = lds + buf * (Ti::kLdsA + Ti::kLdsB);
-        pa.fire(a, k0, la, wave);
-        pb.fire(b, k0, la + Ti::kLdsA, wave);
+    auto fire = [&](int k0, T *panel) {
+        pa.fire(a, k0, panel, wave);
+        pb.fire(b, k0, panel + Ti::kLdsA, wave);
     };
-    if (K > 0)
-        fire(0, 0);
-    int buf = 0;
-    for (int k0 = 0; k0 < K; k0 += BK, buf ^= 1) {
-        // This panel has landed, and the other buffer's reads are complete in
-        // every wave: it may be filled again.
-        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+    if constexpr (SrcA::kListed) {
+        a.refill(0);
+        __syncthreads();
+    }
+#pragma unroll
+    for (int q = 0; q < S - 1; ++q)
+        if (q * BK < K)
+            fire(q * BK, lds + q * kPanel);
+    int now = 0, next = S - 1;
+    for (int k0 = 0; k0 < K; k0 += BK) {
+        if constexpr (SrcA::kListed)
+            a.refill(k0 + (S - 1) * BK);
+        // This panel has landed when no more than the S - 2 panels after it, all
+        // whole ones, are in flight; the buffer of the panel before it is
+        // free once every wave has read it.
+        if (k0 + (S - 1) * BK <= K)
+            asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((S - 2) * kLoads) : "memory");
+        else
+            asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
-        // This panel's LDS reads go first: the compiler waits for every load
-        // in flight before a transposing read that follows it.
-        const T *la = lds + buf * (Ti::kLdsA + Ti::kLdsB);
-        typename Ti::Panel p;
-        p.read(la, la + Ti::kLdsA, wm, wn, lane);
-        __builtin_amdgcn_sched_barrier(0);
-        if (k0 + BK < K)
-            fire(k0 + BK, buf ^ 1);
-        __builtin_amdgcn_sched_barrier(0);
-        tile.multiply(p);
+        const int ahead = k0 + (S - 1) * BK;
+        panel_step<E>(tile, lds + now * kPanel, lds + next * kPanel,
+                      [&](T *panel) {
+                          if (ahead < K)
+                              fire(ahead, panel);
+                      },
+                      wm, wn, lane);
+        now = now + 1 == S ? 0 : now + 1;
+        next = next + 1 == S ? 0 : next + 1;
     }
 }
 
-template <class E, bool DMA, class Ti, class SrcA, class SrcB>
+template <class E, bool DMA, int S, class Ti, class SrcA, class SrcB>
 __device__ inline void sum_panels(Ti &tile, int K, const SrcA &a, const SrcB &b, typename E::T *lds, int tid, int wm,
                                   int wn)
 {
     if constexpr (DMA)
-        sum_panels_dma<E>(tile, K, a, b, lds, tid, wm, wn);
+        sum_panels_dma<E, S>(tile, K, a, b, lds, tid, wm, wn);
     else
         sum_panels_staged<E>(tile, K, a, b, lds, tid, wm, wn);
 }
 
-// Rows that the direct loads can address: 16-byte aligned, a whole number of
-// chunks long, `span` rows of ld elements within 2^31 bytes.
-inline bool dma_rows(int type, const void *p, int64_t ld, int64_t cols, int64_t span)
+// Rows that the direct loads can address: on 4-byte boundaries, `span` rows of ld
+// elements within 2^31 bytes.
+inline bool dma_rows(int type, const void *p, int64_t ld, int64_t span)
 {
-    const int b = type_bytes(type), chunk = 16 / b;
-    return aligned_to(p, 16) && ld % chunk == 0 && cols % chunk == 0 && span * ld < (int64_t)kNowhere / b;
+    const int b = type_bytes(type);
+    return aligned_to(p, 4) && ld * b % 4 == 0 && span * ld < (int64_t)kNowhere / b - 16;
+}
+
+// Rows that stores of four elements can write.
+inline bool vector_rows(int type, const void *p, int64_t ld, int64_t stride, int64_t cols)
+{
+    return aligned_to(p, 4 * type_bytes(type)) && ld % 4 == 0 && stride % 4 == 0 && cols % 4 == 0;
 }
 
 }  // namespace rows

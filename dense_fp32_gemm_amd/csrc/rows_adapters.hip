@@ -1,16 +1,20 @@
 // Low-rank adapters of many requests beside a shared product
 // (include/gemm_f32_rows.h):  Y(t) = X(t).W + scale[a] (X(t).A_a).B_a.
 //
-//  1. down_kernel: U = X(t).A_a, 16 rows of X a wave, the K sum split over
-//     workgroups; binary32 partial sums to the workspace.
+// Few rows (the tiles of X.W would leave compute units idle), two launches:
+//  1. step_kernel: X.W with K split over workgroups, and U = X(t).A_a, likewise,
+//     as further workgroups of the same launch; binary32 partial sums to the workspace.
+//  2. join_kernel: adds the parts in order and the row's U . B_a, vector FMAs.
+// Many rows, three launches:
+//  1. down_kernel: U = X(t).A_a, binary32 partial sums.
 //  2. factor_kernel: adds the splits, scales, and writes each row of U as the
 //     up-projection's operand: binary32 as it is, 16-bit types as high + low
 //     parts (two 16-bit numbers per value: 16 to 22 bits instead of 8 to 11,
 //     so that rounding U adds nothing to the rounding of Y) times a power of two
 //     per row, which keeps them inside the type's range.
 //  3. adapters_kernel: the tile of X.W, then for each adapter among its
-//     rows the product of U's rows with B_a into a second set of sums,
-//     of which only that adapter's rows are added.
+//     rows the product of U's rows with B_a, of which only that adapter's rows
+//     are added.
 //
 // An adapter's weights meet only its own rows' sums: infinities or NaN in one
 // adapter do not reach other requests.
@@ -25,24 +29,32 @@ struct AdapterArgs {
     const int *adapter;
     const float *scale;
     void *Y;
-    float *partial;      // [splits][T][R]
-    void *factor;        // [T][depth] elements
-    float *unscale;      // [T]
+    float *partial_u;    // [splits_u][T][R]
+    float *partial_y;    // few rows: [splits][T][pitch]
+    void *factor;        // many rows: [T][depth] elements
+    float *unscale;      // many rows: [T]
     int64_t ldx, ldw, lda, ldb, ldy, stride_a, stride_b;
     int T, N, K, R, n;
-    int splits, split_k; // down-projection: workgroups along K, k's of each
-    int depth;           // of factor's rows
+    int splits_u, split_ku;  // down-projection: parts along K, k's of each
+    int slots;               // waves that share a row tile's adapters
+    int ranks;               // blocks of ranks
+    int splits, split_k;     // few rows: parts of X.W along K
+    int pitch;
+    int depth;               // of factor's rows
     int tiles_m, tiles_n;
+    int big_m;               // many rows: rows of tiles of the large kind, the rest are small ones
     int xcds;
-    bool vector_y;       // Y's rows take stores of four elements
+    bool vector_y;           // Y's rows take stores of four elements
 };
 
-// Rank indices a panel of the up-projection holds: 16-bit panels are 64 deep,
-// 32 high parts and then the 32 low parts of the same ranks.
+// Elements in a 128-byte panel row; rank indices such a panel of the up-projection
+// holds: 16-bit panels are 64 deep, 32 high parts and then the low parts of the
+// same ranks.
 template <class E>
 constexpr int panel_deep() { return 128 / E::kBytes; }
+constexpr int kPanelRanks = 32;
 template <class E>
-int factor_depth(int R) { return (int)ceil_div(R, 32) * panel_deep<E>(); }
+int factor_depth(int R) { return (int)ceil_div(R, kPanelRanks) * panel_deep<E>(); }
 
 // B_a's rows as the second operand of the up-projection: twice per panel for
 // the 16-bit types.
@@ -54,13 +66,13 @@ struct UpRows : Across<E, RN, NT> {
         : Base(base_, tid_, depth, ld_, first_, cols_, R_), R(R_)
     {
     }
-    __device__ inline int rank(int i, int k0) const { return k0 / panel_deep<E>() * 32 + this->krow(i) % 32; }
-    __device__ inline int64_t step() const { return 32 * this->ld; }
-    __device__ inline bool partial(int k0) const { return (k0 / panel_deep<E>() + 1) * 32 > R; }
+    __device__ inline int rank(int i, int k0) const { return k0 / Base::kDeep * kPanelRanks + this->krow(i) % kPanelRanks; }
+    __device__ inline int64_t step() const { return kPanelRanks * this->ld; }
+    __device__ inline bool partial(int k0) const { return (k0 / Base::kDeep + 1) * kPanelRanks > R; }
     __device__ inline int left(int i, int k0) const { return rank(i, k0) < R ? Base::left(i, k0) : 0; }
     __device__ inline int64_t offset(int i, int) const
     {
-        return this->krow(i) % 32 * this->ld + (int64_t)this->col(i) * E::kBytes;
+        return this->krow(i) % kPanelRanks * this->ld + (int64_t)this->col(i) * E::kBytes;
     }
 };
 
@@ -87,36 +99,157 @@ __device__ inline int adapter_of(const AdapterArgs &g, int64_t t, bool there)
     return a >= 0 && a < g.n ? a : -1;
 }
 
-// One wave: U of 16 rows over split_k of K.  RN: rank rounded up.
+// ---------------------------------------------------------------------------
+// Down-projection.  One wave: 16 rows, one part of K, RN ranks, and every
+// slots-th adapter among the rows.  RN is 16 or 64 (more ranks: further waves).
+// ---------------------------------------------------------------------------
+constexpr int kDownWaves = 4;
+template <int RN>
+constexpr int down_stages() { return RN == 16 ? 4 : 2; }
+template <class E, int RN>
+constexpr int down_lds() { return down_stages<RN>() * (16 + RN) * panel_deep<E>(); }   // elements of a wave
+
 template <class E, int RN, bool DMA>
-__global__ __launch_bounds__(kWave) void down_kernel(AdapterArgs g)
+__device__ inline void down_item(const AdapterArgs &g, int64_t item, typename E::T *lds, int lane)
 {
     using Ti = Tile<E, true, false, 16, RN, 1, 1>;
     using T = typename E::T;
-    __shared__ __attribute__((aligned(16))) T lds[2 * (Ti::kLdsA + Ti::kLdsB)];
-    const int lane = threadIdx.x;
-    const int t0 = blockIdx.x * 16, k0 = blockIdx.y * g.split_k, K = min(g.split_k, g.K - k0);
+    const int64_t tiles = (g.T + 15) / 16;
+    if (item >= tiles * g.splits_u * g.slots * g.ranks)
+        return;
+    // neighbouring waves: the parts of K and the adapters of one row tile
+    const int split = (int)(item % g.splits_u), slot = (int)(item / g.splits_u % g.slots);
+    const int rank0 = (int)(item / ((int64_t)g.splits_u * g.slots) % g.ranks) * RN;
+    const int t0 = (int)(item / ((int64_t)g.splits_u * g.slots * g.ranks)) * 16;
+    const int k0 = split * g.split_ku, K = min(g.split_ku, g.K - k0);
     const int which = adapter_of(g, t0 + lane, lane < 16 && t0 + lane < g.T);
+    int nth = 0;
     each_adapter<16>(which, -1, [&](int a, uint64_t members, uint64_t) {
+        if (nth++ % g.slots != slot)
+            return;
         Ti tile;
         tile.clear();
         const Along<E, 16, kWave> x((const T *)g.X + t0 * g.ldx + k0, lane, K,
                                     [&](int, int r) { return members >> r & 1 ? r * g.ldx * E::kBytes : -1; });
-        const Across<E, RN, kWave> w((const T *)g.A + a * g.stride_a + k0 * g.lda, lane, K, g.lda, 0, g.R);
-        __syncthreads();
-        sum_panels<E, DMA, 2>(tile, K, x, w, lds, lane, 0, 0);
+        const Across<E, RN, kWave> w((const T *)g.A + a * g.stride_a + k0 * g.lda, lane, K, g.lda, rank0, g.R);
+        group_sync<kWave>();
+        sum_panels<E, DMA, down_stages<RN>()>(tile, K, x, w, lds, lane, 0, 0);
         tile.each(0, 0, lane, [&](int r, int c, f32x4 v) {
             if (members >> r & 1) {
-                float *u = g.partial + ((int64_t)blockIdx.y * g.T + t0 + r) * g.R + c;
+                float *u = g.partial_u + ((int64_t)split * g.T + t0 + r) * g.R + rank0 + c;
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    if (c + i < g.R)
+                    if (rank0 + c + i < g.R)
                         u[i] = v[i];
             }
         });
     });
 }
 
+template <class E, int RN, bool DMA>
+__global__ __launch_bounds__(kDownWaves *kWave) void down_kernel(AdapterArgs g)
+{
+    __shared__ __attribute__((aligned(16))) typename E::T lds[kDownWaves * down_lds<E, RN>()];
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    down_item<E, RN, DMA>(g, (int64_t)blockIdx.x * kDownWaves + wave, lds + wave * down_lds<E, RN>(), threadIdx.x % kWave);
+}
+
+// ---------------------------------------------------------------------------
+// Few rows
+// ---------------------------------------------------------------------------
+constexpr int kStepBN = 64, kStepStages = 4;
+
+// Workgroups 0 .. tiles_m * tiles_n * splits - 1: parts of X.W; then the down-projection.
+template <class E, int BM, int RN, bool DMA>
+__global__ __launch_bounds__(kDownWaves *kWave) void step_kernel(AdapterArgs g)
+{
+    using T = typename E::T;
+    constexpr int WM = BM == 16 ? 1 : 2, WN = 4 / WM, NT = kDownWaves * kWave;
+    using Ti = Tile<E, true, false, BM, kStepBN, WM, WN>;
+    constexpr int kTileLds = (DMA ? kStepStages : 2) * (Ti::kLdsA + Ti::kLdsB), kDownLds = kDownWaves * down_lds<E, RN>();
+    __shared__ __attribute__((aligned(16))) T lds[kTileLds > kDownLds ? kTileLds : kDownLds];
+    const int tid = threadIdx.x, lane = tid % kWave, wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+    const int parts = g.tiles_m * g.tiles_n * g.splits;
+    if ((int)blockIdx.x >= parts) {
+        down_item<E, RN, DMA>(g, (int64_t)((int)blockIdx.x - parts) * kDownWaves + wave, lds + wave * down_lds<E, RN>(), lane);
+        return;
+    }
+    const int wm = wave / WN, wn = wave % WN;
+    const int tm = blockIdx.x % g.tiles_m, rest = blockIdx.x / g.tiles_m;   // rows share W's panels
+    const int n0 = rest % g.tiles_n * kStepBN, split = rest / g.tiles_n;
+    const int m0 = tm * BM, k0 = split * g.split_k, K = min(g.split_k, g.K - k0);
+    Ti tile;
+    tile.clear();
+    const Along<E, BM, NT> x((const T *)g.X + m0 * g.ldx + k0, tid, K,
+                             [&](int, int r) { return m0 + r < g.T ? r * g.ldx * E::kBytes : -1; });
+    const Across<E, kStepBN, NT> w((const T *)g.W + k0 * g.ldw, tid, K, g.ldw, n0, g.N);
+    sum_panels<E, DMA, kStepStages>(tile, K, x, w, lds, tid, wm, wn);
+    tile.each(wm, wn, lane, [&](int r, int c, f32x4 v) {
+        // whole groups of four: rows of the parts are padded to a multiple of eight
+        if (m0 + r < g.T && n0 + c < g.N)
+            *reinterpret_cast<f32x4 *>(g.partial_y + ((int64_t)split * g.T + m0 + r) * g.pitch + n0 + c) = v;
+    });
+}
+
+// One wave: a chunk per lane of one row's columns.
+template <class E>
+__global__ __launch_bounds__(kWave) void join_kernel(AdapterArgs g)
+{
+    using T = typename E::T;
+    __shared__ float u[GEMM_F32_MAX_RANK];
+    const int lane = threadIdx.x;
+    const int64_t t = blockIdx.y;
+    const int n = (blockIdx.x * kWave + lane) * E::kChunk;
+    const int a = g.R > 0 && g.n > 0 ? adapter_of(g, t, true) : -1;
+    if (a >= 0) {
+        const float s = g.scale != nullptr ? g.scale[a] : 1.f;
+        for (int r = lane; r < g.R; r += kWave) {
+            float sum = 0.f;
+            for (int i = 0; i < g.splits_u; ++i)
+                sum += g.partial_u[((int64_t)i * g.T + t) * g.R + r];
+            u[r] = s * sum;
+        }
+    }
+    __syncthreads();
+    if (n >= g.N)
+        return;
+    float sum[E::kChunk] = {};
+    for (int i = 0; i < g.splits; ++i) {
+        const float *p = g.partial_y + ((int64_t)i * g.T + t) * g.pitch + n;
+#pragma unroll
+        for (int e = 0; e < E::kChunk; e += 4) {
+            const f32x4 v = *reinterpret_cast<const f32x4 *>(p + e);
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                sum[e + q] += v[q];
+        }
+    }
+    if (a >= 0) {
+        const T *B = (const T *)g.B + a * g.stride_b + n;
+        constexpr int kBatch = 8;                    // rows of B in flight
+        for (int r0 = 0; r0 < g.R; r0 += kBatch) {
+            Chunk<E> b[kBatch];
+#pragma unroll
+            for (int q = 0; q < kBatch; ++q)
+                b[q].raw = load_chunk<E, false>(B + (int64_t)(r0 + q) * g.ldb, r0 + q < g.R ? g.N - n : 0);
+#pragma unroll
+            for (int q = 0; q < kBatch; ++q)
+                if (r0 + q < g.R)
+#pragma unroll
+                    for (int e = 0; e < E::kChunk; ++e)
+                        sum[e] = fmaf(u[r0 + q], (float)b[q].e[e], sum[e]);
+        }
+    }
+    Chunk<E> o;
+#pragma unroll
+    for (int e = 0; e < E::kChunk; ++e)
+        o.e[e] = (T)sum[e];
+    store_chunk<E, false>((T *)g.Y + t * g.ldy + n, o, g.N - n);
+}
+
+// ---------------------------------------------------------------------------
+// Many rows
+// ---------------------------------------------------------------------------
 // A wave per row.
 constexpr int kFactorThreads = 256;
 
@@ -141,8 +274,8 @@ __global__ __launch_bounds__(kFactorThreads) void factor_kernel(AdapterArgs g)
         const int r = q * kWave + lane;
         u[q] = 0.f;
         if (r < g.R)
-            for (int i = 0; i < g.splits; ++i)
-                u[q] += g.partial[((int64_t)i * g.T + t) * g.R + r];
+            for (int i = 0; i < g.splits_u; ++i)
+                u[q] += g.partial_u[((int64_t)i * g.T + t) * g.R + r];
         u[q] *= s;
         top = fmaxf(top, fabsf(u[q]));
     }
@@ -173,26 +306,22 @@ __global__ __launch_bounds__(kFactorThreads) void factor_kernel(AdapterArgs g)
     }
 }
 
-template <class E, int BM, int BN, int WM, int WN, bool DMA>
-__global__ __launch_bounds__(WM *WN *kWave) void adapters_kernel(AdapterArgs g)
+// One tile of Y, rows from m0 on.
+template <class E, int BM, int BN, int WM, int WN, int S, bool DMA>
+__device__ inline void adapters_tile(const AdapterArgs &g, int m0, int n0, typename E::T *lds)
 {
     using Ti = Tile<E, true, false, BM, BN, WM, WN>;
     using T = typename E::T;
     constexpr int NT = Ti::kThreads;
-    __shared__ __attribute__((aligned(16))) T lds[2 * (Ti::kLdsA + Ti::kLdsB)];
-    const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
+    const int tid = threadIdx.x, lane = tid % kWave, wave = __builtin_amdgcn_readfirstlane(tid / kWave);
     const int wm = wave / WN, wn = wave % WN;
-    const int total = gridDim.x, per = total / g.xcds, rem = total % g.xcds, xcd = blockIdx.x % g.xcds;
-    const int t = xcd * per + min(xcd, rem) + blockIdx.x / g.xcds;   // contiguous tiles per die
-    const int m0 = t % g.tiles_m * BM, n0 = t / g.tiles_m * BN;
-
     Ti tile;
     tile.clear();
     {
         const Along<E, BM, NT> x((const T *)g.X + m0 * g.ldx, tid, g.K,
                                  [&](int, int r) { return m0 + r < g.T ? r * g.ldx * E::kBytes : -1; });
         const Across<E, BN, NT> w((const T *)g.W, tid, g.K, g.ldw, n0, g.N);
-        sum_panels<E, DMA, 2>(tile, g.K, x, w, lds, tid, wm, wn);
+        sum_panels<E, DMA, S>(tile, g.K, x, w, lds, tid, wm, wn);
     }
     if (g.R > 0 && g.n > 0) {
         const int which0 = adapter_of(g, m0 + lane, lane < BM && m0 + lane < g.T);
@@ -202,21 +331,36 @@ __global__ __launch_bounds__(WM *WN *kWave) void adapters_kernel(AdapterArgs g)
             const Along<E, BM, NT> u((const T *)g.factor + (int64_t)m0 * g.depth, tid, g.depth,
                                      [&](int, int r) { return member(r) ? (int64_t)r * g.depth * E::kBytes : -1; });
             const UpRows<E, BN, NT> b((const T *)g.B + a * g.stride_b, tid, g.depth, g.ldb, n0, g.N, g.R);
-            Ti add;
-            add.clear();
-            __syncthreads();
-            sum_panels<E, DMA, 2>(add, g.depth, u, b, lds, tid, wm, wn);
+            // Panel by panel, each panel's sums of one 16-row block at a time: a second
+            // set of sums for the whole tile would halve the waves a SIMD holds.
+            for (int k0 = 0; k0 < g.depth; k0 += Ti::kDeep) {
+                __syncthreads();
+                load_panel<E, DMA, NT>(u, k0, lds, tid);
+                load_panel<E, DMA, NT>(b, k0, lds + Ti::kLdsA, tid);
+                asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+                __syncthreads();
+                typename Ti::Panel p;
+                p.read(lds, lds + Ti::kLdsA, wm, wn, lane);
 #pragma unroll
-            for (int m = 0; m < Ti::kFm; ++m) {
-                const int r = wm * (BM / WM) + Ti::Fa::row_of(m, lane % 16);
-                if (!member(r))
-                    continue;
-                const float f = E::kBytes == 4 ? 1.f : g.unscale[m0 + r];
+                for (int m = 0; m < Ti::kFm; ++m) {
+                    f32x4 add[Ti::kFn];
 #pragma unroll
-                for (int n = 0; n < Ti::kFn; ++n)
+                    for (int n = 0; n < Ti::kFn; ++n) {
+                        add[n] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        tile.acc[m][n][i] = fmaf(f, add.acc[m][n][i], tile.acc[m][n][i]);
+                        for (int step = 0; step < Ti::kSteps; ++step)
+                            add[n] = mfma_step<E>(p.b[step].q[n], p.a[step].q[m], add[n]);
+                    }
+                    const int r = wm * (BM / WM) + Ti::Fa::row_of(m, lane % 16);
+                    if (!member(r))
+                        continue;
+                    const float f = E::kBytes == 4 ? 1.f : g.unscale[m0 + r];
+#pragma unroll
+                    for (int n = 0; n < Ti::kFn; ++n)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            tile.acc[m][n][i] = fmaf(f, add[n][i], tile.acc[m][n][i]);
+                }
             }
         });
     }
@@ -234,68 +378,145 @@ __global__ __launch_bounds__(WM *WN *kWave) void adapters_kernel(AdapterArgs g)
         store(std::false_type{});
 }
 
+// tiles_m rows of tiles: big_m of 128 rows, then tiles of 16 rows.
+template <class E, bool DMA>
+__global__ __launch_bounds__(256, 2) void adapters_kernel(AdapterArgs g)
+{
+    constexpr int kBN = 128;
+    __shared__ __attribute__((aligned(16))) typename E::T lds[2 * (128 + kBN) * panel_deep<E>()];
+    const int total = gridDim.x, per = total / g.xcds, rem = total % g.xcds, xcd = blockIdx.x % g.xcds;
+    const int t = xcd * per + min(xcd, rem) + blockIdx.x / g.xcds;   // contiguous tiles per die
+    const int tm = t % g.tiles_m, n0 = t / g.tiles_m * kBN;
+    if (tm < g.big_m)
+        adapters_tile<E, 128, kBN, 2, 2, 2, DMA>(g, tm * 128, n0, lds);
+    else
+        adapters_tile<E, 16, kBN, 1, 4, 2, DMA>(g, g.big_m * 128 + (tm - g.big_m) * 16, n0, lds);
+}
+
 // ---------------------------------------------------------------------------
 // Host side
 // ---------------------------------------------------------------------------
-// Workgroups along K of the down-projection: about a thousand waves in all,
-// at least four panels each.
-int down_splits(int T, int K, int panel)
-{
-    const int64_t tiles = ceil_div(T, 16), panels = ceil_div(K, panel);
-    int64_t s = 1024 / tiles;
-    if (s > panels / 4)
-        s = panels / 4;
-    return (int)(s < 1 ? 1 : s > 32 ? 32 : s);
-}
-
-struct Workspace {
-    size_t partial, factor, unscale, bytes;   // offsets
+// How a call is split; sized for 256 compute units whatever the device, so
+// that the workspace depends on the arguments alone.
+struct Split {
+    bool few;
+    int splits, split_k;                             // X.W, few rows
+    int splits_u, split_ku, slots, ranks, rank_block;
+    int pitch, depth;
+    size_t partial_y, factor, unscale, bytes;        // workspace offsets
 };
+
 size_t round16(size_t n) { return (n + 15) / 16 * 16; }
 
+// Parts of `panels` panels: `want` of them, none under `least` panels.
+void cut(int64_t panels, int64_t want, int64_t least, int panel, int *parts, int *length)
+{
+    int64_t s = want < panels / least ? want : panels / least;
+    if (s < 1)
+        s = 1;
+    const int64_t each = panels > 0 ? ceil_div(panels, s) : 0;
+    *parts = panels > 0 ? (int)ceil_div(panels, each) : 1;
+    *length = (int)(each * panel);
+}
+
 template <class E>
-Workspace workspace(int T, int K, int R)
+Split plan(int T, int N, int K, int R)
 {
-    Workspace w;
-    w.partial = 0;
-    w.factor = round16((size_t)down_splits(T, K, panel_deep<E>()) * (size_t)T * (size_t)R * 4);
-    w.unscale = w.factor + round16((size_t)T * (size_t)factor_depth<E>(R) * E::kBytes);
-    w.bytes = w.unscale + round16((size_t)T * 4);
-    return w;
-}
-
-template <class E, int RN>
-void launch_down(const AdapterArgs &g, bool dma, hipStream_t stream)
-{
-    const dim3 grid((unsigned)ceil_div(g.T, 16), (unsigned)g.splits);
-    if (dma)
-        down_kernel<E, RN, true><<<grid, kWave, 0, stream>>>(g);
-    else
-        down_kernel<E, RN, false><<<grid, kWave, 0, stream>>>(g);
-}
-
-template <class E, int BM, int BN, int WM, int WN>
-int launch_tiles(AdapterArgs g, bool dma, hipStream_t stream)
-{
-    const int64_t tm = ceil_div(g.T, BM), tn = ceil_div(g.N, BN);
-    if (tm * tn > (int64_t)UINT32_MAX / 256)
-        return GEMM_F32_ERR_DIM;
-    g.tiles_m = (int)tm;
-    g.tiles_n = (int)tn;
-    if (dma)
-        adapters_kernel<E, BM, BN, WM, WN, true><<<(int)(tm * tn), WM * WN * kWave, 0, stream>>>(g);
-    else
-        adapters_kernel<E, BM, BN, WM, WN, false><<<(int)(tm * tn), WM * WN * kWave, 0, stream>>>(g);
-    return launched();
+    Split p{};
+    const int panel = panel_deep<E>();
+    const int64_t panels = ceil_div(K, panel), rows16 = ceil_div(T, 16);
+    p.few = ceil_div(T, 128) * ceil_div(N, 128) < 128 && T <= 512;
+    p.rank_block = R <= 16 ? 16 : 64;
+    p.ranks = (int)ceil_div(R, p.rank_block);
+    if (R > 0) {
+        // about a thousand waves: up to 16 for the adapters of a row tile when rows are few
+        p.slots = p.few ? (T < 16 ? T : 16) : 2;
+        cut(panels, 1024 / (rows16 * p.slots * p.ranks), 4, panel, &p.splits_u, &p.split_ku);
+    }
+    if (p.few) {
+        const int64_t tiles = ceil_div(T, T <= 16 ? 16 : 64) * ceil_div(N, kStepBN);
+        cut(panels, 512 / tiles, 4, panel, &p.splits, &p.split_k);
+        p.pitch = (int)ceil_div(N, 8) * 8;
+    }
+    p.depth = factor_depth<E>(R);
+    size_t at = round16((size_t)p.splits_u * (size_t)T * (size_t)R * 4);
+    p.partial_y = at;
+    if (p.few) {
+        at += round16((size_t)p.splits * (size_t)T * (size_t)p.pitch * 4);
+    } else if (R > 0) {
+        p.factor = at;
+        at += round16((size_t)T * (size_t)p.depth * E::kBytes);
+        p.unscale = at;
+        at += round16((size_t)T * 4);
+    }
+    p.bytes = at;
+    return p;
 }
 
 // A grid has fewer than 2^32 threads, and there is a wave per token.
 constexpr int kMaxTokens = 1 << 25;
-
 // Most rows of an operand that one panel's offsets span (a tile's, or a panel's depth).
 constexpr int kPanelRows = 256;
 
 bool short_ld(int64_t ld, int cols) { return ld < at_least_one(cols); }
+
+template <class E, int RN>
+int64_t down_blocks(const AdapterArgs &g)
+{
+    return ceil_div(ceil_div(g.T, 16) * g.splits_u * g.slots * g.ranks, kDownWaves);
+}
+
+template <class E, int RN>
+int run_few(AdapterArgs g, bool low, bool dma, hipStream_t stream)
+{
+    const int64_t down = low ? down_blocks<E, RN>(g) : 0;
+    auto launch = [&](auto bm, auto direct) {
+        constexpr int BM = decltype(bm)::value;
+        g.tiles_m = (int)ceil_div(g.T, BM);
+        g.tiles_n = (int)ceil_div(g.N, kStepBN);
+        const int64_t grid = (int64_t)g.tiles_m * g.tiles_n * g.splits + down;
+        step_kernel<E, BM, RN, decltype(direct)::value><<<(unsigned)grid, kDownWaves * kWave, 0, stream>>>(g);
+    };
+    if (g.T <= 16 && dma)
+        launch(std::integral_constant<int, 16>{}, std::true_type{});
+    else if (g.T <= 16)
+        launch(std::integral_constant<int, 16>{}, std::false_type{});
+    else if (dma)
+        launch(std::integral_constant<int, 64>{}, std::true_type{});
+    else
+        launch(std::integral_constant<int, 64>{}, std::false_type{});
+    const dim3 grid((unsigned)ceil_div(g.N, kWave * E::kChunk), (unsigned)g.T);
+    join_kernel<E><<<grid, kWave, 0, stream>>>(g);
+    return launched();
+}
+
+template <class E, int RN>
+int run_many(AdapterArgs g, bool low, bool dma, bool dma_down, hipStream_t stream)
+{
+    // Up to 32 rows behind the last whole tile: tiles of 16 rows.
+    g.big_m = g.T / 128;
+    const int rest = g.T - g.big_m * 128;
+    if (rest > 32)
+        ++g.big_m;
+    const int64_t tm = g.big_m + (rest > 32 ? 0 : ceil_div(rest, 16)), tn = ceil_div(g.N, 128);
+    if (tm * tn > (int64_t)UINT32_MAX / 256)
+        return GEMM_F32_ERR_DIM;
+    g.tiles_m = (int)tm;
+    g.tiles_n = (int)tn;
+    if (low) {
+        const int64_t blocks = down_blocks<E, RN>(g);
+        if (dma_down)
+            down_kernel<E, RN, true><<<(unsigned)blocks, kDownWaves * kWave, 0, stream>>>(g);
+        else
+            down_kernel<E, RN, false><<<(unsigned)blocks, kDownWaves * kWave, 0, stream>>>(g);
+        factor_kernel<E><<<(unsigned)ceil_div(g.T, kFactorThreads / kWave), kFactorThreads, 0, stream>>>(g);
+    }
+    if (dma)
+        adapters_kernel<E, true><<<(unsigned)(tm * tn), 256, 0, stream>>>(g);
+    else
+        adapters_kernel<E, false><<<(unsigned)(tm * tn), 256, 0, stream>>>(g);
+    return launched();
+}
 
 }  // namespace
 }  // namespace rows
@@ -306,10 +527,10 @@ extern "C" {
 
 size_t gemm_f32_adapters_ws_size(int type, int T, int N, int K, int R)
 {
-    if (T <= 0 || T > kMaxTokens || N <= 0 || K < 0 || R <= 0 || R > GEMM_F32_MAX_RANK)
+    if (T <= 0 || T > kMaxTokens || N <= 0 || K < 0 || R < 0 || R > GEMM_F32_MAX_RANK)
         return 0;
     size_t bytes = 0;
-    with_type(type, [&](auto e) { bytes = workspace<decltype(e)>(T, K, R).bytes; });
+    with_type(type, [&](auto e) { bytes = plan<decltype(e)>(T, N, K, R).bytes; });
     return bytes;
 }
 
@@ -335,54 +556,40 @@ int gemm_f32_adapters(int type, int T, int N, int K, int R, int n, const void *X
     if (!aligned_to(X, b) || !aligned_to(W, b) || !aligned_to(Y, b) ||
         (low && (!aligned_to(A, b) || !aligned_to(B, b) || !aligned_to(adapter, 4) || !aligned_to(scale, 4))))
         return GEMM_F32_ERR_ALIGN;
-    const size_t need = low ? gemm_f32_adapters_ws_size(type, T, N, K, R) : 0;
+    const size_t need = gemm_f32_adapters_ws_size(type, T, N, K, R);
     if (need > 0 && (ws == nullptr || ws_bytes < need || !aligned_to(ws, 16)))
         return GEMM_F32_ERR_WORKSPACE;
 
-    const bool dma_x = dma_rows(type, X, ldx, kPanelRows);
-    const bool dma_main = dma_x && dma_rows(type, W, ldw, kPanelRows) &&
-                          (!low || (dma_rows(type, B, ldb, kPanelRows) && (n == 1 || stride_b * b % 4 == 0)));
-    const bool dma_down = dma_x && low && dma_rows(type, A, lda, kPanelRows) && (n == 1 || stride_a * b % 4 == 0);
+    const bool dma_x = dma_rows(type, X, ldx, kPanelRows), dma_w = dma_rows(type, W, ldw, kPanelRows);
+    const bool dma_a = !low || (dma_rows(type, A, lda, kPanelRows) && (n == 1 || stride_a * b % 4 == 0));
+    const bool dma_b = !low || (dma_rows(type, B, ldb, kPanelRows) && (n == 1 || stride_b * b % 4 == 0));
     int rc = GEMM_F32_OK;
     with_type(type, [&](auto e) {
         using E = decltype(e);
+        const Split p = plan<E>(T, N, K, R);
         AdapterArgs g{};
         g.X = X, g.W = W, g.A = A, g.B = B, g.Y = Y;
         g.adapter = adapter, g.scale = scale;
+        g.partial_u = (float *)ws;
+        g.partial_y = (float *)((char *)ws + p.partial_y);
+        g.factor = (char *)ws + p.factor;
+        g.unscale = (float *)((char *)ws + p.unscale);
         g.ldx = ldx, g.ldw = ldw, g.lda = lda, g.ldb = ldb, g.ldy = ldy;
         g.stride_a = stride_a, g.stride_b = stride_b;
-        g.T = T, g.N = N, g.K = K, g.R = R, g.n = n;
+        g.T = T, g.N = N, g.K = K, g.R = low ? R : 0, g.n = n;
+        g.splits_u = p.splits_u, g.split_ku = p.split_ku, g.slots = p.slots, g.ranks = p.ranks;
+        g.splits = p.splits, g.split_k = p.split_k;
+        g.pitch = p.pitch, g.depth = p.depth;
         g.xcds = gemm_f32_internal::current_device().xcds;
         g.vector_y = vector_rows(type, Y, ldy, 0, N);
-        if (low) {
-            const Workspace w = workspace<E>(T, K, R);
-            g.partial = (float *)((char *)ws + w.partial);
-            g.factor = (char *)ws + w.factor;
-            g.unscale = (float *)((char *)ws + w.unscale);
-            g.depth = factor_depth<E>(R);
-            g.splits = down_splits(T, K, panel_deep<E>());
-            // whole panels, so that every split starts on a 16-byte boundary
-            g.split_k = (int)(ceil_div(ceil_div(K, g.splits), panel_deep<E>()) * panel_deep<E>());
-            if (g.split_k > 0)
-                g.splits = (int)ceil_div(K, g.split_k);
-            if (R <= 16)
-                launch_down<E, 16>(g, dma_down, stream);
-            else if (R <= 32)
-                launch_down<E, 32>(g, dma_down, stream);
-            else if (R <= 64)
-                launch_down<E, 64>(g, dma_down, stream);
-            else if (R <= 128)
-                launch_down<E, 128>(g, dma_down, stream);
-            else
-                launch_down<E, 256>(g, dma_down, stream);
-            factor_kernel<E><<<(unsigned)ceil_div(T, kFactorThreads / kWave), kFactorThreads, 0, stream>>>(g);
-            rc = launched();
-            if (rc != GEMM_F32_OK)
-                return;
-        }
-        // Up to 16 rows: tiles of 16, which read W once without spending
-        // matrix instructions on rows that are not there.
-        rc = T <= 16 ? launch_tiles<E, 16, 128, 1, 4>(g, dma_main, stream) : launch_tiles<E, 128, 128, 2, 2>(g, dma_main, stream);
+        if (p.few && p.rank_block == 16)
+            rc = run_few<E, 16>(g, low, dma_x && dma_w && dma_a, stream);
+        else if (p.few)
+            rc = run_few<E, 64>(g, low, dma_x && dma_w && dma_a, stream);
+        else if (p.rank_block == 16)
+            rc = run_many<E, 16>(g, low, dma_x && dma_w && dma_b, dma_x && dma_a, stream);
+        else
+            rc = run_many<E, 64>(g, low, dma_x && dma_w && dma_b, dma_x && dma_a, stream);
     });
     return rc;
 }

@@ -389,6 +389,17 @@ struct Gathered : Across<E, RN, NT, CH> {
 // their base.  Else the chunks are staged through registers into two
 // buffers, element by element at a row's end.
 // ---------------------------------------------------------------------------
+// Between a group's writes to LDS and its reads of them: a barrier, or only program
+// order where the group is one wave (whose LDS accesses are in order).
+template <int NT>
+__device__ inline void group_sync()
+{
+    if constexpr (NT > kWave)
+        __syncthreads();
+    else
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+}
+
 template <class E, class Ti, class SrcA, class SrcB>
 __device__ inline void sum_panels_staged(Ti &tile, int K, const SrcA &a, const SrcB &b, typename E::T *lds, int tid,
                                          int wm, int wn)
@@ -425,7 +436,7 @@ __device__ inline void sum_panels_staged(Ti &tile, int K, const SrcA &a, const S
 #pragma unroll
         for (int i = 0; i < SrcB::kCount; ++i)
             put(lb, SrcB::kSlots, i, rb[i]);
-        __syncthreads();         // the other buffer's readers passed the last one
+        group_sync<NT>();        // the other buffer's readers passed the last one
         if (k0 + BK < K)
             fetch(k0 + BK);
         typename Ti::Panel p;
@@ -498,6 +509,26 @@ struct PanelLoads<E, Gathered<E, RN, NT, CH>, NT> {
     }
 };
 
+// The panel at k0 of one operand into LDS, complete after the wait and barrier that follow.
+template <class E, bool DMA, int NT, class Src>
+__device__ inline void load_panel(const Src &src, int k0, typename E::T *panel, int tid)
+{
+    using T = typename E::T;
+    if constexpr (DMA) {
+        const PanelLoads<E, Src, NT> loads(src);
+        loads.fire(src, k0, panel, __builtin_amdgcn_readfirstlane(tid / kWave));
+    } else {
+        const char *p = src.base + (int64_t)(k0 / Src::kDeep) * src.step();
+#pragma unroll
+        for (int i = 0; i < Src::kCount; ++i) {
+            const int slot = tid + i * NT, n = src.left(i, k0);
+            if (Src::kSlots % NT == 0 || slot < Src::kSlots)
+                *reinterpret_cast<u32x4 *>(panel + slot * E::kChunk) =
+                    load_chunk<E, false>((const T *)(p + (n > 0 ? src.offset(i, k0) : 0)), n);
+        }
+    }
+}
+
 // One panel: the next one's loads into `next`, this one's sums from `now`.  The
 // two do not overlap; saying so keeps the compiler from waiting for
 // the loads before it reads.
@@ -520,7 +551,7 @@ __device__ inline void sum_panels_dma(Ti &tile, int K, const SrcA &a, const SrcB
     // A wave's loads per panel (where the slots are no multiple of the threads the last
     // waves have fewer, and wait for more than they must).
     constexpr int kLoads = SrcA::kSlots / NT + SrcB::kSlots / NT;
-    const int lane = tid % kWave, wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+    const int lane = tid % kWave, wave = NT == kWave ? 0 : __builtin_amdgcn_readfirstlane(tid / kWave);
     const PanelLoads<E, SrcA, NT> pa(a);
     const PanelLoads<E, SrcB, NT> pb(b);
     auto fire = [&](int k0, T *panel) {
@@ -546,7 +577,8 @@ __device__ inline void sum_panels_dma(Ti &tile, int K, const SrcA &a, const SrcB
             asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((S - 2) * kLoads) : "memory");
         else
             asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
-        __builtin_amdgcn_s_barrier();
+        if constexpr (NT > kWave)
+            __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
         const int ahead = k0 + (S - 1) * BK;
         panel_step<E>(tile, lds + now * kPanel, lds + next * kPanel,

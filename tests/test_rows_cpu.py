@@ -147,7 +147,7 @@ def test_adapters_refuses(change, rc):
 
 
 def test_adapters_workspace():
-    assert gb.gemm_f32_adapters_ws_size(0, 8, 8, 8, 0) == gb.gemm_f32_adapters_ws_size(0, 0, 8, 8, 4) == 0
+    assert gb.gemm_f32_adapters_ws_size(0, 8, 8, 8, -1) == gb.gemm_f32_adapters_ws_size(0, 0, 8, 8, 4) == 0
     assert gb.gemm_f32_adapters_ws_size(7, 8, 8, 8, 4) == 0
     for type_ in (0, 1, 2):
         assert gb.gemm_f32_adapters_ws_size(type_, 8, 8, 8, 4) % 16 == 0 < gb.gemm_f32_adapters_ws_size(type_, 8, 8, 8, 4)

@@ -317,8 +317,9 @@ _types = None
 
 def _type(t) -> int:
     global _types
-    if _types is None:
+    if _types is None or _lib is None:
         import torch
+        load()
         _types = {torch.float32: GEMM_F32_TYPE_F32, torch.bfloat16: GEMM_F32_TYPE_BF16,
                   torch.float16: GEMM_F32_TYPE_F16}
     if t.dtype not in _types:
@@ -367,28 +368,42 @@ def _vector(t, name: str, dtype, device, shape) -> int:
     return t.data_ptr()
 
 
-class _On:
-    """Makes the tensors' device and the given stream current around a call."""
+_current_device = _current_raw_stream = None
 
-    def __init__(self, device, stream):
+
+def _here(device) -> int:
+    """The current stream of `device`, the current device (a HIP stream address)."""
+    global _current_device, _current_raw_stream
+    if _current_device is None:
         import torch
-        self.exits = []
-        if device.index != torch.cuda.current_device():
-            guard = torch.cuda.device(device)
-            guard.__enter__()
-            self.exits.append(guard)
-        if stream is not None:
-            guard = torch.cuda.stream(stream)
-            guard.__enter__()
-            self.exits.append(guard)
-        self.stream = (stream if stream is not None else torch.cuda.current_stream()).cuda_stream
+        _current_device = torch.cuda.current_device
+        # the raw address, without the Stream object around it where torch offers it
+        _current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                                      lambda index: torch.cuda.current_stream(index).cuda_stream)
+    return _current_raw_stream(device.index)
 
-    def __enter__(self):
-        return self.stream
 
-    def __exit__(self, *exc):
-        for guard in reversed(self.exits):
-            guard.__exit__(*exc)
+def _elsewhere(device, stream) -> bool:
+    """Whether a call has to be made under another device or stream than the current ones."""
+    return stream is not None or (_current_device or _device_now)() != device.index
+
+
+def _device_now() -> int:
+    import torch
+    return torch.cuda.current_device()
+
+
+def _call_on(device, stream, fn, *args, **kwargs):
+    """fn with the tensors' device and the given stream made current."""
+    import torch
+    with torch.cuda.device(device), torch.cuda.stream(stream):
+        return fn(*args, **kwargs)
+
+
+def _fit(*sizes):
+    """Refuses sizes that a C int cannot hold (ctypes would wrap them)."""
+    if max(sizes) > INT32_MAX:
+        raise ValueError(f"size {max(sizes)} does not fit the C ABI's 32-bit int")
 
 
 def _check(rc: int, what: str):
@@ -418,13 +433,18 @@ def route(logits, k: int, *, bias=None, score: str = "softmax", groups: int = 1,
     if logits.dim() != 2:
         raise ValueError("logits must be [T, E]")
     type_, ldl, mode = _type(logits), _matrix(logits, "logits"), _score(score)
+    device = logits.device
+    if _elsewhere(device, stream):
+        return _call_on(device, stream, route, logits, k, bias=bias, score=score, groups=groups,
+                        keep_groups=keep_groups, group_top=group_top, normalize=normalize, scale=scale)
     T, E = logits.shape
-    b = 0 if bias is None else _vector(bias, "bias", torch.float32, logits.device, (E,))
-    with _On(logits.device, stream) as s:
-        weight = torch.empty((T, max(k, 0)), dtype=torch.float32, device=logits.device)
-        index = torch.empty((T, max(k, 0)), dtype=torch.int32, device=logits.device)
-        _check(gemm_f32_route(type_, T, E, k, logits.data_ptr(), ldl, b, mode, groups, keep_groups, group_top,
-                              int(bool(normalize)), scale, weight.data_ptr(), index.data_ptr(), s), "gemm_f32_route")
+    _fit(T, E, k, ldl, groups, keep_groups, group_top)
+    b = 0 if bias is None else _vector(bias, "bias", torch.float32, device, (E,))
+    weight = logits.new_empty((T, max(k, 0)), dtype=torch.float32)
+    index = logits.new_empty((T, max(k, 0)), dtype=torch.int32)
+    _check(_lib.gemm_f32_route(type_, T, E, k, logits.data_ptr(), ldl, b, mode, groups, keep_groups, group_top,
+                               bool(normalize), scale, weight.data_ptr(), index.data_ptr(), _here(device)),
+           "gemm_f32_route")
     return weight, index
 
 
@@ -435,16 +455,20 @@ def route_grad(logits, index, dweight, *, score: str = "softmax", normalize: boo
     if logits.dim() != 2 or index.dim() != 2:
         raise ValueError("logits must be [T, E] and index [T, k]")
     type_, ldl, mode = _type(logits), _matrix(logits, "logits"), _score(score)
+    device = logits.device
+    if _elsewhere(device, stream):
+        return _call_on(device, stream, route_grad, logits, index, dweight, score=score, normalize=normalize,
+                        scale=scale, out=out)
     T, E = logits.shape
     k = index.shape[1]
-    i = _vector(index, "index", torch.int32, logits.device, (T, k))
-    w = _vector(dweight, "dweight", torch.float32, logits.device, (T, k))
-    with _On(logits.device, stream) as s:
-        if out is None:
-            out = torch.empty((T, E), dtype=logits.dtype, device=logits.device)
-        ldo = _matrix(out, "out", logits, (T, E))
-        _check(gemm_f32_route_grad(type_, T, E, k, logits.data_ptr(), ldl, mode, int(bool(normalize)), scale, i, w,
-                                   out.data_ptr(), ldo, s), "gemm_f32_route_grad")
+    i = _vector(index, "index", torch.int32, device, (T, k))
+    w = _vector(dweight, "dweight", torch.float32, device, (T, k))
+    if out is None:
+        out = logits.new_empty((T, E))
+    ldo = _matrix(out, "out", logits, (T, E))
+    _fit(T, E, k, ldl, ldo)
+    _check(_lib.gemm_f32_route_grad(type_, T, E, k, logits.data_ptr(), ldl, mode, bool(normalize), scale, i, w,
+                                    out.data_ptr(), ldo, _here(device)), "gemm_f32_route_grad")
     return out
 
 
@@ -459,20 +483,22 @@ def expert_map(index, experts: int, *, stream=None):
     import torch
     if not index.is_cuda:
         raise TypeError("index must be on a GPU")
-    i = _vector(index, "index", torch.int32, index.device, index.shape)
+    device = index.device
+    i = _vector(index, "index", torch.int32, device, index.shape)
+    if _elsewhere(device, stream):
+        return _call_on(device, stream, expert_map, index, experts)
     S = index.numel()
     need = gemm_f32_expert_map_ws_size(S, experts)
-    with _On(index.device, stream) as s:
-        offsets = torch.empty(max(experts, 0) + 1, dtype=torch.int32, device=index.device)
-        order = torch.empty(S, dtype=torch.int32, device=index.device)
-        position = torch.empty_like(index)
-        ws = torch.empty(need, dtype=torch.uint8, device=index.device) if need else None
-        _check(gemm_f32_expert_map(S, experts, i, offsets.data_ptr(), order.data_ptr(), position.data_ptr(),
-                                   ws.data_ptr() if need else 0, need, s), "gemm_f32_expert_map")
+    offsets = index.new_empty(max(experts, 0) + 1)
+    order = index.new_empty(S)
+    position = torch.empty_like(index)
+    ws = index.new_empty(need, dtype=torch.uint8) if need else None
+    _check(_lib.gemm_f32_expert_map(S, experts, i, offsets.data_ptr(), order.data_ptr(), position.data_ptr(),
+                                    ws.data_ptr() if need else 0, need, _here(device)), "gemm_f32_expert_map")
     return offsets, order, position
 
 
-def _grouped_args(X, W, offsets, order, per_row):
+def _grouped_args(X, offsets, order):
     """What forward and weight gradient have in common: places, rows, addresses."""
     import torch
     G = offsets.numel() - 1
@@ -495,17 +521,20 @@ def grouped_matmul(X, W, offsets, *, order=None, per_row: int = 1, out=None, str
     if X.dim() != 2 or W.dim() != 3:
         raise ValueError("X must be [rows, K] and W [G, K, N]")
     type_, ldx = _type(X), _matrix(X, "X")
-    G, P, o, r = _grouped_args(X, W, offsets, order, per_row)
+    device = X.device
+    if _elsewhere(device, stream):
+        return _call_on(device, stream, grouped_matmul, X, W, offsets, order=order, per_row=per_row, out=out)
+    G, P, o, r = _grouped_args(X, offsets, order)
     rows, K = X.shape
     N = W.shape[2]
     ldw = _matrix(W, "W", X, (G, K, N))
     stride = _stack(W, "W", ldw)
-    with _On(X.device, stream) as s:
-        if out is None:
-            out = torch.empty((P, N), dtype=X.dtype, device=X.device)
-        ldy = _matrix(out, "out", X, (P, N))
-        _check(gemm_f32_grouped(type_, G, P, N, K, o, r, per_row, rows, X.data_ptr(), ldx, W.data_ptr(), ldw, stride,
-                                out.data_ptr(), ldy, s), "gemm_f32_grouped")
+    if out is None:
+        out = X.new_empty((P, N))
+    ldy = _matrix(out, "out", X, (P, N))
+    _fit(G, P, N, K, per_row, rows, ldx, ldw, ldy)
+    _check(_lib.gemm_f32_grouped(type_, G, P, N, K, o, r, per_row, rows, X.data_ptr(), ldx, W.data_ptr(), ldw, stride,
+                                 out.data_ptr(), ldy, _here(device)), "gemm_f32_grouped")
     return out
 
 
@@ -518,16 +547,19 @@ def grouped_grad_x(dY, W, offsets, *, out=None, stream=None):
     if dY.dim() != 2 or W.dim() != 3:
         raise ValueError("dY must be [P, N] and W [G, K, N]")
     type_, lddy = _type(dY), _matrix(dY, "dY")
-    G, P, o, _ = _grouped_args(dY, W, offsets, None, 1)
+    device = dY.device
+    if _elsewhere(device, stream):
+        return _call_on(device, stream, grouped_grad_x, dY, W, offsets, out=out)
+    G, P, o, _ = _grouped_args(dY, offsets, None)
     N, K = dY.shape[1], W.shape[1]
     ldw = _matrix(W, "W", dY, (G, K, N))
     stride = _stack(W, "W", ldw)
-    with _On(dY.device, stream) as s:
-        if out is None:
-            out = torch.empty((P, K), dtype=dY.dtype, device=dY.device)
-        lddx = _matrix(out, "out", dY, (P, K))
-        _check(gemm_f32_grouped_grad_x(type_, G, P, N, K, o, dY.data_ptr(), lddy, W.data_ptr(), ldw, stride,
-                                       out.data_ptr(), lddx, s), "gemm_f32_grouped_grad_x")
+    if out is None:
+        out = dY.new_empty((P, K))
+    lddx = _matrix(out, "out", dY, (P, K))
+    _fit(G, P, N, K, lddy, ldw, lddx)
+    _check(_lib.gemm_f32_grouped_grad_x(type_, G, P, N, K, o, dY.data_ptr(), lddy, W.data_ptr(), ldw, stride,
+                                        out.data_ptr(), lddx, _here(device)), "gemm_f32_grouped_grad_x")
     return out
 
 
@@ -537,17 +569,20 @@ def grouped_grad_w(X, dY, offsets, *, order=None, per_row: int = 1, out=None, st
     if X.dim() != 2 or dY.dim() != 2:
         raise ValueError("X must be [rows, K] and dY [P, N]")
     type_, ldx = _type(X), _matrix(X, "X")
-    G, P, o, r = _grouped_args(X, None, offsets, order, per_row)
+    device = X.device
+    if _elsewhere(device, stream):
+        return _call_on(device, stream, grouped_grad_w, X, dY, offsets, order=order, per_row=per_row, out=out)
+    G, P, o, r = _grouped_args(X, offsets, order)
     rows, K = X.shape
     N = dY.shape[1]
     lddy = _matrix(dY, "dY", X, (P, N))
-    with _On(X.device, stream) as s:
-        if out is None:
-            out = torch.empty((G, K, N), dtype=X.dtype, device=X.device)
-        lddw = _matrix(out, "out", X, (G, K, N))
-        stride = _stack(out, "out", lddw)
-        _check(gemm_f32_grouped_grad_w(type_, G, P, N, K, o, r, per_row, rows, X.data_ptr(), ldx, dY.data_ptr(), lddy,
-                                       out.data_ptr(), lddw, stride, s), "gemm_f32_grouped_grad_w")
+    if out is None:
+        out = X.new_empty((G, K, N))
+    lddw = _matrix(out, "out", X, (G, K, N))
+    stride = _stack(out, "out", lddw)
+    _fit(G, P, N, K, per_row, rows, ldx, lddy, lddw)
+    _check(_lib.gemm_f32_grouped_grad_w(type_, G, P, N, K, o, r, per_row, rows, X.data_ptr(), ldx, dY.data_ptr(), lddy,
+                                        out.data_ptr(), lddw, stride, _here(device)), "gemm_f32_grouped_grad_w")
     return out
 
 
@@ -560,16 +595,19 @@ def combine(Y, position, weight=None, *, out=None, stream=None):
     if Y.dim() != 2 or position.dim() != 2:
         raise ValueError("Y must be [P, N] and position [T, k]")
     type_, ldy = _type(Y), _matrix(Y, "Y")
+    device = Y.device
+    if _elsewhere(device, stream):
+        return _call_on(device, stream, combine, Y, position, weight, out=out)
     P, N = Y.shape
     T, k = position.shape
-    at = _vector(position, "position", torch.int32, Y.device, (T, k))
-    w = 0 if weight is None else _vector(weight, "weight", torch.float32, Y.device, (T, k))
-    with _On(Y.device, stream) as s:
-        if out is None:
-            out = torch.empty((T, N), dtype=Y.dtype, device=Y.device)
-        ldo = _matrix(out, "out", Y, (T, N))
-        _check(gemm_f32_combine(type_, T, k, N, P, at, w, Y.data_ptr(), ldy, out.data_ptr(), ldo, s),
-               "gemm_f32_combine")
+    at = _vector(position, "position", torch.int32, device, (T, k))
+    w = 0 if weight is None else _vector(weight, "weight", torch.float32, device, (T, k))
+    if out is None:
+        out = Y.new_empty((T, N))
+    ldo = _matrix(out, "out", Y, (T, N))
+    _fit(T, k, N, P, ldy, ldo)
+    _check(_lib.gemm_f32_combine(type_, T, k, N, P, at, w, Y.data_ptr(), ldy, out.data_ptr(), ldo, _here(device)),
+           "gemm_f32_combine")
     return out
 
 
@@ -582,18 +620,22 @@ def combine_grad(dout, Y, position, weight=None, *, out=None, stream=None):
     if Y.dim() != 2 or position.dim() != 2:
         raise ValueError("Y must be [P, N] and position [T, k]")
     type_, ldy = _type(Y), _matrix(Y, "Y")
+    device = Y.device
+    if _elsewhere(device, stream):
+        return _call_on(device, stream, combine_grad, dout, Y, position, weight, out=out)
     P, N = Y.shape
     T, k = position.shape
     lddo = _matrix(dout, "dout", Y, (T, N))
-    at = _vector(position, "position", torch.int32, Y.device, (T, k))
-    w = 0 if weight is None else _vector(weight, "weight", torch.float32, Y.device, (T, k))
-    with _On(Y.device, stream) as s:
-        if out is None:
-            out = torch.empty((P, N), dtype=Y.dtype, device=Y.device)
-        lddy = _matrix(out, "out", Y, (P, N))
-        dweight = torch.empty((T, k), dtype=torch.float32, device=Y.device)
-        _check(gemm_f32_combine_grad(type_, T, k, N, P, at, w, Y.data_ptr(), ldy, dout.data_ptr(), lddo,
-                                     out.data_ptr(), lddy, dweight.data_ptr(), s), "gemm_f32_combine_grad")
+    at = _vector(position, "position", torch.int32, device, (T, k))
+    w = 0 if weight is None else _vector(weight, "weight", torch.float32, device, (T, k))
+    if out is None:
+        out = Y.new_empty((P, N))
+    lddy = _matrix(out, "out", Y, (P, N))
+    dweight = Y.new_empty((T, k), dtype=torch.float32)
+    _fit(T, k, N, P, ldy, lddo, lddy)
+    _check(_lib.gemm_f32_combine_grad(type_, T, k, N, P, at, w, Y.data_ptr(), ldy, dout.data_ptr(), lddo,
+                                      out.data_ptr(), lddy, dweight.data_ptr(), _here(device)),
+           "gemm_f32_combine_grad")
     return [out, dweight]
 
 
@@ -608,22 +650,24 @@ def adapter_matmul(X, W, A, B, adapter, scale=None, *, out=None, workspace=None,
     if X.dim() != 2 or W.dim() != 2 or A.dim() != 3 or B.dim() != 3:
         raise ValueError("X must be [T, K], W [K, N], A [n, K, R] and B [n, R, N]")
     type_, ldx = _type(X), _matrix(X, "X")
+    device = X.device
+    if _elsewhere(device, stream):
+        return _call_on(device, stream, adapter_matmul, X, W, A, B, adapter, scale, out=out, workspace=workspace)
     T, K = X.shape
     N, n, R = W.shape[1], A.shape[0], A.shape[2]
     ldw, lda, ldb = _matrix(W, "W", X, (K, N)), _matrix(A, "A", X, (n, K, R)), _matrix(B, "B", X, (n, R, N))
     sa, sb = _stack(A, "A", lda), _stack(B, "B", ldb)
-    a = _vector(adapter, "adapter", torch.int32, X.device, (T,))
-    c = 0 if scale is None else _vector(scale, "scale", torch.float32, X.device, (n,))
-    need = gemm_f32_adapters_ws_size(type_, T, N, K, R)
-    with _On(X.device, stream) as s:
-        if out is None:
-            out = torch.empty((T, N), dtype=X.dtype, device=X.device)
-        ldy = _matrix(out, "out", X, (T, N))
-        if workspace is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=X.device)
-        elif workspace.dtype != torch.uint8 or workspace.device != X.device or not workspace.is_contiguous():
-            raise TypeError("workspace must be a contiguous uint8 tensor on the operands' device")
-        _check(gemm_f32_adapters(type_, T, N, K, R, n, X.data_ptr(), ldx, W.data_ptr(), ldw, A.data_ptr(), lda, sa,
-                                 B.data_ptr(), ldb, sb, a, c, out.data_ptr(), ldy, workspace.data_ptr(),
-                                 workspace.numel(), s), "gemm_f32_adapters")
+    a = _vector(adapter, "adapter", torch.int32, device, (T,))
+    c = 0 if scale is None else _vector(scale, "scale", torch.float32, device, (n,))
+    if out is None:
+        out = X.new_empty((T, N))
+    ldy = _matrix(out, "out", X, (T, N))
+    _fit(T, N, K, R, n, ldx, ldw, lda, ldb, ldy)
+    if workspace is None:
+        workspace = X.new_empty(_lib.gemm_f32_adapters_ws_size(type_, T, N, K, R), dtype=torch.uint8)
+    elif workspace.dtype != torch.uint8 or workspace.device != device or not workspace.is_contiguous():
+        raise TypeError("workspace must be a contiguous uint8 tensor on the operands' device")
+    _check(_lib.gemm_f32_adapters(type_, T, N, K, R, n, X.data_ptr(), ldx, W.data_ptr(), ldw, A.data_ptr(), lda, sa,
+                                  B.data_ptr(), ldb, sb, a, c, out.data_ptr(), ldy, workspace.data_ptr(),
+                                  workspace.numel(), _here(device)), "gemm_f32_adapters")
     return out

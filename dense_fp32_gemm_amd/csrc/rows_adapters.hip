@@ -339,8 +339,10 @@ __device__ inline void adapters_tile(const AdapterArgs &g, int m0, int n0, typen
                 load_panel<E, DMA, NT>(b, k0, lds + Ti::kLdsA, tid);
                 asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
                 __syncthreads();
-                typename Ti::Panel p;
-                p.read(lds, lds + Ti::kLdsA, wm, wn, lane);
+                typename Ti::Step p[Ti::kSteps];
+#pragma unroll
+                for (int step = 0; step < Ti::kSteps; ++step)
+                    p[step].read(lds, step, wm, wn, lane);
 #pragma unroll
                 for (int m = 0; m < Ti::kFm; ++m) {
                     f32x4 add[Ti::kFn];
@@ -349,7 +351,7 @@ __device__ inline void adapters_tile(const AdapterArgs &g, int m0, int n0, typen
                         add[n] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                         for (int step = 0; step < Ti::kSteps; ++step)
-                            add[n] = mfma_step<E>(p.b[step].q[n], p.a[step].q[m], add[n]);
+                            add[n] = mfma_step<E>(p[step].b.q[n], p[step].a.q[m], add[n]);
                     }
                     const int r = wm * (BM / WM) + Ti::Fa::row_of(m, lane % 16);
                     if (!member(r))

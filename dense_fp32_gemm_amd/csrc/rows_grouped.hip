@@ -23,9 +23,11 @@ struct GroupedArgs {
     int G, P, rows;          // rows: of X
     Divisor per_row;
     int M, N, K;             // grad_w: M x N of dW; else columns N of C, summed K
-    int tiles_n;
     int xcds;
     bool vector_c;           // C's rows take stores of four elements
+    int tiles_n;
+    int most_m;              // row tiles there can be
+    int slots;               // workgroups the device holds at once
 };
 
 // Workgroups are dealt to the dies round-robin; renumbered so that each die
@@ -43,10 +45,13 @@ __device__ inline void group_range(const int *offsets, int g, int P, int &lo, in
     hi = min(max(offsets[g + 1], lo), P);
 }
 
-// Tile number -> group and row tile within it, by counting the row tiles of
-// every group (64 groups at a time, a lane each).  Every wave of the
-// workgroup computes it for itself.  Returns false past the last tile.
-__device__ inline bool find_tile(const GroupedArgs &g, int bm, int &group, int &lo, int &hi, int &tm, int &tn)
+struct Place {
+    int group, lo, hi;       // the group's places
+    int tm, tn;              // row tile within the group, column tile
+};
+
+// Row tiles of all groups (64 groups at a time, a lane each), the same in every lane.
+__device__ inline int row_tiles(const GroupedArgs &g, int bm)
 {
     const int lane = threadIdx.x % kWave;
     int total = 0;
@@ -60,12 +65,16 @@ __device__ inline bool find_tile(const GroupedArgs &g, int bm, int &group, int &
             n += __shfl_xor(n, d);
         total += n;
     }
-    // Rising offsets never have more tiles than workgroups; others are cut there.
-    total = __builtin_amdgcn_readfirstlane(min(total, (int)(gridDim.x / g.tiles_n)) * g.tiles_n);
-    if ((int)blockIdx.x >= total)
-        return false;
-    const int t = die_contiguous(blockIdx.x, total, g.xcds);
+    return __builtin_amdgcn_readfirstlane(total);
+}
+
+// Tile t, counted group by group and column by column within a group (W's
+// panels are shared).  Every wave of the workgroup computes it for itself.
+__device__ inline Place locate(const GroupedArgs &g, int bm, int t)
+{
+    const int lane = threadIdx.x % kWave;
     int before = 0;                                  // row tiles of the groups before
+    Place p{0, 0, 0, 0, 0};
     for (int g0 = 0; g0 < g.G; g0 += kWave) {
         int a = 0, b = 0;
         if (g0 + lane < g.G)
@@ -80,52 +89,51 @@ __device__ inline bool find_tile(const GroupedArgs &g, int bm, int &group, int &
         const uint64_t past = __ballot(before + scan > t / g.tiles_n);
         if (past) {
             const int at = (int)__builtin_ctzll(past);
-            group = g0 + at;
-            lo = __builtin_amdgcn_readlane(a, at);
-            hi = __builtin_amdgcn_readlane(b, at);
             const int mine = __builtin_amdgcn_readlane(n, at);
             const int first = before + __builtin_amdgcn_readlane(scan, at) - mine;
-            const int r = t - first * g.tiles_n;     // column by column: W's panels are shared
-            tm = r % mine;
-            tn = r / mine;
-            return true;
+            const int r = t - first * g.tiles_n;
+            p = Place{g0 + at, __builtin_amdgcn_readlane(a, at), __builtin_amdgcn_readlane(b, at), r % mine, r / mine};
+            break;
         }
         before += __builtin_amdgcn_readlane(scan, kWave - 1);
     }
-    return false;
+    // scalars, whatever the compiler makes of the loop
+    return Place{__builtin_amdgcn_readfirstlane(p.group), __builtin_amdgcn_readfirstlane(p.lo),
+                 __builtin_amdgcn_readfirstlane(p.hi), __builtin_amdgcn_readfirstlane(p.tm),
+                 __builtin_amdgcn_readfirstlane(p.tn)};
 }
 
+// Workgroup w's part of `total` tiles on a device that holds `slots` workgroups
+// at once: whole tiles while they fill rounds of slots; the tiles of a last
+// round that fills at most half (a quarter) of the slots are cut into two (four).
+struct Part {
+    int tile, cut, piece;    // cut: 1, 2 or 4 pieces; tile < 0: nothing to do
+};
+__device__ inline Part part_of(int w, int total, int slots, int xcds)
+{
+    const int whole = total / slots * slots, rest = total - whole;
+    if (w < whole)
+        return Part{die_contiguous(w, whole, xcds), 1, 0};
+    const int cut = 4 * rest <= slots ? 4 : 2 * rest <= slots ? 2 : 1;
+    if (w - whole >= rest * cut)
+        return Part{-1, 1, 0};
+    const int q = die_contiguous(w - whole, rest * cut, xcds);
+    return Part{whole + q / cut, cut, q % cut};
+}
+
+// One tile: rows m0 .. m_end - 1 (places; of dW: rows of the matrix), columns from n0 on.
 template <class E, Op OP, int BM, int BN, int WM, int WN, int CH, int S, bool DMA>
-__global__ __launch_bounds__(WM *WN *kWave) void grouped_kernel(GroupedArgs g)
+__device__ inline void grouped_tile(const GroupedArgs &g, int group, int lo, int hi, int m0, int m_end, int n0,
+                                    typename E::T *lds, uint32_t *ahead)
 {
     constexpr bool kAlongA = OP != kGradW, kAlongB = OP == kGradX;
     using Ti = Tile<E, kAlongA, kAlongB, BM, BN, WM, WN, CH>;
     using T = typename E::T;
     constexpr int NT = Ti::kThreads;
-    __shared__ __attribute__((aligned(16))) T lds[(DMA ? S : 2) * (Ti::kLdsA + Ti::kLdsB)];
-    __shared__ uint32_t ahead[OP == kGradW && DMA ? 1024 : 1];
-    const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
-    const int wm = wave / WN, wn = wave % WN;
-
-    int group, lo, hi, tm, tn;
-    if constexpr (OP == kGradW) {
-        const int tiles_m = (g.M + BM - 1) / BM, per = tiles_m * g.tiles_n;
-        const int t = die_contiguous(blockIdx.x, gridDim.x, g.xcds);
-        group = t / per;
-        tm = t % per % tiles_m;
-        tn = t % per / tiles_m;
-        group_range(g.offsets, group, g.P, lo, hi);
-    } else if (!find_tile(g, BM, group, lo, hi, tm, tn)) {
+    if (m0 >= m_end || n0 >= g.N)
         return;                                      // the whole workgroup
-    }
-    group = __builtin_amdgcn_readfirstlane(group);
-    lo = __builtin_amdgcn_readfirstlane(lo);
-    hi = __builtin_amdgcn_readfirstlane(hi);
-    tm = __builtin_amdgcn_readfirstlane(tm);
-    tn = __builtin_amdgcn_readfirstlane(tn);
-    const int m0 = OP == kGradW ? tm * BM : lo + tm * BM;
-    const int m_end = OP == kGradW ? g.M : hi;
-    const int n0 = tn * BN;
+    const int tid = threadIdx.x, lane = tid % kWave, wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+    const int wm = wave / WN, wn = wave % WN;
     const T *A = (const T *)g.A, *B = (const T *)g.B;
 
     Ti tile;
@@ -176,6 +184,48 @@ __global__ __launch_bounds__(WM *WN *kWave) void grouped_kernel(GroupedArgs g)
         store(std::true_type{});
     else
         store(std::false_type{});
+}
+
+template <class E, Op OP, int BM, int BN, int WM, int WN, int CH, int S, bool CUT, bool DMA>
+__global__ __launch_bounds__(WM *WN *kWave, CH == 4 ? 4 : 2) void grouped_kernel(GroupedArgs g)
+{
+    constexpr int kPanel = (BM + BN) * CH * E::kChunk;
+    __shared__ __attribute__((aligned(16))) typename E::T lds[(DMA ? S : 2) * kPanel];
+    __shared__ uint32_t ahead[OP == kGradW && DMA ? 1024 : 1];
+    const int tiles_m = OP == kGradW ? (g.M + BM - 1) / BM : 0;
+    // Rising offsets never have more tiles than the grid has; others are cut there.
+    const int total = OP == kGradW ? g.G * tiles_m * g.tiles_n : min(row_tiles(g, BM), g.most_m) * g.tiles_n;
+    Part part{-1, 1, 0};
+    if constexpr (CUT)
+        part = part_of(blockIdx.x, total, g.slots, g.xcds);
+    else if ((int)blockIdx.x < total)
+        part.tile = die_contiguous(blockIdx.x, total, g.xcds);
+    if (part.tile < 0)
+        return;                                      // the whole workgroup
+    Place p;
+    if constexpr (OP == kGradW) {
+        const int per = tiles_m * g.tiles_n, r = part.tile % per;
+        p.group = part.tile / per;
+        p.tm = r % tiles_m;
+        p.tn = r / tiles_m;
+        group_range(g.offsets, p.group, g.P, p.lo, p.hi);
+        p.lo = __builtin_amdgcn_readfirstlane(p.lo);
+        p.hi = __builtin_amdgcn_readfirstlane(p.hi);
+    } else {
+        p = locate(g, BM, part.tile);
+    }
+    const int m0 = (OP == kGradW ? 0 : p.lo) + p.tm * BM, m_end = OP == kGradW ? g.M : p.hi, n0 = p.tn * BN;
+    if (!CUT || part.cut == 1)
+        grouped_tile<E, OP, BM, BN, WM, WN, CH, S, DMA>(g, p.group, p.lo, p.hi, m0, m_end, n0, lds, ahead);
+    if constexpr (CUT) {
+        if (part.cut == 2)
+            grouped_tile<E, OP, BM / 2, BN, WM, WN, CH, S, DMA>(g, p.group, p.lo, p.hi, m0 + part.piece * (BM / 2), m_end,
+                                                               n0, lds, ahead);
+        else if (part.cut == 4)
+            grouped_tile<E, OP, BM / 2, BN / 2, WM, WN, CH, S, DMA>(g, p.group, p.lo, p.hi,
+                                                                   m0 + part.piece % 2 * (BM / 2), m_end,
+                                                                   n0 + part.piece / 2 * (BN / 2), lds, ahead);
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -286,21 +336,26 @@ constexpr int64_t kMaxTiles = UINT32_MAX / 512;
 static_assert(kCombineThreads <= 512, "grid limit");
 int token_grid(int T) { return T < kMaxTiles ? T : (int)kMaxTiles; }
 
-template <class E, Op OP, int BM, int BN, int WM, int WN, int CH, int S>
+// PER_CU: workgroups of a kernel that cuts its last tiles on a compute unit (0: it does not).
+template <class E, Op OP, int BM, int BN, int WM, int WN, int CH, int S, int PER_CU>
 int launch_tile(GroupedArgs g, bool dma, hipStream_t stream)
 {
     g.tiles_n = (int)ceil_div(g.N, BN);
     // Every group ends in at most one partial tile.
     const int64_t tiles_m = OP == kGradW ? g.G * ceil_div(g.M, BM) : g.P / BM + (g.G < g.P ? g.G : g.P);
-    const int64_t grid = tiles_m * g.tiles_n;
+    g.slots = (int)gemm_f32_internal::current_device().cus * PER_CU;
+    // Cutting the last round adds at most three pieces for a quarter of the slots.
+    const int64_t grid = tiles_m * g.tiles_n + g.slots;
     if (grid > kMaxTiles)
         return GEMM_F32_ERR_DIM;
-    if (grid == 0)
+    if (tiles_m * g.tiles_n == 0)
         return GEMM_F32_OK;
+    g.most_m = (int)tiles_m;
+    constexpr bool kCut = PER_CU > 0;
     if (dma)
-        grouped_kernel<E, OP, BM, BN, WM, WN, CH, S, true><<<(int)grid, WM * WN * kWave, 0, stream>>>(g);
+        grouped_kernel<E, OP, BM, BN, WM, WN, CH, S, kCut, true><<<(int)grid, WM * WN * kWave, 0, stream>>>(g);
     else
-        grouped_kernel<E, OP, BM, BN, WM, WN, CH, S, false><<<(int)grid, WM * WN * kWave, 0, stream>>>(g);
+        grouped_kernel<E, OP, BM, BN, WM, WN, CH, S, kCut, false><<<(int)grid, WM * WN * kWave, 0, stream>>>(g);
     return launched();
 }
 
@@ -314,14 +369,20 @@ int launch_grouped(int type, const GroupedArgs &g, bool dma, hipStream_t stream)
             // Few rows a group: tiles of 16 rows read each weight once without
             // spending matrix instructions on rows that are not there.
             if (g.P <= 32 * (int64_t)g.G) {
-                rc = launch_tile<E, OP, 16, 128, 1, 4, 8, 3>(g, dma, stream);
+                rc = launch_tile<E, OP, 16, 128, 1, 4, 8, 3, 0>(g, dma, stream);
                 return;
             }
         }
-        if constexpr (E::kBytes == 4)
-            rc = launch_tile<E, OP, 64, 64, 2, 2, 8, 2>(g, dma, stream);
-        else
-            rc = launch_tile<E, OP, 128, 256, 2, 4, 4, 3>(g, dma, stream);
+        if constexpr (E::kBytes == 4) {
+            rc = launch_tile<E, OP, 64, 64, 2, 2, 8, 2, 0>(g, dma, stream);
+        } else {
+            // Half a tile a group is lost on average.
+            const int64_t rows = OP == kGradW ? 2 * g.G * ceil_div(g.M, 256) : 2 * (g.P / 256) + (g.G < g.P ? g.G : g.P);
+            if (rows * ceil_div(g.N, 256) * 2 >= 3 * gemm_f32_internal::current_device().cus)
+                rc = launch_tile<E, OP, 256, 256, 2, 4, 8, 2, 1>(g, dma, stream);
+            else
+                rc = launch_tile<E, OP, 128, 128, 2, 2, 8, 2, 2>(g, dma, stream);
+        }
     });
     return rc;
 }
@@ -365,8 +426,8 @@ int gemm_f32_grouped(int type, int G, int P, int N, int K, const int *offsets, c
     if (!aligned_to(offsets, 4) || !aligned_to(order, 4) || !aligned_to(X, b) || !aligned_to(W, b) || !aligned_to(Y, b))
         return GEMM_F32_ERR_ALIGN;
     const bool dma = dma_rows(type, X, ldx, rows) && dma_rows(type, W, ldw, kPanelRows) && stride_w * b % 4 == 0;
-    const GroupedArgs g{offsets, order, X, W, Y, ldx, ldw, ldy, stride_w, G, P, rows, Divisor(order != nullptr ? per_row : 1), 0, N, K, 0,
-                        gemm_f32_internal::current_device().xcds, vector_rows(type, Y, ldy, 0, N)};
+    const GroupedArgs g{offsets, order, X, W, Y, ldx, ldw, ldy, stride_w, G, P, rows, Divisor(order != nullptr ? per_row : 1), 0, N, K,
+                        gemm_f32_internal::current_device().xcds, vector_rows(type, Y, ldy, 0, N), 0, 0, 0};
     return launch_grouped<kForward>(type, g, dma, stream);
 }
 
@@ -386,8 +447,8 @@ int gemm_f32_grouped_grad_x(int type, int G, int P, int N, int K, const int *off
     if (!aligned_to(offsets, 4) || !aligned_to(dY, b) || !aligned_to(W, b) || !aligned_to(dX, b))
         return GEMM_F32_ERR_ALIGN;
     const bool dma = dma_rows(type, dY, lddy, kPanelRows) && dma_rows(type, W, ldw, kPanelRows) && stride_w * b % 4 == 0;
-    const GroupedArgs g{offsets, nullptr, dY, W, dX, lddy, ldw, lddx, stride_w, G, P, P, Divisor(1), 0, K, N, 0,
-                        gemm_f32_internal::current_device().xcds, vector_rows(type, dX, lddx, 0, K)};
+    const GroupedArgs g{offsets, nullptr, dY, W, dX, lddy, ldw, lddx, stride_w, G, P, P, Divisor(1), 0, K, N,
+                        gemm_f32_internal::current_device().xcds, vector_rows(type, dX, lddx, 0, K), 0, 0, 0};
     return launch_grouped<kGradX>(type, g, dma, stream);
 }
 
@@ -412,8 +473,8 @@ int gemm_f32_grouped_grad_w(int type, int G, int P, int N, int K, const int *off
     if (!aligned_to(offsets, 4) || !aligned_to(order, 4) || !aligned_to(X, b) || !aligned_to(dY, b) || !aligned_to(dW, b))
         return GEMM_F32_ERR_ALIGN;
     const bool dma = dma_rows(type, X, ldx, rows) && dma_rows(type, dY, lddy, kPanelRows);
-    const GroupedArgs g{offsets, order, X, dY, dW, ldx, lddy, lddw, stride_dw, G, P, rows, Divisor(order != nullptr ? per_row : 1), K, N, 0, 0,
-                        gemm_f32_internal::current_device().xcds, vector_rows(type, dW, lddw, stride_dw, N)};
+    const GroupedArgs g{offsets, order, X, dY, dW, ldx, lddy, lddw, stride_dw, G, P, rows, Divisor(order != nullptr ? per_row : 1), K, N, 0,
+                        gemm_f32_internal::current_device().xcds, vector_rows(type, dW, lddw, stride_dw, N), 0, 0, 0};
     return launch_grouped<kGradW>(type, g, dma, stream);
 }
 

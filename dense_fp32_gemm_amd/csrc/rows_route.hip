@@ -373,20 +373,21 @@ __global__ __launch_bounds__(kRouteThreads) void route_grad_kernel(RouteGradArgs
 // ---------------------------------------------------------------------------
 // Slot map
 // ---------------------------------------------------------------------------
-constexpr int kSlotThreads = 256;
+constexpr int kSlotThreads = 1024;
 constexpr int kSlotWaves = kSlotThreads / kWave;
 constexpr int kSlotChunk = 2048;                     // slots of a workgroup
 constexpr int kSlotSteps = kSlotChunk / kSlotThreads;
+static_assert(GEMM_F32_MAX_EXPERTS == kSlotThreads, "a thread per expert");
 
 // counts[b][e]: slots of workgroup b's chunk that go to expert e.
 __global__ __launch_bounds__(kSlotThreads) void count_slots(const int *index, int S, int E, int *counts)
 {
     __shared__ int hist[GEMM_F32_MAX_EXPERTS];
     const int tid = threadIdx.x;
-    for (int e = tid; e < E; e += kSlotThreads)
-        hist[e] = 0;
+    hist[tid] = 0;
     __syncthreads();
     const int64_t first = (int64_t)blockIdx.x * kSlotChunk;
+#pragma unroll
     for (int i = 0; i < kSlotSteps; ++i) {
         const int64_t s = first + i * kSlotThreads + tid;
         const int e = s < S ? index[s] : -1;
@@ -394,60 +395,82 @@ __global__ __launch_bounds__(kSlotThreads) void count_slots(const int *index, in
             atomicAdd(&hist[e], 1);                  // LDS, whole numbers: any order
     }
     __syncthreads();
-    for (int e = tid; e < E; e += kSlotThreads)
-        counts[(int64_t)blockIdx.x * E + e] = hist[e];
+    if (tid < E)
+        counts[(int64_t)blockIdx.x * E + tid] = hist[tid];
 }
 
-// Each workgroup places its chunk.  Wave w takes slots w*512 .. of the chunk, 64
-// at a time in rising order; base[w][e] is the next place of expert e for wave w.
-// counts is NULL when one workgroup has all the slots.
+// Each workgroup places its chunk of kSlotChunk slots.  It needs, per expert, the slots
+// of all chunks and of the chunks before its own: from counts, or (NULL) by
+// counting all S slots itself, which needs no first launch.
+// Wave w takes kSlotChunk / kSlotWaves slots, 64 at a time in rising order;
+// base[w][e] is the next place of expert e for wave w.
 __global__ __launch_bounds__(kSlotThreads) void place_slots(const int *index, int S, int E, const int *counts,
                                                             int *offsets, int *order, int *position)
 {
     __shared__ int base[kSlotWaves][GEMM_F32_MAX_EXPERTS];
+    __shared__ int others[2][GEMM_F32_MAX_EXPERTS];  // slots of the chunks before and behind
     __shared__ int wave_total[kSlotWaves];
-    constexpr int kPer = GEMM_F32_MAX_EXPERTS / kSlotThreads;   // experts of a thread, side by side
     constexpr int kWaveSlots = kSlotChunk / kSlotWaves, kWaveSteps = kWaveSlots / kWave;
     const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
     const int64_t first = (int64_t)blockIdx.x * kSlotChunk;
-    for (int e = tid; e < kSlotWaves * GEMM_F32_MAX_EXPERTS; e += kSlotThreads)
-        (&base[0][0])[e] = 0;
-    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kSlotWaves; ++w)
+        base[w][tid] = 0;
+    others[0][tid] = others[1][tid] = 0;
     int mine[kWaveSteps];
 #pragma unroll
     for (int i = 0; i < kWaveSteps; ++i) {
         const int64_t s = first + wave * kWaveSlots + i * kWave + lane;
-        const int e = s < S ? index[s] : -1;
-        mine[i] = e >= 0 && e < E ? e : -1;
+        mine[i] = s < S ? index[s] : -1;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kWaveSteps; ++i) {
+        if (mine[i] >= E)
+            mine[i] = -1;
         if (mine[i] >= 0)
             atomicAdd(&base[wave][mine[i]], 1);
     }
-    __syncthreads();
-
-    // Thread tid: experts tid*kPer .. ; all slots of each, and those before
-    // this workgroup's.
-    int total[kPer], before[kPer];
+    int before = 0, total = 0;                       // of expert tid
+    if (counts == nullptr) {
+        constexpr int kBatch = 8;                    // loads in flight
+        for (int64_t s0 = 0; s0 < S; s0 += kBatch * kSlotThreads) {
+            int e[kBatch];
 #pragma unroll
-    for (int q = 0; q < kPer; ++q) {
-        const int e = tid * kPer + q;
-        total[q] = before[q] = 0;
-        if (counts == nullptr) {
+            for (int q = 0; q < kBatch; ++q) {
+                const int64_t s = s0 + q * kSlotThreads + tid;
+                const bool own = s >= first && s < first + kSlotChunk;
+                e[q] = s < S && !own ? index[s] : -1;
+            }
 #pragma unroll
-            for (int w = 0; w < kSlotWaves; ++w)
-                total[q] += base[w][e];
-        } else if (e < E) {
-            for (int b = 0; b < (int)gridDim.x; ++b) {
-                const int n = counts[(int64_t)b * E + e];
-                total[q] += n;
-                before[q] += b < (int)blockIdx.x ? n : 0;
+            for (int q = 0; q < kBatch; ++q)
+                if (e[q] >= 0 && e[q] < E)
+                    atomicAdd(&others[s0 + q * kSlotThreads >= first][e[q]], 1);   // chunks are whole multiples of the threads
+        }
+        __syncthreads();
+        before = others[0][tid];
+        total = before + others[1][tid];
+    } else {
+        if (tid < E) {
+            constexpr int kBatch = 8;
+            for (int b0 = 0; b0 < (int)gridDim.x; b0 += kBatch) {
+                int n[kBatch];
+#pragma unroll
+                for (int q = 0; q < kBatch; ++q)
+                    n[q] = b0 + q < (int)gridDim.x && b0 + q != (int)blockIdx.x ? counts[(int64_t)(b0 + q) * E + tid] : 0;
+#pragma unroll
+                for (int q = 0; q < kBatch; ++q) {
+                    total += n[q];
+                    before += b0 + q < (int)blockIdx.x ? n[q] : 0;
+                }
             }
         }
+        __syncthreads();
     }
-    int sum = 0;
 #pragma unroll
-    for (int q = 0; q < kPer; ++q)
-        sum += total[q];
-    int scan = sum;                                  // inclusive over the wave
+    for (int w = 0; w < kSlotWaves; ++w)
+        total += base[w][tid];
+    int scan = total;                                // inclusive over the wave
 #pragma unroll
     for (int d = 1; d < kWave; d *= 2) {
         const int x = __shfl_up(scan, d);
@@ -456,28 +479,23 @@ __global__ __launch_bounds__(kSlotThreads) void place_slots(const int *index, in
     if (lane == kWave - 1)
         wave_total[wave] = scan;
     __syncthreads();
-    int at = scan - sum, placed = 0;
+    int at = scan - total, placed = 0;
 #pragma unroll
     for (int w = 0; w < kSlotWaves; ++w) {
         at += w < wave ? wave_total[w] : 0;
         placed += wave_total[w];
     }
-#pragma unroll
-    for (int q = 0; q < kPer; ++q) {
-        const int e = tid * kPer + q;
-        if (blockIdx.x == 0 && e < E)
-            offsets[e] = at;
-        int next = at + before[q];
-#pragma unroll
-        for (int w = 0; w < kSlotWaves; ++w) {
-            const int n = base[w][e];
-            base[w][e] = next;
-            next += n;
-        }
-        at += total[q];
-    }
+    if (blockIdx.x == 0 && tid < E)
+        offsets[tid] = at;
     if (blockIdx.x == 0 && tid == 0)
         offsets[E] = placed;
+    int next_place = at + before;
+#pragma unroll
+    for (int w = 0; w < kSlotWaves; ++w) {
+        const int n = base[w][tid];
+        base[w][tid] = next_place;
+        next_place += n;
+    }
     __syncthreads();
 
     // Places: slots of one expert within 64 find each other bit by bit.
@@ -512,6 +530,10 @@ __global__ __launch_bounds__(kSlotThreads) void place_slots(const int *index, in
 }
 
 int64_t slot_chunks(int64_t S) { return S <= kSlotChunk ? 1 : ceil_div(S, kSlotChunk); }
+
+// Up to this many slots every workgroup counts them all; more are counted in a
+// launch of their own.
+constexpr int64_t kCountedInPlace = 1 << 17;
 
 // A grid has fewer than 2^32 threads, a wave of them per token.
 constexpr int kMaxTokens = (int)(UINT32_MAX / kWave) - kRouteWaves;
@@ -605,8 +627,7 @@ size_t gemm_f32_expert_map_ws_size(int S, int E)
 {
     if (S < 0 || E < 1 || E > GEMM_F32_MAX_EXPERTS)
         return 0;
-    const int64_t chunks = slot_chunks(S);
-    return chunks > 1 ? (size_t)chunks * (size_t)E * sizeof(int) : 0;
+    return S > kCountedInPlace ? (size_t)slot_chunks(S) * (size_t)E * sizeof(int) : 0;
 }
 
 int gemm_f32_expert_map(int S, int E, const int *index, int *offsets, int *order, int *position, void *workspace,

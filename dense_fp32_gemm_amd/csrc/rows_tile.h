@@ -80,6 +80,7 @@ struct Fragments {
     using T = typename E::T;
     // rows a group of fragments read together covers, /16
     static constexpr int kV = E::kBytes == 2 || ALONG ? 1 : F % 4 == 0 ? 4 : F % 2 == 0 ? 2 : 1;
+    static constexpr int kReads = ALONG ? F : E::kBytes == 2 ? 2 * F : 4 * F / kV;   // LDS instructions
     u32x4 q[F];      // 8 16-bit values, or 4 binary32 (k = 4*(l/16) + 0..3)
 
     __device__ inline void read(const T *panel, int row0, int step, int lane)
@@ -145,6 +146,7 @@ struct Tile {
     static constexpr int kThreads = WM * WN * kWave;
     static constexpr int kFm = BM / WM / 16, kFn = BN / WN / 16;
     static constexpr int CH = CH_, kDeep = CH * E::kChunk, kSteps = CH / 4;
+    static constexpr int kMfma = kFm * kFn * (E::kBytes == 2 ? 1 : 4);     // matrix instructions of a step
     static constexpr int kLdsA = BM * kDeep, kLdsB = BN * kDeep;           // elements of a panel
     using Fa = Fragments<E, A_ALONG, BM, CH, kFm>;
     using Fb = Fragments<E, B_ALONG, BN, CH, kFn>;
@@ -162,29 +164,24 @@ struct Tile {
                 acc[m][n] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
 
-    // The panel's fragments, all steps.
-    struct Panel {
-        Fa a[kSteps];
-        Fb b[kSteps];
-        __device__ inline void read(const T *la, const T *lb, int wm, int wn, int lane)
+    // One step's fragments of a panel.
+    struct Step {
+        Fa a;
+        Fb b;
+        __device__ inline void read(const T *panel, int step, int wm, int wn, int lane)
         {
-#pragma unroll
-            for (int step = 0; step < kSteps; ++step) {
-                a[step].read(la, wm * (BM / WM), step, lane);
-                b[step].read(lb, wn * (BN / WN), step, lane);
-            }
+            a.read(panel, wm * (BM / WM), step, lane);
+            b.read(panel + kLdsA, wn * (BN / WN), step, lane);
         }
     };
 
-    __device__ inline void multiply(const Panel &p)
+    __device__ inline void multiply(const Step &s)
     {
 #pragma unroll
-        for (int step = 0; step < kSteps; ++step)
+        for (int m = 0; m < kFm; ++m)
 #pragma unroll
-            for (int m = 0; m < kFm; ++m)
-#pragma unroll
-                for (int n = 0; n < kFn; ++n)
-                    acc[m][n] = mfma_step<E>(p.b[step].q[n], p.a[step].q[m], acc[m][n]);
+            for (int n = 0; n < kFn; ++n)
+                acc[m][n] = mfma_step<E>(s.b.q[n], s.a.q[m], acc[m][n]);
     }
 
     // f(row, column, 4 neighbouring columns' sums) over the lane's results,
@@ -384,8 +381,9 @@ struct Gathered : Across<E, RN, NT, CH> {
 // The K loop: adds the K-long sums to the tile.
 //
 // DMA: buffer loads write panels straight into a ring of S LDS buffers of
-// kLdsA + kLdsB elements, S - 1 panels ahead of the matrix cores, one
-// barrier per panel.  For rows on 4-byte boundaries less than 2^31 bytes from
+// kLdsA + kLdsB elements, up to S panels ahead of the matrix cores, one
+// barrier per panel; with 128-byte panels, fragments are read half a panel
+// before they are multiplied.  For rows on 4-byte boundaries less than 2^31 bytes from
 // their base.  Else the chunks are staged through registers into two
 // buffers, element by element at a row's end.
 // ---------------------------------------------------------------------------
@@ -439,9 +437,12 @@ __device__ inline void sum_panels_staged(Ti &tile, int K, const SrcA &a, const S
         group_sync<NT>();        // the other buffer's readers passed the last one
         if (k0 + BK < K)
             fetch(k0 + BK);
-        typename Ti::Panel p;
-        p.read(la, lb, wm, wn, lane);
-        tile.multiply(p);
+#pragma unroll
+        for (int step = 0; step < Ti::kSteps; ++step) {
+            typename Ti::Step f;
+            f.read(la, step, wm, wn, lane);
+            tile.multiply(f);
+        }
     }
 }
 
@@ -529,17 +530,43 @@ __device__ inline void load_panel(const Src &src, int k0, typename E::T *panel, 
     }
 }
 
-// One panel: the next one's loads into `next`, this one's sums from `now`.  The
-// two do not overlap; saying so keeps the compiler from waiting for
-// the loads before it reads.
+// Half a panel's work: fragments of one step are read while those of the other
+// step, read half a panel ago, are multiplied.  `freed` (what fire() fills) and
+// `panel` (what is read) do not overlap; saying so keeps the compiler
+// from waiting for the loads in flight before it reads.
 template <class E, class Ti, class Fire>
-__device__ __forceinline__ void panel_step(Ti &tile, const typename E::T *__restrict__ now, typename E::T *__restrict__ next,
-                                           Fire &&fire, int wm, int wn, int lane)
+__device__ __forceinline__ void half_panel(Ti &tile, const typename E::T *__restrict__ panel, typename E::T *__restrict__ freed,
+                                           Fire &&fire, int step, typename Ti::Step &read, const typename Ti::Step &done,
+                                           int wm, int wn, int lane)
 {
-    fire(next);
-    typename Ti::Panel p;
-    p.read(now, now + Ti::kLdsA, wm, wn, lane);
-    tile.multiply(p);
+    fire(freed);
+    __builtin_amdgcn_sched_barrier(0);
+    read.read(panel, step, wm, wn, lane);
+    tile.multiply(done);
+    // One LDS read behind each matrix instruction while there are any: issued in a
+    // row, the reads of all waves would queue and the matrix cores idle.
+    constexpr int kReads = Ti::Fa::kReads + Ti::Fb::kReads, kMfma = Ti::kMfma;
+#pragma unroll
+    for (int i = 0; i < kReads && i < kMfma - 1; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+    }
+    __builtin_amdgcn_sched_group_barrier(0x100, kReads, 0);
+    __builtin_amdgcn_sched_group_barrier(0x008, kMfma, 0);
+    __builtin_amdgcn_sched_barrier(0);
+}
+
+// One-step panels: the panel S - 1 ahead is loaded into `freed`, then this one's
+// fragments are read and multiplied.  Half the fragments' registers: twice the
+// waves, which overlap one another's reads.
+template <class E, class Ti, class Fire>
+__device__ __forceinline__ void whole_panel(Ti &tile, const typename E::T *__restrict__ panel, typename E::T *__restrict__ freed,
+                                            Fire &&fire, int wm, int wn, int lane)
+{
+    fire(freed);
+    typename Ti::Step f;
+    f.read(panel, 0, wm, wn, lane);
+    tile.multiply(f);
 }
 
 template <class E, int S, class Ti, class SrcA, class SrcB>
@@ -552,44 +579,74 @@ __device__ inline void sum_panels_dma(Ti &tile, int K, const SrcA &a, const SrcB
     // waves have fewer, and wait for more than they must).
     constexpr int kLoads = SrcA::kSlots / NT + SrcB::kSlots / NT;
     const int lane = tid % kWave, wave = NT == kWave ? 0 : __builtin_amdgcn_readfirstlane(tid / kWave);
+    if (K <= 0)
+        return;
     const PanelLoads<E, SrcA, NT> pa(a);
     const PanelLoads<E, SrcB, NT> pb(b);
     auto fire = [&](int k0, T *panel) {
         pa.fire(a, k0, panel, wave);
         pb.fire(b, k0, panel + Ti::kLdsA, wave);
     };
-    if constexpr (SrcA::kListed) {
-        a.refill(0);
-        __syncthreads();
-    }
-#pragma unroll
-    for (int q = 0; q < S - 1; ++q)
-        if (q * BK < K)
-            fire(q * BK, lds + q * kPanel);
-    int now = 0, next = S - 1;
-    for (int k0 = 0; k0 < K; k0 += BK) {
-        if constexpr (SrcA::kListed)
-            a.refill(k0 + (S - 1) * BK);
-        // This panel has landed when no more than the S - 2 panels after it, all
-        // whole ones, are in flight; the buffer of the panel before it is
-        // free once every wave has read it.
-        if (k0 + (S - 1) * BK <= K)
-            asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((S - 2) * kLoads) : "memory");
+    // The panel at k0 has landed when no more than `after` whole panels behind
+    // it are in flight, and every wave's LDS accesses so far are complete.
+    auto landed = [&](int k0, auto after) {
+        if (k0 + (decltype(after)::value + 1) * BK <= K)
+            asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(decltype(after)::value * kLoads) : "memory");
         else
             asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
         if constexpr (NT > kWave)
             __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
-        const int ahead = k0 + (S - 1) * BK;
-        panel_step<E>(tile, lds + now * kPanel, lds + next * kPanel,
-                      [&](T *panel) {
-                          if (ahead < K)
-                              fire(ahead, panel);
-                      },
-                      wm, wn, lane);
-        now = now + 1 == S ? 0 : now + 1;
-        next = next + 1 == S ? 0 : next + 1;
+    };
+    if constexpr (SrcA::kListed) {
+        a.refill(0);
+        __syncthreads();
     }
+    if constexpr (Ti::kSteps == 1) {
+#pragma unroll
+        for (int q = 0; q < S - 1; ++q)
+            if (q * BK < K)
+                fire(q * BK, lds + q * kPanel);
+        int now = 0, next = S - 1;
+        for (int k0 = 0; k0 < K; k0 += BK) {
+            if constexpr (SrcA::kListed)
+                a.refill(k0 + (S - 1) * BK);
+            landed(k0, std::integral_constant<int, S - 2>{});
+            whole_panel<E>(tile, lds + now * kPanel, lds + next * kPanel,
+                           [&](T *freed) {
+                               if (k0 + (S - 1) * BK < K)
+                                   fire(k0 + (S - 1) * BK, freed);
+                           },
+                           wm, wn, lane);
+            now = now + 1 == S ? 0 : now + 1;
+            next = next + 1 == S ? 0 : next + 1;
+        }
+        return;
+    }
+#pragma unroll
+    for (int q = 0; q < S; ++q)
+        if (q * BK < K)
+            fire(q * BK, lds + q * kPanel);
+    typename Ti::Step f0, f1;
+    landed(0, std::integral_constant<int, S - 1>{});
+    f0.read(lds, 0, wm, wn, lane);
+    int now = 0;
+    for (int k0 = BK; k0 < K; k0 += BK) {            // k0: the panel after this one
+        T *panel = lds + now * kPanel;
+        half_panel<E>(tile, panel, (T *)nullptr, [](T *) {}, 1, f1, f0, wm, wn, lane);
+        if constexpr (SrcA::kListed)
+            a.refill(k0 + (S - 1) * BK);
+        landed(k0, std::integral_constant<int, S - 2>{});
+        now = now + 1 == S ? 0 : now + 1;
+        half_panel<E>(tile, lds + now * kPanel, panel,
+                      [&](T *freed) {
+                          if (k0 + (S - 1) * BK < K)
+                              fire(k0 + (S - 1) * BK, freed);
+                      },
+                      0, f0, f1, wm, wn, lane);
+    }
+    half_panel<E>(tile, lds + now * kPanel, (T *)nullptr, [](T *) {}, 1, f1, f0, wm, wn, lane);
+    tile.multiply(f1);
 }
 
 template <class E, bool DMA, int S, class Ti, class SrcA, class SrcB>

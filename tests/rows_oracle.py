@@ -95,9 +95,13 @@ def route_grad(logits, index, dweight, score, normalize, scale):
 
 def expert_map(index, experts):
     flat = index.reshape(-1).tolist()
+    members = [[] for _ in range(experts)]
+    for s, x in enumerate(flat):
+        if 0 <= x < experts:
+            members[x].append(s)
     order, offsets = [], [0]
-    for e in range(experts):
-        order += [s for s, x in enumerate(flat) if x == e]
+    for mine in members:
+        order += mine
         offsets.append(len(order))
     position = [-1] * len(flat)
     for p, s in enumerate(order):

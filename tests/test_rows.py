@@ -140,7 +140,8 @@ def test_route_grad_adds_what_an_index_named_twice_gets(dev):
     oracle.close(both, want.cpu(), want.cpu().abs() * 2.0 ** -23, "twice")
 
 
-@pytest.mark.parametrize("S,E", [(0, 3), (1, 1), (5, 4), (64, 64), (2047, 7), (2048, 1024), (2049, 3), (6000, 130), (20001, 1000)])
+@pytest.mark.parametrize("S,E", [(0, 3), (1, 1), (5, 4), (64, 64), (2047, 7), (2048, 1024), (2049, 3), (6000, 130), (20001, 1000), (131072, 9),
+                                 (131073, 64), (150001, 256)])
 def test_expert_map(dev, S, E):
     g = seeded("map", S, E)
     index = torch.randint(-1, E + 1, (S,), generator=g, dtype=torch.int32)      # -1 and E: left out

@@ -60,17 +60,17 @@ def test_route_grad_refuses(change, rc):
 
 @pytest.mark.parametrize("change,rc", [
     (dict(S=-1), "DIM"), (dict(E=0), "DIM"), (dict(E=1025), "DIM"), (dict(offsets=0), "NULL"), (dict(index=0), "NULL"),
-    (dict(position=0), "NULL"), (dict(order=FAKE + 2), "ALIGN"), (dict(S=100000), "WORKSPACE"),
-    (dict(S=100000, workspace=FAKE, workspace_bytes=16), "WORKSPACE"),
-    (dict(S=100000, workspace=FAKE + 4, workspace_bytes=1 << 30), "WORKSPACE")])
+    (dict(position=0), "NULL"), (dict(order=FAKE + 2), "ALIGN"), (dict(S=200000), "WORKSPACE"),
+    (dict(S=200000, workspace=FAKE, workspace_bytes=16), "WORKSPACE"),
+    (dict(S=200000, workspace=FAKE + 4, workspace_bytes=1 << 30), "WORKSPACE")])
 def test_expert_map_refuses(change, rc):
     base = dict(S=10, E=4, index=FAKE, offsets=FAKE, order=FAKE, position=FAKE)
     assert gb.gemm_f32_expert_map(**{**base, **change}) == getattr(gb, "GEMM_F32_ERR_" + rc)
 
 
-def test_expert_map_workspace_grows_only_past_one_workgroup():
-    assert gb.gemm_f32_expert_map_ws_size(0, 8) == gb.gemm_f32_expert_map_ws_size(2048, 1024) == 0
-    assert gb.gemm_f32_expert_map_ws_size(2049, 8) > 0
+def test_expert_map_workspace_only_for_many_slots():
+    assert gb.gemm_f32_expert_map_ws_size(0, 8) == gb.gemm_f32_expert_map_ws_size(1 << 17, 1024) == 0
+    assert gb.gemm_f32_expert_map_ws_size((1 << 17) + 1, 8) > 0
     assert gb.gemm_f32_expert_map_ws_size(-1, 8) == gb.gemm_f32_expert_map_ws_size(9, 0) == 0
 
 

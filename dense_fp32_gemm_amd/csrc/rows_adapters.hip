@@ -43,6 +43,7 @@ struct AdapterArgs {
     int depth;               // of factor's rows
     int tiles_m, tiles_n;
     int big_m;               // many rows: rows of tiles of the large kind, the rest are small ones
+    int slots_big;           // workgroups of them the device holds at once
     int xcds;
     bool vector_y;           // Y's rows take stores of four elements
 };
@@ -76,20 +77,22 @@ struct UpRows : Across<E, RN, NT> {
     }
 };
 
-// Calls f(a, members) for each adapter a among up to 128 rows, members being
-// bit masks of its rows.  which: the adapter of row `lane` and of row 64 + lane, -1:
-// none.  The same in every wave.
-template <int ROWS, class Fn>
-__device__ inline void each_adapter(int which0, int which1, Fn &&f)
+// Calls f(a) for each adapter a among a tile's rows, from the highest number down.
+// which[q]: the adapter of row 64 * q + lane, -1: none.  The same in every wave.
+template <int WORDS, class Fn>
+__device__ inline void each_adapter(const int (&which)[WORDS], Fn &&f)
 {
-    uint64_t left0 = __ballot(which0 >= 0), left1 = ROWS > kWave ? __ballot(which1 >= 0) : 0;
-    while (left0 | left1) {
-        const int a = left0 ? __builtin_amdgcn_readlane(which0, (int)__builtin_ctzll(left0))
-                            : __builtin_amdgcn_readlane(which1, (int)__builtin_ctzll(left1));
-        const uint64_t m0 = __ballot(which0 == a), m1 = ROWS > kWave ? __ballot(which1 == a) : 0;
-        f(a, m0, m1);
-        left0 &= ~m0;
-        left1 &= ~m1;
+    int above = INT32_MAX;                           // adapters from here on are done
+    for (;;) {
+        uint32_t best = 0;                           // number + 1
+#pragma unroll
+        for (int q = 0; q < WORDS; ++q)
+            best = max(best, which[q] < above ? (uint32_t)(which[q] + 1) : 0u);
+        best = wave_max(best);
+        if (best == 0)
+            return;
+        above = (int)best - 1;
+        f(above);
     }
 }
 
@@ -122,9 +125,10 @@ __device__ inline void down_item(const AdapterArgs &g, int64_t item, typename E:
     const int rank0 = (int)(item / ((int64_t)g.splits_u * g.slots) % g.ranks) * RN;
     const int t0 = (int)(item / ((int64_t)g.splits_u * g.slots * g.ranks)) * 16;
     const int k0 = split * g.split_ku, K = min(g.split_ku, g.K - k0);
-    const int which = adapter_of(g, t0 + lane, lane < 16 && t0 + lane < g.T);
+    const int which[1] = {adapter_of(g, t0 + lane, lane < 16 && t0 + lane < g.T)};
     int nth = 0;
-    each_adapter<16>(which, -1, [&](int a, uint64_t members, uint64_t) {
+    each_adapter(which, [&](int a) {
+        const uint64_t members = __ballot(which[0] == a);
         if (nth++ % g.slots != slot)
             return;
         Ti tile;
@@ -200,34 +204,49 @@ __global__ __launch_bounds__(kWave) void join_kernel(AdapterArgs g)
     const int lane = threadIdx.x;
     const int64_t t = blockIdx.y;
     const int n = (blockIdx.x * kWave + lane) * E::kChunk;
-    const int a = g.R > 0 && g.n > 0 ? adapter_of(g, t, true) : -1;
+    // The parts first: they wait for nothing.  kBatch parts' loads in flight.
+    constexpr int kBatch = 8;
+    float sum[E::kChunk] = {};
+    auto add_parts = [&](int i0) {
+        f32x4 v[kBatch][E::kChunk / 4];
+#pragma unroll
+        for (int q = 0; q < kBatch; ++q)
+#pragma unroll
+            for (int e = 0; e < E::kChunk / 4; ++e)
+                v[q][e] = i0 + q < g.splits && n < g.N
+                              ? *reinterpret_cast<const f32x4 *>(g.partial_y + ((int64_t)(i0 + q) * g.T + t) * g.pitch + n + 4 * e)
+                              : f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int q = 0; q < kBatch; ++q)
+#pragma unroll
+            for (int e = 0; e < E::kChunk; ++e)
+                sum[e] += v[q][e / 4][e % 4];
+    };
+    const int a = g.R > 0 ? adapter_of(g, t, true) : -1;
+    add_parts(0);
+    for (int i = kBatch; i < g.splits; i += kBatch)
+        add_parts(i);
     if (a >= 0) {
         const float s = g.scale != nullptr ? g.scale[a] : 1.f;
         for (int r = lane; r < g.R; r += kWave) {
-            float sum = 0.f;
-            for (int i = 0; i < g.splits_u; ++i)
-                sum += g.partial_u[((int64_t)i * g.T + t) * g.R + r];
-            u[r] = s * sum;
+            float part[kBatch], low = 0.f;
+            for (int i0 = 0; i0 < g.splits_u; i0 += kBatch) {
+#pragma unroll
+                for (int q = 0; q < kBatch; ++q)
+                    part[q] = i0 + q < g.splits_u ? g.partial_u[((int64_t)(i0 + q) * g.T + t) * g.R + r] : 0.f;
+#pragma unroll
+                for (int q = 0; q < kBatch; ++q)
+                    low += part[q];
+            }
+            u[r] = s * low;
         }
     }
     __syncthreads();
     if (n >= g.N)
         return;
-    float sum[E::kChunk] = {};
-    for (int i = 0; i < g.splits; ++i) {
-        const float *p = g.partial_y + ((int64_t)i * g.T + t) * g.pitch + n;
-#pragma unroll
-        for (int e = 0; e < E::kChunk; e += 4) {
-            const f32x4 v = *reinterpret_cast<const f32x4 *>(p + e);
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-                sum[e + q] += v[q];
-        }
-    }
     if (a >= 0) {
         const T *B = (const T *)g.B + a * g.stride_b + n;
-        constexpr int kBatch = 8;                    // rows of B in flight
-        for (int r0 = 0; r0 < g.R; r0 += kBatch) {
+        for (int r0 = 0; r0 < g.R; r0 += kBatch) {   // kBatch rows of B in flight
             Chunk<E> b[kBatch];
 #pragma unroll
             for (int q = 0; q < kBatch; ++q)
@@ -313,6 +332,8 @@ __device__ inline void adapters_tile(const AdapterArgs &g, int m0, int n0, typen
     using Ti = Tile<E, true, false, BM, BN, WM, WN>;
     using T = typename E::T;
     constexpr int NT = Ti::kThreads;
+    if (m0 >= g.T || n0 >= g.N)
+        return;                                      // the whole workgroup
     const int tid = threadIdx.x, lane = tid % kWave, wave = __builtin_amdgcn_readfirstlane(tid / kWave);
     const int wm = wave / WN, wn = wave % WN;
     Ti tile;
@@ -323,15 +344,29 @@ __device__ inline void adapters_tile(const AdapterArgs &g, int m0, int n0, typen
         const Across<E, BN, NT> w((const T *)g.W, tid, g.K, g.ldw, n0, g.N);
         sum_panels<E, DMA, S>(tile, g.K, x, w, lds, tid, wm, wn);
     }
-    if (g.R > 0 && g.n > 0) {
-        const int which0 = adapter_of(g, m0 + lane, lane < BM && m0 + lane < g.T);
-        const int which1 = adapter_of(g, m0 + 64 + lane, 64 + lane < BM && m0 + 64 + lane < g.T);
-        each_adapter<BM>(which0, which1, [&](int a, uint64_t members0, uint64_t members1) {
-            auto member = [&](int r) { return (r < 64 ? members0 >> r : members1 >> (r - 64)) & 1; };
-            const Along<E, BM, NT> u((const T *)g.factor + (int64_t)m0 * g.depth, tid, g.depth,
-                                     [&](int, int r) { return member(r) ? (int64_t)r * g.depth * E::kBytes : -1; });
+    if (g.R > 0) {
+        using SrcU = Along<E, BM, NT>;
+        constexpr int kWords = (BM + kWave - 1) / kWave;
+        // The adapters of the tile's rows; of the rows this thread loads; of those it adds to.
+        int which[kWords], loads[SrcU::kCount], adds[Ti::kFm];
+#pragma unroll
+        for (int q = 0; q < kWords; ++q)
+            which[q] = adapter_of(g, m0 + q * kWave + lane, q * kWave + lane < BM && m0 + q * kWave + lane < g.T);
+#pragma unroll
+        for (int i = 0; i < SrcU::kCount; ++i) {
+            const int r = SrcU::row_of(i, tid);
+            loads[i] = adapter_of(g, m0 + r, r < BM && m0 + r < g.T);
+        }
+#pragma unroll
+        for (int m = 0; m < Ti::kFm; ++m) {
+            const int r = wm * (BM / WM) + Ti::Fa::row_of(m, lane % 16);
+            adds[m] = adapter_of(g, m0 + r, m0 + r < g.T);
+        }
+        each_adapter(which, [&](int a) {
+            const SrcU u((const T *)g.factor + (int64_t)m0 * g.depth, tid, g.depth,
+                         [&](int i, int r) { return loads[i] == a ? (int64_t)r * g.depth * E::kBytes : -1; });
             const UpRows<E, BN, NT> b((const T *)g.B + a * g.stride_b, tid, g.depth, g.ldb, n0, g.N, g.R);
-            // Panel by panel, each panel's sums of one 16-row block at a time: a second
+            // Step by step, each step's sums of one 16-row block at a time: a second
             // set of sums for the whole tile would halve the waves a SIMD holds.
             for (int k0 = 0; k0 < g.depth; k0 += Ti::kDeep) {
                 __syncthreads();
@@ -339,29 +374,23 @@ __device__ inline void adapters_tile(const AdapterArgs &g, int m0, int n0, typen
                 load_panel<E, DMA, NT>(b, k0, lds + Ti::kLdsA, tid);
                 asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
                 __syncthreads();
-                typename Ti::Step p[Ti::kSteps];
 #pragma unroll
-                for (int step = 0; step < Ti::kSteps; ++step)
-                    p[step].read(lds, step, wm, wn, lane);
+                for (int step = 0; step < Ti::kSteps; ++step) {
+                    typename Ti::Step p;
+                    p.read(lds, step, wm, wn, lane);
 #pragma unroll
-                for (int m = 0; m < Ti::kFm; ++m) {
-                    f32x4 add[Ti::kFn];
+                    for (int m = 0; m < Ti::kFm; ++m) {
+                        const int r = wm * (BM / WM) + Ti::Fa::row_of(m, lane % 16);
+                        const bool mine = adds[m] == a;
+                        const float f = E::kBytes == 4 || !mine ? 1.f : g.unscale[m0 + r];
 #pragma unroll
-                    for (int n = 0; n < Ti::kFn; ++n) {
-                        add[n] = f32x4{0.f, 0.f, 0.f, 0.f};
+                        for (int n = 0; n < Ti::kFn; ++n) {
+                            const f32x4 add = mfma_step<E>(p.b.q[n], p.a.q[m], f32x4{0.f, 0.f, 0.f, 0.f});
 #pragma unroll
-                        for (int step = 0; step < Ti::kSteps; ++step)
-                            add[n] = mfma_step<E>(p[step].b.q[n], p[step].a.q[m], add[n]);
+                            for (int i = 0; i < 4; ++i)
+                                tile.acc[m][n][i] = mine ? fmaf(f, add[i], tile.acc[m][n][i]) : tile.acc[m][n][i];
+                        }
                     }
-                    const int r = wm * (BM / WM) + Ti::Fa::row_of(m, lane % 16);
-                    if (!member(r))
-                        continue;
-                    const float f = E::kBytes == 4 ? 1.f : g.unscale[m0 + r];
-#pragma unroll
-                    for (int n = 0; n < Ti::kFn; ++n)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            tile.acc[m][n][i] = fmaf(f, add[n][i], tile.acc[m][n][i]);
                 }
             }
         });
@@ -380,19 +409,37 @@ __device__ inline void adapters_tile(const AdapterArgs &g, int m0, int n0, typen
         store(std::false_type{});
 }
 
-// tiles_m rows of tiles: big_m of 128 rows, then tiles of 16 rows.
+// The tiles of many rows.  16-bit types: 256 x 256, one workgroup a compute unit, the
+// panels' rate from L2 being what bounds them; binary32, bound by the matrix
+// cores: 128 x 128, two.
+template <class E>
+struct Big {
+    static constexpr int B = E::kBytes == 2 ? 256 : 128, WM = 2, WN = E::kBytes == 2 ? 4 : 2;
+    static constexpr int kThreads = WM * WN * kWave, kPerCu = E::kBytes == 2 ? 1 : 2;
+};
+
+// big_m rows of large tiles, the last round of them cut; then tiles of 16 rows.
 template <class E, bool DMA>
-__global__ __launch_bounds__(256, 2) void adapters_kernel(AdapterArgs g)
+__global__ __launch_bounds__(Big<E>::kThreads, 2) void adapters_kernel(AdapterArgs g)
 {
-    constexpr int kBN = 128;
-    __shared__ __attribute__((aligned(16))) typename E::T lds[2 * (128 + kBN) * panel_deep<E>()];
-    const int total = gridDim.x, per = total / g.xcds, rem = total % g.xcds, xcd = blockIdx.x % g.xcds;
-    const int t = xcd * per + min(xcd, rem) + blockIdx.x / g.xcds;   // contiguous tiles per die
-    const int tm = t % g.tiles_m, n0 = t / g.tiles_m * kBN;
-    if (tm < g.big_m)
-        adapters_tile<E, 128, kBN, 2, 2, 2, DMA>(g, tm * 128, n0, lds);
+    constexpr int B = Big<E>::B, WM = Big<E>::WM, WN = Big<E>::WN;
+    __shared__ __attribute__((aligned(16))) typename E::T lds[2 * 2 * B * panel_deep<E>()];
+    const int small = (g.tiles_m - g.big_m) * g.tiles_n;
+    if ((int)blockIdx.x < small) {
+        const int tm = blockIdx.x % (g.tiles_m - g.big_m), tn = blockIdx.x / (g.tiles_m - g.big_m);
+        adapters_tile<E, 16, B, 1, WM * WN, 2, DMA>(g, g.big_m * B + tm * 16, tn * B, lds);
+        return;
+    }
+    const Part part = part_of(blockIdx.x - small, g.big_m * g.tiles_n, g.slots_big, g.xcds);
+    if (part.tile < 0)
+        return;
+    const int m0 = part.tile % g.big_m * B, n0 = part.tile / g.big_m * B;
+    if (part.cut == 1)
+        adapters_tile<E, B, B, WM, WN, 2, DMA>(g, m0, n0, lds);
+    else if (part.cut == 2)
+        adapters_tile<E, B / 2, B, WM, WN, 2, DMA>(g, m0 + part.piece * (B / 2), n0, lds);
     else
-        adapters_tile<E, 16, kBN, 1, 4, 2, DMA>(g, g.big_m * 128 + (tm - g.big_m) * 16, n0, lds);
+        adapters_tile<E, B / 2, B / 2, WM, WN, 2, DMA>(g, m0 + part.piece % 2 * (B / 2), n0 + part.piece / 2 * (B / 2), lds);
 }
 
 // ---------------------------------------------------------------------------
@@ -496,12 +543,16 @@ template <class E, int RN>
 int run_many(AdapterArgs g, bool low, bool dma, bool dma_down, hipStream_t stream)
 {
     // Up to 32 rows behind the last whole tile: tiles of 16 rows.
-    g.big_m = g.T / 128;
-    const int rest = g.T - g.big_m * 128;
+    constexpr int B = Big<E>::B;
+    g.big_m = g.T / B;
+    const int rest = g.T - g.big_m * B;
     if (rest > 32)
         ++g.big_m;
-    const int64_t tm = g.big_m + (rest > 32 ? 0 : ceil_div(rest, 16)), tn = ceil_div(g.N, 128);
-    if (tm * tn > (int64_t)UINT32_MAX / 256)
+    const int64_t tm = g.big_m + (rest > 32 ? 0 : ceil_div(rest, 16)), tn = ceil_div(g.N, B);
+    g.slots_big = (int)gemm_f32_internal::current_device().cus * Big<E>::kPerCu;
+    // cutting the last round adds at most three pieces for a quarter of the slots
+    const int64_t grid = tm * tn + g.slots_big;
+    if (grid > (int64_t)UINT32_MAX / Big<E>::kThreads)
         return GEMM_F32_ERR_DIM;
     g.tiles_m = (int)tm;
     g.tiles_n = (int)tn;
@@ -514,9 +565,9 @@ int run_many(AdapterArgs g, bool low, bool dma, bool dma_down, hipStream_t strea
         factor_kernel<E><<<(unsigned)ceil_div(g.T, kFactorThreads / kWave), kFactorThreads, 0, stream>>>(g);
     }
     if (dma)
-        adapters_kernel<E, true><<<(unsigned)(tm * tn), 256, 0, stream>>>(g);
+        adapters_kernel<E, true><<<(unsigned)grid, Big<E>::kThreads, 0, stream>>>(g);
     else
-        adapters_kernel<E, false><<<(unsigned)(tm * tn), 256, 0, stream>>>(g);
+        adapters_kernel<E, false><<<(unsigned)grid, Big<E>::kThreads, 0, stream>>>(g);
     return launched();
 }
 

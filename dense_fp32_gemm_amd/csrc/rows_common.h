@@ -118,6 +118,28 @@ __device__ inline void store_chunk(typename E::T *p, const Chunk<E> &c, int64_t 
     }
 }
 
+// ---------------------------------------------------------------------------
+// Wave-wide maximum
+// ---------------------------------------------------------------------------
+template <int CTRL>
+__device__ inline uint32_t dpp(uint32_t x)
+{
+    return (uint32_t)__builtin_amdgcn_update_dpp((int)x, (int)x, CTRL, 0xf, 0xf, false);
+}
+
+// The wave's largest x, in a scalar: rotations within rows of 16 lanes, then
+// the four rows.  All lanes must be active.
+__device__ inline uint32_t wave_max(uint32_t x)
+{
+    x = max(x, dpp<0x128>(x));   // row_ror:8
+    x = max(x, dpp<0x124>(x));
+    x = max(x, dpp<0x122>(x));
+    x = max(x, dpp<0x121>(x));
+    const uint32_t a = max((uint32_t)__builtin_amdgcn_readlane((int)x, 0), (uint32_t)__builtin_amdgcn_readlane((int)x, 16));
+    const uint32_t b = max((uint32_t)__builtin_amdgcn_readlane((int)x, 32), (uint32_t)__builtin_amdgcn_readlane((int)x, 48));
+    return max(a, b);
+}
+
 }  // namespace rows
 
 #endif

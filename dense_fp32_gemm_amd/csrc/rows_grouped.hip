@@ -30,14 +30,6 @@ struct GroupedArgs {
     int slots;               // workgroups the device holds at once
 };
 
-// Workgroups are dealt to the dies round-robin; renumbered so that each die
-// gets a contiguous range of tiles, whose operands its L2 then shares.
-__device__ inline int die_contiguous(int w, int total, int xcds)
-{
-    const int per = total / xcds, rem = total % xcds, xcd = w % xcds;
-    return xcd * per + (xcd < rem ? xcd : rem) + w / xcds;
-}
-
 // Group g's range of places, clamped to 0..P.
 __device__ inline void group_range(const int *offsets, int g, int P, int &lo, int &hi)
 {
@@ -101,24 +93,6 @@ __device__ inline Place locate(const GroupedArgs &g, int bm, int t)
     return Place{__builtin_amdgcn_readfirstlane(p.group), __builtin_amdgcn_readfirstlane(p.lo),
                  __builtin_amdgcn_readfirstlane(p.hi), __builtin_amdgcn_readfirstlane(p.tm),
                  __builtin_amdgcn_readfirstlane(p.tn)};
-}
-
-// Workgroup w's part of `total` tiles on a device that holds `slots` workgroups
-// at once: whole tiles while they fill rounds of slots; the tiles of a last
-// round that fills at most half (a quarter) of the slots are cut into two (four).
-struct Part {
-    int tile, cut, piece;    // cut: 1, 2 or 4 pieces; tile < 0: nothing to do
-};
-__device__ inline Part part_of(int w, int total, int slots, int xcds)
-{
-    const int whole = total / slots * slots, rest = total - whole;
-    if (w < whole)
-        return Part{die_contiguous(w, whole, xcds), 1, 0};
-    const int cut = 4 * rest <= slots ? 4 : 2 * rest <= slots ? 2 : 1;
-    if (w - whole >= rest * cut)
-        return Part{-1, 1, 0};
-    const int q = die_contiguous(w - whole, rest * cut, xcds);
-    return Part{whole + q / cut, cut, q % cut};
 }
 
 // One tile: rows m0 .. m_end - 1 (places; of dW: rows of the matrix), columns from n0 on.
@@ -359,6 +333,20 @@ int launch_tile(GroupedArgs g, bool dma, hipStream_t stream)
     return launched();
 }
 
+// Tiles by the rows a group has on average and by how many tiles there are (us a
+// call, one MI355X, K = 2048 -> N = 1024 unless said):
+//  * up to 32 rows a group (binary32: 64), a tile of 32 x 64: many workgroups, each weight
+//    read once or twice (32 rows over 32 groups, bf16: 13.4 against 17.2 for 64 x 128; 512 rows
+//    over 16 groups: 17.7 against 17.8, 768 rows: 19.7 against 18.0; binary32, 1024
+//    rows over 16 groups: 60 against 69 for 64 x 64, 1536 rows: equal);
+//  * binary32 else: 64 x 64 (4096 rows over 8 groups, N = 2048: 293 against 310 for 128 x 64
+//    and 312 for 128 x 128, whose last round leaves more units idle);
+//  * 16-bit types, 256 x 256 tiles for three fifths of the compute units or
+//    more: those, the last round cut (2000 rows over 8 groups, N = 4096: 56 against 76
+//    for 64 x 128; 65536 rows over 64: 288 against 355 for 128 x 128). A compute unit
+//    takes about 16 bytes a clock of panels from L2 whatever the tile, and the
+//    largest tile needs the fewest per product;
+//  * fewer: 64 x 128 (4096 rows over 8 groups, K = N = 1024: 19.4 against 21.6).
 template <Op OP>
 int launch_grouped(int type, const GroupedArgs &g, bool dma, hipStream_t stream)
 {
@@ -366,10 +354,8 @@ int launch_grouped(int type, const GroupedArgs &g, bool dma, hipStream_t stream)
     with_type(type, [&](auto e) {
         using E = decltype(e);
         if constexpr (OP != kGradW) {
-            // Few rows a group: tiles of 16 rows read each weight once without
-            // spending matrix instructions on rows that are not there.
-            if (g.P <= 32 * (int64_t)g.G) {
-                rc = launch_tile<E, OP, 16, 128, 1, 4, 8, 3, 0>(g, dma, stream);
+            if (g.P <= (E::kBytes == 4 ? 64 : 32) * (int64_t)g.G) {
+                rc = launch_tile<E, OP, 32, 64, 1, 4, 8, 4, 0>(g, dma, stream);
                 return;
             }
         }
@@ -378,10 +364,10 @@ int launch_grouped(int type, const GroupedArgs &g, bool dma, hipStream_t stream)
         } else {
             // Half a tile a group is lost on average.
             const int64_t rows = OP == kGradW ? 2 * g.G * ceil_div(g.M, 256) : 2 * (g.P / 256) + (g.G < g.P ? g.G : g.P);
-            if (rows * ceil_div(g.N, 256) * 2 >= 3 * gemm_f32_internal::current_device().cus)
+            if (rows * ceil_div(g.N, 256) * 5 >= 6 * gemm_f32_internal::current_device().cus)
                 rc = launch_tile<E, OP, 256, 256, 2, 4, 8, 2, 1>(g, dma, stream);
             else
-                rc = launch_tile<E, OP, 128, 128, 2, 2, 8, 2, 2>(g, dma, stream);
+                rc = launch_tile<E, OP, 64, 128, 2, 2, 8, 3, 0>(g, dma, stream);
         }
     });
     return rc;

@@ -31,29 +31,10 @@ struct RouteArgs {
 };
 
 // ---------------------------------------------------------------------------
-// Wave-wide reductions
+// Wave-wide sums
 // ---------------------------------------------------------------------------
 template <int CTRL>
-__device__ inline uint32_t dpp(uint32_t x)
-{
-    return (uint32_t)__builtin_amdgcn_update_dpp((int)x, (int)x, CTRL, 0xf, 0xf, false);
-}
-
-// The wave's largest x, in a scalar: rotations within rows of 16 lanes, then
-// the four rows.  All lanes must be active.
-__device__ inline uint32_t wave_max(uint32_t x)
-{
-    x = max(x, dpp<0x128>(x));   // row_ror:8
-    x = max(x, dpp<0x124>(x));
-    x = max(x, dpp<0x122>(x));
-    x = max(x, dpp<0x121>(x));
-    const uint32_t a = max((uint32_t)__builtin_amdgcn_readlane((int)x, 0), (uint32_t)__builtin_amdgcn_readlane((int)x, 16));
-    const uint32_t b = max((uint32_t)__builtin_amdgcn_readlane((int)x, 32), (uint32_t)__builtin_amdgcn_readlane((int)x, 48));
-    return max(a, b);
-}
-
-template <int CTRL>
-__device__ inline double dpp(double x)
+__device__ inline double dpp_double(double x)
 {
     const uint64_t u = __double_as_longlong(x);
     const uint32_t lo = dpp<CTRL>((uint32_t)u), hi = dpp<CTRL>((uint32_t)(u >> 32));
@@ -71,10 +52,10 @@ __device__ inline double read_lane(double x, int lane)
 // The wave's sum, the same in every lane.
 __device__ inline double wave_sum(double x)
 {
-    x += dpp<0x128>(x);
-    x += dpp<0x124>(x);
-    x += dpp<0x122>(x);
-    x += dpp<0x121>(x);
+    x += dpp_double<0x128>(x);
+    x += dpp_double<0x124>(x);
+    x += dpp_double<0x122>(x);
+    x += dpp_double<0x121>(x);
     return (read_lane(x, 0) + read_lane(x, 16)) + (read_lane(x, 32) + read_lane(x, 48));
 }
 

@@ -659,6 +659,35 @@ __device__ inline void sum_panels(Ti &tile, int K, const SrcA &a, const SrcB &b,
         sum_panels_staged<E>(tile, K, a, b, lds, tid, wm, wn);
 }
 
+// ---------------------------------------------------------------------------
+// Tile numbering
+// ---------------------------------------------------------------------------
+// Workgroups are dealt to the dies round-robin; renumbered so that each die
+// gets a contiguous range of tiles, whose operands its L2 then shares.
+__device__ inline int die_contiguous(int w, int total, int xcds)
+{
+    const int per = total / xcds, rem = total % xcds, xcd = w % xcds;
+    return xcd * per + (xcd < rem ? xcd : rem) + w / xcds;
+}
+
+// Workgroup w's part of `total` tiles on a device that holds `slots` workgroups
+// at once: whole tiles while they fill rounds of slots; the tiles of a last
+// round that fills at most half (a quarter) of the slots are cut into two (four).
+struct Part {
+    int tile, cut, piece;    // cut: 1, 2 or 4 pieces; tile < 0: nothing to do
+};
+__device__ inline Part part_of(int w, int total, int slots, int xcds)
+{
+    const int whole = total / slots * slots, rest = total - whole;
+    if (w < whole)
+        return Part{die_contiguous(w, whole, xcds), 1, 0};
+    const int cut = 4 * rest <= slots ? 4 : 2 * rest <= slots ? 2 : 1;
+    if (w - whole >= rest * cut)
+        return Part{-1, 1, 0};
+    const int q = die_contiguous(w - whole, rest * cut, xcds);
+    return Part{whole + q / cut, cut, q % cut};
+}
+
 // Rows that the direct loads can address: on 4-byte boundaries, `span` rows of ld
 // elements within 2^31 bytes.
 inline bool dma_rows(int type, const void *p, int64_t ld, int64_t span)

@@ -220,6 +220,35 @@ def test_grouped_and_its_gradients(dev, dtype, pad, T, E, k, K, N):
     assert (full[:, :, N:] == 7.0).all()
 
 
+def close_on_gpu(got, want, size, terms, what):
+    """oracle.product_bound, evaluated where the (large) tensors are."""
+    bound = oracle.product_bound(want, size, terms, got.dtype)
+    bad = ~((got.double() - want).abs() <= bound)
+    assert not bad.any(), f"{what}: {int(bad.sum())} of {bad.numel()} off, first at {torch.nonzero(bad)[0].tolist()}"
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=IDS)
+@pytest.mark.parametrize("T,E,k,K,N", [(1900, 3, 2, 40, 2500), (2000, 2, 2, 24, 4400), (2300, 4, 2, 72, 4400), (520, 2, 1, 700, 600)])
+def test_grouped_large_tiles_whole_and_cut(dev, dtype, T, E, k, K, N):
+    """Enough tiles for the large kinds: whole rounds, and a last round cut into two and four."""
+    g = seeded("large", T, E, k, K, N)
+    offsets, order, position = places(g, T, k, E)
+    X, W = normal(g, T, K, dtype=dtype).to(dev), normal(g, E, K, N, dtype=dtype).to(dev)
+    dY = normal(g, T * k, N, dtype=dtype).to(dev)
+    off, ord_ = offsets.to(dev), order.to(dev)
+    say("large tiles", T, E, k, K, N, dtype)
+    Y = gb.grouped_matmul(X, W, off, order=ord_, per_row=k)
+    dX = gb.grouped_grad_x(dY, W, off)
+    dW = gb.grouped_grad_w(X, dY, off, order=ord_, per_row=k)
+    rows = X.double()[torch.div(ord_.long(), k, rounding_mode="floor")]
+    for e in range(E):
+        lo, hi = int(offsets[e]), int(offsets[e + 1])
+        x, w, d = rows[lo:hi], W[e].double(), dY[lo:hi].double()
+        close_on_gpu(Y[lo:hi], torch.mm(x, w), torch.mm(x.abs(), w.abs()), K + 1, "Y")
+        close_on_gpu(dX[lo:hi], torch.mm(d, w.t().contiguous()), torch.mm(d.abs(), w.abs().t().contiguous()), N + 1, "dX")
+        close_on_gpu(dW[e], torch.mm(x.t().contiguous(), d), torch.mm(x.abs().t().contiguous(), d.abs()), hi - lo + 1, "dW")
+
+
 @pytest.mark.parametrize("dtype", TYPES, ids=IDS)
 @pytest.mark.parametrize("K,N", [(64, 136), (77, 61)])
 def test_grouped_without_order_and_rows_out_of_range(dev, dtype, K, N):
@@ -302,7 +331,7 @@ ADAPTERS = [
     # T, K, N, R, n
     (1, 1, 1, 1, 1), (1, 64, 128, 16, 3), (3, 130, 70, 5, 2), (16, 256, 264, 8, 40), (17, 200, 72, 24, 4), (64, 512, 256, 32, 64),
     (130, 96, 136, 33, 3), (300, 128, 200, 64, 5), (20, 64, 64, 200, 2), (50, 1000, 63, 4, 50), (5, 0, 8, 4, 2), (9, 40, 40, 0, 3),
-    (33, 4096, 256, 16, 30),
+    (33, 4096, 256, 16, 30), (515, 64, 200, 8, 4), (780, 130, 72, 40, 5), (560, 72, 330, 130, 2),
 ]
 
 
@@ -345,7 +374,30 @@ def test_adapters(dev, dtype, pad, runs, T, K, N, R, n):
 
 
 @pytest.mark.parametrize("dtype", TYPES, ids=IDS)
-@pytest.mark.parametrize("T", [3, 40, 150])
+@pytest.mark.parametrize("T,N,R,n,run", [(2055, 4160, 8, 3, 700), (2100, 2300, 40, 60, 3), (4100, 4200, 16, 2, 4100)])
+def test_adapters_large_tiles_whole_and_cut(dev, dtype, T, N, R, n, run):
+    """Whole large tiles, cut ones, and the small ones behind them; `run` rows of an adapter side by side."""
+    K = 40
+    g = seeded("large adapters", T, N, R, n)
+    X, W = normal(g, T, K, dtype=dtype).to(dev), normal(g, K, N, dtype=dtype).to(dev)
+    A, B = normal(g, n, K, R, dtype=dtype, scale=K ** -0.5).to(dev), normal(g, n, R, N, dtype=dtype).to(dev)
+    adapter = ((torch.arange(T) // run) % (n + 1) - 1).int()
+    scale = 0.5 + torch.rand(n, generator=g)
+    say("large adapters", T, N, R, n, dtype)
+    got = gb.adapter_matmul(X, W, A, B, adapter.to(dev), scale.to(dev))
+    want, size = torch.mm(X.double(), W.double()), torch.mm(X.double().abs(), W.double().abs())
+    for a in range(n):
+        mine = torch.nonzero(adapter == a).flatten().to(dev)
+        s, x = float(scale[a]), X.double()[mine]
+        want[mine] += s * torch.mm(torch.mm(x, A[a].double()), B[a].double())
+        size[mine] += s * torch.mm(torch.mm(x.abs(), A[a].double().abs()), B[a].double().abs())
+    # U is kept to 2^-16 of its row's largest at least: R terms of that, relative to the magnitudes' sum
+    close_on_gpu(got, want, size * (1 + (0 if dtype == torch.float32 else R * 2.0 ** -16 / (2 * 2.0 ** -23 * (K + 2 * R + 4)))),
+                 K + 2 * R + 4, "Y")
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=IDS)
+@pytest.mark.parametrize("T", [3, 40, 150, 600])
 def test_adapters_infinities_stay_with_their_requests(dev, dtype, T):
     g = seeded("inf adapters", T)
     X, W = normal(g, T, 64, dtype=dtype), normal(g, 64, 72, dtype=dtype)
@@ -362,12 +414,13 @@ def test_adapters_infinities_stay_with_their_requests(dev, dtype, T):
 
 
 @pytest.mark.parametrize("factor", [2.0 ** -30, 2.0 ** 14])
-def test_adapters_half_precision_range(dev, factor):
+@pytest.mark.parametrize("T", [20, 600])
+def test_adapters_half_precision_range(dev, T, factor):
     """The low-rank intermediate may lie outside the 16-bit type's range."""
     g = seeded("range")
-    X, W = normal(g, 20, 64, dtype=torch.float16, scale=2.0 ** -3), normal(g, 64, 40, dtype=torch.float16)
+    X, W = normal(g, T, 64, dtype=torch.float16, scale=2.0 ** -3), normal(g, 64, 40, dtype=torch.float16)
     A, B = normal(g, 2, 64, 8, dtype=torch.float16), normal(g, 2, 8, 40, dtype=torch.float16, scale=2.0 ** -8)
-    adapter = (torch.arange(20) % 2).int()
+    adapter = (torch.arange(T) % 2).int()
     scale = torch.tensor([factor, factor])
     say("half range", factor)
     W *= 0

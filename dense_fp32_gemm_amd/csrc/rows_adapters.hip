@@ -423,7 +423,9 @@ template <class E, bool DMA>
 __global__ __launch_bounds__(Big<E>::kThreads, 2) void adapters_kernel(AdapterArgs g)
 {
     constexpr int B = Big<E>::B, WM = Big<E>::WM, WN = Big<E>::WN;
-    __shared__ __attribute__((aligned(16))) typename E::T lds[2 * 2 * B * panel_deep<E>()];
+    // two panels of the whole tile, three of a half, four of a quarter
+    constexpr int kHalf = E::kBytes == 2 ? 3 : 2, kQuarter = E::kBytes == 2 ? 4 : 2;
+    __shared__ __attribute__((aligned(16))) typename E::T lds[(kHalf == 3 ? 9 : 8) * (B / 2) * panel_deep<E>()];
     const int small = (g.tiles_m - g.big_m) * g.tiles_n;
     if ((int)blockIdx.x < small) {
         const int tm = blockIdx.x % (g.tiles_m - g.big_m), tn = blockIdx.x / (g.tiles_m - g.big_m);
@@ -437,9 +439,9 @@ __global__ __launch_bounds__(Big<E>::kThreads, 2) void adapters_kernel(AdapterAr
     if (part.cut == 1)
         adapters_tile<E, B, B, WM, WN, 2, DMA>(g, m0, n0, lds);
     else if (part.cut == 2)
-        adapters_tile<E, B / 2, B, WM, WN, 2, DMA>(g, m0 + part.piece * (B / 2), n0, lds);
+        adapters_tile<E, B / 2, B, WM, WN, kHalf, DMA>(g, m0 + part.piece * (B / 2), n0, lds);
     else
-        adapters_tile<E, B / 2, B / 2, WM, WN, 2, DMA>(g, m0 + part.piece % 2 * (B / 2), n0 + part.piece / 2 * (B / 2), lds);
+        adapters_tile<E, B / 2, B / 2, WM, WN, kQuarter, DMA>(g, m0 + part.piece % 2 * (B / 2), n0 + part.piece / 2 * (B / 2), lds);
 }
 
 // ---------------------------------------------------------------------------

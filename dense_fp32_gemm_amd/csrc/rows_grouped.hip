@@ -164,7 +164,9 @@ template <class E, Op OP, int BM, int BN, int WM, int WN, int CH, int S, bool CU
 __global__ __launch_bounds__(WM *WN *kWave, CH == 4 ? 4 : 2) void grouped_kernel(GroupedArgs g)
 {
     constexpr int kPanel = (BM + BN) * CH * E::kChunk;
-    __shared__ __attribute__((aligned(16))) typename E::T lds[(DMA ? S : 2) * kPanel];
+    // (S = 2) two panels of the whole tile, three of a half, four of a quarter
+    __shared__ __attribute__((aligned(16))) typename E::T lds[CUT && DMA ? 9 * kPanel / 4 : (DMA ? S : 2) * kPanel];
+    static_assert(!CUT || (S == 2 && BM == BN), "panels of cut tiles");
     __shared__ uint32_t ahead[OP == kGradW && DMA ? 1024 : 1];
     const int tiles_m = OP == kGradW ? (g.M + BM - 1) / BM : 0;
     // Rising offsets never have more tiles than the grid has; others are cut there.
@@ -193,10 +195,10 @@ __global__ __launch_bounds__(WM *WN *kWave, CH == 4 ? 4 : 2) void grouped_kernel
         grouped_tile<E, OP, BM, BN, WM, WN, CH, S, DMA>(g, p.group, p.lo, p.hi, m0, m_end, n0, lds, ahead);
     if constexpr (CUT) {
         if (part.cut == 2)
-            grouped_tile<E, OP, BM / 2, BN, WM, WN, CH, S, DMA>(g, p.group, p.lo, p.hi, m0 + part.piece * (BM / 2), m_end,
+            grouped_tile<E, OP, BM / 2, BN, WM, WN, CH, 3, DMA>(g, p.group, p.lo, p.hi, m0 + part.piece * (BM / 2), m_end,
                                                                n0, lds, ahead);
         else if (part.cut == 4)
-            grouped_tile<E, OP, BM / 2, BN / 2, WM, WN, CH, S, DMA>(g, p.group, p.lo, p.hi,
+            grouped_tile<E, OP, BM / 2, BN / 2, WM, WN, CH, 4, DMA>(g, p.group, p.lo, p.hi,
                                                                    m0 + part.piece % 2 * (BM / 2), m_end,
                                                                    n0 + part.piece / 2 * (BN / 2), lds, ahead);
     }

@@ -42,8 +42,7 @@ struct AdapterArgs {
     int pitch;
     int depth;               // of factor's rows
     int tiles_m, tiles_n;
-    int big_m;               // many rows: rows of tiles of the large kind, the rest are small ones
-    int slots_big;           // workgroups of them the device holds at once
+    int slots_big;           // many rows: workgroups the device holds at once
     int xcds;
     bool vector_y;           // Y's rows take stores of four elements
 };
@@ -71,29 +70,23 @@ struct UpRows : Across<E, RN, NT> {
     __device__ inline int64_t step() const { return kPanelRanks * this->ld; }
     __device__ inline bool partial(int k0) const { return (k0 / Base::kDeep + 1) * kPanelRanks > R; }
     __device__ inline int left(int i, int k0) const { return rank(i, k0) < R ? Base::left(i, k0) : 0; }
+    __device__ inline int inside(int i, int k0) const { return left(i, k0); }
     __device__ inline int64_t offset(int i, int) const
     {
         return this->krow(i) % kPanelRanks * this->ld + (int64_t)this->col(i) * E::kBytes;
     }
 };
 
-// Calls f(a) for each adapter a among a tile's rows, from the highest number down.
-// which[q]: the adapter of row 64 * q + lane, -1: none.  The same in every wave.
-template <int WORDS, class Fn>
-__device__ inline void each_adapter(const int (&which)[WORDS], Fn &&f)
+// The highest adapter number under `above` among a tile's rows, -1 if there is
+// none.  which[q]: the adapter of row 64 * q + lane, -1: none.  The same in every lane and wave.
+template <int WORDS>
+__device__ inline int next_adapter(const int (&which)[WORDS], int above)
 {
-    int above = INT32_MAX;                           // adapters from here on are done
-    for (;;) {
-        uint32_t best = 0;                           // number + 1
+    uint32_t best = 0;                               // number + 1
 #pragma unroll
-        for (int q = 0; q < WORDS; ++q)
-            best = max(best, which[q] < above ? (uint32_t)(which[q] + 1) : 0u);
-        best = wave_max(best);
-        if (best == 0)
-            return;
-        above = (int)best - 1;
-        f(above);
-    }
+    for (int q = 0; q < WORDS; ++q)
+        best = max(best, which[q] < above ? (uint32_t)(which[q] + 1) : 0u);
+    return (int)wave_max(best) - 1;
 }
 
 __device__ inline int adapter_of(const AdapterArgs &g, int64_t t, bool there)
@@ -104,11 +97,11 @@ __device__ inline int adapter_of(const AdapterArgs &g, int64_t t, bool there)
 
 // ---------------------------------------------------------------------------
 // Down-projection.  One wave: 16 rows, one part of K, RN ranks, and every
-// slots-th adapter among the rows.  RN is 16 or 64 (more ranks: further waves).
+// slots-th adapter among the rows.  RN is 16, 32 or 64 (more ranks: further waves).
 // ---------------------------------------------------------------------------
 constexpr int kDownWaves = 4;
 template <int RN>
-constexpr int down_stages() { return RN == 16 ? 4 : 2; }
+constexpr int down_stages() { return RN == 16 ? 4 : RN == 32 ? 3 : 2; }
 template <class E, int RN>
 constexpr int down_lds() { return down_stages<RN>() * (16 + RN) * panel_deep<E>(); }   // elements of a wave
 
@@ -127,14 +120,15 @@ __device__ inline void down_item(const AdapterArgs &g, int64_t item, typename E:
     const int k0 = split * g.split_ku, K = min(g.split_ku, g.K - k0);
     const int which[1] = {adapter_of(g, t0 + lane, lane < 16 && t0 + lane < g.T)};
     int nth = 0;
-    each_adapter(which, [&](int a) {
-        const uint64_t members = __ballot(which[0] == a);
+    for (int a = next_adapter(which, INT32_MAX); a >= 0; a = next_adapter(which, a)) {
         if (nth++ % g.slots != slot)
-            return;
+            continue;
+        const uint64_t members = __ballot(which[0] == a);
         Ti tile;
         tile.clear();
-        const Along<E, 16, kWave> x((const T *)g.X + t0 * g.ldx + k0, lane, K,
-                                    [&](int, int r) { return members >> r & 1 ? r * g.ldx * E::kBytes : -1; });
+        // Rows of other adapters come along; their sums are not stored.
+        const Along<E, 16, kWave> x((const T *)g.X + t0 * g.ldx + k0, lane, K, g.ldx, g.T - t0,
+                                    [&](int, int r) { return t0 + r < g.T ? r * g.ldx * E::kBytes : -1; });
         const Across<E, RN, kWave> w((const T *)g.A + a * g.stride_a + k0 * g.lda, lane, K, g.lda, rank0, g.R);
         group_sync<kWave>();
         sum_panels<E, DMA, down_stages<RN>()>(tile, K, x, w, lds, lane, 0, 0);
@@ -147,7 +141,7 @@ __device__ inline void down_item(const AdapterArgs &g, int64_t item, typename E:
                         u[i] = v[i];
             }
         });
-    });
+    }
 }
 
 template <class E, int RN, bool DMA>
@@ -184,7 +178,7 @@ __global__ __launch_bounds__(kDownWaves *kWave) void step_kernel(AdapterArgs g)
     const int m0 = tm * BM, k0 = split * g.split_k, K = min(g.split_k, g.K - k0);
     Ti tile;
     tile.clear();
-    const Along<E, BM, NT> x((const T *)g.X + m0 * g.ldx + k0, tid, K,
+    const Along<E, BM, NT> x((const T *)g.X + m0 * g.ldx + k0, tid, K, g.ldx, g.T - m0,
                              [&](int, int r) { return m0 + r < g.T ? r * g.ldx * E::kBytes : -1; });
     const Across<E, kStepBN, NT> w((const T *)g.W + k0 * g.ldw, tid, K, g.ldw, n0, g.N);
     sum_panels<E, DMA, kStepStages>(tile, K, x, w, lds, tid, wm, wn);
@@ -339,61 +333,65 @@ __device__ inline void adapters_tile(const AdapterArgs &g, int m0, int n0, typen
     Ti tile;
     tile.clear();
     {
-        const Along<E, BM, NT> x((const T *)g.X + m0 * g.ldx, tid, g.K,
+        const Along<E, BM, NT> x((const T *)g.X + m0 * g.ldx, tid, g.K, g.ldx, g.T - m0,
                                  [&](int, int r) { return m0 + r < g.T ? r * g.ldx * E::kBytes : -1; });
         const Across<E, BN, NT> w((const T *)g.W, tid, g.K, g.ldw, n0, g.N);
         sum_panels<E, DMA, S>(tile, g.K, x, w, lds, tid, wm, wn);
     }
     if (g.R > 0) {
-        using SrcU = Along<E, BM, NT>;
         constexpr int kWords = (BM + kWave - 1) / kWave;
-        // The adapters of the tile's rows; of the rows this thread loads; of those it adds to.
-        int which[kWords], loads[SrcU::kCount], adds[Ti::kFm];
+        int which[kWords], adds[Ti::kFm];            // adapters of the tile's rows; of those this lane adds to
+        float unscale[Ti::kFm];
 #pragma unroll
         for (int q = 0; q < kWords; ++q)
             which[q] = adapter_of(g, m0 + q * kWave + lane, q * kWave + lane < BM && m0 + q * kWave + lane < g.T);
 #pragma unroll
-        for (int i = 0; i < SrcU::kCount; ++i) {
-            const int r = SrcU::row_of(i, tid);
-            loads[i] = adapter_of(g, m0 + r, r < BM && m0 + r < g.T);
-        }
-#pragma unroll
         for (int m = 0; m < Ti::kFm; ++m) {
             const int r = wm * (BM / WM) + Ti::Fa::row_of(m, lane % 16);
             adds[m] = adapter_of(g, m0 + r, m0 + r < g.T);
+            unscale[m] = E::kBytes == 2 && adds[m] >= 0 ? g.unscale[m0 + r] : 1.f;
         }
-        each_adapter(which, [&](int a) {
-            const SrcU u((const T *)g.factor + (int64_t)m0 * g.depth, tid, g.depth,
-                         [&](int i, int r) { return loads[i] == a ? (int64_t)r * g.depth * E::kBytes : -1; });
+        // Every row's U, whichever adapter made it (rows without one hold anything):
+        // a row of sums is taken only with its own adapter's B.
+        const Along<E, BM, NT> u((const T *)g.factor + (int64_t)m0 * g.depth, tid, g.depth, g.depth, g.T - m0,
+                                 [&](int, int r) { return m0 + r < g.T ? (int64_t)r * g.depth * E::kBytes : -1; });
+        for (int k0 = 0; k0 < g.depth; k0 += Ti::kDeep)
+        for (int a = next_adapter(which, INT32_MAX); a >= 0; a = next_adapter(which, a)) {
             const UpRows<E, BN, NT> b((const T *)g.B + a * g.stride_b, tid, g.depth, g.ldb, n0, g.N, g.R);
-            // Step by step, each step's sums of one 16-row block at a time: a second
-            // set of sums for the whole tile would halve the waves a SIMD holds.
-            for (int k0 = 0; k0 < g.depth; k0 += Ti::kDeep) {
-                __syncthreads();
-                load_panel<E, DMA, NT>(u, k0, lds, tid);
-                load_panel<E, DMA, NT>(b, k0, lds + Ti::kLdsA, tid);
-                asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
-                __syncthreads();
+            __syncthreads();
+            load_panel<E, DMA, NT>(u, k0, lds, tid);
+            load_panel<E, DMA, NT>(b, k0, lds + Ti::kLdsA, tid);
+            asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+            __syncthreads();
+            // The sums of one 16-row block at a time: a second set for the whole
+            // tile would halve the waves a SIMD holds.
+            typename Ti::Fb fb[Ti::kSteps];
 #pragma unroll
-                for (int step = 0; step < Ti::kSteps; ++step) {
-                    typename Ti::Step p;
-                    p.read(lds, step, wm, wn, lane);
+            for (int step = 0; step < Ti::kSteps; ++step)
+                fb[step].read(lds + Ti::kLdsA, wn * (BN / WN), step, lane);
 #pragma unroll
-                    for (int m = 0; m < Ti::kFm; ++m) {
-                        const int r = wm * (BM / WM) + Ti::Fa::row_of(m, lane % 16);
-                        const bool mine = adds[m] == a;
-                        const float f = E::kBytes == 4 || !mine ? 1.f : g.unscale[m0 + r];
+            for (int m = 0; m < Ti::kFm; ++m) {
+                Fragments<E, true, BM, Ti::CH, 1> fa[Ti::kSteps];
 #pragma unroll
-                        for (int n = 0; n < Ti::kFn; ++n) {
-                            const f32x4 add = mfma_step<E>(p.b.q[n], p.a.q[m], f32x4{0.f, 0.f, 0.f, 0.f});
+                for (int step = 0; step < Ti::kSteps; ++step)
+                    fa[step].read(lds, wm * (BM / WM) + 16 * m, step, lane);
+                f32x4 add[Ti::kFn];
 #pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                tile.acc[m][n][i] = mine ? fmaf(f, add[i], tile.acc[m][n][i]) : tile.acc[m][n][i];
-                        }
-                    }
+                for (int n = 0; n < Ti::kFn; ++n) {
+                    add[n] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int step = 0; step < Ti::kSteps; ++step)
+                        add[n] = mfma_step<E>(fb[step].q[n], fa[step].q[0], add[n]);
                 }
+                const bool mine = adds[m] == a;
+#pragma unroll
+                for (int n = 0; n < Ti::kFn; ++n)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)      // in place, nothing of the others' rows
+                        tile.acc[m][n][i] = fmaf(unscale[m], mine ? add[n][i] : 0.f, tile.acc[m][n][i]);
+                __builtin_amdgcn_sched_barrier(0);   // one block's sums at a time in registers
             }
-        });
+        }
     }
     T *Y = (T *)g.Y;
     auto store = [&](auto vec) {
@@ -409,39 +407,40 @@ __device__ inline void adapters_tile(const AdapterArgs &g, int m0, int n0, typen
         store(std::false_type{});
 }
 
-// The tiles of many rows.  16-bit types: 256 x 256, one workgroup a compute unit, the
-// panels' rate from L2 being what bounds them; binary32, bound by the matrix
-// cores: 128 x 128, two.
-template <class E>
+// The tiles of many rows.  16-bit types: BM x 256 (see many_rows()), one workgroup
+// a compute unit; 256 x 256 tiles cut the last round.  binary32, bound by the matrix
+// cores: 64 x 64.
+template <class E, int BM>
 struct Big {
-    static constexpr int B = E::kBytes == 2 ? 256 : 128, WM = 2, WN = E::kBytes == 2 ? 4 : 2;
-    static constexpr int kThreads = WM * WN * kWave, kPerCu = E::kBytes == 2 ? 1 : 2;
+    static constexpr int BN = E::kBytes == 2 ? 256 : 64, WM = 2, WN = E::kBytes == 2 ? 4 : 2;
+    static constexpr int kThreads = WM * WN * kWave;
+    static constexpr bool kCut = BM == 256;
+    static constexpr int S = BM == 128 || BM == 160 ? 3 : 2;                 // panels in LDS
+    static constexpr int kLds = (kCut ? 9 * 128 : S * (BM + BN)) * panel_deep<E>();   // cut: three of a half, four of a quarter
 };
 
-// big_m rows of large tiles, the last round of them cut; then tiles of 16 rows.
-template <class E, bool DMA>
-__global__ __launch_bounds__(Big<E>::kThreads, 2) void adapters_kernel(AdapterArgs g)
+template <class E, int BM, bool DMA>
+__global__ __launch_bounds__((Big<E, BM>::kThreads), 2) void adapters_kernel(AdapterArgs g)
 {
-    constexpr int B = Big<E>::B, WM = Big<E>::WM, WN = Big<E>::WN;
-    // two panels of the whole tile, three of a half, four of a quarter
-    constexpr int kHalf = E::kBytes == 2 ? 3 : 2, kQuarter = E::kBytes == 2 ? 4 : 2;
-    __shared__ __attribute__((aligned(16))) typename E::T lds[(kHalf == 3 ? 9 : 8) * (B / 2) * panel_deep<E>()];
-    const int small = (g.tiles_m - g.big_m) * g.tiles_n;
-    if ((int)blockIdx.x < small) {
-        const int tm = blockIdx.x % (g.tiles_m - g.big_m), tn = blockIdx.x / (g.tiles_m - g.big_m);
-        adapters_tile<E, 16, B, 1, WM * WN, 2, DMA>(g, g.big_m * B + tm * 16, tn * B, lds);
-        return;
+    using B = Big<E, BM>;
+    __shared__ __attribute__((aligned(16))) typename E::T lds[B::kLds];
+    const int total = g.tiles_m * g.tiles_n;
+    if constexpr (!B::kCut) {
+        const int t = die_contiguous(blockIdx.x, total, g.xcds);
+        adapters_tile<E, BM, B::BN, B::WM, B::WN, B::S, DMA>(g, t % g.tiles_m * BM, t / g.tiles_m * B::BN, lds);
+    } else {
+        constexpr int H = BM / 2, BN = B::BN;
+        const Part part = part_of(blockIdx.x, total, g.slots_big, g.xcds);
+        if (part.tile < 0)
+            return;
+        const int m0 = part.tile % g.tiles_m * BM, n0 = part.tile / g.tiles_m * BN;
+        if (part.cut == 1)
+            adapters_tile<E, BM, BN, B::WM, B::WN, 2, DMA>(g, m0, n0, lds);
+        else if (part.cut == 2)
+            adapters_tile<E, H, BN, B::WM, B::WN, 3, DMA>(g, m0 + part.piece * H, n0, lds);
+        else
+            adapters_tile<E, H, BN / 2, B::WM, B::WN, 4, DMA>(g, m0 + part.piece % 2 * H, n0 + part.piece / 2 * (BN / 2), lds);
     }
-    const Part part = part_of(blockIdx.x - small, g.big_m * g.tiles_n, g.slots_big, g.xcds);
-    if (part.tile < 0)
-        return;
-    const int m0 = part.tile % g.big_m * B, n0 = part.tile / g.big_m * B;
-    if (part.cut == 1)
-        adapters_tile<E, B, B, WM, WN, 2, DMA>(g, m0, n0, lds);
-    else if (part.cut == 2)
-        adapters_tile<E, B / 2, B, WM, WN, kHalf, DMA>(g, m0 + part.piece * (B / 2), n0, lds);
-    else
-        adapters_tile<E, B / 2, B / 2, WM, WN, kQuarter, DMA>(g, m0 + part.piece % 2 * (B / 2), n0 + part.piece / 2 * (B / 2), lds);
 }
 
 // ---------------------------------------------------------------------------
@@ -477,11 +476,11 @@ Split plan(int T, int N, int K, int R)
     const int panel = panel_deep<E>();
     const int64_t panels = ceil_div(K, panel), rows16 = ceil_div(T, 16);
     p.few = ceil_div(T, 128) * ceil_div(N, 128) < 128 && T <= 512;
-    p.rank_block = R <= 16 ? 16 : 64;
+    p.rank_block = R <= 16 ? 16 : R <= 32 && !p.few ? 32 : 64;
     p.ranks = (int)ceil_div(R, p.rank_block);
     if (R > 0) {
         // about a thousand waves: up to 16 for the adapters of a row tile when rows are few
-        p.slots = p.few ? (T < 16 ? T : 16) : 2;
+        p.slots = p.few ? (T < 16 ? T : 16) : 1;
         cut(panels, 1024 / (rows16 * p.slots * p.ranks), 4, panel, &p.splits_u, &p.split_ku);
     }
     if (p.few) {
@@ -541,23 +540,45 @@ int run_few(AdapterArgs g, bool low, bool dma, hipStream_t stream)
     return launched();
 }
 
-template <class E, int RN>
-int run_many(AdapterArgs g, bool low, bool dma, bool dma_down, hipStream_t stream)
+template <class E, int BM>
+int launch_many(AdapterArgs g, bool dma, hipStream_t stream)
 {
-    // Up to 32 rows behind the last whole tile: tiles of 16 rows.
-    constexpr int B = Big<E>::B;
-    g.big_m = g.T / B;
-    const int rest = g.T - g.big_m * B;
-    if (rest > 32)
-        ++g.big_m;
-    const int64_t tm = g.big_m + (rest > 32 ? 0 : ceil_div(rest, 16)), tn = ceil_div(g.N, B);
-    g.slots_big = (int)gemm_f32_internal::current_device().cus * Big<E>::kPerCu;
+    using B = Big<E, BM>;
+    const int64_t tm = ceil_div(g.T, BM), tn = ceil_div(g.N, B::BN);
+    g.slots_big = (int)gemm_f32_internal::current_device().cus;
     // cutting the last round adds at most three pieces for a quarter of the slots
-    const int64_t grid = tm * tn + g.slots_big;
-    if (grid > (int64_t)UINT32_MAX / Big<E>::kThreads)
+    const int64_t grid = tm * tn + (B::kCut ? g.slots_big : 0);
+    if (grid > (int64_t)UINT32_MAX / B::kThreads)
         return GEMM_F32_ERR_DIM;
     g.tiles_m = (int)tm;
     g.tiles_n = (int)tn;
+    if (dma)
+        adapters_kernel<E, BM, true><<<(unsigned)grid, B::kThreads, 0, stream>>>(g);
+    else
+        adapters_kernel<E, BM, false><<<(unsigned)grid, B::kThreads, 0, stream>>>(g);
+    return launched();
+}
+
+// The tile: its panels' rate from L2 bounds a compute unit, so the cost of a round is BM +
+// 256; the lowest tiles that fit one round, else 256 x 256.
+template <class E>
+int many_rows(const AdapterArgs &g, bool dma, hipStream_t stream)
+{
+    if constexpr (E::kBytes == 4) {
+        return launch_many<E, 64>(g, dma, stream);
+    } else {
+        const int64_t cus = gemm_f32_internal::current_device().cus, tn = ceil_div(g.N, 256);
+        if (ceil_div(g.T, 128) * tn <= cus)
+            return launch_many<E, 128>(g, dma, stream);
+        if (ceil_div(g.T, 160) * tn <= cus)
+            return launch_many<E, 160>(g, dma, stream);
+        return launch_many<E, 256>(g, dma, stream);
+    }
+}
+
+template <class E, int RN>
+int run_many(const AdapterArgs &g, bool low, bool dma, bool dma_down, hipStream_t stream)
+{
     if (low) {
         const int64_t blocks = down_blocks<E, RN>(g);
         if (dma_down)
@@ -566,11 +587,7 @@ int run_many(AdapterArgs g, bool low, bool dma, bool dma_down, hipStream_t strea
             down_kernel<E, RN, false><<<(unsigned)blocks, kDownWaves * kWave, 0, stream>>>(g);
         factor_kernel<E><<<(unsigned)ceil_div(g.T, kFactorThreads / kWave), kFactorThreads, 0, stream>>>(g);
     }
-    if (dma)
-        adapters_kernel<E, true><<<(unsigned)grid, Big<E>::kThreads, 0, stream>>>(g);
-    else
-        adapters_kernel<E, false><<<(unsigned)grid, Big<E>::kThreads, 0, stream>>>(g);
-    return launched();
+    return many_rows<E>(g, dma, stream);
 }
 
 }  // namespace
@@ -641,6 +658,8 @@ int gemm_f32_adapters(int type, int T, int N, int K, int R, int n, const void *X
             rc = run_few<E, 16>(g, low, dma_x && dma_w && dma_a, stream);
         else if (p.few)
             rc = run_few<E, 64>(g, low, dma_x && dma_w && dma_a, stream);
+        else if (p.rank_block == 32)
+            rc = run_many<E, 32>(g, low, dma_x && dma_w && dma_b, dma_x && dma_a, stream);
         else if (p.rank_block == 16)
             rc = run_many<E, 16>(g, low, dma_x && dma_w && dma_b, dma_x && dma_a, stream);
         else

@@ -127,14 +127,14 @@ __device__ inline void grouped_tile(const GroupedArgs &g, int group, int lo, int
             for (int i = 0; i < Src::kCount; ++i)
                 row[i] = m0 + Src::row_of(i, tid);
         }
-        const Src a(A, tid, g.K,
+        const Src a(A, tid, g.K, g.lda, g.rows,
                     [&](int i, int r) { return m0 + r < m_end && row[i] < g.rows ? row[i] * g.lda * E::kBytes : -1; });
         const Across<E, BN, NT, CH> b(B + group * g.stride, tid, g.K, g.ldb, n0, g.N);
         sum_panels<E, DMA, S>(tile, g.K, a, b, lds, tid, wm, wn);
     } else if constexpr (OP == kGradX) {
-        const Along<E, BM, NT, CH> a(A + m0 * g.lda, tid, g.K,
+        const Along<E, BM, NT, CH> a(A + m0 * g.lda, tid, g.K, g.lda, g.P - m0,
                                  [&](int, int r) { return m0 + r < m_end ? r * g.lda * E::kBytes : -1; });
-        const Along<E, BN, NT, CH> b(B + group * g.stride + n0 * g.ldb, tid, g.K,
+        const Along<E, BN, NT, CH> b(B + group * g.stride + n0 * g.ldb, tid, g.K, g.ldb, g.N - n0,
                                  [&](int, int r) { return n0 + r < g.N ? r * g.ldb * E::kBytes : -1; });
         sum_panels<E, DMA, S>(tile, g.K, a, b, lds, tid, wm, wn);
     } else {

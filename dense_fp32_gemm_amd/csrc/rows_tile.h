@@ -151,7 +151,8 @@ struct Tile {
     using Fa = Fragments<E, A_ALONG, BM, CH, kFm>;
     using Fb = Fragments<E, B_ALONG, BN, CH, kFn>;
     static_assert(BM % (16 * WM) == 0 && BN % (16 * WN) == 0, "wave tile");
-    static_assert((BM & (BM - 1)) == 0 && (BN & (BN - 1)) == 0, "the chunk permutations are made for powers of two");
+    static_assert((A_ALONG || (BM & (BM - 1)) == 0) && (B_ALONG || (BN & (BN - 1)) == 0),
+                  "the chunk permutations across rows are made for powers of two");
 
     f32x4 acc[kFm][kFn];
 
@@ -251,6 +252,14 @@ __device__ inline const char *uniform(const void *p)
     return (const char *)((uint64_t)hi << 32 | lo);
 }
 
+// Bytes from a panel's base, `done` bytes into an operand of `bytes` bytes, to its
+// end in whole dwords, as a buffer's size: loads past it give zeros.
+__device__ inline uint32_t bytes_left(int64_t bytes, int64_t done)
+{
+    const int64_t n = (bytes + 3) / 4 * 4 - done;
+    return (uint32_t)(n < 0 ? 0 : n < (int64_t)kNowhere ? n : (int64_t)kNowhere);
+}
+
 // Operand rows contiguous in the summed index.  row(i, r): byte offset from base of the
 // panel's row r (of chunk i), negative if there is none; rows are K elements long.
 template <class E, int RN, int NT, int CH = 8>
@@ -260,34 +269,45 @@ struct Along {
     static constexpr int kSlots = RN * CH, kDeep = CH * E::kChunk, kCount = (kSlots + NT - 1) / NT;
     const char *base;
     int64_t off[kCount];
-    int k[kCount], K, tid;                           // k: the chunk's first in panel 0
+    int64_t ld;                                      // bytes between rows
+    int K, tid, rows;                                // rows: from base on
 
-    static constexpr bool kGuardTail = true;
-    __device__ inline uint32_t extent(int64_t) const { return kNowhere; }
+    static constexpr bool kAlong = true;
+    // Bytes from the panel's base to the operand's end: the last chunk of a row that is no whole
+    // number of chunks long reads what follows (and is cleared in LDS), zeros past the end.
+    __device__ inline uint32_t extent(int64_t done) const { return bytes_left((rows - 1) * ld + (int64_t)K * E::kBytes, done); }
     // Panel row of chunk i.
     static __device__ inline int row_of(int i, int tid) { return (tid + i * NT) / CH; }
 
     template <class Row>
-    __device__ inline Along(const T *base_, int tid, int K_, Row &&row) : base(uniform(base_)), K(__builtin_amdgcn_readfirstlane(K_)), tid(tid)
+    __device__ inline Along(const T *base_, int tid_, int K_, int64_t ld_, int rows_, Row &&row)
+        : base(uniform(base_)), ld(ld_ * E::kBytes), K(__builtin_amdgcn_readfirstlane(K_)), tid(tid_), rows(rows_)
     {
 #pragma unroll
         for (int i = 0; i < kCount; ++i) {
             const int slot = tid + i * NT, r = slot / CH;
-            k[i] = (slot % CH ^ swz_along<CH>(r)) * E::kChunk;
             const int64_t o = kSlots % NT == 0 || slot < kSlots ? row(i, r) : -1;
-            off[i] = o < 0 ? -1 : o + k[i] * E::kBytes;
+            off[i] = o < 0 ? -1 : o + first_k(i) * E::kBytes;
         }
     }
     __device__ inline int64_t step() const { return kDeep * E::kBytes; }   // bytes from panel to panel
     // Whether chunks that panel 0 has may be missing from the panel at k0.
     __device__ inline bool partial(int k0) const { return K - k0 < kDeep; }
-    // Elements from chunk i of the panel at k0 to its row's end (none: zeros), and its offset.
-    __device__ inline int left(int i, int k0) const { return off[i] < 0 ? 0 : K - k0 - k[i]; }
+    // First k of chunk i in panel 0.  (Recomputed where it is needed: registers are short.)
+    __device__ inline int first_k(int i) const
+    {
+        const int slot = tid + i * NT;
+        return (slot % CH ^ swz_along<CH>(slot / CH)) * E::kChunk;
+    }
+    // Elements from chunk i of the panel at k0 to its row's end (none: zeros), and its
+    // offset; inside() for a row that is there.
+    __device__ inline int inside(int i, int k0) const { return K - k0 - first_k(i); }
+    __device__ inline int left(int i, int k0) const { return off[i] < 0 ? 0 : inside(i, k0); }
     __device__ inline int64_t offset(int i, int) const { return off[i]; }
 };
 
-// Operand rows contiguous across the summed index: row(k) is the byte offset of k row k
-// from panel to panel step_ bytes further, columns first .. of cols.
+// Operand rows contiguous across the summed index: K of them, ld elements apart, columns
+// first .. of cols.
 template <class E, int RN, int NT, int CH = 8>
 struct Across {
     using T = typename E::T;
@@ -308,15 +328,11 @@ struct Across {
         : Across(base_, tid_, K_, ld_, first_, cols_, K_)
     {
     }
-    static constexpr bool kGuardTail = false;
+    static constexpr bool kAlong = false;
     // Bytes from the panel's base to the operand's end: a chunk that crosses the last
     // row's end reads zeros there (one that crosses another row's end reads the
     // next row's start, for columns that are not stored).  Whole dwords.
-    __device__ inline uint32_t extent(int64_t done) const
-    {
-        const int64_t n = ((rows - 1) * ld + (int64_t)cols * E::kBytes + 3) / 4 * 4 - done;
-        return (uint32_t)(n < (int64_t)kNowhere ? n : (int64_t)kNowhere);
-    }
+    __device__ inline uint32_t extent(int64_t done) const { return bytes_left((rows - 1) * ld + (int64_t)cols * E::kBytes, done); }
     __device__ inline int krow(int i) const { return (tid + i * NT) / kPer; }
     __device__ inline int col(int i) const
     {
@@ -331,6 +347,7 @@ struct Across {
     {
         return (kSlots % NT == 0 || tid + i * NT < kSlots) && k0 + krow(i) < K ? cols - col(i) : 0;
     }
+    __device__ inline int inside(int i, int k0) const { return left(i, k0); }
     __device__ inline int64_t offset(int i, int) const { return krow(i) * ld + (int64_t)col(i) * E::kBytes; }
 };
 
@@ -472,20 +489,10 @@ struct PanelLoads {
 #pragma unroll
             for (int i = 0; i < Src::kCount; ++i)
                 load(i, off[i]);
-        } else if (!Src::kGuardTail || src.K % E::kChunk == 0) {
+        } else {
 #pragma unroll
             for (int i = 0; i < Src::kCount; ++i)
-                load(i, src.left(i, k0) > 0 ? off[i] : kNowhere);
-        } else {
-            // The last chunk of a row that is no whole number of chunks long:
-            // element by element, what lies behind the row must not be summed.
-#pragma unroll
-            for (int i = 0; i < Src::kCount; ++i) {
-                const int slot = src.tid + i * NT, n = src.left(i, k0);
-                if (Src::kSlots % NT == 0 || slot < Src::kSlots)
-                    *reinterpret_cast<u32x4 *>(panel + slot * E::kChunk) =
-                        load_chunk<E, false>((const T *)(src.base + done + (n > 0 ? src.offset(i, k0) : 0)), n);
-            }
+                load(i, src.inside(i, k0) > 0 ? off[i] : kNowhere);
         }
     }
 };
@@ -510,7 +517,8 @@ struct PanelLoads<E, Gathered<E, RN, NT, CH>, NT> {
     }
 };
 
-// The panel at k0 of one operand into LDS, complete after the wait and barrier that follow.
+// The panel at k0 of one operand (rows a whole number of chunks long, if along) into LDS,
+// complete after the wait and barrier that follow.
 template <class E, bool DMA, int NT, class Src>
 __device__ inline void load_panel(const Src &src, int k0, typename E::T *panel, int tid)
 {
@@ -526,6 +534,24 @@ __device__ inline void load_panel(const Src &src, int k0, typename E::T *panel, 
             if (Src::kSlots % NT == 0 || slot < Src::kSlots)
                 *reinterpret_cast<u32x4 *>(panel + slot * E::kChunk) =
                     load_chunk<E, false>((const T *)(p + (n > 0 ? src.offset(i, k0) : 0)), n);
+        }
+    }
+}
+
+// Zeros over what the last chunk of an "along" operand's rows, K elements long, brought from
+// behind them, in the panel at k0 that they end in (K no whole number of chunks).
+template <class E, class Src, int RN, int CH, int NT>
+__device__ inline void clear_tail(const Src &src, int k0, typename E::T *panel, int tid)
+{
+    if constexpr (Src::kAlong) {
+        const int chunk = (src.K - k0) / E::kChunk, from = src.K % E::kChunk;
+        if (from == 0)
+            return;
+        for (int r = tid; r < RN; r += NT) {
+            typename E::T *p = panel + lds_chunk<E, true, RN, CH>(r, chunk);
+#pragma unroll 1
+            for (int e = from; e < E::kChunk; ++e)
+                p[e] = (typename E::T)0.f;
         }
     }
 }
@@ -579,17 +605,17 @@ __device__ inline void sum_panels_dma(Ti &tile, int K, const SrcA &a, const SrcB
     // waves have fewer, and wait for more than they must).
     constexpr int kLoads = SrcA::kSlots / NT + SrcB::kSlots / NT;
     const int lane = tid % kWave, wave = NT == kWave ? 0 : __builtin_amdgcn_readfirstlane(tid / kWave);
-    if (K <= 0)
-        return;
+    // (An empty sum runs one panel of zeros: a way around the loop would cost a second
+    // set of registers for the sums.)
     const PanelLoads<E, SrcA, NT> pa(a);
     const PanelLoads<E, SrcB, NT> pb(b);
     auto fire = [&](int k0, T *panel) {
         pa.fire(a, k0, panel, wave);
         pb.fire(b, k0, panel + Ti::kLdsA, wave);
     };
-    // The panel at k0 has landed when no more than `after` whole panels behind
-    // it are in flight, and every wave's LDS accesses so far are complete.
-    auto landed = [&](int k0, auto after) {
+    // The panel at k0 (in `panel`) has landed when no more than `after` whole panels
+    // behind it are in flight, and every wave's LDS accesses so far are complete.
+    auto landed = [&](int k0, T *panel, auto after) {
         if (k0 + (decltype(after)::value + 1) * BK <= K)
             asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(decltype(after)::value * kLoads) : "memory");
         else
@@ -597,6 +623,11 @@ __device__ inline void sum_panels_dma(Ti &tile, int K, const SrcA &a, const SrcB
         if constexpr (NT > kWave)
             __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
+        if ((SrcA::kAlong || SrcB::kAlong) && K % E::kChunk != 0 && k0 + BK > K) {
+            clear_tail<E, SrcA, Ti::BM, Ti::CH, NT>(a, k0, panel, tid);
+            clear_tail<E, SrcB, Ti::BN, Ti::CH, NT>(b, k0, panel + Ti::kLdsA, tid);
+            group_sync<NT>();
+        }
     };
     if constexpr (SrcA::kListed) {
         a.refill(0);
@@ -605,13 +636,13 @@ __device__ inline void sum_panels_dma(Ti &tile, int K, const SrcA &a, const SrcB
     if constexpr (Ti::kSteps == 1) {
 #pragma unroll
         for (int q = 0; q < S - 1; ++q)
-            if (q * BK < K)
+            if (q == 0 || q * BK < K)
                 fire(q * BK, lds + q * kPanel);
         int now = 0, next = S - 1;
         for (int k0 = 0; k0 < K; k0 += BK) {
             if constexpr (SrcA::kListed)
                 a.refill(k0 + (S - 1) * BK);
-            landed(k0, std::integral_constant<int, S - 2>{});
+            landed(k0, lds + now * kPanel, std::integral_constant<int, S - 2>{});
             whole_panel<E>(tile, lds + now * kPanel, lds + next * kPanel,
                            [&](T *freed) {
                                if (k0 + (S - 1) * BK < K)
@@ -625,10 +656,10 @@ __device__ inline void sum_panels_dma(Ti &tile, int K, const SrcA &a, const SrcB
     }
 #pragma unroll
     for (int q = 0; q < S; ++q)
-        if (q * BK < K)
+        if (q == 0 || q * BK < K)
             fire(q * BK, lds + q * kPanel);
     typename Ti::Step f0, f1;
-    landed(0, std::integral_constant<int, S - 1>{});
+    landed(0, lds, std::integral_constant<int, S - 1>{});
     f0.read(lds, 0, wm, wn, lane);
     int now = 0;
     for (int k0 = BK; k0 < K; k0 += BK) {            // k0: the panel after this one
@@ -636,8 +667,8 @@ __device__ inline void sum_panels_dma(Ti &tile, int K, const SrcA &a, const SrcB
         half_panel<E>(tile, panel, (T *)nullptr, [](T *) {}, 1, f1, f0, wm, wn, lane);
         if constexpr (SrcA::kListed)
             a.refill(k0 + (S - 1) * BK);
-        landed(k0, std::integral_constant<int, S - 2>{});
         now = now + 1 == S ? 0 : now + 1;
+        landed(k0, lds + now * kPanel, std::integral_constant<int, S - 2>{});
         half_panel<E>(tile, lds + now * kPanel, panel,
                       [&](T *freed) {
                           if (k0 + (S - 1) * BK < K)

@@ -75,6 +75,8 @@ struct UpRows : Across<E, RN, NT> {
     {
         return this->krow(i) % kPanelRanks * this->ld + (int64_t)this->col(i) * E::kBytes;
     }
+    static_assert(kPanelRanks % Base::kRowStep == 0, "a thread's rows wrap together");
+    static __device__ inline int row_step(int i) { return i * Base::kRowStep % kPanelRanks; }
 };
 
 // The highest adapter number under `above` among a tile's rows, -1 if there is

@@ -272,7 +272,7 @@ struct Along {
     int64_t ld;                                      // bytes between rows
     int K, tid, rows;                                // rows: from base on
 
-    static constexpr bool kAlong = true;
+    static constexpr bool kAlong = true, kOneColumn = false;
     // Bytes from the panel's base to the operand's end: the last chunk of a row that is no whole
     // number of chunks long reads what follows (and is cleared in LDS), zeros past the end.
     __device__ inline uint32_t extent(int64_t done) const { return bytes_left((rows - 1) * ld + (int64_t)K * E::kBytes, done); }
@@ -333,14 +333,21 @@ struct Across {
     // row's end reads zeros there (one that crosses another row's end reads the
     // next row's start, for columns that are not stored).  Whole dwords.
     __device__ inline uint32_t extent(int64_t done) const { return bytes_left((rows - 1) * ld + (int64_t)cols * E::kBytes, done); }
-    __device__ inline int krow(int i) const { return (tid + i * NT) / kPer; }
+    // A thread's chunks are kRowStep k rows apart, and mostly in one column: the chunk
+    // permutation depends on k's bits 0, 1 and 3 only.
+    static constexpr int kRowStep = NT / kPer;
+    static constexpr bool kOneColumn = E::kBytes == 4 || RN < 64 || kRowStep % 16 == 0 || kCount == 1;
+    static_assert(NT % kPer == 0, "a thread's chunks keep their place in the k row");
+    __device__ inline int krow(int i) const { return tid / kPer + i * kRowStep; }
     __device__ inline int col(int i) const
     {
-        int c = (tid + i * NT) % kPer;
+        int c = tid % kPer;
         if constexpr (E::kBytes == 2)
-            c ^= swz_across<RN>(krow(i));
+            c ^= swz_across<RN>(krow(kOneColumn ? 0 : i));
         return first + c * E::kChunk;
     }
+    // k rows from chunk 0 to chunk i, as loaded.
+    static __device__ inline int row_step(int i) { return i * kRowStep; }
     __device__ inline int64_t step() const { return kDeep * ld; }
     __device__ inline bool partial(int k0) const { return K - k0 < kDeep; }
     __device__ inline int left(int i, int k0) const
@@ -464,16 +471,30 @@ __device__ inline void sum_panels_staged(Ti &tile, int K, const SrcA &a, const S
 }
 
 // The panel loads of one operand by one wave: lane l's 16 bytes land at the
-// wave's LDS base + 16 * l.
+// wave's LDS base + 16 * l.  Offsets that differ by whole rows are one register.
 template <class E, class Src, int NT>
 struct PanelLoads {
+    static_assert(Src::kSlots % kWave == 0, "whole waves");
     using T = typename E::T;
-    uint32_t off[Src::kCount];
+    static constexpr bool kOne = Src::kOneColumn;
+    uint32_t off[kOne ? 1 : Src::kCount];
     __device__ inline PanelLoads(const Src &src)
     {
+        if constexpr (kOne) {
+            off[0] = src.col(0) < src.cols ? (uint32_t)src.offset(0, 0) : kNowhere;
+        } else {
 #pragma unroll
-        for (int i = 0; i < Src::kCount; ++i)
-            off[i] = src.left(i, 0) > 0 ? (uint32_t)src.offset(i, 0) : kNowhere;
+            for (int i = 0; i < Src::kCount; ++i)
+                off[i] = src.left(i, 0) > 0 ? (uint32_t)src.offset(i, 0) : kNowhere;
+        }
+    }
+    // Past kNowhere, where that is what off[0] is: rows span less than 2^31 bytes.
+    __device__ inline uint32_t at(const Src &src, int i) const
+    {
+        if constexpr (!kOne)
+            return off[i];
+        else
+            return off[0] + (uint32_t)Src::row_step(i) * (uint32_t)src.ld;
     }
     __device__ inline void fire(const Src &src, int k0, T *panel, int wave) const
     {
@@ -488,11 +509,11 @@ struct PanelLoads {
         if (!src.partial(k0)) {
 #pragma unroll
             for (int i = 0; i < Src::kCount; ++i)
-                load(i, off[i]);
+                load(i, at(src, i));
         } else {
 #pragma unroll
             for (int i = 0; i < Src::kCount; ++i)
-                load(i, src.inside(i, k0) > 0 ? off[i] : kNowhere);
+                load(i, src.inside(i, k0) > 0 ? at(src, i) : kNowhere);
         }
     }
 };
@@ -506,11 +527,13 @@ struct PanelLoads<E, Gathered<E, RN, NT, CH>, NT> {
     {
         static_assert(Src::kSlots % NT == 0 && Src::kBlock % Src::kDeep == 0, "whole panels");
         const auto rsrc = __builtin_amdgcn_make_buffer_rsrc((void *)src.base, 0, (int)src.extent(0), kRawBufferFlags);
+        static_assert(Src::kOneColumn, "one column a thread");
+        const int col = src.col(0);
         const uint32_t *block = src.ahead + (k0 / Src::kBlock % 2) * Src::kBlock + k0 % Src::kBlock;
 #pragma unroll
         for (int i = 0; i < Src::kCount; ++i) {
             const uint32_t row = block[src.krow(i)];
-            const uint32_t o = row == kNowhere || src.col(i) >= src.cols ? kNowhere : row + src.col(i) * E::kBytes;
+            const uint32_t o = row == kNowhere || col >= src.cols ? kNowhere : row + col * E::kBytes;
             auto *dst = (lds_ptr<void>)(panel + (i * NT + wave * kWave) * E::kChunk);
             __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, dst, 16, o, 0, 0, 0);
         }
@@ -590,9 +613,12 @@ __device__ __forceinline__ void whole_panel(Ti &tile, const typename E::T *__res
                                             Fire &&fire, int wm, int wn, int lane)
 {
     fire(freed);
-    typename Ti::Step f;
-    f.read(panel, 0, wm, wn, lane);
-    tile.multiply(f);
+#pragma unroll
+    for (int step = 0; step < Ti::kSteps; ++step) {
+        typename Ti::Step f;
+        f.read(panel, step, wm, wn, lane);
+        tile.multiply(f);
+    }
 }
 
 template <class E, int S, class Ti, class SrcA, class SrcB>
@@ -633,7 +659,7 @@ __device__ inline void sum_panels_dma(Ti &tile, int K, const SrcA &a, const SrcB
         a.refill(0);
         __syncthreads();
     }
-    if constexpr (Ti::kSteps == 1) {
+    if constexpr (Ti::kSteps == 1 || SrcA::kListed) {
 #pragma unroll
         for (int q = 0; q < S - 1; ++q)
             if (q == 0 || q * BK < K)

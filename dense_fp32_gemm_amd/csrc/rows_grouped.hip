@@ -221,76 +221,89 @@ struct CombineArgs {
     int T, k, N, P;
 };
 
+// kSlots results' loads in flight a thread; the sum stays in the order of j.
 template <class E, bool VEC>
 __global__ __launch_bounds__(kCombineThreads) void combine_kernel(CombineArgs g)
 {
     using T = typename E::T;
-    for (int64_t t = blockIdx.x; t < g.T; t += gridDim.x)
-    for (int n = threadIdx.x * E::kChunk; n < g.N; n += kCombineThreads * E::kChunk) {
+    constexpr int kSlots = 8;
+    for (int64_t t = blockIdx.x; t < g.T; t += gridDim.x) {
         const int *position = g.position + t * g.k;
-        float sum[E::kChunk] = {};
-        for (int j = 0; j < g.k; ++j) {
-            const int p = position[j];
-            if (p < 0 || p >= g.P)
-                continue;
-            const float w = g.weight != nullptr ? g.weight[t * g.k + j] : 1.f;
-            Chunk<E> y;
-            y.raw = load_chunk<E, VEC>((const T *)g.Y + p * g.ldy + n, g.N - n);
+        for (int n = threadIdx.x * E::kChunk; n < g.N; n += kCombineThreads * E::kChunk) {
+            float sum[E::kChunk] = {};
+            for (int j0 = 0; j0 < g.k; j0 += kSlots) {
+                Chunk<E> y[kSlots];
+                float w[kSlots];
+                bool there[kSlots];
+#pragma unroll
+                for (int q = 0; q < kSlots; ++q) {
+                    const int p = j0 + q < g.k ? position[j0 + q] : -1;
+                    there[q] = p >= 0 && p < g.P;
+                    w[q] = there[q] && g.weight != nullptr ? g.weight[t * g.k + j0 + q] : 1.f;
+                    y[q].raw = load_chunk<E, VEC>((const T *)g.Y + (there[q] ? p : 0) * g.ldy + n, there[q] ? g.N - n : 0);
+                }
+#pragma unroll
+                for (int q = 0; q < kSlots; ++q)
+                    if (there[q]) {
+#pragma unroll
+                        for (int i = 0; i < E::kChunk; ++i)
+                            sum[i] = fmaf(w[q], (float)y[q].e[i], sum[i]);
+                    }
+            }
+            Chunk<E> o;
 #pragma unroll
             for (int i = 0; i < E::kChunk; ++i)
-                sum[i] = fmaf(w, (float)y.e[i], sum[i]);
+                o.e[i] = (T)sum[i];
+            store_chunk<E, VEC>((T *)g.out + t * g.ldo + n, o, g.N - n);
         }
-        Chunk<E> o;
-#pragma unroll
-        for (int i = 0; i < E::kChunk; ++i)
-            o.e[i] = (T)sum[i];
-        store_chunk<E, VEC>((T *)g.out + t * g.ldo + n, o, g.N - n);
     }
 }
 
+// The inner product in binary32: a thread's chunks, then the waves' lanes, then the waves.
 template <class E, bool VEC>
 __global__ __launch_bounds__(kCombineThreads) void combine_grad_kernel(CombineArgs g)
 {
     using T = typename E::T;
     __shared__ float part[kCombineThreads / kWave];
     const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
-    for (int64_t t = blockIdx.x; t < g.T; t += gridDim.x)
-    for (int j = 0; j < g.k; ++j) {
-        const int p = g.position[t * g.k + j];
-        const bool there = p >= 0 && p < g.P;
-        const float w = g.weight != nullptr ? g.weight[t * g.k + j] : 1.f;
-        float sum = 0.f;
-        if (there) {
-            for (int n = threadIdx.x * E::kChunk; n < g.N; n += kCombineThreads * E::kChunk) {
-                Chunk<E> d;
-                d.raw = load_chunk<E, VEC>((const T *)g.dout + t * g.lddo + n, g.N - n);
-                if (g.dweight != nullptr) {
-                    Chunk<E> y;
-                    y.raw = load_chunk<E, VEC>((const T *)g.Y + p * g.ldy + n, g.N - n);
+    for (int64_t t = blockIdx.x; t < g.T; t += gridDim.x) {
+        for (int j = 0; j < g.k; ++j) {
+            const int p = g.position[t * g.k + j];
+            const bool there = p >= 0 && p < g.P;
+            const float w = g.weight != nullptr ? g.weight[t * g.k + j] : 1.f;
+            float sum = 0.f;
+            if (there) {
+                for (int n = threadIdx.x * E::kChunk; n < g.N; n += kCombineThreads * E::kChunk) {
+                    Chunk<E> d;
+                    d.raw = load_chunk<E, VEC>((const T *)g.dout + t * g.lddo + n, g.N - n);
+                    if (g.dweight != nullptr) {
+                        Chunk<E> y;
+                        y.raw = load_chunk<E, VEC>((const T *)g.Y + p * g.ldy + n, g.N - n);
 #pragma unroll
-                    for (int i = 0; i < E::kChunk; ++i)
-                        sum = fmaf((float)y.e[i], (float)d.e[i], sum);
-                }
-                if (g.dY != nullptr) {
-                    Chunk<E> o;
+                        for (int i = 0; i < E::kChunk; ++i)
+                            sum = fmaf((float)y.e[i], (float)d.e[i], sum);
+                    }
+                    if (g.dY != nullptr) {
+                        Chunk<E> o;
 #pragma unroll
-                    for (int i = 0; i < E::kChunk; ++i)
-                        o.e[i] = (T)(w * (float)d.e[i]);
-                    store_chunk<E, VEC>((T *)g.dY + p * g.lddy + n, o, g.N - n);
+                        for (int i = 0; i < E::kChunk; ++i)
+                            o.e[i] = (T)(w * (float)d.e[i]);
+                        store_chunk<E, VEC>((T *)g.dY + p * g.lddy + n, o, g.N - n);
+                    }
                 }
             }
-        }
-        if (g.dweight == nullptr)
-            continue;
+            if (g.dweight == nullptr)
+                continue;
 #pragma unroll
-        for (int d = kWave / 2; d > 0; d /= 2)
-            sum += __shfl_xor(sum, d);
-        if (lane == 0)
-            part[wave] = sum;
-        __syncthreads();
-        if (threadIdx.x == 0)
-            g.dweight[t * g.k + j] = (part[0] + part[1]) + (part[2] + part[3]);
-        __syncthreads();
+            for (int d = kWave / 2; d > 0; d /= 2)
+                sum += __shfl_xor(sum, d);
+            if (lane == 0)
+                part[wave] = sum;
+            __syncthreads();
+            if (threadIdx.x == 0)
+                g.dweight[t * g.k + j] = (part[0] + part[1]) + (part[2] + part[3]);
+            __syncthreads();
+        }
     }
 }
 

@@ -1,9 +1,9 @@
 // Routing of tokens to experts, its gradient, and the slot map
 // (include/gemm_f32_rows.h).
 //
-//  * route_kernel: one wave per token.  A lane holds every 64th expert; the
-//    choice is k rounds of a wave-wide maximum over 64-bit keys.
-//  * route_grad_kernel: one wave per token, the same layout.
+//  * route_kernel: 16 or 64 lanes per token, each with every 16th (64th) expert; the
+//    choice is k rounds of a maximum over integer keys.
+//  * route_grad_kernel: the same layout.
 //  * count_slots, place_slots: a stable counting sort of the slots by expert,
 //    a workgroup per kSlotChunk slots.
 //
@@ -11,12 +11,14 @@
 // neighbouring scores, and a score rounded to 24 bits makes ties (and with
 // them wrong choices) of what the formula tells apart.
 
+#include <type_traits>
+
 #include "rows_common.h"
 
 namespace rows {
 namespace {
 
-constexpr int kRouteWaves = 4;       // tokens of a workgroup
+constexpr int kRouteWaves = 4;
 constexpr int kRouteThreads = kRouteWaves * kWave;
 
 struct RouteArgs {
@@ -28,11 +30,37 @@ struct RouteArgs {
     int T, E, k, groups, keep_groups, group_top;
     bool softmax, normalize;
     float scale;
+    Divisor per_group;
 };
 
 // ---------------------------------------------------------------------------
-// Wave-wide sums
+// L lanes (16 or 64) share a token; lane i of them holds experts i, i + L, ...
+// Reductions over the token's lanes give every one of them the result.
 // ---------------------------------------------------------------------------
+template <int L, class Fn>
+__device__ inline uint32_t reduce(uint32_t x, Fn &&f)
+{
+    x = f(x, dpp<0x128>(x));     // rotations within 16 lanes
+    x = f(x, dpp<0x124>(x));
+    x = f(x, dpp<0x122>(x));
+    x = f(x, dpp<0x121>(x));
+    if constexpr (L == 64) {
+        x = f(x, (uint32_t)__shfl_xor((int)x, 16));
+        x = f(x, (uint32_t)__shfl_xor((int)x, 32));
+    }
+    return x;
+}
+template <int L>
+__device__ inline uint32_t token_max(uint32_t x)
+{
+    return reduce<L>(x, [](uint32_t a, uint32_t b) { return max(a, b); });
+}
+template <int L>
+__device__ inline uint32_t token_min(uint32_t x)
+{
+    return reduce<L>(x, [](uint32_t a, uint32_t b) { return min(a, b); });
+}
+
 template <int CTRL>
 __device__ inline double dpp_double(double x)
 {
@@ -41,22 +69,18 @@ __device__ inline double dpp_double(double x)
     return __longlong_as_double((int64_t)((uint64_t)hi << 32 | lo));
 }
 
-__device__ inline double read_lane(double x, int lane)
-{
-    const uint64_t u = __double_as_longlong(x);
-    const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)u, lane);
-    const uint32_t hi = __builtin_amdgcn_readlane((int)(u >> 32), lane);
-    return __longlong_as_double((int64_t)((uint64_t)hi << 32 | lo));
-}
-
-// The wave's sum, the same in every lane.
-__device__ inline double wave_sum(double x)
+template <int L>
+__device__ inline double token_sum(double x)
 {
     x += dpp_double<0x128>(x);
     x += dpp_double<0x124>(x);
     x += dpp_double<0x122>(x);
     x += dpp_double<0x121>(x);
-    return (read_lane(x, 0) + read_lane(x, 16)) + (read_lane(x, 32) + read_lane(x, 48));
+    if constexpr (L == 64) {
+        x += __shfl_xor(x, 16);
+        x += __shfl_xor(x, 32);
+    }
+    return x;
 }
 
 // ---------------------------------------------------------------------------
@@ -75,33 +99,20 @@ __device__ inline uint64_t order_key(double x)
     return x != x ? ~uint64_t(0) : (u >> 63) ? ~u : u | uint64_t(1) << 63;
 }
 
-// One round of a choice: the largest key of the wave and the lowest index
-// that has it.  key is the lane's best key and at its index; the result is
-// the same in every lane, found = false when all keys are 0.  The high
-// words settle nearly every round; the low words and then the indices are
-// compared only among lanes that tie so far.
-__device__ inline bool wave_best(uint64_t key, int at, int &found_at)
+// The token's largest key among its lanes' best ones.
+template <int L>
+__device__ inline uint32_t top_key(uint32_t best) { return token_max<L>(best); }
+template <int L>
+__device__ inline uint64_t top_key(uint64_t best)
 {
-    const uint32_t hi = (uint32_t)(key >> 32), lo = (uint32_t)key;
-    const uint32_t top = wave_max(hi);
-    if (top == 0)
-        return false;
-    uint64_t tie = __ballot(hi == top);
-    if (__popcll(tie) > 1) {
-        const uint32_t low = wave_max(hi == top ? lo : 0u);
-        tie = __ballot(hi == top && lo == low);
-        if (__popcll(tie) > 1) {
-            found_at = (int)~wave_max(hi == top && lo == low ? ~(uint32_t)at : 0u);
-            return true;
-        }
-    }
-    found_at = __builtin_amdgcn_readlane(at, (int)__builtin_ctzll(tie));
-    return true;
+    const uint32_t hi = token_max<L>((uint32_t)(best >> 32));
+    const uint32_t lo = token_max<L>((uint32_t)(best >> 32) == hi ? (uint32_t)best : 0u);
+    return (uint64_t)hi << 32 | lo;
 }
 
 // The row's largest logit among lanes' l[] (NaN ignored: the exponentials
 // carry it), 0 for a row without any.
-template <int V>
+template <int L, int V>
 __device__ inline float row_max(const float (&l)[V])
 {
     uint32_t best = order_key(-INFINITY);
@@ -109,13 +120,13 @@ __device__ inline float row_max(const float (&l)[V])
     for (int v = 0; v < V; ++v)
         if (l[v] == l[v])
             best = max(best, order_key(l[v]));
-    best = wave_max(best);
+    best = token_max<L>(best);
     const float m = __uint_as_float((best & 0x80000000u) ? best & 0x7fffffffu : ~best);
     return m == -INFINITY ? 0.f : m;
 }
 
 // Scores of the row, binary64.
-template <int V>
+template <int L, int V>
 __device__ inline void scores(const float (&l)[V], bool softmax, double (&s)[V])
 {
     if (!softmax) {
@@ -124,73 +135,122 @@ __device__ inline void scores(const float (&l)[V], bool softmax, double (&s)[V])
             s[v] = 1.0 / (1.0 + exp(-(double)l[v]));
         return;
     }
-    const double m = row_max<V>(l);
+    const double m = row_max<L, V>(l);
     double sum = 0.0;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
         s[v] = exp((double)l[v] - m);
         sum += s[v];
     }
-    sum = wave_sum(sum);
+    sum = token_sum<L>(sum);
     const double inv = sum == 0.0 ? 0.0 : 1.0 / sum;
 #pragma unroll
     for (int v = 0; v < V; ++v)
         s[v] *= inv;
 }
 
-template <class E, int V>
-__device__ inline void load_row(const typename E::T *row, int E_, int lane, float (&l)[V])
+template <class E, int L, int V>
+__device__ inline void load_row(const typename E::T *row, int experts, int i, float (&l)[V])
 {
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-        const int e = v * kWave + lane;
-        l[v] = e < E_ ? (float)row[e] : -INFINITY;
+        const int e = v * L + i;
+        l[v] = e < experts ? (float)row[e] : -INFINITY;
     }
 }
 
-template <class E, int V>
-__global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs g)
+// s of expert e, from the lane of the token that holds it.
+template <int L, int V>
+__device__ inline double score_of(const double (&s)[V], int e)
 {
-    __shared__ double group_c[kRouteWaves][V * kWave];
-    const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
-    const int64_t t = (int64_t)blockIdx.x * kRouteWaves + wave;
-    if (t >= g.T)
-        return;                                      // whole waves; no barrier below
-    const typename E::T *row = (const typename E::T *)g.logits + t * g.ldl;
-    float l[V];
-    load_row<E, V>(row, g.E, lane, l);
-    const bool by_score = g.bias != nullptr;         // keys are c, else logits
-    const bool need_s = by_score || g.groups > 1 || (g.softmax && !g.normalize);
-    double s[V];
-    if (need_s)
-        scores<V>(l, g.softmax, s);
-
-    uint64_t key[V];
-    double c[V];
+    double x = 0.0;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-        const int e = v * kWave + lane;
-        const float b = by_score && e < g.E ? g.bias[e] : 0.f;
+        const double y = __shfl(s[v], e >= 0 ? e % L : 0, L);
+        x = e >= 0 && e / L == v ? y : x;
+    }
+    return x;
+}
+
+// k rounds: the largest key of the token, of those the lowest expert; lane j of
+// the token gets the j-th choice (-1: none), k <= L.
+template <int L, int V, class Key>
+__device__ inline int choose(Key (&key)[V], int k, int i)
+{
+    int chosen = -1;
+    for (int j = 0; j < k; ++j) {
+        Key best = key[0];
+#pragma unroll
+        for (int v = 1; v < V; ++v)
+            best = key[v] > best ? key[v] : best;
+        const Key top = top_key<L>(best);
+        uint32_t at = UINT32_MAX;
+#pragma unroll
+        for (int v = V - 1; v >= 0; --v)
+            at = key[v] == top ? (uint32_t)(v * L + i) : at;
+        at = token_min<L>(at);
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            key[v] = (uint32_t)(v * L + i) == at ? 0 : key[v];
+        chosen = i == j && top != 0 ? (int)at : chosen;
+    }
+    return chosen;
+}
+
+// KEY64: keys are c (a bias), else the logits'.
+template <class E, int L, int V, bool KEY64>
+__global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs g)
+{
+    constexpr int R = kWave / L, kPad = 32;          // tokens of a wave; experts between gaps of one in LDS
+    constexpr int kLine = L * V + L * V / kPad + 1;
+    __shared__ double group_c[kRouteWaves][R][kLine];
+    const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+    const int i = lane % L, r = lane / L;
+    const int64_t t0 = ((int64_t)blockIdx.x * kRouteWaves + wave) * R;
+    if (t0 >= g.T)
+        return;                                      // whole waves; no barrier below
+    const bool live = t0 + r < g.T;                  // lanes past the last token work on a copy of it
+    const int64_t t = live ? t0 + r : g.T - 1;
+    const typename E::T *row = (const typename E::T *)g.logits + t * g.ldl;
+    float l[V];
+    load_row<E, L, V>(row, g.E, i, l);
+    const bool need_s = KEY64 || g.groups > 1 || (g.softmax && !g.normalize);
+    double s[V], c[V];
+    if (need_s)
+        scores<L, V>(l, g.softmax, s);
+
+    using Key = typename std::conditional<KEY64, uint64_t, uint32_t>::type;
+    Key key[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const int e = v * L + i;
+        const float b = KEY64 && e < g.E ? g.bias[e] : 0.f;
         c[v] = need_s ? s[v] + (double)b : 0.0;
         const bool there = e < g.E && l[v] != -INFINITY && b != -INFINITY;
-        key[v] = !there ? 0 : by_score ? order_key(c[v]) : (uint64_t)order_key(l[v]) << 32;
+        if constexpr (KEY64)
+            key[v] = there ? order_key(c[v]) : 0;
+        else
+            key[v] = there ? order_key(l[v]) : 0;
     }
 
     if (g.groups > 1) {
         // Lane q sums the best of group q; it stays if fewer than
         // keep_groups groups come before it.
         const int per = g.E / g.groups;
-        volatile double *mine = group_c[wave];       // the wave's own: written and read in program order
+        volatile double *mine = group_c[wave][r];    // the wave's own: written and read in program order
 #pragma unroll
-        for (int v = 0; v < V; ++v)
-            mine[v * kWave + lane] = key[v] ? c[v] : -INFINITY;
+        for (int v = 0; v < V; ++v) {
+            const int e = v * L + i;
+            mine[e + e / kPad] = key[v] ? c[v] : -INFINITY;
+        }
         __builtin_amdgcn_wave_barrier();
         uint64_t score = 0;
-        if (lane < g.groups) {
+        if (i < g.groups) {
             double first = -INFINITY, second = -INFINITY;
             bool nan = false;
-            for (int i = 0; i < per; ++i) {
-                const double x = mine[lane * per + i];
+            for (int q = 0; q < per; ++q) {
+                const int e = i * per + q;
+                const double x = mine[e + e / kPad];
                 nan |= x != x;
                 second = x > first ? first : x > second ? x : second;
                 first = x > first ? x : first;
@@ -202,40 +262,19 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs g)
         }
         int before = 0;
         for (int q = 0; q < g.groups; ++q) {
-            const uint64_t other = (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(score >> 32), q) << 32 |
-                                   (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)score, q);
-            before += other > score || (other == score && q < lane);
+            const uint64_t other = (uint64_t)(uint32_t)__shfl((int)(score >> 32), q, L) << 32 |
+                                   (uint32_t)__shfl((int)(uint32_t)score, q, L);
+            before += other > score || (other == score && q < i);
         }
-        const uint64_t kept = __ballot(lane < g.groups && before < g.keep_groups);
+        const uint64_t kept = __ballot(i < g.groups && before < g.keep_groups) >> (r * L);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            const int e = v * kWave + lane;
-            if (e < g.E && !(kept >> (e / per) & 1))
+            const int e = v * L + i;
+            if (e < g.E && !(kept >> g.per_group.of(e) & 1))
                 key[v] = 0;
         }
     }
-
-    // k rounds; lane j keeps the j-th choice.
-    int chosen = -1;
-    for (int j = 0; j < g.k; ++j) {
-        uint64_t best = key[0];
-        int at = lane;
-#pragma unroll
-        for (int v = 1; v < V; ++v)
-            if (key[v] > best) {
-                best = key[v];
-                at = v * kWave + lane;
-            }
-        int e;
-        if (!wave_best(best, at, e))
-            break;
-#pragma unroll
-        for (int v = 0; v < V; ++v)
-            if (v * kWave + lane == e)
-                key[v] = 0;
-        if (lane == j)
-            chosen = e;
-    }
+    const int chosen = choose<L, V>(key, g.k, i);
 
     // Weights of the chosen, a lane each.
     double w = 0.0;
@@ -245,25 +284,18 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs g)
     } else if (g.normalize) {
         // softmax over the chosen alone: the other terms cancel
         const float one[1] = {lj};
-        const double m = row_max<1>(one);
+        const double m = row_max<L, 1>(one);
         w = chosen >= 0 ? exp((double)lj - m) : 0.0;
     } else {
-        double sum = 0.0;                            // s of the chosen, from its owner
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const double x = __shfl(s[v], chosen >= 0 ? chosen % kWave : 0);
-            if (chosen >= 0 && chosen / kWave == v)
-                sum = x;
-        }
-        w = sum;
+        w = score_of<L, V>(s, chosen);
     }
     if (g.normalize) {
-        const double sum = wave_sum(w);
+        const double sum = token_sum<L>(w);
         w = sum == 0.0 ? 0.0 : w / sum;
     }
-    if (lane < g.k) {
-        g.index[t * g.k + lane] = chosen;
-        g.weight[t * g.k + lane] = chosen >= 0 ? (float)(w * (double)g.scale) : 0.f;
+    if (live && i < g.k) {
+        g.index[t * g.k + i] = chosen;
+        g.weight[t * g.k + i] = chosen >= 0 ? (float)(w * (double)g.scale) : 0.f;
     }
 }
 
@@ -278,21 +310,25 @@ struct RouteGradArgs {
     float scale;
 };
 
-template <class E, int V>
+template <class E, int L, int V>
 __global__ __launch_bounds__(kRouteThreads) void route_grad_kernel(RouteGradArgs g)
 {
+    constexpr int R = kWave / L;
     const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
-    const int64_t t = (int64_t)blockIdx.x * kRouteWaves + wave;
-    if (t >= g.T)
+    const int i = lane % L, r = lane / L;
+    const int64_t t0 = ((int64_t)blockIdx.x * kRouteWaves + wave) * R;
+    if (t0 >= g.T)
         return;
+    const bool live = t0 + r < g.T;
+    const int64_t t = live ? t0 + r : g.T - 1;
     const typename E::T *row = (const typename E::T *)g.logits + t * g.ldl;
     typename E::T *out = (typename E::T *)g.dlogits + t * g.lddl;
 
     // Lane j holds the j-th choice.
-    int chosen = lane < g.k ? g.index[t * g.k + lane] : -1;
+    int chosen = i < g.k ? g.index[t * g.k + i] : -1;
     if (chosen < 0 || chosen >= g.E)
         chosen = -1;
-    const double dw = chosen >= 0 ? (double)g.dweight[t * g.k + lane] * (double)g.scale : 0.0;
+    const double dw = chosen >= 0 ? (double)g.dweight[t * g.k + i] * (double)g.scale : 0.0;
     const float lj = chosen >= 0 ? (float)row[chosen] : -INFINITY;
 
     double up;                                       // what the chosen logit gets
@@ -303,32 +339,25 @@ __global__ __launch_bounds__(kRouteThreads) void route_grad_kernel(RouteGradArgs
         // 1 - s without cancellation
         const double rest = chosen >= 0 ? 1.0 / (1.0 + exp((double)lj)) : 0.0;
         if (g.normalize) {
-            const double sum = wave_sum(sj);
+            const double sum = token_sum<L>(sj);
             const double w = sum == 0.0 ? 0.0 : sj / sum;
-            up = w * (dw - wave_sum(w * dw)) * rest;
+            up = w * (dw - token_sum<L>(w * dw)) * rest;
         } else {
             up = sj * rest * dw;
         }
     } else if (g.normalize) {
         const float one[1] = {lj};
-        const double m = row_max<1>(one);
+        const double m = row_max<L, 1>(one);
         const double x = chosen >= 0 ? exp((double)lj - m) : 0.0;
-        const double sum = wave_sum(x);
+        const double sum = token_sum<L>(x);
         const double w = sum == 0.0 ? 0.0 : x / sum;
-        up = w * (dw - wave_sum(w * dw));
+        up = w * (dw - token_sum<L>(w * dw));
     } else {
         float l[V];
-        load_row<E, V>(row, g.E, lane, l);
-        scores<V>(l, true, s);
-        double sj = 0.0;
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const double x = __shfl(s[v], chosen >= 0 ? chosen % kWave : 0);
-            if (chosen >= 0 && chosen / kWave == v)
-                sj = x;
-        }
-        up = sj * dw;
-        all = wave_sum(up);
+        load_row<E, L, V>(row, g.E, i, l);
+        scores<L, V>(l, true, s);
+        up = score_of<L, V>(s, chosen) * dw;
+        all = token_sum<L>(up);
     }
 
     double d[V];
@@ -336,17 +365,16 @@ __global__ __launch_bounds__(kRouteThreads) void route_grad_kernel(RouteGradArgs
     for (int v = 0; v < V; ++v)
         d[v] = g.softmax && !g.normalize ? -s[v] * all : 0.0;
     for (int j = 0; j < g.k; ++j) {
-        const int e = __builtin_amdgcn_readlane(chosen, j);
-        const double x = read_lane(up, j);
+        const int e = __shfl(chosen, j, L);
+        const double x = __shfl(up, j, L);
 #pragma unroll
         for (int v = 0; v < V; ++v)
-            if (v * kWave + lane == e)
-                d[v] += x;
+            d[v] += v * L + i == e ? x : 0.0;
     }
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-        const int e = v * kWave + lane;
-        if (e < g.E)
+        const int e = v * L + i;
+        if (live && e < g.E)
             out[e] = (typename E::T)d[v];
     }
 }
@@ -513,11 +541,15 @@ __global__ __launch_bounds__(kSlotThreads) void place_slots(const int *index, in
 int64_t slot_chunks(int64_t S) { return S <= kSlotChunk ? 1 : ceil_div(S, kSlotChunk); }
 
 // Up to this many slots every workgroup counts them all; more are counted in a
-// launch of their own.
-constexpr int64_t kCountedInPlace = 1 << 17;
+// launch of their own (16384 slots: 7.7 us in one launch; 65536: 14 us against 10 in
+// two, 131072: 23 against 12).
+constexpr int64_t kCountedInPlace = 1 << 15;
 
 // A grid has fewer than 2^32 threads, a wave of them per token.
 constexpr int kMaxTokens = (int)(UINT32_MAX / kWave) - kRouteWaves;
+
+// Tokens from which 16 lanes take one of more than 128 experts.
+constexpr int kNarrowFrom = 4096;
 
 int check_route(int type, int T, int E, int k, int64_t ldl)
 {
@@ -528,20 +560,31 @@ int check_route(int type, int T, int E, int k, int64_t ldl)
     return ldl < E ? GEMM_F32_ERR_LD : GEMM_F32_OK;
 }
 
-// f(E{}, integral constant V) with 64 * V >= experts.
-template <class E, class Fn>
-void with_width(int experts, Fn &&f)
+// f(L, V, tokens of a workgroup) for the lanes of a token and the experts of a
+// lane, as integral constants.  16 lanes a token (four tokens a wave) need a quarter of
+// the instructions of a choice; 64 where the experts, the choices or the groups are too
+// many for them, and where tokens are too few to fill the device's waves (512 tokens,
+// 256 experts, bias and groups: 11.7 us against 14.8; 8192 tokens: 24 against 18; 16383
+// tokens, 128 experts, no bias: 16.7 against 7.6; 256 tokens, 128 experts: 5.6 against 4.4).
+template <class Fn>
+void with_width(int T, int experts, int most, Fn &&f)
 {
-    if (experts <= 64)
-        f(std::integral_constant<int, 1>{});
-    else if (experts <= 128)
-        f(std::integral_constant<int, 2>{});
-    else if (experts <= 256)
-        f(std::integral_constant<int, 4>{});
-    else if (experts <= 512)
-        f(std::integral_constant<int, 8>{});
-    else
-        f(std::integral_constant<int, 16>{});
+    auto wide = [&](auto v) { f(std::integral_constant<int, 64>{}, v, kRouteWaves); };
+    auto narrow = [&](auto v) { f(std::integral_constant<int, 16>{}, v, kRouteWaves * 4); };
+    if (most <= 16 && (experts <= 128 || (experts <= 256 && T >= kNarrowFrom))) {
+        if (experts <= 64)
+            narrow(std::integral_constant<int, 4>{});
+        else if (experts <= 128)
+            narrow(std::integral_constant<int, 8>{});
+        else
+            narrow(std::integral_constant<int, 16>{});
+    } else if (experts <= 64) {
+        wide(std::integral_constant<int, 1>{});
+    } else if (experts <= 256) {
+        wide(std::integral_constant<int, 4>{});
+    } else {
+        wide(std::integral_constant<int, 16>{});
+    }
 }
 
 }  // namespace
@@ -569,11 +612,16 @@ int gemm_f32_route(int type, int T, int E, int k, const void *logits, int ldl, c
     if (!aligned_to(logits, type_bytes(type)) || !aligned_to(bias, 4) || !aligned_to(weight, 4) || !aligned_to(index, 4))
         return GEMM_F32_ERR_ALIGN;
     const RouteArgs g{logits, bias, weight, index, ldl, T, E, k, groups, keep_groups, group_top,
-                      score == GEMM_F32_SCORE_SOFTMAX, normalize != 0, scale};
-    const int grid = (int)ceil_div(T, kRouteWaves);
+                      score == GEMM_F32_SCORE_SOFTMAX, normalize != 0, scale, Divisor(E / groups)};
     with_type(type, [&](auto e) {
         using El = decltype(e);
-        with_width<El>(E, [&](auto v) { route_kernel<El, v.value><<<grid, kRouteThreads, 0, stream>>>(g); });
+        with_width(T, E, k > groups ? k : groups, [&](auto lanes, auto v, int tokens) {
+            const int grid = (int)ceil_div(T, tokens);
+            if (bias != nullptr)
+                route_kernel<El, lanes.value, v.value, true><<<grid, kRouteThreads, 0, stream>>>(g);
+            else
+                route_kernel<El, lanes.value, v.value, false><<<grid, kRouteThreads, 0, stream>>>(g);
+        });
     });
     return launched();
 }
@@ -596,10 +644,11 @@ int gemm_f32_route_grad(int type, int T, int E, int k, const void *logits, int l
         return GEMM_F32_ERR_ALIGN;
     const RouteGradArgs g{logits, index, dweight, dlogits, ldl, lddl, T, E, k,
                           score == GEMM_F32_SCORE_SOFTMAX, normalize != 0, scale};
-    const int grid = (int)ceil_div(T, kRouteWaves);
     with_type(type, [&](auto e) {
         using El = decltype(e);
-        with_width<El>(E, [&](auto v) { route_grad_kernel<El, v.value><<<grid, kRouteThreads, 0, stream>>>(g); });
+        with_width(T, E, k, [&](auto lanes, auto v, int tokens) {
+            route_grad_kernel<El, lanes.value, v.value><<<(int)ceil_div(T, tokens), kRouteThreads, 0, stream>>>(g);
+        });
     });
     return launched();
 }

@@ -659,7 +659,8 @@ __device__ inline void sum_panels_dma(Ti &tile, int K, const SrcA &a, const SrcB
         a.refill(0);
         __syncthreads();
     }
-    if constexpr (Ti::kSteps == 1 || SrcA::kListed) {
+    // (With rows from a list, 16-bit types have no registers left to read ahead.)
+    if constexpr (Ti::kSteps == 1 || (SrcA::kListed && E::kBytes == 2)) {
 #pragma unroll
         for (int q = 0; q < S - 1; ++q)
             if (q == 0 || q * BK < K)

@@ -55,6 +55,10 @@ ROUTES = [
     (3, 1000, 5, dict(score="sigmoid", bias=True, groups=40, keep_groups=7, group_top=2)),
     (12, 64, 3, dict(groups=64, keep_groups=5, group_top=2, score="sigmoid", normalize=True)),
     (8, 12, 12, dict(groups=4, keep_groups=2, group_top=2, bias=True, normalize=True)),
+    # many tokens: four to a wave
+    (1025, 40, 4, dict(normalize=True)), (1030, 100, 16, dict(score="sigmoid", bias=True)), (4099, 256, 8, dict()),
+    (4097, 200, 8, dict(score="sigmoid", normalize=True, bias=True, groups=10, keep_groups=4, group_top=2)),
+    (1026, 120, 3, dict(groups=8, keep_groups=2, group_top=1, normalize=True)),
 ]
 
 
@@ -97,7 +101,7 @@ def test_route(dev, dtype, case):
     oracle.close(w, want_w, want_w.abs() * (2.0 ** -24 + 2.0 ** -40) + 2.0 ** -150, "weight")
 
 
-GRADS = [(1, 1, 1), (9, 8, 2), (14, 65, 8), (7, 256, 8), (7, 1000, 64)]
+GRADS = [(1, 1, 1), (9, 8, 2), (14, 65, 8), (7, 256, 8), (7, 1000, 64), (1031, 50, 3), (1025, 128, 16), (4098, 200, 8)]
 
 
 @pytest.mark.parametrize("dtype", TYPES, ids=IDS)
@@ -140,8 +144,8 @@ def test_route_grad_adds_what_an_index_named_twice_gets(dev):
     oracle.close(both, want.cpu(), want.cpu().abs() * 2.0 ** -23, "twice")
 
 
-@pytest.mark.parametrize("S,E", [(0, 3), (1, 1), (5, 4), (64, 64), (2047, 7), (2048, 1024), (2049, 3), (6000, 130), (20001, 1000), (131072, 9),
-                                 (131073, 64), (150001, 256)])
+@pytest.mark.parametrize("S,E", [(0, 3), (1, 1), (5, 4), (64, 64), (2047, 7), (2048, 1024), (2049, 3), (6000, 130), (20001, 1000), (32768, 9),
+                                 (32769, 64), (150001, 256)])
 def test_expert_map(dev, S, E):
     g = seeded("map", S, E)
     index = torch.randint(-1, E + 1, (S,), generator=g, dtype=torch.int32)      # -1 and E: left out

@@ -69,8 +69,8 @@ def test_expert_map_refuses(change, rc):
 
 
 def test_expert_map_workspace_only_for_many_slots():
-    assert gb.gemm_f32_expert_map_ws_size(0, 8) == gb.gemm_f32_expert_map_ws_size(1 << 17, 1024) == 0
-    assert gb.gemm_f32_expert_map_ws_size((1 << 17) + 1, 8) > 0
+    assert gb.gemm_f32_expert_map_ws_size(0, 8) == gb.gemm_f32_expert_map_ws_size(1 << 15, 1024) == 0
+    assert gb.gemm_f32_expert_map_ws_size((1 << 15) + 1, 8) > 0
     assert gb.gemm_f32_expert_map_ws_size(-1, 8) == gb.gemm_f32_expert_map_ws_size(9, 0) == 0
 
 

@@ -383,7 +383,9 @@ __device__ inline void adapters_tile(const AdapterArgs &g, int m0, int n0, typen
                     add[n] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                     for (int step = 0; step < Ti::kSteps; ++step)
-                        add[n] = mfma_step<E>(fb[step].q[n], fa[step].q[0], add[n]);
+#pragma unroll
+                        for (int s = 0; s < kPerStep<E>; ++s)
+                            add[n] = mfma<E>(fb[step].q[n], fa[step].q[0], add[n], s);
                 }
                 const bool mine = adds[m] == a;
 #pragma unroll

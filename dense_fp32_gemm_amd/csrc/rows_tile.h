@@ -121,20 +121,19 @@ struct Fragments {
     static __device__ inline int row_of(int f, int i) { return (f / kV) * 16 * kV + kV * i + f % kV; }
 };
 
-// d += a . b of one 16 x 16 block and one k step; see the top for the order.
+// d += a . b of one 16 x 16 block and the s-th instruction of a k step (kPerStep
+// of them); see the top for the order.
 template <class E>
-__device__ inline f32x4 mfma_step(u32x4 b, u32x4 a, f32x4 d)
+constexpr int kPerStep = E::kBytes == 4 ? 4 : 1;
+template <class E>
+__device__ inline f32x4 mfma(u32x4 b, u32x4 a, f32x4 d, int s)
 {
-    if constexpr (E::kBytes == 4) {
-#pragma unroll
-        for (int s = 0; s < 4; ++s)
-            d = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(b[s]), __uint_as_float(a[s]), d, 0, 0, 0);
-        return d;
-    } else if constexpr (std::is_same<E, Bf16>::value) {
+    if constexpr (E::kBytes == 4)
+        return __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(b[s]), __uint_as_float(a[s]), d, 0, 0, 0);
+    else if constexpr (std::is_same<E, Bf16>::value)
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, b), __builtin_bit_cast(bf16x8, a), d, 0, 0, 0);
-    } else {
+    else
         return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, b), __builtin_bit_cast(f16x8, a), d, 0, 0, 0);
-    }
 }
 
 // A workgroup's BM x BN tile, WM x WN waves of (BM/WM) x (BN/WN), panels of CH chunks
@@ -146,7 +145,7 @@ struct Tile {
     static constexpr int kThreads = WM * WN * kWave;
     static constexpr int kFm = BM / WM / 16, kFn = BN / WN / 16;
     static constexpr int CH = CH_, kDeep = CH * E::kChunk, kSteps = CH / 4;
-    static constexpr int kMfma = kFm * kFn * (E::kBytes == 2 ? 1 : 4);     // matrix instructions of a step
+    static constexpr int kMfma = kFm * kFn * kPerStep<E>;                 // matrix instructions of a step
     static constexpr int kLdsA = BM * kDeep, kLdsB = BN * kDeep;           // elements of a panel
     using Fa = Fragments<E, A_ALONG, BM, CH, kFm>;
     using Fb = Fragments<E, B_ALONG, BN, CH, kFn>;
@@ -178,11 +177,15 @@ struct Tile {
 
     __device__ inline void multiply(const Step &s)
     {
+        // block by block within an instruction of the step: neighbouring
+        // instructions do not wait for one another's sums
 #pragma unroll
-        for (int m = 0; m < kFm; ++m)
+        for (int i = 0; i < kPerStep<E>; ++i)
 #pragma unroll
-            for (int n = 0; n < kFn; ++n)
-                acc[m][n] = mfma_step<E>(s.b.q[n], s.a.q[m], acc[m][n]);
+            for (int m = 0; m < kFm; ++m)
+#pragma unroll
+                for (int n = 0; n < kFn; ++n)
+                    acc[m][n] = mfma<E>(s.b.q[n], s.a.q[m], acc[m][n], i);
     }
 
     // f(row, column, 4 neighbouring columns' sums) over the lane's results,

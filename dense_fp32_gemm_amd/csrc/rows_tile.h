@@ -255,12 +255,10 @@ __device__ inline const char *uniform(const void *p)
     return (const char *)((uint64_t)hi << 32 | lo);
 }
 
-// Bytes from a panel's base, `done` bytes into an operand of `bytes` bytes, to its
-// end in whole dwords, as a buffer's size: loads past it give zeros.
-__device__ inline uint32_t bytes_left(int64_t bytes, int64_t done)
+// `bytes` as a buffer's size: loads past it give zeros, and so does kNowhere.
+__device__ inline uint32_t buffer_size(int64_t bytes)
 {
-    const int64_t n = (bytes + 3) / 4 * 4 - done;
-    return (uint32_t)(n < 0 ? 0 : n < (int64_t)kNowhere ? n : (int64_t)kNowhere);
+    return (uint32_t)(bytes < 0 ? 0 : bytes < (int64_t)kNowhere ? bytes : (int64_t)kNowhere);
 }
 
 // Operand rows contiguous in the summed index.  row(i, r): byte offset from base of the
@@ -276,9 +274,9 @@ struct Along {
     int K, tid, rows;                                // rows: from base on
 
     static constexpr bool kAlong = true, kOneColumn = false;
-    // Bytes from the panel's base to the operand's end: the last chunk of a row that is no whole
-    // number of chunks long reads what follows (and is cleared in LDS), zeros past the end.
-    __device__ inline uint32_t extent(int64_t done) const { return bytes_left((rows - 1) * ld + (int64_t)K * E::kBytes, done); }
+    // Bytes from base to the operand's end, in whole dwords: the last chunk of a row that is no
+    // whole number of chunks long reads what follows (and is cleared in LDS), zeros past the end.
+    __device__ inline int64_t extent() const { return ((rows - 1) * ld + (int64_t)K * E::kBytes + 3) / 4 * 4; }
     // Panel row of chunk i.
     static __device__ inline int row_of(int i, int tid) { return (tid + i * NT) / CH; }
 
@@ -332,10 +330,10 @@ struct Across {
     {
     }
     static constexpr bool kAlong = false;
-    // Bytes from the panel's base to the operand's end: a chunk that crosses the last
+    // Bytes from base to the operand's end, in whole dwords: a chunk that crosses the last
     // row's end reads zeros there (one that crosses another row's end reads the
-    // next row's start, for columns that are not stored).  Whole dwords.
-    __device__ inline uint32_t extent(int64_t done) const { return bytes_left((rows - 1) * ld + (int64_t)cols * E::kBytes, done); }
+    // next row's start, for columns that are not stored).
+    __device__ inline int64_t extent() const { return ((rows - 1) * ld + (int64_t)cols * E::kBytes + 3) / 4 * 4; }
     // A thread's chunks are kRowStep k rows apart, and mostly in one column: the chunk
     // permutation depends on k's bits 0, 1 and 3 only.
     static constexpr int kRowStep = NT / kPer;
@@ -475,14 +473,20 @@ __device__ inline void sum_panels_staged(Ti &tile, int K, const SrcA &a, const S
 
 // The panel loads of one operand by one wave: lane l's 16 bytes land at the
 // wave's LDS base + 16 * l.  Offsets that differ by whole rows are one register.
+// fire() takes the panels one after the other, from the one at `from` on.
 template <class E, class Src, int NT>
 struct PanelLoads {
     static_assert(Src::kSlots % kWave == 0, "whole waves");
     using T = typename E::T;
     static constexpr bool kOne = Src::kOneColumn;
     uint32_t off[kOne ? 1 : Src::kCount];
-    __device__ inline PanelLoads(const Src &src)
+    const char *base;                                // of the next panel
+    int64_t bytes, step;                             // from there to the operand's end; to the panel after it
+    __device__ inline PanelLoads(const Src &src, int from = 0) : step(src.step())
     {
+        const int64_t done = from / Src::kDeep * step;
+        base = src.base + done;
+        bytes = src.extent() - done;
         if constexpr (kOne) {
             off[0] = src.col(0) < src.cols ? (uint32_t)src.offset(0, 0) : kNowhere;
         } else {
@@ -499,10 +503,11 @@ struct PanelLoads {
         else
             return off[0] + (uint32_t)Src::row_step(i) * (uint32_t)src.ld;
     }
-    __device__ inline void fire(const Src &src, int k0, T *panel, int wave) const
+    __device__ inline void fire(const Src &src, int k0, T *panel, int wave)
     {
-        const int64_t done = (int64_t)(k0 / Src::kDeep) * src.step();
-        const auto rsrc = __builtin_amdgcn_make_buffer_rsrc((void *)(src.base + done), 0, (int)src.extent(done), kRawBufferFlags);
+        const auto rsrc = __builtin_amdgcn_make_buffer_rsrc((void *)base, 0, (int)buffer_size(bytes), kRawBufferFlags);
+        base += step;
+        bytes -= step;
         auto load = [&](int i, uint32_t o) {
             if (Src::kSlots % NT != 0 && (i * NT + wave * kWave) >= Src::kSlots)
                 return;                              // whole waves: kSlots is a multiple of 64
@@ -526,10 +531,10 @@ struct PanelLoads<E, Gathered<E, RN, NT, CH>, NT> {
     using Src = Gathered<E, RN, NT, CH>;
     using T = typename E::T;
     __device__ inline PanelLoads(const Src &) {}
-    __device__ inline void fire(const Src &src, int k0, T *panel, int wave) const
+    __device__ inline void fire(const Src &src, int k0, T *panel, int wave)
     {
         static_assert(Src::kSlots % NT == 0 && Src::kBlock % Src::kDeep == 0, "whole panels");
-        const auto rsrc = __builtin_amdgcn_make_buffer_rsrc((void *)src.base, 0, (int)src.extent(0), kRawBufferFlags);
+        const auto rsrc = __builtin_amdgcn_make_buffer_rsrc((void *)src.base, 0, (int)buffer_size(src.extent()), kRawBufferFlags);
         static_assert(Src::kOneColumn, "one column a thread");
         const int col = src.col(0);
         const uint32_t *block = src.ahead + (k0 / Src::kBlock % 2) * Src::kBlock + k0 % Src::kBlock;
@@ -550,7 +555,7 @@ __device__ inline void load_panel(const Src &src, int k0, typename E::T *panel, 
 {
     using T = typename E::T;
     if constexpr (DMA) {
-        const PanelLoads<E, Src, NT> loads(src);
+        PanelLoads<E, Src, NT> loads(src, k0);
         loads.fire(src, k0, panel, __builtin_amdgcn_readfirstlane(tid / kWave));
     } else {
         const char *p = src.base + (int64_t)(k0 / Src::kDeep) * src.step();
@@ -636,8 +641,8 @@ __device__ inline void sum_panels_dma(Ti &tile, int K, const SrcA &a, const SrcB
     const int lane = tid % kWave, wave = NT == kWave ? 0 : __builtin_amdgcn_readfirstlane(tid / kWave);
     // (An empty sum runs one panel of zeros: a way around the loop would cost a second
     // set of registers for the sums.)
-    const PanelLoads<E, SrcA, NT> pa(a);
-    const PanelLoads<E, SrcB, NT> pb(b);
+    PanelLoads<E, SrcA, NT> pa(a);
+    PanelLoads<E, SrcB, NT> pb(b);
     auto fire = [&](int k0, T *panel) {
         pa.fire(a, k0, panel, wave);
         pb.fire(b, k0, panel + Ti::kLdsA, wave);

@@ -292,7 +292,7 @@ __global__ __launch_bounds__(kFactorThreads) void factor_kernel(AdapterArgs g)
             for (int i = 0; i < g.splits_u; ++i)
                 u[q] += g.partial_u[((int64_t)i * g.T + t) * g.R + r];
         u[q] *= s;
-        top = fmaxf(top, fabsf(u[q]));
+        top = fmaxf(top, fabsf(u[q]) < INFINITY ? fabsf(u[q]) : 0.f);
     }
     if constexpr (E::kBytes == 4) {
 #pragma unroll
@@ -303,8 +303,8 @@ __global__ __launch_bounds__(kFactorThreads) void factor_kernel(AdapterArgs g)
 #pragma unroll
         for (int d = kWave / 2; d > 0; d /= 2)
             top = fmaxf(top, __shfl_xor(top, d));
-        // the row's largest value to [1, 2); rows without one as they are
-        const int up = top > 0.f && top < INFINITY ? max(ilogbf(top), -100) : 0;
+        // the row's largest finite value to [1, 2); rows without one as they are
+        const int up = top > 0.f ? max(ilogbf(top), -100) : 0;
 #pragma unroll
         for (int q = 0; q < kPer; ++q) {
             const int r = q * kWave + lane;
@@ -357,43 +357,44 @@ __device__ inline void adapters_tile(const AdapterArgs &g, int m0, int n0, typen
         // a row of sums is taken only with its own adapter's B.
         const Along<E, BM, NT> u((const T *)g.factor + (int64_t)m0 * g.depth, tid, g.depth, g.depth, g.T - m0,
                                  [&](int, int r) { return m0 + r < g.T ? (int64_t)r * g.depth * E::kBytes : -1; });
-        for (int k0 = 0; k0 < g.depth; k0 += Ti::kDeep)
-        for (int a = next_adapter(which, INT32_MAX); a >= 0; a = next_adapter(which, a)) {
-            const UpRows<E, BN, NT> b((const T *)g.B + a * g.stride_b, tid, g.depth, g.ldb, n0, g.N, g.R);
-            __syncthreads();
-            load_panel<E, DMA, NT>(u, k0, lds, tid);
-            load_panel<E, DMA, NT>(b, k0, lds + Ti::kLdsA, tid);
-            asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
-            __syncthreads();
-            // The sums of one 16-row block at a time: a second set for the whole
-            // tile would halve the waves a SIMD holds.
-            typename Ti::Fb fb[Ti::kSteps];
-#pragma unroll
-            for (int step = 0; step < Ti::kSteps; ++step)
-                fb[step].read(lds + Ti::kLdsA, wn * (BN / WN), step, lane);
-#pragma unroll
-            for (int m = 0; m < Ti::kFm; ++m) {
-                Fragments<E, true, BM, Ti::CH, 1> fa[Ti::kSteps];
+        for (int k0 = 0; k0 < g.depth; k0 += Ti::kDeep) {
+            for (int a = next_adapter(which, INT32_MAX); a >= 0; a = next_adapter(which, a)) {
+                const UpRows<E, BN, NT> b((const T *)g.B + a * g.stride_b, tid, g.depth, g.ldb, n0, g.N, g.R);
+                __syncthreads();
+                load_panel<E, DMA, NT>(u, k0, lds, tid);
+                load_panel<E, DMA, NT>(b, k0, lds + Ti::kLdsA, tid);
+                asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+                __syncthreads();
+                // The sums of one 16-row block at a time: a second set for the whole
+                // tile would halve the waves a SIMD holds.
+                typename Ti::Fb fb[Ti::kSteps];
 #pragma unroll
                 for (int step = 0; step < Ti::kSteps; ++step)
-                    fa[step].read(lds, wm * (BM / WM) + 16 * m, step, lane);
-                f32x4 add[Ti::kFn];
+                    fb[step].read(lds + Ti::kLdsA, wn * (BN / WN), step, lane);
 #pragma unroll
-                for (int n = 0; n < Ti::kFn; ++n) {
-                    add[n] = f32x4{0.f, 0.f, 0.f, 0.f};
+                for (int m = 0; m < Ti::kFm; ++m) {
+                    Fragments<E, true, BM, 1> fa[Ti::kSteps];
 #pragma unroll
                     for (int step = 0; step < Ti::kSteps; ++step)
+                        fa[step].read(lds, wm * (BM / WM) + 16 * m, step, lane);
+                    f32x4 add[Ti::kFn];
 #pragma unroll
-                        for (int s = 0; s < kPerStep<E>; ++s)
-                            add[n] = mfma<E>(fb[step].q[n], fa[step].q[0], add[n], s);
+                    for (int n = 0; n < Ti::kFn; ++n) {
+                        add[n] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                        for (int step = 0; step < Ti::kSteps; ++step)
+#pragma unroll
+                            for (int s = 0; s < kPerStep<E>; ++s)
+                                add[n] = mfma<E>(fb[step].q[n], fa[step].q[0], add[n], s);
+                    }
+                    const bool mine = adds[m] == a;
+#pragma unroll
+                    for (int n = 0; n < Ti::kFn; ++n)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)      // in place, nothing of the others' rows
+                            tile.acc[m][n][i] = fmaf(unscale[m], mine ? add[n][i] : 0.f, tile.acc[m][n][i]);
+                    __builtin_amdgcn_sched_barrier(0);   // one block's sums at a time in registers
                 }
-                const bool mine = adds[m] == a;
-#pragma unroll
-                for (int n = 0; n < Ti::kFn; ++n)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)      // in place, nothing of the others' rows
-                        tile.acc[m][n][i] = fmaf(unscale[m], mine ? add[n][i] : 0.f, tile.acc[m][n][i]);
-                __builtin_amdgcn_sched_barrier(0);   // one block's sums at a time in registers
             }
         }
     }
@@ -624,6 +625,9 @@ int gemm_f32_adapters(int type, int T, int N, int K, int R, int n, const void *X
         return GEMM_F32_ERR_LD;
     if (T == 0 || N == 0)
         return GEMM_F32_OK;
+    const int64_t tile = type == GEMM_F32_TYPE_F32 ? 64 : 256, threads = type == GEMM_F32_TYPE_F32 ? 256 : 512;
+    if (ceil_div(T, tile) * ceil_div(N, tile) > UINT32_MAX / threads - 1024)
+        return GEMM_F32_ERR_DIM;                     // a grid has fewer than 2^32 threads
     const bool low = R > 0 && n > 0;
     if (Y == nullptr || (K > 0 && (X == nullptr || W == nullptr)) ||
         (low && (B == nullptr || adapter == nullptr || (K > 0 && A == nullptr))))

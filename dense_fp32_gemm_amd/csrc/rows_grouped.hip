@@ -96,12 +96,12 @@ __device__ inline Place locate(const GroupedArgs &g, int bm, int t)
 }
 
 // One tile: rows m0 .. m_end - 1 (places; of dW: rows of the matrix), columns from n0 on.
-template <class E, Op OP, int BM, int BN, int WM, int WN, int CH, int S, bool DMA>
+template <class E, Op OP, int BM, int BN, int WM, int WN, int S, bool DMA>
 __device__ inline void grouped_tile(const GroupedArgs &g, int group, int lo, int hi, int m0, int m_end, int n0,
                                     typename E::T *lds, uint32_t *ahead)
 {
     constexpr bool kAlongA = OP != kGradW, kAlongB = OP == kGradX;
-    using Ti = Tile<E, kAlongA, kAlongB, BM, BN, WM, WN, CH>;
+    using Ti = Tile<E, kAlongA, kAlongB, BM, BN, WM, WN>;
     using T = typename E::T;
     constexpr int NT = Ti::kThreads;
     if (m0 >= m_end || n0 >= g.N)
@@ -113,7 +113,7 @@ __device__ inline void grouped_tile(const GroupedArgs &g, int group, int lo, int
     Ti tile;
     tile.clear();
     if constexpr (OP == kForward) {
-        using Src = Along<E, BM, NT, CH>;
+        using Src = Along<E, BM, NT>;
         int row[Src::kCount];                        // of X; the loads side by side, then the rest
         if (g.order != nullptr) {
 #pragma unroll
@@ -129,20 +129,20 @@ __device__ inline void grouped_tile(const GroupedArgs &g, int group, int lo, int
         }
         const Src a(A, tid, g.K, g.lda, g.rows,
                     [&](int i, int r) { return m0 + r < m_end && row[i] < g.rows ? row[i] * g.lda * E::kBytes : -1; });
-        const Across<E, BN, NT, CH> b(B + group * g.stride, tid, g.K, g.ldb, n0, g.N);
+        const Across<E, BN, NT> b(B + group * g.stride, tid, g.K, g.ldb, n0, g.N);
         sum_panels<E, DMA, S>(tile, g.K, a, b, lds, tid, wm, wn);
     } else if constexpr (OP == kGradX) {
-        const Along<E, BM, NT, CH> a(A + m0 * g.lda, tid, g.K, g.lda, g.P - m0,
+        const Along<E, BM, NT> a(A + m0 * g.lda, tid, g.K, g.lda, g.P - m0,
                                  [&](int, int r) { return m0 + r < m_end ? r * g.lda * E::kBytes : -1; });
-        const Along<E, BN, NT, CH> b(B + group * g.stride + n0 * g.ldb, tid, g.K, g.ldb, g.N - n0,
+        const Along<E, BN, NT> b(B + group * g.stride + n0 * g.ldb, tid, g.K, g.ldb, g.N - n0,
                                  [&](int, int r) { return n0 + r < g.N ? r * g.ldb * E::kBytes : -1; });
         sum_panels<E, DMA, S>(tile, g.K, a, b, lds, tid, wm, wn);
     } else {
         const int *list = g.order != nullptr ? g.order + lo : nullptr;
         const T *X = g.order != nullptr ? A : A + lo * g.lda;
         const int rows = g.order != nullptr ? g.rows : hi - lo;
-        const Gathered<E, BM, NT, CH> a(X, tid, hi - lo, g.lda, m0, g.M, list, g.per_row, rows, ahead);
-        const Across<E, BN, NT, CH> b(B + lo * g.ldb, tid, hi - lo, g.ldb, n0, g.N);
+        const Gathered<E, BM, NT> a(X, tid, hi - lo, g.lda, m0, g.M, list, g.per_row, rows, ahead);
+        const Across<E, BN, NT> b(B + lo * g.ldb, tid, hi - lo, g.ldb, n0, g.N);
         sum_panels<E, DMA, S>(tile, hi - lo, a, b, lds, tid, wm, wn);
     }
 
@@ -160,10 +160,10 @@ __device__ inline void grouped_tile(const GroupedArgs &g, int group, int lo, int
         store(std::false_type{});
 }
 
-template <class E, Op OP, int BM, int BN, int WM, int WN, int CH, int S, bool CUT, bool DMA>
-__global__ __launch_bounds__(WM *WN *kWave, CH == 4 ? 4 : 2) void grouped_kernel(GroupedArgs g)
+template <class E, Op OP, int BM, int BN, int WM, int WN, int S, bool CUT, bool DMA>
+__global__ __launch_bounds__(WM *WN *kWave, 2) void grouped_kernel(GroupedArgs g)
 {
-    constexpr int kPanel = (BM + BN) * CH * E::kChunk;
+    constexpr int kPanel = (BM + BN) * kDeep16 * E::kChunk;
     // (S = 2) two panels of the whole tile, three of a half, four of a quarter
     __shared__ __attribute__((aligned(16))) typename E::T lds[CUT && DMA ? 9 * kPanel / 4 : (DMA ? S : 2) * kPanel];
     static_assert(!CUT || (S == 2 && BM == BN), "panels of cut tiles");
@@ -192,13 +192,13 @@ __global__ __launch_bounds__(WM *WN *kWave, CH == 4 ? 4 : 2) void grouped_kernel
     }
     const int m0 = (OP == kGradW ? 0 : p.lo) + p.tm * BM, m_end = OP == kGradW ? g.M : p.hi, n0 = p.tn * BN;
     if (!CUT || part.cut == 1)
-        grouped_tile<E, OP, BM, BN, WM, WN, CH, S, DMA>(g, p.group, p.lo, p.hi, m0, m_end, n0, lds, ahead);
+        grouped_tile<E, OP, BM, BN, WM, WN, S, DMA>(g, p.group, p.lo, p.hi, m0, m_end, n0, lds, ahead);
     if constexpr (CUT) {
         if (part.cut == 2)
-            grouped_tile<E, OP, BM / 2, BN, WM, WN, CH, 3, DMA>(g, p.group, p.lo, p.hi, m0 + part.piece * (BM / 2), m_end,
+            grouped_tile<E, OP, BM / 2, BN, WM, WN, 3, DMA>(g, p.group, p.lo, p.hi, m0 + part.piece * (BM / 2), m_end,
                                                                n0, lds, ahead);
         else if (part.cut == 4)
-            grouped_tile<E, OP, BM / 2, BN / 2, WM, WN, CH, 4, DMA>(g, p.group, p.lo, p.hi,
+            grouped_tile<E, OP, BM / 2, BN / 2, WM, WN, 4, DMA>(g, p.group, p.lo, p.hi,
                                                                    m0 + part.piece % 2 * (BM / 2), m_end,
                                                                    n0 + part.piece / 2 * (BN / 2), lds, ahead);
     }
@@ -326,7 +326,7 @@ static_assert(kCombineThreads <= 512, "grid limit");
 int token_grid(int T) { return T < kMaxTiles ? T : (int)kMaxTiles; }
 
 // PER_CU: workgroups of a kernel that cuts its last tiles on a compute unit (0: it does not).
-template <class E, Op OP, int BM, int BN, int WM, int WN, int CH, int S, int PER_CU>
+template <class E, Op OP, int BM, int BN, int WM, int WN, int S, int PER_CU>
 int launch_tile(GroupedArgs g, bool dma, hipStream_t stream)
 {
     g.tiles_n = (int)ceil_div(g.N, BN);
@@ -342,9 +342,9 @@ int launch_tile(GroupedArgs g, bool dma, hipStream_t stream)
     g.most_m = (int)tiles_m;
     constexpr bool kCut = PER_CU > 0;
     if (dma)
-        grouped_kernel<E, OP, BM, BN, WM, WN, CH, S, kCut, true><<<(int)grid, WM * WN * kWave, 0, stream>>>(g);
+        grouped_kernel<E, OP, BM, BN, WM, WN, S, kCut, true><<<(int)grid, WM * WN * kWave, 0, stream>>>(g);
     else
-        grouped_kernel<E, OP, BM, BN, WM, WN, CH, S, kCut, false><<<(int)grid, WM * WN * kWave, 0, stream>>>(g);
+        grouped_kernel<E, OP, BM, BN, WM, WN, S, kCut, false><<<(int)grid, WM * WN * kWave, 0, stream>>>(g);
     return launched();
 }
 
@@ -370,19 +370,19 @@ int launch_grouped(int type, const GroupedArgs &g, bool dma, hipStream_t stream)
         using E = decltype(e);
         if constexpr (OP != kGradW) {
             if (g.P <= (E::kBytes == 4 ? 64 : 32) * (int64_t)g.G) {
-                rc = launch_tile<E, OP, 32, 64, 1, 4, 8, 4, 0>(g, dma, stream);
+                rc = launch_tile<E, OP, 32, 64, 1, 4, 4, 0>(g, dma, stream);
                 return;
             }
         }
         if constexpr (E::kBytes == 4) {
-            rc = launch_tile<E, OP, 64, 64, 2, 2, 8, 2, 0>(g, dma, stream);
+            rc = launch_tile<E, OP, 64, 64, 2, 2, 2, 0>(g, dma, stream);
         } else {
             // Half a tile a group is lost on average.
             const int64_t rows = OP == kGradW ? 2 * g.G * ceil_div(g.M, 256) : 2 * (g.P / 256) + (g.G < g.P ? g.G : g.P);
             if (rows * ceil_div(g.N, 256) * 5 >= 6 * gemm_f32_internal::current_device().cus)
-                rc = launch_tile<E, OP, 256, 256, 2, 4, 8, 2, 1>(g, dma, stream);
+                rc = launch_tile<E, OP, 256, 256, 2, 4, 2, 1>(g, dma, stream);
             else
-                rc = launch_tile<E, OP, 64, 128, 2, 2, 8, 3, 0>(g, dma, stream);
+                rc = launch_tile<E, OP, 64, 128, 2, 2, 3, 0>(g, dma, stream);
         }
     });
     return rc;

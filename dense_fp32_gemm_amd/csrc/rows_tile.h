@@ -1,9 +1,9 @@
 // One output tile of a product on the matrix cores, from panels in LDS.
 //
-// Panels are CH 16-byte chunks (8: 128 bytes, 4: 64 bytes) deep in the summed
-// index, kDeep elements.  An operand lies in LDS as it lies in memory:
+// Panels are kDeep16 16-byte chunks (128 bytes) deep in the summed index, kDeep
+// elements.  An operand lies in LDS as it lies in memory:
 //
-//  * summed index contiguous ("along"): [row][kDeep], CH chunks per row; chunk
+//  * summed index contiguous ("along"): [row][kDeep], eight chunks per row; chunk
 //    c of row r stands at c ^ swz(r), so that 16 rows read at one chunk
 //    column fall on distinct banks;
 //  * row index contiguous ("across"): [kDeep][rows].  The 16-bit types read
@@ -27,21 +27,14 @@
 
 namespace rows {
 
-// Chunk permutation of row r of an "along" panel of CH chunks per row.  A
-// 128-bit LDS read serves lanes {0-3, 12-15, 20-27} together, then {4-11, 16-19,
-// 28-31}, and the same 32 further: rows 0-3 and 12-15 of one chunk column with
-// rows 4-11 of the next.  Both permutations put those 16 chunks on
-// the 16 distinct quarters of the 256 bytes that the banks span (128-byte rows:
-// r>>1, 64-byte rows: r>>2 times 2 in the field of four elements).
-template <int CH>
-__device__ inline int swz_along(int r)
-{
-    static_assert(CH == 8 || CH == 4, "panels are 128 or 64 bytes deep");
-    if constexpr (CH == 8)
-        return (r >> 1) & 7;
-    const int q = (r >> 2) & 3;
-    return ((q << 1) & 3) ^ ((q & 2) ? 3 : 0);
-}
+constexpr int kDeep16 = 8;                           // 16-byte chunks of a panel in the summed index
+
+// Chunk permutation of row r of an "along" panel.  A 128-bit LDS read serves lanes
+// {0-3, 12-15, 20-27} together, then {4-11, 16-19, 28-31}, and the same 32
+// further: rows 0-3 and 12-15 of one chunk column with rows 4-11 of the next.
+// The permutation puts those 16 chunks on the 16 distinct quarters of the 256
+// bytes that the banks span.
+__device__ inline int swz_along(int r) { return (r >> 1) & 7; }
 
 // Chunk permutation of k row k of an "across" panel of RN rows (16-bit types).
 template <int RN>
@@ -56,11 +49,11 @@ __device__ inline int swz_across(int k)
 }
 
 // LDS element offset of chunk c of row r (along) or of k row r (across).
-template <class E, bool ALONG, int RN, int CH>
+template <class E, bool ALONG, int RN>
 __device__ inline int lds_chunk(int r, int c)
 {
     if constexpr (ALONG)
-        return (r * CH + (c ^ swz_along<CH>(r))) * E::kChunk;
+        return (r * kDeep16 + (c ^ swz_along(r))) * E::kChunk;
     else if constexpr (E::kBytes == 2)
         return r * RN + (c ^ swz_across<RN>(r)) * E::kChunk;
     else
@@ -75,7 +68,7 @@ using lds_ptr = __attribute__((address_space(3))) T *;
 
 // Fragments of F consecutive 16-row blocks from row `row0` of a panel, one
 // k step (32 k of a 16-bit type, 16 of binary32: four chunks).
-template <class E, bool ALONG, int RN, int CH, int F>
+template <class E, bool ALONG, int RN, int F>
 struct Fragments {
     using T = typename E::T;
     // rows a group of fragments read together covers, /16
@@ -89,14 +82,14 @@ struct Fragments {
         if constexpr (ALONG) {
 #pragma unroll
             for (int f = 0; f < F; ++f)
-                q[f] = *reinterpret_cast<const u32x4 *>(panel + lds_chunk<E, true, RN, CH>(row0 + 16 * f + i, 4 * step + h));
+                q[f] = *reinterpret_cast<const u32x4 *>(panel + lds_chunk<E, true, RN>(row0 + 16 * f + i, 4 * step + h));
         } else if constexpr (E::kBytes == 2) {
             const int k = 32 * step + 8 * h + i / 4;     // this lane's row of the 4 x 16 block
 #pragma unroll
             for (int f = 0; f < F; ++f) {
                 const int col = row0 + 16 * f + 4 * (i % 4);
-                const T *p0 = panel + lds_chunk<E, false, RN, CH>(k, col / 8) + col % 8;
-                const T *p1 = panel + lds_chunk<E, false, RN, CH>(k + 4, col / 8) + col % 8;
+                const T *p0 = panel + lds_chunk<E, false, RN>(k, col / 8) + col % 8;
+                const T *p1 = panel + lds_chunk<E, false, RN>(k + 4, col / 8) + col % 8;
                 const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr<s16x4>)p0);
                 const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr<s16x4>)p1);
                 q[f] = __builtin_bit_cast(u32x4, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
@@ -136,19 +129,18 @@ __device__ inline f32x4 mfma(u32x4 b, u32x4 a, f32x4 d, int s)
         return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, b), __builtin_bit_cast(f16x8, a), d, 0, 0, 0);
 }
 
-// A workgroup's BM x BN tile, WM x WN waves of (BM/WM) x (BN/WN), panels of CH chunks
-// of the summed index.
-template <class E, bool A_ALONG, bool B_ALONG, int BM_, int BN_, int WM_, int WN_, int CH_ = 8>
+// A workgroup's BM x BN tile, WM x WN waves of (BM/WM) x (BN/WN).
+template <class E, bool A_ALONG, bool B_ALONG, int BM_, int BN_, int WM_, int WN_>
 struct Tile {
     using T = typename E::T;
     static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_;
     static constexpr int kThreads = WM * WN * kWave;
     static constexpr int kFm = BM / WM / 16, kFn = BN / WN / 16;
-    static constexpr int CH = CH_, kDeep = CH * E::kChunk, kSteps = CH / 4;
+    static constexpr int kDeep = kDeep16 * E::kChunk, kSteps = kDeep16 / 4;
     static constexpr int kMfma = kFm * kFn * kPerStep<E>;                 // matrix instructions of a step
     static constexpr int kLdsA = BM * kDeep, kLdsB = BN * kDeep;           // elements of a panel
-    using Fa = Fragments<E, A_ALONG, BM, CH, kFm>;
-    using Fb = Fragments<E, B_ALONG, BN, CH, kFn>;
+    using Fa = Fragments<E, A_ALONG, BM, kFm>;
+    using Fb = Fragments<E, B_ALONG, BN, kFn>;
     static_assert(BM % (16 * WM) == 0 && BN % (16 * WN) == 0, "wave tile");
     static_assert((A_ALONG || (BM & (BM - 1)) == 0) && (B_ALONG || (BN & (BN - 1)) == 0),
                   "the chunk permutations across rows are made for powers of two");
@@ -263,11 +255,11 @@ __device__ inline uint32_t buffer_size(int64_t bytes)
 
 // Operand rows contiguous in the summed index.  row(i, r): byte offset from base of the
 // panel's row r (of chunk i), negative if there is none; rows are K elements long.
-template <class E, int RN, int NT, int CH = 8>
+template <class E, int RN, int NT>
 struct Along {
     using T = typename E::T;
     static constexpr bool kListed = false;
-    static constexpr int kSlots = RN * CH, kDeep = CH * E::kChunk, kCount = (kSlots + NT - 1) / NT;
+    static constexpr int kSlots = RN * kDeep16, kDeep = kDeep16 * E::kChunk, kCount = (kSlots + NT - 1) / NT;
     const char *base;
     int64_t off[kCount];
     int64_t ld;                                      // bytes between rows
@@ -278,7 +270,7 @@ struct Along {
     // whole number of chunks long reads what follows (and is cleared in LDS), zeros past the end.
     __device__ inline int64_t extent() const { return ((rows - 1) * ld + (int64_t)K * E::kBytes + 3) / 4 * 4; }
     // Panel row of chunk i.
-    static __device__ inline int row_of(int i, int tid) { return (tid + i * NT) / CH; }
+    static __device__ inline int row_of(int i, int tid) { return (tid + i * NT) / kDeep16; }
 
     template <class Row>
     __device__ inline Along(const T *base_, int tid_, int K_, int64_t ld_, int rows_, Row &&row)
@@ -286,7 +278,7 @@ struct Along {
     {
 #pragma unroll
         for (int i = 0; i < kCount; ++i) {
-            const int slot = tid + i * NT, r = slot / CH;
+            const int slot = tid + i * NT, r = slot / kDeep16;
             const int64_t o = kSlots % NT == 0 || slot < kSlots ? row(i, r) : -1;
             off[i] = o < 0 ? -1 : o + first_k(i) * E::kBytes;
         }
@@ -298,7 +290,7 @@ struct Along {
     __device__ inline int first_k(int i) const
     {
         const int slot = tid + i * NT;
-        return (slot % CH ^ swz_along<CH>(slot / CH)) * E::kChunk;
+        return (slot % kDeep16 ^ swz_along(slot / kDeep16)) * E::kChunk;
     }
     // Elements from chunk i of the panel at k0 to its row's end (none: zeros), and its
     // offset; inside() for a row that is there.
@@ -309,11 +301,11 @@ struct Along {
 
 // Operand rows contiguous across the summed index: K of them, ld elements apart, columns
 // first .. of cols.
-template <class E, int RN, int NT, int CH = 8>
+template <class E, int RN, int NT>
 struct Across {
     using T = typename E::T;
     static constexpr bool kListed = false;
-    static constexpr int kSlots = RN * CH, kDeep = CH * E::kChunk, kCount = (kSlots + NT - 1) / NT;
+    static constexpr int kSlots = RN * kDeep16, kDeep = kDeep16 * E::kChunk, kCount = (kSlots + NT - 1) / NT;
     static constexpr int kPer = RN / E::kChunk;      // chunks of a k row
     const char *base;
     int64_t ld;                                      // bytes between k rows
@@ -362,9 +354,9 @@ struct Across {
 // The same with k rows in any order: k row k is row list[k] / per_row of
 // `rows` (negative or past them: zeros).  The direct loads take the rows' offsets
 // from LDS, where refill() puts kBlock of them at a time.
-template <class E, int RN, int NT, int CH = 8>
-struct Gathered : Across<E, RN, NT, CH> {
-    using Base = Across<E, RN, NT, CH>;
+template <class E, int RN, int NT>
+struct Gathered : Across<E, RN, NT> {
+    using Base = Across<E, RN, NT>;
     static constexpr int kBlock = 512;
     static constexpr bool kListed = true;
     const int *list;                                 // NULL: k itself
@@ -407,8 +399,8 @@ struct Gathered : Across<E, RN, NT, CH> {
 //
 // DMA: buffer loads write panels straight into a ring of S LDS buffers of
 // kLdsA + kLdsB elements, up to S panels ahead of the matrix cores, one
-// barrier per panel; with 128-byte panels, fragments are read half a panel
-// before they are multiplied.  For rows on 4-byte boundaries less than 2^31 bytes from
+// barrier per panel; fragments are read half a panel before they are
+// multiplied.  For rows on 4-byte boundaries less than 2^31 bytes from
 // their base.  Else the chunks are staged through registers into two
 // buffers, element by element at a row's end.
 // ---------------------------------------------------------------------------
@@ -526,9 +518,9 @@ struct PanelLoads {
     }
 };
 
-template <class E, int RN, int NT, int CH>
-struct PanelLoads<E, Gathered<E, RN, NT, CH>, NT> {
-    using Src = Gathered<E, RN, NT, CH>;
+template <class E, int RN, int NT>
+struct PanelLoads<E, Gathered<E, RN, NT>, NT> {
+    using Src = Gathered<E, RN, NT>;
     using T = typename E::T;
     __device__ inline PanelLoads(const Src &) {}
     __device__ inline void fire(const Src &src, int k0, T *panel, int wave)
@@ -571,7 +563,7 @@ __device__ inline void load_panel(const Src &src, int k0, typename E::T *panel, 
 
 // Zeros over what the last chunk of an "along" operand's rows, K elements long, brought from
 // behind them, in the panel at k0 that they end in (K no whole number of chunks).
-template <class E, class Src, int RN, int CH, int NT>
+template <class E, class Src, int RN, int NT>
 __device__ inline void clear_tail(const Src &src, int k0, typename E::T *panel, int tid)
 {
     if constexpr (Src::kAlong) {
@@ -579,7 +571,7 @@ __device__ inline void clear_tail(const Src &src, int k0, typename E::T *panel, 
         if (from == 0)
             return;
         for (int r = tid; r < RN; r += NT) {
-            typename E::T *p = panel + lds_chunk<E, true, RN, CH>(r, chunk);
+            typename E::T *p = panel + lds_chunk<E, true, RN>(r, chunk);
 #pragma unroll 1
             for (int e = from; e < E::kChunk; ++e)
                 p[e] = (typename E::T)0.f;
@@ -613,9 +605,8 @@ __device__ __forceinline__ void half_panel(Ti &tile, const typename E::T *__rest
     __builtin_amdgcn_sched_barrier(0);
 }
 
-// One-step panels: the panel S - 1 ahead is loaded into `freed`, then this one's
-// fragments are read and multiplied.  Half the fragments' registers: twice the
-// waves, which overlap one another's reads.
+// The panel S - 1 ahead is loaded into `freed`, then this one's fragments are
+// read and multiplied, a step after the other: half the fragments' registers.
 template <class E, class Ti, class Fire>
 __device__ __forceinline__ void whole_panel(Ti &tile, const typename E::T *__restrict__ panel, typename E::T *__restrict__ freed,
                                             Fire &&fire, int wm, int wn, int lane)
@@ -658,8 +649,8 @@ __device__ inline void sum_panels_dma(Ti &tile, int K, const SrcA &a, const SrcB
             __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
         if ((SrcA::kAlong || SrcB::kAlong) && K % E::kChunk != 0 && k0 + BK > K) {
-            clear_tail<E, SrcA, Ti::BM, Ti::CH, NT>(a, k0, panel, tid);
-            clear_tail<E, SrcB, Ti::BN, Ti::CH, NT>(b, k0, panel + Ti::kLdsA, tid);
+            clear_tail<E, SrcA, Ti::BM, NT>(a, k0, panel, tid);
+            clear_tail<E, SrcB, Ti::BN, NT>(b, k0, panel + Ti::kLdsA, tid);
             group_sync<NT>();
         }
     };
@@ -668,7 +659,7 @@ __device__ inline void sum_panels_dma(Ti &tile, int K, const SrcA &a, const SrcB
         __syncthreads();
     }
     // (With rows from a list, 16-bit types have no registers left to read ahead.)
-    if constexpr (Ti::kSteps == 1 || (SrcA::kListed && E::kBytes == 2)) {
+    if constexpr (SrcA::kListed && E::kBytes == 2) {
 #pragma unroll
         for (int q = 0; q < S - 1; ++q)
             if (q == 0 || q * BK < K)

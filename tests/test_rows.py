@@ -433,6 +433,21 @@ def test_adapters_half_precision_range(dev, T, factor):
     oracle.close(got, want, oracle.product_bound(want, size, 64 + 20, torch.float16) + 2.0 ** -16 * size, "Y")
 
 
+@pytest.mark.parametrize("T", [20, 600])
+def test_adapters_half_precision_infinity_beside_large_values(dev, T):
+    """X . A of +inf and of -120000, past the type's range: their sum is +inf."""
+    X = torch.full((T, 2), 60000.0, dtype=torch.float16)
+    A = torch.tensor([[INF, -1.0], [1.0, -1.0]], dtype=torch.float16)[None]
+    B, W = torch.ones(1, 2, 24, dtype=torch.float16), torch.ones(2, 24, dtype=torch.float16)
+    adapter = torch.full((T,), -1, dtype=torch.int32)
+    adapter[5] = 0
+    say("infinity beside large", T)
+    got = gb.adapter_matmul((X * 2.0 ** -3).to(dev), W.to(dev), A.to(dev), B.to(dev), adapter.to(dev),
+                            torch.tensor([8.0], device=dev)).cpu()
+    assert (got[5] == INF).all()
+    assert (got[adapter < 0] == 15000.0).all()       # 2 * 7500, exact
+
+
 # --- together, as a layer uses them ----------------------------------------------------
 def test_expert_layer_forward_and_backward(dev):
     """Router, map, two expert products with silu between, weighted sum; all gradients against 64-bit autograd."""

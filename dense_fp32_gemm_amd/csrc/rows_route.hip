@@ -4,7 +4,7 @@
 //  * route_kernel: 16 or 64 lanes per token, each with every 16th (64th) expert; the
 //    choice is k rounds of a maximum over integer keys.
 //  * route_grad_kernel: the same layout.
-//  * count_slots, place_slots: a stable counting sort of the slots by expert,
+//  * count_slots, sum_counts, place_slots: a stable counting sort of the slots by expert,
 //    a workgroup per kSlotChunk slots.
 //
 // Scores are binary64: which expert is taken hangs on differences between
@@ -408,13 +408,57 @@ __global__ __launch_bounds__(kSlotThreads) void count_slots(const int *index, in
         counts[(int64_t)blockIdx.x * E + tid] = hist[tid];
 }
 
+// counts[b][e] becomes the slots of expert e in the chunks before b, counts[chunks][e]
+// those in all of them.  A workgroup per 64 experts, a wave per part of the chunks.
+__global__ __launch_bounds__(kSlotThreads) void sum_counts(int *counts, int chunks, int E)
+{
+    __shared__ int part[kSlotWaves][kWave];
+    constexpr int kBatch = 8;                        // loads in flight
+    const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+    const int e = blockIdx.x * kWave + lane;
+    const int64_t each = (chunks + kSlotWaves - 1) / kSlotWaves;
+    const int64_t first = wave * each, last = first + each < chunks ? first + each : chunks;
+    int n[kBatch];
+    auto load = [&](int64_t b0) {
+#pragma unroll
+        for (int q = 0; q < kBatch; ++q)
+            n[q] = e < E && b0 + q < last ? counts[(b0 + q) * E + e] : 0;
+    };
+    int sum = 0;
+    for (int64_t b0 = first; b0 < last; b0 += kBatch) {
+        load(b0);
+#pragma unroll
+        for (int q = 0; q < kBatch; ++q)
+            sum += n[q];
+    }
+    part[wave][lane] = sum;
+    __syncthreads();
+    int before = 0, total = 0;
+#pragma unroll
+    for (int w = 0; w < kSlotWaves; ++w) {
+        before += w < wave ? part[w][lane] : 0;
+        total += part[w][lane];
+    }
+    for (int64_t b0 = first; b0 < last; b0 += kBatch) {
+        load(b0);
+#pragma unroll
+        for (int q = 0; q < kBatch; ++q) {
+            if (e < E && b0 + q < last)
+                counts[(b0 + q) * E + e] = before;
+            before += n[q];
+        }
+    }
+    if (wave == 0 && e < E)
+        counts[(int64_t)chunks * E + e] = total;
+}
+
 // Each workgroup places its chunk of kSlotChunk slots.  It needs, per expert, the slots
-// of all chunks and of the chunks before its own: from counts, or (NULL) by
-// counting all S slots itself, which needs no first launch.
+// of all chunks and of the chunks before its own: from counts (`summed`: from
+// sums of them), or (NULL) by counting all S slots itself, which needs no first launch.
 // Wave w takes kSlotChunk / kSlotWaves slots, 64 at a time in rising order;
 // base[w][e] is the next place of expert e for wave w.
 __global__ __launch_bounds__(kSlotThreads) void place_slots(const int *index, int S, int E, const int *counts,
-                                                            int *offsets, int *order, int *position)
+                                                            bool summed, int *offsets, int *order, int *position)
 {
     __shared__ int base[kSlotWaves][GEMM_F32_MAX_EXPERTS];
     __shared__ int others[2][GEMM_F32_MAX_EXPERTS];  // slots of the chunks before and behind
@@ -460,7 +504,10 @@ __global__ __launch_bounds__(kSlotThreads) void place_slots(const int *index, in
         before = others[0][tid];
         total = before + others[1][tid];
     } else {
-        if (tid < E) {
+        if (tid < E && summed) {
+            before = counts[(int64_t)blockIdx.x * E + tid];
+            total = counts[(int64_t)gridDim.x * E + tid];
+        } else if (tid < E) {
             constexpr int kBatch = 8;
             for (int b0 = 0; b0 < (int)gridDim.x; b0 += kBatch) {
                 int n[kBatch];
@@ -476,9 +523,11 @@ __global__ __launch_bounds__(kSlotThreads) void place_slots(const int *index, in
         }
         __syncthreads();
     }
+    if (!summed) {
 #pragma unroll
-    for (int w = 0; w < kSlotWaves; ++w)
-        total += base[w][tid];
+        for (int w = 0; w < kSlotWaves; ++w)
+            total += base[w][tid];
+    }
     int scan = total;                                // inclusive over the wave
 #pragma unroll
     for (int d = 1; d < kWave; d *= 2) {
@@ -544,6 +593,11 @@ int64_t slot_chunks(int64_t S) { return S <= kSlotChunk ? 1 : ceil_div(S, kSlotC
 // launch of their own (16384 slots: 7.7 us in one launch; 65536: 14 us against 10 in
 // two, 131072: 23 against 12).
 constexpr int64_t kCountedInPlace = 1 << 15;
+// From this many chunks on their counts are summed in a launch of their own; fewer,
+// and every workgroup of the last launch adds them up itself (65536 slots: 9.9
+// against 11.4 us with the sums, 131072: 12.3 against 12.0, 1048576: 46 against 22,
+// 16777216: 7600 against 214).
+constexpr int64_t kSummedFrom = 64;
 
 // A grid has fewer than 2^32 threads, a wave of them per token.
 constexpr int kMaxTokens = (int)(UINT32_MAX / kWave) - kRouteWaves;
@@ -657,7 +711,7 @@ size_t gemm_f32_expert_map_ws_size(int S, int E)
 {
     if (S < 0 || E < 1 || E > GEMM_F32_MAX_EXPERTS)
         return 0;
-    return S > kCountedInPlace ? (size_t)slot_chunks(S) * (size_t)E * sizeof(int) : 0;
+    return S > kCountedInPlace ? (size_t)(slot_chunks(S) + 1) * (size_t)E * sizeof(int) : 0;
 }
 
 int gemm_f32_expert_map(int S, int E, const int *index, int *offsets, int *order, int *position, void *workspace,
@@ -676,7 +730,10 @@ int gemm_f32_expert_map(int S, int E, const int *index, int *offsets, int *order
     int *counts = need > 0 ? (int *)workspace : nullptr;
     if (counts != nullptr)
         count_slots<<<grid, kSlotThreads, 0, stream>>>(index, S, E, counts);
-    place_slots<<<grid, kSlotThreads, 0, stream>>>(index, S, E, counts, offsets, order, position);
+    const bool summed = counts != nullptr && grid >= kSummedFrom;
+    if (summed)
+        sum_counts<<<(int)ceil_div(E, kWave), kSlotThreads, 0, stream>>>(counts, grid, E);
+    place_slots<<<grid, kSlotThreads, 0, stream>>>(index, S, E, counts, summed, offsets, order, position);
     return launched();
 }
 

@@ -68,7 +68,7 @@ struct UpRows : Across<E, RN, NT> {
     }
     __device__ inline int rank(int i, int k0) const { return k0 / Base::kDeep * kPanelRanks + this->krow(i) % kPanelRanks; }
     __device__ inline int64_t step() const { return kPanelRanks * this->ld; }
-    __device__ inline bool partial(int k0) const { return (k0 / Base::kDeep + 1) * kPanelRanks > R; }
+    __device__ inline bool last(int k0) const { return (k0 / Base::kDeep + 1) * kPanelRanks + E::kChunk >= R; }
     __device__ inline int left(int i, int k0) const { return rank(i, k0) < R ? Base::left(i, k0) : 0; }
     __device__ inline int inside(int i, int k0) const { return left(i, k0); }
     __device__ inline int64_t offset(int i, int) const
@@ -420,7 +420,7 @@ struct Big {
     static constexpr int BN = E::kBytes == 2 ? 256 : 64, WM = 2, WN = E::kBytes == 2 ? 4 : 2;
     static constexpr int kThreads = WM * WN * kWave;
     static constexpr bool kCut = BM == 256;
-    static constexpr int S = BM == 128 || BM == 160 ? 3 : 2;                 // panels in LDS
+    static constexpr int S = BM == 160 ? 3 : 2;                              // panels in LDS
     static constexpr int kLds = (kCut ? 9 * 128 : S * (BM + BN)) * panel_deep<E>();   // cut: three of a half, four of a quarter
 };
 
@@ -474,13 +474,20 @@ void cut(int64_t panels, int64_t want, int64_t least, int panel, int *parts, int
     *length = (int)(each * panel);
 }
 
+// Few rows: fewer than 128 tiles of 128 x 128, and no more rows than the parts' own traffic
+// allows (us a call, R = 16, 8 adapters, few against many.  bf16, K = N = 4096: 64
+// rows 21 and 77, 384: 46 and 58, 512: 61 and 57, 1024: 91 and 60; K = N = 2048, 768 rows: 36
+// and 37; K = N = 1024: 512 rows 19 and 28, 1500: 26 and 28, 2048: 28 and 29.
+// binary32, K = N = 1024: 512 rows 28 and 41, 1024: 42 and 41).
+// Ranks: many rows of 17 to 32 take a block of 32 of them (2050 rows, R = 32: 105 against
+// 108 with 64; 8192 rows, K = N = 1024: 45 against 47).
 template <class E>
 Split plan(int T, int N, int K, int R)
 {
     Split p{};
     const int panel = panel_deep<E>();
     const int64_t panels = ceil_div(K, panel), rows16 = ceil_div(T, 16);
-    p.few = ceil_div(T, 128) * ceil_div(N, 128) < 128 && T <= 512;
+    p.few = ceil_div(T, 128) * ceil_div(N, 128) < 128 && T <= (E::kBytes == 4 ? 512 : 2048);
     p.rank_block = R <= 16 ? 16 : R <= 32 && !p.few ? 32 : 64;
     p.ranks = (int)ceil_div(R, p.rank_block);
     if (R > 0) {
@@ -564,8 +571,11 @@ int launch_many(AdapterArgs g, bool dma, hipStream_t stream)
     return launched();
 }
 
-// The tile: its panels' rate from L2 bounds a compute unit, so the cost of a round is BM +
-// 256; the lowest tiles that fit one round, else 256 x 256.
+// The tile: its panels' rate from L2 bounds a compute unit, so the cost of a round is about
+// BM + 256.  256 x 256, whose last round is cut into halves or quarters, but 160 x
+// 256 where those fit one round and the halves of the others do not (bf16, K = N = 4096, R =
+// 16, us a call, 256 against 160: 1024 rows 64 and 93, 2050: 125 and 95, 2560:
+// 123 and 97, 2600: 124 and 155, 8192: 274 and 324).  binary32: 64 x 64.
 template <class E>
 int many_rows(const AdapterArgs &g, bool dma, hipStream_t stream)
 {
@@ -573,9 +583,7 @@ int many_rows(const AdapterArgs &g, bool dma, hipStream_t stream)
         return launch_many<E, 64>(g, dma, stream);
     } else {
         const int64_t cus = gemm_f32_internal::current_device().cus, tn = ceil_div(g.N, 256);
-        if (ceil_div(g.T, 128) * tn <= cus)
-            return launch_many<E, 128>(g, dma, stream);
-        if (ceil_div(g.T, 160) * tn <= cus)
+        if (2 * ceil_div(g.T, 256) * tn > cus && ceil_div(g.T, 160) * tn <= cus)
             return launch_many<E, 160>(g, dma, stream);
         return launch_many<E, 256>(g, dma, stream);
     }

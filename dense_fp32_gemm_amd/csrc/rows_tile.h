@@ -284,8 +284,9 @@ struct Along {
         }
     }
     __device__ inline int64_t step() const { return kDeep * E::kBytes; }   // bytes from panel to panel
-    // Whether chunks that panel 0 has may be missing from the panel at k0.
-    __device__ inline bool partial(int k0) const { return K - k0 < kDeep; }
+    // Whether the panel at k0 is the last: chunks that panel 0 has may be missing from it,
+    // and others reach past a row's end.
+    __device__ inline bool last(int k0) const { return K - k0 <= kDeep; }
     // First k of chunk i in panel 0.  (Recomputed where it is needed: registers are short.)
     __device__ inline int first_k(int i) const
     {
@@ -342,7 +343,9 @@ struct Across {
     // k rows from chunk 0 to chunk i, as loaded.
     static __device__ inline int row_step(int i) { return i * kRowStep; }
     __device__ inline int64_t step() const { return kDeep * ld; }
-    __device__ inline bool partial(int k0) const { return K - k0 < kDeep; }
+    // Whether k rows may be missing from the panel at k0, or a chunk of it (of kChunk k rows
+    // where they are one element long) reaches past the last one.
+    __device__ inline bool last(int k0) const { return K - k0 <= kDeep + E::kChunk; }
     __device__ inline int left(int i, int k0) const
     {
         return (kSlots % NT == 0 || tid + i * NT < kSlots) && k0 + krow(i) < K ? cols - col(i) : 0;
@@ -473,12 +476,10 @@ struct PanelLoads {
     static constexpr bool kOne = Src::kOneColumn;
     uint32_t off[kOne ? 1 : Src::kCount];
     const char *base;                                // of the next panel
-    int64_t bytes, step;                             // from there to the operand's end; to the panel after it
+    int64_t step;                                    // to the panel after it
     __device__ inline PanelLoads(const Src &src, int from = 0) : step(src.step())
     {
-        const int64_t done = from / Src::kDeep * step;
-        base = src.base + done;
-        bytes = src.extent() - done;
+        base = src.base + from / Src::kDeep * step;
         if constexpr (kOne) {
             off[0] = src.col(0) < src.cols ? (uint32_t)src.offset(0, 0) : kNowhere;
         } else {
@@ -497,24 +498,25 @@ struct PanelLoads {
     }
     __device__ inline void fire(const Src &src, int k0, T *panel, int wave)
     {
-        const auto rsrc = __builtin_amdgcn_make_buffer_rsrc((void *)base, 0, (int)buffer_size(bytes), kRawBufferFlags);
-        base += step;
-        bytes -= step;
-        auto load = [&](int i, uint32_t o) {
+        auto load = [&](uint32_t size, int i, uint32_t o) {
+            const auto rsrc = __builtin_amdgcn_make_buffer_rsrc((void *)base, 0, (int)size, kRawBufferFlags);
             if (Src::kSlots % NT != 0 && (i * NT + wave * kWave) >= Src::kSlots)
                 return;                              // whole waves: kSlots is a multiple of 64
             auto *dst = (lds_ptr<void>)(panel + (i * NT + wave * kWave) * E::kChunk);
             __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, dst, 16, o, 0, 0, 0);
         };
-        if (!src.partial(k0)) {
+        // The operand's end and missing chunks matter to its last panel alone (last()).
+        if (!src.last(k0)) {
 #pragma unroll
             for (int i = 0; i < Src::kCount; ++i)
-                load(i, at(src, i));
+                load(kNowhere, i, at(src, i));
         } else {
+            const uint32_t size = buffer_size(src.extent() - (base - src.base));
 #pragma unroll
             for (int i = 0; i < Src::kCount; ++i)
-                load(i, src.inside(i, k0) > 0 ? at(src, i) : kNowhere);
+                load(size, i, src.inside(i, k0) > 0 ? at(src, i) : kNowhere);
         }
+        base += step;
     }
 };
 

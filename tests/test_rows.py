@@ -336,6 +336,7 @@ ADAPTERS = [
     (1, 1, 1, 1, 1), (1, 64, 128, 16, 3), (3, 130, 70, 5, 2), (16, 256, 264, 8, 40), (17, 200, 72, 24, 4), (64, 512, 256, 32, 64),
     (130, 96, 136, 33, 3), (300, 128, 200, 64, 5), (20, 64, 64, 200, 2), (50, 1000, 63, 4, 50), (5, 0, 8, 4, 2), (9, 40, 40, 0, 3),
     (33, 4096, 256, 16, 30), (515, 64, 200, 8, 4), (780, 130, 72, 40, 5), (560, 72, 330, 130, 2),
+    (2060, 64, 200, 8, 4), (2055, 130, 72, 40, 5), (2049, 72, 330, 130, 2), (2051, 66, 1, 33, 2),
 ]
 
 
@@ -401,7 +402,7 @@ def test_adapters_large_tiles_whole_and_cut(dev, dtype, T, N, R, n, run):
 
 
 @pytest.mark.parametrize("dtype", TYPES, ids=IDS)
-@pytest.mark.parametrize("T", [3, 40, 150, 600])
+@pytest.mark.parametrize("T", [3, 40, 150, 600, 2100])
 def test_adapters_infinities_stay_with_their_requests(dev, dtype, T):
     g = seeded("inf adapters", T)
     X, W = normal(g, T, 64, dtype=dtype), normal(g, 64, 72, dtype=dtype)
@@ -418,7 +419,7 @@ def test_adapters_infinities_stay_with_their_requests(dev, dtype, T):
 
 
 @pytest.mark.parametrize("factor", [2.0 ** -30, 2.0 ** 14])
-@pytest.mark.parametrize("T", [20, 600])
+@pytest.mark.parametrize("T", [20, 600, 2100])
 def test_adapters_half_precision_range(dev, T, factor):
     """The low-rank intermediate may lie outside the 16-bit type's range."""
     g = seeded("range")
@@ -433,7 +434,7 @@ def test_adapters_half_precision_range(dev, T, factor):
     oracle.close(got, want, oracle.product_bound(want, size, 64 + 20, torch.float16) + 2.0 ** -16 * size, "Y")
 
 
-@pytest.mark.parametrize("T", [20, 600])
+@pytest.mark.parametrize("T", [20, 600, 2100])
 def test_adapters_half_precision_infinity_beside_large_values(dev, T):
     """X . A of +inf and of -120000, past the type's range: their sum is +inf."""
     X = torch.full((T, 2), 60000.0, dtype=torch.float16)

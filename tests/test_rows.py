@@ -563,6 +563,75 @@ def test_calls_on_another_stream_and_in_a_graph(dev):
             assert torch.equal(a, b)
 
 
+def test_two_streams_at_once(dev):
+    """Calls with workspaces of their own on two streams, many times, give what they give one after the other."""
+    T, E, k, N, R = 300, 64, 8, 136, 16
+    sides = [torch.cuda.Stream(), torch.cuda.Stream()]
+    sets = []
+    for q in range(2):
+        g = seeded("streams", q)
+        index = torch.randint(-1, E, (T * 500, k), generator=g, dtype=torch.int32).to(dev)
+        X, W = normal(g, T, 256, dtype=torch.float16).to(dev), normal(g, 256, N, dtype=torch.float16).to(dev)
+        A, B = normal(g, 5, 256, R, dtype=torch.float16).to(dev), normal(g, 5, R, N, dtype=torch.float16).to(dev)
+        adapter = torch.randint(-1, 5, (T,), generator=g, dtype=torch.int32).to(dev)
+        sets.append((index, X, W, A, B, adapter))
+
+    def both(index, X, W, A, B, adapter, stream=None):
+        return [*gb.expert_map(index, E, stream=stream), gb.adapter_matmul(X, W, A, B, adapter, stream=stream)]
+
+    say("one after the other")
+    want = [both(*s) for s in sets]
+    torch.cuda.synchronize()
+    say("at once")
+    got = [[], []]
+    for _ in range(10):
+        for q in range(2):
+            got[q].append(both(*sets[q], stream=sides[q]))
+    torch.cuda.synchronize()
+    for q in range(2):
+        for run in got[q]:
+            for a, b in zip(run, want[q]):
+                assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=IDS)
+def test_offsets_past_the_places_are_clamped(dev, dtype):
+    g = seeded("clamped", dtype)
+    X, W = normal(g, 10, 24, dtype=dtype).to(dev), normal(g, 2, 24, 40, dtype=dtype).to(dev)
+    dY = normal(g, 10, 40, dtype=dtype).to(dev)
+    right = torch.tensor([0, 3, 10], dtype=torch.int32, device=dev)
+    for wrong in ([-4, 3, 50], [0, 3, 2 ** 31 - 1], [-2 ** 31, 3, 11]):
+        say("offsets", wrong, dtype)
+        o = torch.tensor(wrong, dtype=torch.int32, device=dev)
+        assert torch.equal(gb.grouped_matmul(X, W, o), gb.grouped_matmul(X, W, right))
+        assert torch.equal(gb.grouped_grad_x(dY, W, o), gb.grouped_grad_x(dY, W, right))
+        assert torch.equal(gb.grouped_grad_w(X, dY, o), gb.grouped_grad_w(X, dY, right))
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=IDS)
+@pytest.mark.parametrize("K", [57, 63, 64, 65, 71, 72, 73, 128, 136])
+@pytest.mark.parametrize("N", [1, 2, 7])
+def test_narrow_matrices_at_the_end_of_their_memory(dev, dtype, K, N):
+    """Rows of a few elements, whose last chunks would span several rows; what follows is NaN."""
+    g = seeded("narrow", K, N)
+    ld = N + N % 2
+    W = normal(g, 2, K, N, dtype=dtype)
+    buf = torch.full((2 * K * ld + 64,), NAN, dtype=dtype, device=dev)
+    Wd = buf[:2 * K * ld].view(2, K, ld)[:, :, :N]
+    Wd.copy_(W.to(dev))
+    X = normal(g, 40, K, dtype=dtype)
+    offsets = torch.tensor([0, 17, 40], dtype=torch.int32)
+    say("narrow", K, N, dtype)
+    want, size = grouped_want(X, W, offsets, torch.arange(40, dtype=torch.int32), 1)
+    got = gb.grouped_matmul(X.to(dev), Wd, offsets.to(dev))
+    oracle.close(got, want, oracle.product_bound(want, size, K + 1, dtype), "Y")
+    none = torch.full((40,), -1, dtype=torch.int32, device=dev)
+    want, size = X.double() @ W[1].double(), X.double().abs() @ W[1].double().abs()
+    A, B = torch.zeros(1, K, 4, dtype=dtype, device=dev), torch.zeros(1, 4, N, dtype=dtype, device=dev)
+    got = gb.adapter_matmul(X.to(dev), Wd[1], A, B, none)
+    oracle.close(got, want, oracle.product_bound(want, size, K + 1, dtype), "adapters")
+
+
 def test_far_rows(dev):
     """Offsets past 2^32 bytes: rows far apart in one buffer."""
     ld = (1 << 31) // 64 + 8                                     # 33 rows span over 2^31 elements

@@ -459,7 +459,7 @@ __global__ __launch_bounds__(kSlotThreads) void sum_counts(int *counts, int chun
 // Each workgroup places its chunk of kSlotChunk slots.  It needs, per expert, the slots
 // of all chunks and of the chunks before its own: from counts (`summed`: from
 // sums of them), or (NULL) by counting all S slots itself, which needs no first launch.
-// 65536 slots 7.8 us, 131072, from sums, 5.7 us: chains of LDS atomics and ballots, no bandwidth.
+// 65536 slots 7.8 us, 131072 9.6 us: chains of LDS atomics and ballots, no bandwidth.
 // Wave w takes kSlotChunk / kSlotWaves slots, 64 at a time in rising order;
 // base[w][e] is the next place of expert e for wave w.
 __global__ __launch_bounds__(kSlotThreads) void place_slots(const int *index, int S, int E, const int *counts,
@@ -599,10 +599,10 @@ int64_t slot_chunks(int64_t S) { return S <= kSlotChunk ? 1 : ceil_div(S, kSlotC
 // two, 131072: 23 against 12).
 constexpr int64_t kCountedInPlace = 1 << 15;
 // From this many chunks on their counts are summed in a launch of their own; fewer,
-// and every workgroup of the last launch adds them up itself (65536 slots: 9.9
-// against 11.4 us with the sums, 131072: 12.3 against 12.0, 1048576: 46 against 22,
+// and every workgroup of the last launch adds them up itself (in a graph, 65536 slots: 9.9
+// against 11.4 us with the sums, 131072: 12.3 against 12.0, 262144: 16.6 against 12.8, 1048576: 46 against 22,
 // 16777216: 7600 against 214).
-constexpr int64_t kSummedFrom = 64;
+constexpr int64_t kSummedFrom = 128;
 
 // A grid has fewer than 2^32 threads, a wave of them per token.
 constexpr int kMaxTokens = (int)(UINT32_MAX / kWave) - kRouteWaves;

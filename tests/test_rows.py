@@ -145,7 +145,7 @@ def test_route_grad_adds_what_an_index_named_twice_gets(dev):
 
 
 @pytest.mark.parametrize("S,E", [(0, 3), (1, 1), (5, 4), (64, 64), (2047, 7), (2048, 1024), (2049, 3), (6000, 130), (20001, 1000), (32768, 9),
-                                 (32769, 64), (150001, 256), (1 << 17, 130), ((1 << 17) - 1, 5), ((1 << 19) + 33, 7), (4000001, 1024)])
+                                 (32769, 64), (150001, 256), (1 << 17, 130), ((1 << 18) - 2048, 5), (1 << 18, 130), ((1 << 19) + 33, 7), (4000001, 1024)])
 def test_expert_map(dev, S, E):
     g = seeded("map", S, E)
     index = torch.randint(-1, E + 1, (S,), generator=g, dtype=torch.int32)      # -1 and E: left out

@@ -608,18 +608,41 @@ __device__ __forceinline__ void half_panel(Ti &tile, const typename E::T *__rest
 }
 
 // The panel S - 1 ahead is loaded into `freed`, then this one's fragments are
-// read and multiplied, a step after the other: half the fragments' registers.
+// read and multiplied, the first operand's two row blocks ahead of their use and the
+// second's a step: half the fragments' registers (bf16, 16384 places over 8 groups,
+// 2048 x 2048, both gradients: 342 us against 356 with a step read, then multiplied).
 template <class E, class Ti, class Fire>
 __device__ __forceinline__ void whole_panel(Ti &tile, const typename E::T *__restrict__ panel, typename E::T *__restrict__ freed,
                                             Fire &&fire, int wm, int wn, int lane)
 {
     fire(freed);
+    __builtin_amdgcn_sched_barrier(0);
+    static_assert(Ti::kSteps == 2 && kPerStep<E> == 1 && Ti::kFm >= 2, "the order below");
+    typename Ti::Step f[2];
 #pragma unroll
-    for (int step = 0; step < Ti::kSteps; ++step) {
-        typename Ti::Step f;
-        f.read(panel, step, wm, wn, lane);
-        tile.multiply(f);
+    for (int step = 0; step < 2; ++step) {
+        f[step].b.read(panel + Ti::kLdsA, wn * (Ti::BN / Ti::WN), step, lane);
+        f[step].a.read(panel, wm * (Ti::BM / Ti::WM), step, lane);
+        tile.multiply(f[step]);
     }
+    constexpr int kB = Ti::Fb::kReads, kA = Ti::Fa::kReads / Ti::kFm, kFirst = kB + 2 * kA;   // LDS reads
+    __builtin_amdgcn_sched_group_barrier(0x100, kFirst, 0);
+#pragma unroll
+    for (int step = 0; step < 2; ++step) {
+#pragma unroll
+        for (int m = 0; m < Ti::kFm - 2; ++m) {
+            __builtin_amdgcn_sched_group_barrier(0x008, Ti::kFn, 0);
+            __builtin_amdgcn_sched_group_barrier(0x100, kA, 0);
+        }
+        if (step == 0) {
+            __builtin_amdgcn_sched_group_barrier(0x008, Ti::kFn, 0);
+            __builtin_amdgcn_sched_group_barrier(0x100, kFirst / 2, 0);
+            __builtin_amdgcn_sched_group_barrier(0x008, Ti::kFn, 0);
+            __builtin_amdgcn_sched_group_barrier(0x100, kFirst - kFirst / 2, 0);
+        }
+    }
+    __builtin_amdgcn_sched_group_barrier(0x008, 2 * Ti::kFn, 0);
+    __builtin_amdgcn_sched_barrier(0);
 }
 
 template <class E, int S, class Ti, class SrcA, class SrcB>

@@ -97,8 +97,8 @@ __device__ inline Place locate(const GroupedArgs &g, int bm, int t)
 
 // Tile t of dW.  A group's tiles cost its number of places, so each die's range of t has a
 // slice of every group (both gradients, 4096 x 4 slots over 16 experts of unlike
-// shares, 2048 x 2048, bf16: 352 us against 402 with whole groups to a die; 8192 x 2 over 8:
-// 346 against 445; 1025 x 2 over 8, 1000 x 1023, binary32: 104 against 136).
+// shares, 2048 x 2048, bf16: 351 us against 402 with whole groups to a die; 8192 x 2 over 8:
+// 343 against 445; 1025 x 2 over 8, 1000 x 1023, binary32: 104 against 136).
 __device__ inline Place spread(const GroupedArgs &g, int tiles_m, int t)
 {
     const int per = tiles_m * g.tiles_n;
@@ -109,7 +109,10 @@ __device__ inline Place spread(const GroupedArgs &g, int tiles_m, int t)
         to = (int)((int64_t)per * (s + 1) / g.xcds);
     }
     const int rest = t - g.G * from, r = from + rest % (to - from);
-    return Place{rest / (to - from), 0, 0, r % tiles_m, r / tiles_m};
+    // two columns of tiles side by side, so that a slice shares rows and columns (the first two
+    // cases above: 345 against 351 with one column after the other, 335 against 343)
+    const int band = r / (2 * tiles_m), q = r - band * 2 * tiles_m, wide = min(2, g.tiles_n - 2 * band);
+    return Place{rest / (to - from), 0, 0, q / wide, 2 * band + q % wide};
 }
 
 // One tile: rows m0 .. m_end - 1 (places; of dW: rows of the matrix), columns from n0 on.

@@ -10,8 +10,8 @@
 //  2. factor_kernel: adds the splits, scales, and writes each row of U as the
 //     up-projection's operand: binary32 as it is, 16-bit types as high + low
 //     parts (two 16-bit numbers per value: 16 to 22 bits instead of 8 to 11,
-//     so that rounding U adds nothing to the rounding of Y) times a power of two
-//     per row, which keeps them inside the type's range.
+//     so that rounding U adds little to the rounding of Y) times a power of two
+//     per row, which keeps them inside the type's range (see factor_kernel).
 //  3. adapters_kernel: the tile of X.W, then for each adapter among its
 //     rows the product of U's rows with B_a, of which only that adapter's rows
 //     are added.
@@ -270,6 +270,11 @@ __global__ __launch_bounds__(kWave) void join_kernel(AdapterArgs g)
 // Many rows
 // ---------------------------------------------------------------------------
 // A wave per row.  2050 rows of rank 32: 5 us, latency of the parts.
+//
+// The scale of half rows puts the largest value next to the top of the type's range: a part
+// has 11 bits down to 2^-14 and nothing under 2^-25, so the two together are off by at most
+// 2^-22 of the value or 2^-39 of the row's largest.  (Sums of their products stay
+// under 2^15 * 2^16 * 2 * 256.)  bfloat16 parts have binary32's range and 16 bits together.
 constexpr int kFactorThreads = 256;
 
 template <class E>
@@ -307,8 +312,9 @@ __global__ __launch_bounds__(kFactorThreads) void factor_kernel(AdapterArgs g)
 #pragma unroll
         for (int d = kWave / 2; d > 0; d /= 2)
             top = fmaxf(top, __shfl_xor(top, d));
-        // the row's largest finite value to [1, 2); rows without one as they are
-        const int up = top > 0.f ? max(ilogbf(top), -100) : 0;
+        // the row's largest finite value to [2^14, 2^15), bfloat16 [1, 2); rows without one as they are
+        constexpr int kTop = std::is_same<E, F16>::value ? 14 : 0;
+        const int up = top > 0.f ? max(ilogbf(top), -100) - kTop : 0;
 #pragma unroll
         for (int q = 0; q < kPer; ++q) {
             const int r = q * kWave + lane;

@@ -171,7 +171,9 @@ GEMM_F32_API int gemm_f32_combine_grad(int type, int T, int k, int N, int P,
  *
  * X [T x K], W [K x N], A_a [K x R] at A + a * stride_a, B_a [R x N] at
  * B + a * stride_b, a < n; scale NULL: 1.  Rows whose adapter is outside
- * 0..n-1 get the shared product alone.  X . A_a is kept in binary32.  R = 0 or
+ * 0..n-1 get the shared product alone.  scale[a] * (X . A_a) is a binary32 sum; calls
+ * of many rows keep it in two parts of a 16-bit type, which is off by at most 2^-16 of each
+ * value for bfloat16, and for half by 2^-22 of it or 2^-39 of its row's largest.  R = 0 or
  * n = 0: no additions, and A, B, adapter may be NULL.  R is at most
  * GEMM_F32_MAX_RANK.  Any order of adapters is right; rows of one
  * adapter side by side are fastest.

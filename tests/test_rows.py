@@ -682,3 +682,28 @@ def test_refusals_with_gpu_tensors(dev):
         gb.adapter_matmul(x, W[0], torch.zeros(1, 8, 4, device=dev), torch.zeros(1, 4, 5, device=dev), o[:1].expand(4).contiguous(),
                           workspace=torch.zeros(8, dtype=torch.uint8, device=dev))
     assert e.value.status == gb.GEMM_F32_ERR_WORKSPACE
+
+
+# T, N on both sides of the limit between few rows (binary32 intermediate) and many
+ADAPTER_ROWS = [(20, 24), (2100, 24), (20, 16400)]
+
+
+@pytest.mark.parametrize("T,N", ADAPTER_ROWS)
+@pytest.mark.parametrize("low", [2.0 ** -27, 2.0 ** -31, 1.3e-6, 2.0 ** -13 * 1.7], ids=["2^-27", "2^-31", "1.3e-6", "1.7*2^-13"])
+def test_adapters_half_precision_unlike_ranks(dev, T, N, low):
+    """A rank far below its row's largest one counts where the largest meets zeros."""
+    x = torch.tensor([1.0, low * 2.0 ** 12], dtype=torch.float32).half()
+    X = x.expand(T, 2).contiguous()
+    A = torch.tensor([[1.0, 0.0], [0.0, 2.0 ** -12]], dtype=torch.float16)[None]
+    B = torch.zeros(1, 2, N, dtype=torch.float16)
+    B[0, 1] = 32768.0
+    adapter = torch.zeros(T, dtype=torch.int32)
+    adapter[::3] = -1
+    say("unlike ranks", T, N, low)
+    got = gb.adapter_matmul(X.to(dev), torch.zeros(2, N, dtype=torch.float16, device=dev), A.to(dev), B.to(dev), adapter.to(dev))
+    u = float(x[1]) * 2.0 ** -12                     # exact in binary32, as is its product with 2^15
+    want = torch.where(adapter[:, None] == 0, torch.tensor(u * 32768.0, dtype=torch.float64), torch.zeros((), dtype=torch.float64)).expand(T, N)
+    # x has 11 bits: U is exact in two parts as long as it is a multiple of 2^-39 of the row's largest, 1; the
+    # sum is one product; one rounding to half
+    assert u % 2.0 ** -39 == 0
+    oracle.close(got, want, oracle.STEP[torch.float16] * want.abs() + oracle.TINY[torch.float16], "Y")

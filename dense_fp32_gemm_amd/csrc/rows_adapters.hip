@@ -300,7 +300,7 @@ __global__ __launch_bounds__(kFactorThreads) void factor_kernel(AdapterArgs g)
         if (r < g.R)
             for (int i = 0; i < g.splits_u; ++i)
                 u[q] += g.partial_u[((int64_t)i * g.T + t) * g.R + r];
-        u[q] *= s;
+        u[q] = r < g.R ? u[q] * s : 0.f;             // what pads the ranks stays 0 under an infinite scale
         top = fmaxf(top, fabsf(u[q]) < INFINITY ? fabsf(u[q]) : 0.f);
     }
     if constexpr (E::kBytes == 4) {

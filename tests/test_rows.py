@@ -707,3 +707,20 @@ def test_adapters_half_precision_unlike_ranks(dev, T, N, low):
     # sum is one product; one rounding to half
     assert u % 2.0 ** -39 == 0
     oracle.close(got, want, oracle.STEP[torch.float16] * want.abs() + oracle.TINY[torch.float16], "Y")
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=IDS)
+@pytest.mark.parametrize("T,N", ADAPTER_ROWS)
+@pytest.mark.parametrize("R", [8, 40])
+def test_adapters_infinite_scale(dev, dtype, T, N, R):
+    """scale = inf times a sum without zeros is the infinity of the sum's sign, however many ranks pad a panel."""
+    X = torch.ones(T, 8, dtype=dtype)
+    A = torch.full((2, 8, R), 0.25, dtype=dtype)
+    B = torch.ones(2, R, N, dtype=dtype)
+    B[:, :, N // 2:] = -1.0
+    adapter = (torch.arange(T) % 2).int()
+    say("infinite scale", T, N, R, dtype)
+    got = gb.adapter_matmul(X.to(dev), torch.zeros(8, N, dtype=dtype, device=dev), A.to(dev), B.to(dev), adapter.to(dev),
+                            torch.tensor([INF, 3.0], device=dev)).cpu().double()
+    assert (got[::2, :N // 2] == INF).all() and (got[::2, N // 2:] == -INF).all()
+    assert (got[1::2, :N // 2] == 6.0 * R).all() and (got[1::2, N // 2:] == -6.0 * R).all()       # exact: R * 3 * 2

@@ -365,6 +365,7 @@ __device__ inline void adapters_tile(const AdapterArgs &g, int m0, int n0, typen
             adds[m] = adapter_of(g, m0 + r, m0 + r < g.T);
             unscale[m] = E::kBytes == 2 && adds[m] >= 0 ? g.unscale[m0 + r] : 1.f;
         }
+        static_assert(Ti::kSteps == 2 && (E::kBytes == 4 || Ti::kDeep == 2 * kPanelRanks), "a step for the high parts, one for the low");
         // Every row's U, whichever adapter made it (rows without one hold anything):
         // a row of sums is taken only with its own adapter's B.
         const Along<E, BM, NT> u((const T *)g.factor + (int64_t)m0 * g.depth, tid, g.depth, g.depth, g.T - m0,
@@ -394,10 +395,19 @@ __device__ inline void adapters_tile(const AdapterArgs &g, int m0, int n0, typen
                     for (int n = 0; n < Ti::kFn; ++n) {
                         add[n] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                        for (int step = 0; step < Ti::kSteps; ++step)
+                        for (int step = 0; step < Ti::kSteps; ++step) {
+                            f32x4 sum = add[n];
 #pragma unroll
                             for (int s = 0; s < kPerStep<E>; ++s)
-                                add[n] = mfma<E>(fb[step].q[n], fa[step].q[0], add[n], s);
+                                sum = mfma<E>(fb[step].q[n], fa[step].q[0], sum, s);
+                            // 16-bit types: step 0 holds the high parts, step 1 the low ones, which
+                            // an infinity of B must not meet: their signs differ, or they are 0
+                            if constexpr (E::kBytes == 2)
+#pragma unroll
+                                for (int i = 0; i < 4; ++i)
+                                    sum[i] = step == 0 || fabsf(add[n][i]) < INFINITY ? sum[i] : add[n][i];
+                            add[n] = sum;
+                        }
                     }
                     const bool mine = adds[m] == a;
 #pragma unroll

@@ -724,3 +724,25 @@ def test_adapters_infinite_scale(dev, dtype, T, N, R):
                             torch.tensor([INF, 3.0], device=dev)).cpu().double()
     assert (got[::2, :N // 2] == INF).all() and (got[::2, N // 2:] == -INF).all()
     assert (got[1::2, :N // 2] == 6.0 * R).all() and (got[1::2, N // 2:] == -6.0 * R).all()       # exact: R * 3 * 2
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=IDS)
+@pytest.mark.parametrize("T,N", ADAPTER_ROWS)
+def test_adapters_infinity_in_the_second_factor(dev, dtype, T, N):
+    """An infinity of B times a rank that is no zero is an infinity of the rank's sign, not NaN."""
+    g = seeded("inf of B", T, N)
+    X, W = normal(g, T, 40, dtype=dtype), normal(g, 40, N, dtype=dtype, scale=40 ** -0.5)
+    A, B = normal(g, 3, 40, 33, dtype=dtype, scale=40 ** -0.5), normal(g, 3, 33, N, dtype=dtype)
+    adapter = (torch.arange(T) % 4 - 1).int()
+    low = torch.mm(X.double(), A[1].double())
+    B[1, 3, 5], B[1, 32, 9] = INF, -INF
+    say("infinity of B", T, N, dtype)
+    got = gb.adapter_matmul(X.to(dev), W.to(dev), A.to(dev), B.to(dev), adapter.to(dev)).cpu().double()
+    mine = adapter == 1
+    # 40 products whose magnitudes' sum is under 9.2 are off by under 2 * 41 * 2^-23 * 9.2 < 2^-13; no rank here is that near to zero
+    assert low[mine][:, [3, 32]].abs().min() > 2.0 ** -13
+    assert torch.equal(got[mine][:, 5], INF * low[mine][:, 3].sign())
+    assert torch.equal(got[mine][:, 9], -INF * low[mine][:, 32].sign())
+    others = torch.ones(T, N, dtype=torch.bool)
+    others[mine] = torch.tensor([n not in (5, 9) for n in range(N)])
+    assert got[others].isfinite().all()

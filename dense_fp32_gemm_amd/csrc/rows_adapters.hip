@@ -274,7 +274,9 @@ __global__ __launch_bounds__(kWave) void join_kernel(AdapterArgs g)
 // The scale of half rows puts the largest value next to the top of the type's range: a part
 // has 11 bits down to 2^-14 and nothing under 2^-25, so the two together are off by at most
 // 2^-22 of the value or 2^-39 of the row's largest.  (Sums of their products stay
-// under 2^15 * 2^16 * 2 * 256.)  bfloat16 parts have binary32's range and 16 bits together.
+// under 2^15 * 2^16 * 2 * 256.)  bfloat16 parts have binary32's range and 16 bits together; its
+// rows are left alone but at the range's ends, where a low part would underflow or a high
+// one round to infinity: scaled up to 1, a small row would overflow with large elements of B.
 constexpr int kFactorThreads = 256;
 
 template <class E>
@@ -312,9 +314,12 @@ __global__ __launch_bounds__(kFactorThreads) void factor_kernel(AdapterArgs g)
 #pragma unroll
         for (int d = kWave / 2; d > 0; d /= 2)
             top = fmaxf(top, __shfl_xor(top, d));
-        // the row's largest finite value to [2^14, 2^15), bfloat16 [1, 2); rows without one as they are
-        constexpr int kTop = std::is_same<E, F16>::value ? 14 : 0;
-        const int up = top > 0.f ? max(ilogbf(top), -100) - kTop : 0;
+        // half: the row's largest finite value to [2^14, 2^15); bfloat16: to 2^-60 .. 2^101 if it
+        // lies outside; rows without one as they are
+        const int e = top > 0.f ? ilogbf(top) : 0;
+        int up = e > 100 ? e - 100 : e < -60 ? e + 60 : 0;
+        if (std::is_same<E, F16>::value && top > 0.f)
+            up = max(e, -100) - 14;
 #pragma unroll
         for (int q = 0; q < kPer; ++q) {
             const int r = q * kWave + lane;

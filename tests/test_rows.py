@@ -746,3 +746,17 @@ def test_adapters_infinity_in_the_second_factor(dev, dtype, T, N):
     others = torch.ones(T, N, dtype=torch.bool)
     others[mine] = torch.tensor([n not in (5, 9) for n in range(N)])
     assert got[others].isfinite().all()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("T,N", ADAPTER_ROWS)
+@pytest.mark.parametrize("x,a,b", [(1.0, 2.0 ** -20, 2.0 ** 127), (2.0 ** -66, 2.0 ** -60, 2.0 ** 127), (2.0 ** 63, 2.0 ** 63, 2.0 ** -120),
+                                   (2.0 ** 100, 2.0 ** 10, 2.0 ** -100), (2.0 ** -30, 2.0 ** -30, 2.0 ** 100)])
+def test_adapters_factors_far_from_one(dev, dtype, T, N, x, a, b):
+    """Sums that the type holds although one of their factors is near its largest or smallest value."""
+    X, A = torch.full((T, 1), x, dtype=dtype), torch.full((1, 1, 8), a, dtype=dtype)
+    B = torch.full((1, 8, N), b, dtype=dtype)
+    say("far from one", T, N, x, a, b, dtype)
+    got = gb.adapter_matmul(X.to(dev), torch.zeros(1, N, dtype=dtype, device=dev), A.to(dev), B.to(dev),
+                            torch.zeros(T, dtype=torch.int32, device=dev))
+    assert (got.double() == 8.0 * x * a * b).all()   # powers of two: exact

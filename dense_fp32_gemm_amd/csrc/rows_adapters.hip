@@ -639,7 +639,7 @@ extern "C" {
 
 size_t gemm_f32_adapters_ws_size(int type, int T, int N, int K, int R)
 {
-    if (T <= 0 || T > kMaxTokens || N <= 0 || K < 0 || R < 0 || R > GEMM_F32_MAX_RANK)
+    if (T <= 0 || T > kMaxTokens || N == 0 || bad_size(N) || bad_size(K) || R < 0 || R > GEMM_F32_MAX_RANK)
         return 0;
     size_t bytes = 0;
     with_type(type, [&](auto e) { bytes = plan<decltype(e)>(T, N, K, R).bytes; });
@@ -653,7 +653,7 @@ int gemm_f32_adapters(int type, int T, int N, int K, int R, int n, const void *X
 {
     if (!known_type(type))
         return GEMM_F32_ERR_TYPE;
-    if (T < 0 || T > kMaxTokens || N < 0 || K < 0 || R < 0 || R > GEMM_F32_MAX_RANK || n < 0)
+    if (T < 0 || T > kMaxTokens || bad_size(N) || bad_size(K) || R < 0 || R > GEMM_F32_MAX_RANK || n < 0)
         return GEMM_F32_ERR_DIM;
     if (short_ld(ldx, K) || short_ld(ldw, N) || short_ld(ldy, N) || short_ld(lda, R) || short_ld(ldb, N) ||
         (n > 1 && (stride_a < K * (int64_t)lda || stride_b < R * (int64_t)ldb)))

@@ -413,7 +413,7 @@ int check_grouped(int type, int G, int P, int N, int K)
 {
     if (!known_type(type))
         return GEMM_F32_ERR_TYPE;
-    return G < 0 || P < 0 || N < 0 || K < 0 ? GEMM_F32_ERR_DIM : GEMM_F32_OK;
+    return G < 0 || bad_size(P) || bad_size(N) || bad_size(K) ? GEMM_F32_ERR_DIM : GEMM_F32_OK;
 }
 
 bool short_ld(int64_t ld, int cols) { return ld < at_least_one(cols); }
@@ -505,7 +505,7 @@ int gemm_f32_combine(int type, int T, int k, int N, int P, const int *position, 
 {
     if (!known_type(type))
         return GEMM_F32_ERR_TYPE;
-    if (T < 0 || k < 0 || N < 0 || P < 0)
+    if (T < 0 || bad_size(k) || bad_size(N) || P < 0)
         return GEMM_F32_ERR_DIM;
     if (short_ld(ldy, N) || short_ld(ldo, N))
         return GEMM_F32_ERR_LD;
@@ -534,7 +534,7 @@ int gemm_f32_combine_grad(int type, int T, int k, int N, int P, const int *posit
 {
     if (!known_type(type))
         return GEMM_F32_ERR_TYPE;
-    if (T < 0 || k < 0 || N < 0 || P < 0)
+    if (T < 0 || bad_size(k) || bad_size(N) || P < 0)
         return GEMM_F32_ERR_DIM;
     if ((dweight != nullptr && short_ld(ldy, N)) || short_ld(lddo, N) || (dY != nullptr && short_ld(lddy, N)))
         return GEMM_F32_ERR_LD;

@@ -23,7 +23,8 @@
  * strides (GEMM_F32_ERR_LD), options (GEMM_F32_ERR_OPTION), NULL pointers
  * (GEMM_F32_ERR_NULL), alignment (GEMM_F32_ERR_ALIGN), the workspace
  * (GEMM_F32_ERR_WORKSPACE).  The first failure is returned and nothing is
- * enqueued.  Offsets, orders, positions and adapter numbers live in device
+ * enqueued.  Of the products, sums and adapters N, K, P of the products and k of the
+ * sums are at most 2^31 - 4096 (GEMM_F32_ERR_DIM).  Offsets, orders, positions and adapter numbers live in device
  * memory and are not validated: kernels clamp or skip what is out of range,
  * so wrong ones give wrong results but no access outside the operands.
  */

@@ -230,3 +230,38 @@ def test_oracle_route_ties_masks_and_groups():
     assert oracle.route(l, 2, groups=2, keep_groups=1, group_top=1)[1].tolist() == [[0, 1]]
     bias = torch.tensor([0., 0., 0.6, 0.6])
     assert oracle.route(l, 2, bias=bias, score="sigmoid", groups=2, keep_groups=1, group_top=2)[1].tolist() == [[2, 3]]
+
+
+# --- sizes next to 2^31 -----------------------------------------------------------
+MOST = 2 ** 31 - 4096
+
+
+@pytest.mark.parametrize("size", [MOST + 1, 2 ** 31 - 64, 2 ** 31 - 1])
+@pytest.mark.parametrize("fn,args", [
+    ("grouped", dict(GROUPED, K="size", ldx="size", stride_w="size * 8", W=0)),
+    ("grouped", dict(GROUPED, N="size", ldw="size", ldy="size", stride_w="size * 16", W=0)),
+    ("grouped", dict(GROUPED, P="size", W=0)),
+    ("grouped_grad_x", dict(type=1, G=2, P=4, N="size", K=16, offsets=FAKE, dY=FAKE, lddy="size", W=0, ldw="size", stride_w="size * 16",
+                            dX=FAKE, lddx=16)),
+    ("grouped_grad_w", dict(type=1, G=2, P="size", N=8, K=16, offsets=FAKE, order=FAKE, per_row=2, rows=2, X=FAKE, ldx=16, dY=0, lddy=8,
+                            dW=FAKE, lddw=8, stride_dw=128)),
+    ("combine", dict(type=2, T=3, k=2, N="size", P=6, position=FAKE, weight=0, Y=0, ldy="size", out=FAKE, ldo="size")),
+    ("combine", dict(type=2, T=3, k="size", N=8, P=6, position=FAKE, weight=0, Y=0, ldy=8, out=FAKE, ldo=8)),
+    ("combine_grad", dict(type=2, T=3, k=2, N="size", P=6, position=FAKE, weight=0, Y=0, ldy="size", dout=FAKE, lddo="size", dY=FAKE,
+                          lddy="size", dweight=FAKE)),
+    ("adapters", dict(ADAPTERS, K="size", ldx="size", stride_a="size * 8", W=0)),
+    ("adapters", dict(ADAPTERS, N="size", ldw="size", ldb="size", ldy="size", stride_b="size * 8", W=0)),
+])
+def test_sizes_that_loops_would_step_past_2_31_are_refused(fn, args, size):
+    """Kernels count along a size in 32 bits and step past it: 2^31 - 4096 is the largest.  (A NULL operand
+    keeps a call that is not refused for its size from being launched.)"""
+    change = {k: eval(v, {"size": size}) if isinstance(v, str) else v for k, v in args.items()}
+    assert getattr(gb, "gemm_f32_" + fn)(**change) == gb.GEMM_F32_ERR_DIM
+
+
+@pytest.mark.parametrize("fn,args", [
+    ("grouped", dict(GROUPED, K=MOST, ldx=MOST, stride_w=MOST * 8, W=0)),
+    ("combine", dict(type=2, T=3, k=2, N=MOST, P=6, position=FAKE, weight=0, Y=0, ldy=MOST, out=FAKE, ldo=MOST)),
+    ("adapters", dict(ADAPTERS, K=MOST, ldx=MOST, stride_a=MOST * 8, W=0))])
+def test_the_largest_sizes_are_taken(fn, args):
+    assert getattr(gb, "gemm_f32_" + fn)(**args) == gb.GEMM_F32_ERR_NULL

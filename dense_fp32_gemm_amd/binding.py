@@ -308,7 +308,7 @@ def matmul(A, B, out=None, config: int = -1, stream=None):
 # Matrices are float32, bfloat16 or float16 tensors of one GPU with unit stride
 # in their last dimension (rows may be further apart); index tensors are
 # int32, weights float32, both contiguous.  Work is enqueued on `stream` (the
-# tensors' device's current stream if None), whichever device is current;
+# tensors' device's current stream if None; one of that device), whichever device is current;
 # outputs and workspaces are allocated under that stream.  A call that runs on
 # another stream than the one its inputs were made on needs the caller's own
 # synchronisation, and outputs passed in must not overlap inputs.
@@ -394,8 +394,10 @@ def _device_now() -> int:
 
 
 def _call_on(device, stream, fn, *args, **kwargs):
-    """fn with the tensors' device and the given stream made current."""
+    """fn with the tensors' device and the given stream (of that device) made current."""
     import torch
+    if stream is not None and stream.device != device:
+        raise ValueError(f"the stream is one of {stream.device}, the tensors are on {device}")
     with torch.cuda.device(device), torch.cuda.stream(stream):
         return fn(*args, **kwargs)
 

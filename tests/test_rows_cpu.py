@@ -265,3 +265,14 @@ def test_sizes_that_loops_would_step_past_2_31_are_refused(fn, args, size):
     ("adapters", dict(ADAPTERS, K=MOST, ldx=MOST, stride_a=MOST * 8, W=0))])
 def test_the_largest_sizes_are_taken(fn, args):
     assert getattr(gb, "gemm_f32_" + fn)(**args) == gb.GEMM_F32_ERR_NULL
+
+
+# --- streams and integers that the torch functions are given ------------------------
+def test_a_stream_of_another_device_is_refused():
+    """Run on the tensors' device, the call would ignore the stream; on the stream's, the tensors'."""
+    class Stream:
+        device = torch.device("cuda", 1)
+    ran = []
+    with pytest.raises(ValueError, match="stream"):
+        gb._call_on(torch.device("cuda", 0), Stream(), lambda: ran.append(1))
+    assert not ran

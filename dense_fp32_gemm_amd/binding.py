@@ -404,8 +404,9 @@ def _call_on(device, stream, fn, *args, **kwargs):
 
 def _fit(*sizes):
     """Refuses sizes that a C int cannot hold (ctypes would wrap them)."""
-    if max(sizes) > INT32_MAX:
-        raise ValueError(f"size {max(sizes)} does not fit the C ABI's 32-bit int")
+    for size in (max(sizes), min(sizes)):
+        if not INT32_MIN <= size <= INT32_MAX:
+            raise ValueError(f"size {size} does not fit the C ABI's 32-bit int")
 
 
 def _check(rc: int, what: str):

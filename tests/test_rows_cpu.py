@@ -276,3 +276,10 @@ def test_a_stream_of_another_device_is_refused():
     with pytest.raises(ValueError, match="stream"):
         gb._call_on(torch.device("cuda", 0), Stream(), lambda: ran.append(1))
     assert not ran
+
+
+@pytest.mark.parametrize("value", [-(1 << 32) + 1, -(1 << 31) - 1, 1 << 31, (1 << 32) + 1])
+def test_integers_that_would_wrap_to_valid_ones_are_refused(value):
+    """ctypes passes the low 32 bits: -(2^32) + 1 groups would be one."""
+    with pytest.raises(ValueError, match="32-bit"):
+        gb._fit(4, 8, value)

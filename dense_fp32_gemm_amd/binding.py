@@ -374,7 +374,7 @@ _current_device = _current_raw_stream = None
 def _here(device) -> int:
     """The current stream of `device`, the current device (a HIP stream address)."""
     global _current_device, _current_raw_stream
-    if _current_device is None:
+    if _current_raw_stream is None:                  # the last one set: other threads may be here too
         import torch
         _current_device = torch.cuda.current_device
         # the raw address, without the Stream object around it where torch offers it

@@ -283,3 +283,11 @@ def test_integers_that_would_wrap_to_valid_ones_are_refused(value):
     """ctypes passes the low 32 bits: -(2^32) + 1 groups would be one."""
     with pytest.raises(ValueError, match="32-bit"):
         gb._fit(4, 8, value)
+
+
+def test_first_calls_of_two_threads(monkeypatch):
+    """A thread that finds the other one half way through _here()'s first call looks the functions up itself."""
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda index: 77 + index, raising=False)
+    monkeypatch.setattr(gb, "_current_device", lambda: 0)      # set by the other thread, which has not come further
+    monkeypatch.setattr(gb, "_current_raw_stream", None)
+    assert gb._here(torch.device("cuda", 3)) == 80

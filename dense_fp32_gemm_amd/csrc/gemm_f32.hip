@@ -43,6 +43,8 @@
 #include "gemm_f32.h"
 #include "internal.h"
 
+using namespace gemm_f32_internal;
+
 namespace {
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
@@ -1704,39 +1706,6 @@ const ConfigInfo kConfigs[kNumConfigs] = {
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// The device the work runs on, read once per device: its compute units
-// (the unit the shape rule balances tiles over, and stream-K's worker count)
-// and the dies (XCDs, 32 compute units each on MI355X) workgroups are dealt
-// to round-robin.  A whole MI355X has 256 and 8; a partitioned one fewer.
-// Without a usable device (plans described on a host without a GPU) the
-// whole MI355X is assumed.
-struct Machine {
-    int64_t cus;
-    int xcds;
-};
-constexpr int kMaxDevices = 64;
-std::atomic<int> g_device_cus[kMaxDevices];   // 0: not read yet
-
-Machine machine()
-{
-    constexpr int kDefaultCus = 256, kCusPerXcd = 32;
-    int dev = -1, cu = 0;
-    if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= kMaxDevices) {
-        (void)hipGetLastError();
-        cu = kDefaultCus;
-    } else {
-        cu = g_device_cus[dev].load(std::memory_order_relaxed);
-        if (cu == 0) {
-            if (hipDeviceGetAttribute(&cu, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || cu <= 0) {
-                (void)hipGetLastError();
-                cu = kDefaultCus;
-            }
-            g_device_cus[dev].store(cu, std::memory_order_relaxed);
-        }
-    }
-    return {cu, cu % kCusPerXcd == 0 ? cu / kCusPerXcd : 1};
-}
-
 // The direct-to-LDS kernels address each panel with 32-bit buffer offsets
 // from its corner: the farthest in-range element of an A panel is
 // (BM-1)*lda + BK-1 floats away, of a B panel (BK-1)*ldb + BN-1.
@@ -2145,7 +2114,7 @@ int make_plan(int config, int M, int N, int K, const float *A, int lda,
     }
     int c = config;
     int strip = 0, strip_c = 0;
-    const Machine mach = machine();
+    const Device mach = current_device();
     plan->xcds = mach.xcds;
     if (c < 0) {
         // The rule's direct-to-LDS choice; if its panels are too tall or deep
@@ -2257,7 +2226,7 @@ int splitk_slices(int M, int N, int K)
 {
     if (M < 16 || N < 16 || K <= 0)
         return 1;
-    const int64_t cus = machine().cus;
+    const int64_t cus = current_device().cus;
     const int64_t t = ceil_div(M, TileSplitK::BM) * ceil_div(N, TileSplitK::BN);
     if (2 * t > cus)
         return 1;
@@ -2371,16 +2340,6 @@ int run_noalloc(int M, int N, int K, const float *A, int lda, const float *B, in
 
 }  // namespace
 
-namespace gemm_f32_internal {
-
-Device current_device()
-{
-    const Machine m = machine();
-    return {m.cus, m.xcds};
-}
-
-}  // namespace gemm_f32_internal
-
 extern "C" {
 
 int gemm_f32_ws_noalloc(int M, int N, int K, const float *A, int lda, const float *B, int ldb,
@@ -2486,24 +2445,6 @@ int gemm_f32_describe(int config, int M, int N, int K, const float *A, int lda,
             snprintf(buf + used, (size_t)(buflen - used), " lds=poisoned");
     }
     return rc;
-}
-
-const char *gemm_f32_status_string(int status)
-{
-    switch (status) {
-    case GEMM_F32_OK: return "ok";
-    case GEMM_F32_ERR_DIM: return "M, N or K is negative or the problem is too large to tile";
-    case GEMM_F32_ERR_LD: return "a leading dimension is smaller than its row length";
-    case GEMM_F32_ERR_NULL: return "a required pointer is NULL";
-    case GEMM_F32_ERR_LAUNCH: return "kernel launch failed";
-    case GEMM_F32_ERR_CONFIG: return "unknown kernel configuration";
-    case GEMM_F32_ERR_ALIGN: return "a pointer is not aligned to its elements (4 bytes for binary32)";
-    case GEMM_F32_ERR_SCRATCH: return "the split plan needs more than the library's static scratch holds";
-    case GEMM_F32_ERR_TYPE: return "unknown element type";
-    case GEMM_F32_ERR_OPTION: return "an option is outside its range";
-    case GEMM_F32_ERR_WORKSPACE: return "the workspace is NULL, too small or not 16-byte aligned";
-    default: return "unknown status";
-    }
 }
 
 }  // extern "C"

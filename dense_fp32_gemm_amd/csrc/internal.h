@@ -6,8 +6,14 @@
 
 namespace gemm_f32_internal {
 
-// The current device's compute units, and the dies (XCDs) it deals
-// workgroups to round-robin; read once per device.
+constexpr int kMaxDevices = 64;   // whose properties and addresses are kept
+
+// The device the work runs on, read once per device: its compute units
+// (the unit the shape rules balance tiles over, and stream-K's worker count)
+// and the dies (XCDs, 32 compute units each on MI355X) workgroups are dealt
+// to round-robin.  A whole MI355X has 256 and 8; a partitioned one fewer.
+// Without a usable device (plans described on a host without a GPU) the
+// whole MI355X is assumed.
 struct Device {
     int64_t cus;
     int xcds;

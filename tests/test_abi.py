@@ -483,3 +483,19 @@ def test_poison_lds_flag_reaches_hipcc():
     # the normal build is not the poisoned one
     rc, text = gb.gemm_f32_describe(-1, 512, 512, 512, FAKE, 512, FAKE, 512, FAKE, 512)
     assert "poison" not in text, text
+
+
+def test_every_traffic_record_is_of_the_current_kernel_code():
+    """bench.py quotes a record only while its digest is that of gemm_f32.hip, which holds the kernels and their plans
+    and nothing shared with other sources."""
+    import bench
+    import glob
+    import json
+    records = [json.load(open(p)) for p in glob.glob(os.path.join(ROOT, "profiles", "*_traffic.json"))]
+    assert {"8192x8192x8192", "2048x2048x2048"} <= {r["workload"] for r in records}
+    for r in records:
+        M, N, K = map(int, r["workload"].split("x"))
+        rc, plan = gb.gemm_f32_describe(-1, M, N, K, FAKE, K, FAKE, N, FAKE, N)
+        assert rc == gb.GEMM_F32_OK and plan.split()[0] == r["kernel"], (r["workload"], plan)
+        bytes_, source = bench.measured_traffic(plan, M, N, K)
+        assert bytes_ == int(round(r["bytes_per_launch"])), source

@@ -599,9 +599,12 @@ int64_t slot_chunks(int64_t S) { return S <= kSlotChunk ? 1 : ceil_div(S, kSlotC
 // two, 131072: 23 against 12).
 constexpr int64_t kCountedInPlace = 1 << 15;
 // From this many chunks on their counts are summed in a launch of their own; fewer,
-// and every workgroup of the last launch adds them up itself (in a graph, 65536 slots: 9.9
-// against 11.4 us with the sums, 131072: 12.3 against 12.0, 262144: 16.6 against 12.8, 1048576: 46 against 22,
-// 16777216: 7600 against 214).
+// and every workgroup of the last launch adds them up itself.  That work grows with the square
+// of the slots (in a graph, us without and with the third launch: 65536 slots 9.9 and 11.4,
+// 262144: 16.6 and 12.8, 1048576: 46 and 22, 16777216: 7600 and 214); the launch costs a caller
+// outside of a graph 3 us.  In between, the limit is for that caller (E = 64: 131072 slots 13.7
+// and 16.3, in a graph 11.2 and 11.0; 196608 slots 14.0 and 16.7, in a graph 13.5 and 11.4):
+// what it would lose by the sums is more than what a graph loses without.
 constexpr int64_t kSummedFrom = 128;
 
 // A grid has fewer than 2^32 threads, a wave of them per token.

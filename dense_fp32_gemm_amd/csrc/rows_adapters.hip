@@ -501,20 +501,38 @@ void cut(int64_t panels, int64_t want, int64_t least, int panel, int *parts, int
     *length = (int)(each * panel);
 }
 
-// Few rows: fewer than 128 tiles of 128 x 128, and no more rows than the parts' own traffic
-// allows (us a call, R = 16, 8 adapters, few against many.  bf16, K = N = 4096: 64
-// rows 21 and 77, 384: 46 and 58, 512: 61 and 57, 1024: 91 and 60; K = N = 2048, 768 rows: 36
-// and 37; K = N = 1024: 512 rows 19 and 28, 1500: 26 and 28, 2048: 28 and 29.
-// binary32, K = N = 1024: 512 rows 28 and 41, 1024: 42 and 41).
+// Few rows: fewer than 128 tiles of 128 x 128, and no more rows than the parts' own traffic and
+// join_kernel's reads of B_a, once a row, allow: few_rows().
 // Ranks: many rows of 17 to 32 take a block of 32 of them (2050 rows, R = 32: 105 against
 // 108 with 64; 8192 rows, K = N = 1024: 45 against 47).
+//
+// us a call in a graph, 8 adapters, rows side by side, few against many:
+//   bfloat16, K = N = 1024, R = 16: 512 rows 18 and 24, 1024: 21 and 24, 2048: 27 and 25;
+//     R = 32: 512 rows 24 and 26, 1024: 28 and 25; R = 64: 640 rows 29 and 33, 1024: 31 and 28;
+//     R = 128: 320 rows 32 and 49, 512: 38 and 35; R = 256: 384 rows 54 and 72, 512: 56 and 50,
+//     2048: 99 and 42;
+//   K = N = 2048, R = 64: 512 rows 37 and 40; R = 32: 768 rows 44 and 37;
+//   K = N = 4096, 384 rows: R = 16 48 and 53, R = 64 63 and 61, R = 256 107 and 101;
+//   binary32, K = N = 1024, R = 16: 512 rows 27 and 34; R = 64: 320 rows 37 and 45, 512: 40 and 40;
+//     R = 128: 256 rows 46 and 46, 320: 62 and 54; R = 256: 256 rows 67 and 64, 512: 75 and 57;
+//   K = N = 2048, 512 rows: R = 16 57 and 58, R = 32 72 and 59; K = N = 4096, 384 rows: R = 16 134
+//   and 143, R = 32 141 and 146, R = 64 148 and 152, R = 128 239 and 165.
+// Narrow outputs of more rows gain nothing (bfloat16, K = 8192, N = 64, R = 16: 4096 rows 85 and 86).
+template <class E>
+int few_rows(int R)
+{
+    if (E::kBytes == 4)
+        return R <= 16 ? 512 : R <= 64 ? 320 : 256;
+    return R <= 16 ? 2048 : R <= 64 ? 640 : 384;
+}
+
 template <class E>
 Split plan(int T, int N, int K, int R)
 {
     Split p{};
     const int panel = panel_deep<E>();
     const int64_t panels = ceil_div(K, panel), rows16 = ceil_div(T, 16);
-    p.few = ceil_div(T, 128) * ceil_div(N, 128) < 128 && T <= (E::kBytes == 4 ? 512 : 2048);
+    p.few = ceil_div(T, 128) * ceil_div(N, 128) < 128 && T <= few_rows<E>(R);
     p.rank_block = R <= 16 ? 16 : R <= 32 && !p.few ? 32 : 64;
     p.ranks = (int)ceil_div(R, p.rank_block);
     if (R > 0) {

@@ -760,3 +760,20 @@ def test_adapters_factors_far_from_one(dev, dtype, T, N, x, a, b):
     got = gb.adapter_matmul(X.to(dev), torch.zeros(1, N, dtype=dtype, device=dev), A.to(dev), B.to(dev),
                             torch.zeros(T, dtype=torch.int32, device=dev))
     assert (got.double() == 8.0 * x * a * b).all()   # powers of two: exact
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=IDS)
+@pytest.mark.parametrize("T,R", [(2048, 16), (320, 17), (321, 64), (640, 64), (641, 20), (256, 65), (257, 65), (384, 130), (385, 256)])
+def test_adapters_next_to_the_limits_of_few_rows(dev, dtype, T, R):
+    K, N, n = 200, 136, 4
+    g = seeded("row limits", T, R)
+    X, W = normal(g, T, K, dtype=dtype), normal(g, K, N, dtype=dtype, scale=K ** -0.5)
+    A, B = normal(g, n, K, R, dtype=dtype, scale=K ** -0.5), normal(g, n, R, N, dtype=dtype)
+    adapter = torch.randint(-1, n + 1, (T,), generator=g, dtype=torch.int32)
+    scale = 0.5 + torch.rand(n, generator=g)
+    say("row limits", T, R, dtype)
+    want, size = adapters_want(X, W, A, B, adapter, scale)
+    got = gb.adapter_matmul(X.to(dev), W.to(dev), A.to(dev), B.to(dev), adapter.to(dev), scale.to(dev))
+    # U is off by 2^-16 of itself, or 2^-22 of itself and 2^-39 of its row's largest, which 2^-16 of the magnitudes' sum covers:
+    # the magnitudes of a row's ranks, sums of 200 terms, are alike
+    oracle.close(got, want, oracle.product_bound(want, size, K + R + 4, dtype) + (0 if dtype == torch.float32 else 2.0 ** -16) * size, "Y")

@@ -673,14 +673,14 @@ int gemm_f32_adapters(int type, int T, int N, int K, int R, int n, const void *X
         return GEMM_F32_ERR_TYPE;
     if (T < 0 || T > kMaxTokens || bad_size(N) || bad_size(K) || R < 0 || R > GEMM_F32_MAX_RANK || n < 0)
         return GEMM_F32_ERR_DIM;
+    const int64_t tile = type == GEMM_F32_TYPE_F32 ? 64 : 256, threads = type == GEMM_F32_TYPE_F32 ? 256 : 512;
+    if (ceil_div(T, tile) * ceil_div(N, tile) > UINT32_MAX / threads - 1024)
+        return GEMM_F32_ERR_DIM;                     // a grid has fewer than 2^32 threads
     if (short_ld(ldx, K) || short_ld(ldw, N) || short_ld(ldy, N) || short_ld(lda, R) || short_ld(ldb, N) ||
         (n > 1 && (stride_a < K * (int64_t)lda || stride_b < R * (int64_t)ldb)))
         return GEMM_F32_ERR_LD;
     if (T == 0 || N == 0)
         return GEMM_F32_OK;
-    const int64_t tile = type == GEMM_F32_TYPE_F32 ? 64 : 256, threads = type == GEMM_F32_TYPE_F32 ? 256 : 512;
-    if (ceil_div(T, tile) * ceil_div(N, tile) > UINT32_MAX / threads - 1024)
-        return GEMM_F32_ERR_DIM;                     // a grid has fewer than 2^32 threads
     const bool low = R > 0 && n > 0;
     if (Y == nullptr || (K > 0 && (X == nullptr || W == nullptr)) ||
         (low && (B == nullptr || adapter == nullptr || (K > 0 && A == nullptr))))

@@ -347,18 +347,19 @@ static_assert(kCombineThreads <= 512, "grid limit");
 int token_grid(int T) { return T < kMaxTiles ? T : (int)kMaxTiles; }
 
 // PER_CU: workgroups of a kernel that cuts its last tiles on a compute unit (0: it does not).
+// Without `go` it says whether the tiles fit a grid.
 template <class E, Op OP, int BM, int BN, int WM, int WN, int S, int PER_CU>
-int launch_tile(GroupedArgs g, bool dma, hipStream_t stream)
+int launch_tile(GroupedArgs g, bool dma, hipStream_t stream, bool go)
 {
     g.tiles_n = (int)ceil_div(g.N, BN);
     // Every group ends in at most one partial tile.
     const int64_t tiles_m = OP == kGradW ? g.G * ceil_div(g.M, BM) : g.P / BM + (g.G < g.P ? g.G : g.P);
     g.slots = (int)gemm_f32_internal::current_device().cus * PER_CU;
     // Cutting the last round adds at most three pieces for a quarter of the slots.
-    const int64_t grid = tiles_m * g.tiles_n + g.slots;
-    if (grid > kMaxTiles)
+    const int64_t grid = (tiles_m < kMaxTiles ? tiles_m : kMaxTiles) * g.tiles_n + g.slots;
+    if (tiles_m > kMaxTiles || grid > kMaxTiles)
         return GEMM_F32_ERR_DIM;
-    if (tiles_m * g.tiles_n == 0)
+    if (!go || tiles_m * g.tiles_n == 0)
         return GEMM_F32_OK;
     g.most_m = (int)tiles_m;
     constexpr bool kCut = PER_CU > 0;
@@ -384,36 +385,42 @@ int launch_tile(GroupedArgs g, bool dma, hipStream_t stream)
 //    largest tile needs the fewest per product;
 //  * fewer: 64 x 128 (4096 rows over 8 groups, K = N = 1024: 19.4 against 21.6).
 template <Op OP>
-int launch_grouped(int type, const GroupedArgs &g, bool dma, hipStream_t stream)
+int launch_grouped(int type, const GroupedArgs &g, bool dma, hipStream_t stream, bool go = true)
 {
     int rc = GEMM_F32_OK;
     with_type(type, [&](auto e) {
         using E = decltype(e);
         if constexpr (OP != kGradW) {
             if (g.P <= (E::kBytes == 4 ? 64 : 32) * (int64_t)g.G) {
-                rc = launch_tile<E, OP, 32, 64, 1, 4, 4, 0>(g, dma, stream);
+                rc = launch_tile<E, OP, 32, 64, 1, 4, 4, 0>(g, dma, stream, go);
                 return;
             }
         }
         if constexpr (E::kBytes == 4) {
-            rc = launch_tile<E, OP, 64, 64, 2, 2, 2, 0>(g, dma, stream);
+            rc = launch_tile<E, OP, 64, 64, 2, 2, 2, 0>(g, dma, stream, go);
         } else {
             // Half a tile a group is lost on average.
             const int64_t rows = OP == kGradW ? 2 * g.G * ceil_div(g.M, 256) : 2 * (g.P / 256) + (g.G < g.P ? g.G : g.P);
-            if (rows * ceil_div(g.N, 256) * 5 >= 6 * gemm_f32_internal::current_device().cus)
-                rc = launch_tile<E, OP, 256, 256, 2, 4, 2, 1>(g, dma, stream);
+            if ((rows < kMaxTiles ? rows : kMaxTiles) * ceil_div(g.N, 256) * 5 >= 6 * gemm_f32_internal::current_device().cus)
+                rc = launch_tile<E, OP, 256, 256, 2, 4, 2, 1>(g, dma, stream, go);
             else
-                rc = launch_tile<E, OP, 64, 128, 2, 2, 3, 0>(g, dma, stream);
+                rc = launch_tile<E, OP, 64, 128, 2, 2, 3, 0>(g, dma, stream, go);
         }
     });
     return rc;
 }
 
+// Type and sizes, the number of tiles among them (see launch_tile()).
+template <Op OP>
 int check_grouped(int type, int G, int P, int N, int K)
 {
     if (!known_type(type))
         return GEMM_F32_ERR_TYPE;
-    return G < 0 || bad_size(P) || bad_size(N) || bad_size(K) ? GEMM_F32_ERR_DIM : GEMM_F32_OK;
+    if (G < 0 || bad_size(P) || bad_size(N) || bad_size(K))
+        return GEMM_F32_ERR_DIM;
+    const int cols = OP == kGradX ? K : N;
+    const GroupedArgs g{nullptr, nullptr, nullptr, nullptr, nullptr, 0, 0, 0, 0, G, P, 0, Divisor(1), K, cols, 0, 1, false, 0, 0, 0};
+    return launch_grouped<OP>(type, g, false, nullptr, false);
 }
 
 bool short_ld(int64_t ld, int cols) { return ld < at_least_one(cols); }
@@ -431,7 +438,7 @@ int gemm_f32_grouped(int type, int G, int P, int N, int K, const int *offsets, c
                      const void *X, int ldx, const void *W, int ldw, int64_t stride_w, void *Y, int ldy,
                      hipStream_t stream)
 {
-    const int rc = check_grouped(type, G, P, N, K);
+    const int rc = check_grouped<kForward>(type, G, P, N, K);
     if (rc != GEMM_F32_OK)
         return rc;
     if (rows < 0 || (order == nullptr && rows < P))
@@ -456,7 +463,7 @@ int gemm_f32_grouped(int type, int G, int P, int N, int K, const int *offsets, c
 int gemm_f32_grouped_grad_x(int type, int G, int P, int N, int K, const int *offsets, const void *dY, int lddy,
                             const void *W, int ldw, int64_t stride_w, void *dX, int lddx, hipStream_t stream)
 {
-    const int rc = check_grouped(type, G, P, N, K);
+    const int rc = check_grouped<kGradX>(type, G, P, N, K);
     if (rc != GEMM_F32_OK)
         return rc;
     if (short_ld(lddy, N) || short_ld(ldw, N) || short_ld(lddx, K) || short_stride(stride_w, G, K, ldw))
@@ -478,7 +485,7 @@ int gemm_f32_grouped_grad_w(int type, int G, int P, int N, int K, const int *off
                             int rows, const void *X, int ldx, const void *dY, int lddy, void *dW, int lddw,
                             int64_t stride_dw, hipStream_t stream)
 {
-    const int rc = check_grouped(type, G, P, N, K);
+    const int rc = check_grouped<kGradW>(type, G, P, N, K);
     if (rc != GEMM_F32_OK)
         return rc;
     if (rows < 0 || (order == nullptr && rows < P))

@@ -16,15 +16,23 @@
  * the type of every `void *` matrix of a call.  Sums are binary32 on the matrix
  * cores whatever the type, rounded once to it at the end; routing computes in
  * binary64.  Pointers must be aligned to their elements; rows that are 16-byte
- * aligned (base, leading dimensions and strides) load faster.
+ * aligned (base, leading dimensions and strides) load faster.  16-bit rows that start on
+ * odd elements, an X of the products that spans 2^31 bytes or more, and panels that do (256 rows,
+ * of any operand) take loads through registers, about half as fast.
  *
  * Arguments are validated in this order: the element type
  * (GEMM_F32_ERR_TYPE), sizes (GEMM_F32_ERR_DIM), leading dimensions and
  * strides (GEMM_F32_ERR_LD), options (GEMM_F32_ERR_OPTION), NULL pointers
  * (GEMM_F32_ERR_NULL), alignment (GEMM_F32_ERR_ALIGN), the workspace
  * (GEMM_F32_ERR_WORKSPACE).  The first failure is returned and nothing is
- * enqueued.  Of the products, sums and adapters N, K, P of the products and k of the
- * sums are at most 2^31 - 4096 (GEMM_F32_ERR_DIM).  Offsets, orders, positions and adapter numbers live in device
+ * enqueued.  GEMM_F32_ERR_DIM also refuses what is too large:
+ *   - of the products, sums and adapters N and K, P of the products, k of the sums:
+ *     over 2^31 - 4096;
+ *   - tiles of a product's output, 32 x 64 elements or larger: over 8388607 less the
+ *     device's compute units; of the adapters', 256 x 256 (binary32 64 x 64): over 8387583
+ *     (16776191);
+ *   - T of routing: over 67108859, of the adapters: over 2^25.
+ * Offsets, orders, positions and adapter numbers live in device
  * memory and are not validated: kernels clamp or skip what is out of range,
  * so wrong ones give wrong results but no access outside the operands.
  */

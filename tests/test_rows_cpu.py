@@ -291,3 +291,18 @@ def test_first_calls_of_two_threads(monkeypatch):
     monkeypatch.setattr(gb, "_current_device", lambda: 0)      # set by the other thread, which has not come further
     monkeypatch.setattr(gb, "_current_raw_stream", None)
     assert gb._here(torch.device("cuda", 3)) == 80
+
+
+@pytest.mark.parametrize("fn,args", [
+    ("grouped", dict(GROUPED, P=1 << 30, N=1 << 20, X=0)),                    # and NULL, and short rows
+    ("grouped_grad_x", dict(type=0, G=2, P=1 << 30, N=8, K=1 << 20, offsets=FAKE, dY=0, lddy=1, W=FAKE, ldw=1, stride_w=1, dX=FAKE, lddx=16)),
+    ("grouped_grad_w", dict(type=1, G=1 << 20, P=4, N=1 << 12, K=1 << 12, offsets=0, order=0, per_row=2, rows=4, X=FAKE, ldx=1, dY=FAKE,
+                            lddy=8, dW=FAKE, lddw=8, stride_dw=128)),
+    # more tiles than 64 bits count
+    ("grouped_grad_w", dict(type=0, G=(1 << 31) - 1, P=4, N=1 << 30, K=1 << 30, offsets=0, order=0, per_row=2, rows=4, X=FAKE, ldx=1 << 30,
+                            dY=FAKE, lddy=1 << 30, dW=FAKE, lddw=1 << 30, stride_dw=1 << 60)),
+    ("adapters", dict(ADAPTERS, T=1 << 25, N=1 << 30, Y=0)),
+])
+def test_too_many_tiles_are_refused_with_the_sizes(fn, args):
+    """Sizes come before leading dimensions and pointers, whatever else is wrong."""
+    assert getattr(gb, "gemm_f32_" + fn)(**args) == gb.GEMM_F32_ERR_DIM

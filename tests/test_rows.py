@@ -777,3 +777,87 @@ def test_adapters_next_to_the_limits_of_few_rows(dev, dtype, T, R):
     # U is off by 2^-16 of itself, or 2^-22 of itself and 2^-39 of its row's largest, which 2^-16 of the magnitudes' sum covers:
     # the magnitudes of a row's ranks, sums of 200 terms, are alike
     oracle.close(got, want, oracle.product_bound(want, size, K + R + 4, dtype) + (0 if dtype == torch.float32 else 2.0 ** -16) * size, "Y")
+
+
+def whole_numbers(g, *shape, dtype):
+    """-2 .. 2: every partial sum of under 2^22 products is exact in binary32, so a result is the exact sum rounded once."""
+    return torch.randint(-2, 3, shape, generator=g).to(dtype)
+
+
+def takes_256(grad_w, G, P, M, N, cus):
+    """The rule by which 16-bit products take tiles of 256 x 256."""
+    rows = 2 * G * -(-M // 256) if grad_w else 2 * (P // 256) + min(G, P)
+    return rows * -(-N // 256) * 5 >= 6 * cus
+
+
+def pieces_of_the_last_round(tiles, cus):
+    rest = tiles % cus
+    return 4 if 4 * rest <= cus else 2 if 2 * rest <= cus else 1
+
+
+GROUPS_256 = [1200, 0, 700, 1, 650]      # 12 row tiles of 256; one group longer than 1024 places, one empty
+
+
+@pytest.mark.parametrize("dtype", TYPES[1:], ids=IDS[1:])
+@pytest.mark.parametrize("pad", [0, 1], ids=["odd rows", "even rows"])       # staged loads, direct loads
+@pytest.mark.parametrize("listed", [False, True], ids=["in place", "listed"])
+@pytest.mark.parametrize("op,A,B,pieces", [
+    ("forward", 333, 3579, 1), ("forward", 333, 5627, 4), ("forward", 72, 7165, 2),
+    ("grad_x", 3579, 333, 1), ("grad_x", 5627, 333, 4), ("grad_x", 7165, 72, 2),
+    ("grad_w", 1797, 2309, 1), ("grad_w", 1797, 1801, 4), ("grad_w", 1797, 2101, 2)])
+def test_grouped_tiles_of_256(dev, dtype, pad, listed, op, A, B, pieces):
+    """Every product's largest tile, whole and with its last round cut: sums of whole numbers, equal."""
+    if op == "grad_x" and listed:
+        pytest.skip("places in their own order alone")
+    K, N, G = A, B, len(GROUPS_256)
+    g = seeded("256", op, K, N)
+    offsets = torch.tensor([0] + GROUPS_256, dtype=torch.int32).cumsum(0).int()
+    used = int(offsets[-1])
+    P = used + 3                                     # three places in no group
+    cus = torch.cuda.get_device_properties(dev).multi_processor_count
+    row_tiles = sum(-(-n // 256) for n in GROUPS_256)
+    M, C = (K, N) if op == "grad_w" else (0, N if op == "forward" else K)
+    if cus == 256:
+        assert takes_256(op == "grad_w", G, P, M, C, cus)
+        tiles = (G * -(-M // 256) if op == "grad_w" else row_tiles) * -(-C // 256)
+        assert pieces_of_the_last_round(tiles, cus) == pieces
+    say("tiles of 256", op, K, N, pad, listed, dtype)
+    rows = P if not listed else (P + 1) // 2
+    order = torch.randperm(2 * rows, generator=g)[:P].int()
+    if listed:
+        order[7], order[used:] = -1, -1
+    at = order.long().div(2, rounding_mode="floor").to(dev) if listed else torch.arange(P, device=dev)
+    off = offsets.to(dev)
+    list_ = dict(order=order.to(dev), per_row=2) if listed else {}
+
+    def places_of(X):
+        x = X.double()[at.clamp_min(0)]
+        x[at < 0] = 0.0
+        return x
+
+    def check(got, want, what):
+        assert torch.equal(got, want.to(dtype)), f"{what}: {int((got != want.to(dtype)).sum())} elements differ"
+    if op != "grad_w":
+        W = strided(whole_numbers(g, G, K, N, dtype=dtype), pad, dev)
+        I = strided(whole_numbers(g, rows if op == "forward" else P, K if op == "forward" else N, dtype=dtype), pad, dev)
+        full = torch.full((P, C + pad), 7.0, dtype=dtype, device=dev)
+        if op == "forward":
+            gb.grouped_matmul(I, W, off, out=full[:, :C], **list_)
+        else:
+            gb.grouped_grad_x(I, W, off, out=full[:, :C])
+        x = places_of(I) if op == "forward" else I.double()
+        for e in range(G):
+            lo, hi = int(offsets[e]), int(offsets[e + 1])
+            w = W[e].double() if op == "forward" else W[e].double().t().contiguous()
+            check(full[lo:hi, :C], torch.mm(x[lo:hi], w), (op, e))
+        assert (full[used:] == 7.0).all() and (full[:, C:] == 7.0).all()
+    else:
+        X = strided(whole_numbers(g, rows, K, dtype=dtype), pad, dev)
+        dY = strided(whole_numbers(g, P, N, dtype=dtype), pad, dev)
+        full = torch.full((G, K, N + pad), 7.0, dtype=dtype, device=dev)
+        gb.grouped_grad_w(X, dY, off, out=full[:, :, :N], **list_)
+        x = places_of(X)
+        for e in range(G):
+            lo, hi = int(offsets[e]), int(offsets[e + 1])
+            check(full[e, :, :N], torch.mm(x[lo:hi].t().contiguous(), dY[lo:hi].double()), (op, e))
+        assert (full[:, :, N:] == 7.0).all()

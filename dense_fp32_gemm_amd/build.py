@@ -30,8 +30,9 @@ HIPFLAGS = [
 
 
 # Debug build: -DGEMM_F32_POISON_LDS makes the kernels set every LDS slot to
-# NaN before it is refilled or first written (see kPoisonLds in the source),
-# so a stale LDS read shows up as NaN in C.  gemm_f32_describe() then ends
+# NaN before it is refilled or first written (see kPoisonLds in gemm_f32.hip and rows_tile.h),
+# so a stale LDS read shows up as NaN in the result (of the row-chosen products: the panels of
+# their K loops; not their lists of row offsets).  gemm_f32_describe() then ends
 # with " lds=poisoned".
 POISON_LDS = "-DGEMM_F32_POISON_LDS"
 

@@ -230,6 +230,17 @@ __device__ inline void store4(typename E::T *p, f32x4 v, int64_t left)
     }
 }
 
+// Debug build (-DGEMM_F32_POISON_LDS): every LDS slot that a panel's load is about to fill is
+// first set to NaN of whichever type by the wave that issues the load, so that a read
+// before the panel has landed, or of a buffer that is being refilled, carries NaN into the result
+// instead of older numbers.
+#ifdef GEMM_F32_POISON_LDS
+constexpr bool kPoisonLds = true;
+#else
+constexpr bool kPoisonLds = false;
+#endif
+__device__ inline void poison16(void *p) { *reinterpret_cast<u32x4 *>(p) = u32x4{~0u, ~0u, ~0u, ~0u}; }
+
 // ---------------------------------------------------------------------------
 // Where a thread's chunks of a panel come from.  Chunk i of thread tid is the
 // panel's 16-byte LDS slot tid + i * threads.  base is a uniform address, p[i]
@@ -443,11 +454,21 @@ __device__ inline void sum_panels_staged(Ti &tile, int K, const SrcA &a, const S
         if (slots % NT == 0 || tid + i * NT < slots)
             *reinterpret_cast<u32x4 *>(panel + (tid + i * NT) * E::kChunk) = v;
     };
+    // Poisoned: before the barrier that readers of a panel wait at, all of it and then its data,
+    // so that what is not written before the barrier, or by nobody, is NaN.
+    auto poison = [&](T *panel) {
+        if constexpr (kPoisonLds) {
+            for (int c = tid; c < (Ti::kLdsA + Ti::kLdsB) / E::kChunk; c += NT)
+                poison16(panel + c * E::kChunk);
+            group_sync<NT>();
+        }
+    };
     if (K > 0)
         fetch(0);
     int buf = 0;
     for (int k0 = 0; k0 < K; k0 += BK, buf ^= 1) {
         T *la = lds + buf * (Ti::kLdsA + Ti::kLdsB), *lb = la + Ti::kLdsA;
+        poison(la);
 #pragma unroll
         for (int i = 0; i < SrcA::kCount; ++i)
             put(la, SrcA::kSlots, i, ra[i]);
@@ -463,6 +484,19 @@ __device__ inline void sum_panels_staged(Ti &tile, int K, const SrcA &a, const S
             f.read(la, step, wm, wn, lane);
             tile.multiply(f);
         }
+    }
+}
+
+// NaN over the slots of a panel that the wave's loads will fill (poisoned build).
+template <class Src, class E, int NT>
+__device__ inline void poison_slots(typename E::T *panel, int wave)
+{
+    if constexpr (kPoisonLds) {
+#pragma unroll
+        for (int i = 0; i < Src::kCount; ++i)
+            if (Src::kSlots % NT == 0 || i * NT + wave * kWave < Src::kSlots)
+                poison16(panel + (i * NT + wave * kWave + (int)(threadIdx.x % kWave)) * E::kChunk);
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     }
 }
 
@@ -505,6 +539,7 @@ struct PanelLoads {
             auto *dst = (lds_ptr<void>)(panel + (i * NT + wave * kWave) * E::kChunk);
             __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, dst, 16, o, 0, 0, 0);
         };
+        poison_slots<Src, E, NT>(panel, wave);
         // The operand's end and missing chunks matter to its last panel alone (last()).
         if (!src.last(k0)) {
 #pragma unroll
@@ -531,6 +566,7 @@ struct PanelLoads<E, Gathered<E, RN, NT>, NT> {
         const auto rsrc = __builtin_amdgcn_make_buffer_rsrc((void *)src.base, 0, (int)buffer_size(src.extent()), kRawBufferFlags);
         static_assert(Src::kOneColumn, "one column a thread");
         const int col = src.col(0);
+        poison_slots<Src, E, NT>(panel, wave);
         const uint32_t *block = src.ahead + (k0 / Src::kBlock % 2) * Src::kBlock + k0 % Src::kBlock;
 #pragma unroll
         for (int i = 0; i < Src::kCount; ++i) {

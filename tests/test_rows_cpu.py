@@ -306,3 +306,16 @@ def test_first_calls_of_two_threads(monkeypatch):
 def test_too_many_tiles_are_refused_with_the_sizes(fn, args):
     """Sizes come before leading dimensions and pointers, whatever else is wrong."""
     assert getattr(gb, "gemm_f32_" + fn)(**args) == gb.GEMM_F32_ERR_DIM
+
+
+def test_the_poisoned_build_covers_every_panel_load():
+    """Every direct load into LDS stands behind poison_slots() in its function."""
+    src = open(os.path.join(ROOT, "dense_fp32_gemm_amd", "csrc", "rows_tile.h")).read()
+    assert "#ifdef GEMM_F32_POISON_LDS" in src
+    fires = re.split(r"__device__ inline void fire\(", src)[1:]
+    assert len(fires) == 2 == src.count("__builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc")
+    for body in fires:
+        body = body[:body.index("\n    }\n")]
+        assert "poison_slots<" in body and "buffer_load_lds(" in body
+    for name in ("rows_adapters.hip", "rows_grouped.hip", "rows_route.hip", "rows_common.h"):
+        assert "buffer_load_lds" not in open(os.path.join(ROOT, "dense_fp32_gemm_amd", "csrc", name)).read()

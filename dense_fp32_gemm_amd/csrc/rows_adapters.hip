@@ -133,7 +133,7 @@ __device__ inline void down_item(const AdapterArgs &g, int64_t item, typename E:
                                     [&](int, int r) { return t0 + r < g.T ? r * g.ldx * E::kBytes : -1; });
         const Across<E, RN, kWave> w((const T *)g.A + a * g.stride_a + k0 * g.lda, lane, K, g.lda, rank0, g.R);
         group_sync<kWave>();
-        sum_panels<E, DMA, down_stages<RN>()>(tile, K, x, w, lds, lane, 0, 0);
+        sum_panels<E, DMA, down_stages<RN>(), false>(tile, K, x, w, lds, lane, 0, 0);
         tile.each(0, 0, lane, [&](int r, int c, f32x4 v) {
             if (members >> r & 1) {
                 float *u = g.partial_u + ((int64_t)split * g.T + t0 + r) * g.R + rank0 + c;
@@ -186,7 +186,7 @@ __global__ __launch_bounds__(kDownWaves *kWave) void step_kernel(AdapterArgs g)
     const Along<E, BM, NT> x((const T *)g.X + m0 * g.ldx + k0, tid, K, g.ldx, g.T - m0,
                              [&](int, int r) { return m0 + r < g.T ? r * g.ldx * E::kBytes : -1; });
     const Across<E, kStepBN, NT> w((const T *)g.W + k0 * g.ldw, tid, K, g.ldw, n0, g.N);
-    sum_panels<E, DMA, kStepStages>(tile, K, x, w, lds, tid, wm, wn);
+    sum_panels<E, DMA, kStepStages, false>(tile, K, x, w, lds, tid, wm, wn);
     tile.each(wm, wn, lane, [&](int r, int c, f32x4 v) {
         // whole groups of four: rows of the parts are padded to a multiple of eight
         if (m0 + r < g.T && n0 + c < g.N)

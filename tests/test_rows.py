@@ -861,3 +861,37 @@ def test_grouped_tiles_of_256(dev, dtype, pad, listed, op, A, B, pieces):
             lo, hi = int(offsets[e]), int(offsets[e + 1])
             check(full[e, :, :N], torch.mm(x[lo:hi].t().contiguous(), dY[lo:hi].double()), (op, e))
         assert (full[:, :, N:] == 7.0).all()
+
+
+@pytest.mark.parametrize("rows,K,N", [(8, 4096, 512), (100, 4096, 72), (700, 4096, 200)])
+def test_binary32_sums_are_no_single_long_chain(dev, rows, K, N):
+    """Errors of binary32 products against 64 bits, in the root mean square.
+
+    n additions in one chain of partial sums that grow like sqrt(k) for random signs are off by sqrt(sum over k of
+    (2^-24 / sqrt(3))^2 k) = 2^-24 sqrt(n / 6) of the result's size sqrt(n).  The matrix cores add 4 products an
+    instruction: 4096 k are 1024 additions, 2^-24 * 13 = 7.8e-7, with the instructions' own roundings more; parts of at
+    most 512 + 32 k and 8 parts are 2^-24 * sqrt(136 / 6 + 8 / 6) = 2.9e-7 the same way.  The limit is between the two.
+    """
+    g = seeded("chains", rows, K, N)
+    G = 8
+    offsets = (torch.arange(G + 1) * rows).int()
+    X, W = normal(g, G * rows, K).to(dev), normal(g, G, K, N).to(dev)
+    dY = normal(g, G * rows, N).to(dev)
+    say("chains", rows, K, N)
+
+    def off(got, want):
+        return float((got.double() - want).norm() / want.norm())
+    Y = gb.grouped_matmul(X, W, offsets.to(dev))
+    want = torch.cat([torch.mm(X[e * rows:(e + 1) * rows].double(), W[e].double()) for e in range(G)])
+    assert off(Y, want) < 5.5e-7
+    # the other products, with K the summed index
+    Wt = W.transpose(1, 2).contiguous()                         # [G, N, K]
+    dX = gb.grouped_grad_x(X, Wt, offsets.to(dev))
+    assert off(dX, want) < 5.5e-7
+    long = torch.tensor([0, K], dtype=torch.int32, device=dev)
+    A, B = X[:rows].t().contiguous(), W[0].contiguous()         # [K, rows], [K, N]
+    dW = gb.grouped_grad_w(A, B, long)
+    assert off(dW[0], torch.mm(A.t().double().contiguous(), B.double())) < 5.5e-7
+    Z = gb.adapter_matmul(X.repeat(2, 1)[:600], W[0], torch.zeros(1, K, 33, device=dev), torch.zeros(1, 33, N, device=dev),
+                          torch.full((min(600, 2 * G * rows),), -1, dtype=torch.int32, device=dev))
+    assert off(Z, torch.mm(X.repeat(2, 1)[:600].double(), W[0].double())) < 5.5e-7

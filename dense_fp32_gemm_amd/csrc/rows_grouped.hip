@@ -376,13 +376,13 @@ int launch_tile(GroupedArgs g, bool dma, hipStream_t stream, bool go)
 //    read once or twice (32 rows over 32 groups, bf16: 13.4 against 17.2 for 64 x 128; 512 rows
 //    over 16 groups: 17.7 against 17.8, 768 rows: 19.7 against 18.0; binary32, 1024
 //    rows over 16 groups: 60 against 69 for 64 x 64, 1536 rows: equal);
-//  * binary32 else: 64 x 64 (4096 rows over 8 groups, N = 2048: 281; with slower loads 293 against 310 for 128 x 64
+//  * binary32 else: 64 x 64 (4096 rows over 8 groups, N = 2048: 282; with slower loads 293 against 310 for 128 x 64
 //    and 312 for 128 x 128, whose last round leaves more units idle);
 //  * 16-bit types, 256 x 256 tiles for three fifths of the compute units or
 //    more: those, the last round cut (2000 rows over 8 groups, N = 4096: 56 against 76
 //    for 64 x 128; 65536 rows over 64: 288 against 355 for 128 x 128). A compute unit
-//    takes about 16 bytes a clock of panels from L2 whatever the tile, and the
-//    largest tile needs the fewest per product;
+//    was seen to take up to about 16 bytes a clock of panels from L2; the largest tile needs
+//    the fewest per product, 12 to 14 at its rate here (961 TFLOP/s, an eighth of the rows padding);
 //  * fewer: 64 x 128 (4096 rows over 8 groups, K = N = 1024: 19.4 against 21.6).
 template <Op OP>
 int launch_grouped(int type, const GroupedArgs &g, bool dma, hipStream_t stream, bool go = true)

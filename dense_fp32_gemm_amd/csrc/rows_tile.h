@@ -36,7 +36,9 @@ constexpr int kDeep16 = 8;                           // 16-byte chunks of a pane
 // bytes that the banks span.
 __device__ inline int swz_along(int r) { return (r >> 1) & 7; }
 
-// Chunk permutation of k row k of an "across" panel of RN rows (16-bit types).
+// Chunk permutation of k row k of an "across" panel of RN rows (16-bit types).  Narrower
+// panels than 64 rows have none (the adapters' down-projection of 32 ranks: 40 % of its LDS cycles are
+// conflicts, of a kernel of 11 us).
 template <int RN>
 __device__ inline int swz_across(int k)
 {
@@ -767,7 +769,8 @@ __device__ inline void sum_panels_dma(Ti &tile, int K, const SrcA &a, const SrcB
         a.refill(0);
         __syncthreads();
     }
-    // (With rows from a list, 16-bit types have no registers left to read ahead.)
+    // With rows from a list, 16-bit types read two row blocks ahead instead of half a panel: less
+    // for the registers, of which a step of fragments ahead took the rest (see whole_panel()).
     if constexpr (SrcA::kListed && E::kBytes == 2) {
 #pragma unroll
         for (int q = 0; q < S - 1; ++q)

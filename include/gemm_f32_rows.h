@@ -14,11 +14,11 @@
  *
  * Element types: matrices are binary32, bfloat16 or IEEE half (GEMM_F32_TYPE_*),
  * the type of every `void *` matrix of a call.  Sums are binary32 on the matrix
- * cores whatever the type, rounded once to it at the end; routing computes in
+ * cores whatever the type (adapters: see there), rounded once to it at the end; routing computes in
  * binary64.  Pointers must be aligned to their elements; rows that are 16-byte
  * aligned (base, leading dimensions and strides) load faster.  16-bit rows that start on
- * odd elements, an X of the products that spans 2^31 bytes or more, and panels that do (256 rows,
- * of any operand) take loads through registers, about half as fast.
+ * odd elements take loads through registers, 2 to 4 times slower; so do an X of the products
+ * that spans 2^31 bytes or more, and operands 256 rows of which do, 1.3 to 1.6 times slower.
  *
  * Arguments are validated in this order: the element type
  * (GEMM_F32_ERR_TYPE), sizes (GEMM_F32_ERR_DIM), leading dimensions and

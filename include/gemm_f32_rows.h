@@ -81,7 +81,9 @@ extern "C" {
  *                     s(t, index) / sum over j of s(t, index); 0 where the index
  *                     is -1 and where that sum is 0.
  *
- * The bias chooses and does not weigh.  GEMM_F32_ERR_DIM: E outside
+ * The bias chooses and does not weigh.  A normalised softmax is that of the chosen alone (the row's
+ * sum cancels): NaN among the others does not reach it, and it does not underflow.
+ * GEMM_F32_ERR_DIM: E outside
  * 1..GEMM_F32_MAX_EXPERTS, k outside 1..min(E, GEMM_F32_MAX_CHOSEN).
  * GEMM_F32_ERR_OPTION: unknown score; groups outside 1..GEMM_F32_MAX_CHOSEN or
  * no divisor of E; keep_groups outside 1..groups; group_top not 1 or 2.

@@ -602,9 +602,9 @@ constexpr int64_t kCountedInPlace = 1 << 15;
 // and every workgroup of the last launch adds them up itself.  That work grows with the square
 // of the slots (in a graph, us without and with the third launch: 65536 slots 9.9 and 11.4,
 // 262144: 16.6 and 12.8, 1048576: 46 and 22, 16777216: 7600 and 214); the launch costs a caller
-// outside of a graph 3 us.  In between, the limit is for that caller (E = 64: 131072 slots 13.7
-// and 16.3, in a graph 11.2 and 11.0; 196608 slots 14.0 and 16.7, in a graph 13.5 and 11.4):
-// what it would lose by the sums is more than what a graph loses without.
+// outside of a graph up to 3 us.  In between, where the one loses what the other gains, the limit is
+// for the caller without a graph (131072 slots, E = 64: 13.7 and 16.3, in a graph 11.2 and 11.0;
+// 196608 slots, E = 64: 14.0 and 16.7, in a graph 13.5 and 11.4, E = 256: 15.0 and 16.7, in a graph 14.8 and 12.1).
 constexpr int64_t kSummedFrom = 128;
 
 // A grid has fewer than 2^32 threads, a wave of them per token.

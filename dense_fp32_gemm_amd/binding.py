@@ -1,11 +1,13 @@
-"""ctypes binding of libgemm_f32.so (include/gemm_f32.h, gemm_f32_rows.h), same names.
+"""ctypes binding of libgemm_f32.so (include/gemm_f32.h, gemm_f32_rows.h, gemm_f32_ffn.h), same names.
 
 Argument marshalling only: every step of the product runs in the library's
 HIP kernels.  ``matmul`` is a convenience over ``gemm_f32`` that takes torch
 tensors for device memory and the current torch stream; it validates layout
 and raises on any non-zero status.  ``route``, ``expert_map``, ``grouped_matmul``,
 ``combine``, ``adapter_matmul`` and the ``*_grad`` functions do the same for the
-products whose second matrix is chosen row by row.  There is no fallback: if the library is
+products whose second matrix is chosen row by row, and ``rms_norm``, ``rms_norm_int8``,
+``quantize``, ``int8_matmul``, ``gated_matmul`` and their ``*_grad`` functions for the
+operators of a feed-forward block.  There is no fallback: if the library is
 missing and cannot be built, loading raises.
 """
 from __future__ import annotations
@@ -34,6 +36,8 @@ GEMM_F32_SCORE_SOFTMAX, GEMM_F32_SCORE_SIGMOID = 0, 1
 GEMM_F32_MAX_EXPERTS = 1024
 GEMM_F32_MAX_CHOSEN = 64
 GEMM_F32_MAX_RANK = 256
+GEMM_F32_GATE_NONE, GEMM_F32_GATE_SILU, GEMM_F32_GATE_GELU, GEMM_F32_GATE_GELU_TANH = 0, 1, 2, 3
+GEMM_F32_MAX_INT8_DEPTH = 131071
 
 _lib = None
 
@@ -87,7 +91,15 @@ def load() -> ctypes.CDLL:
                 ("combine", i, [i, i, i, i, i, p, p, p, i, p, i, p]),
                 ("combine_grad", i, [i, i, i, i, i, p, p, p, i, p, i, p, i, p, p]),
                 ("adapters_ws_size", z, [i, i, i, i, i]),
-                ("adapters", i, [i, i, i, i, i, i, p, i, p, i, p, i, l, p, i, l, p, p, p, i, p, z, p])):
+                ("adapters", i, [i, i, i, i, i, i, p, i, p, i, p, i, l, p, i, l, p, p, p, i, p, z, p]),
+                ("rms_norm", i, [i, i, i, p, i, p, i, p, f, p, i, p, i, p]),
+                ("rms_norm_int8", i, [i, i, i, p, i, p, i, p, f, p, i, p, i, p, p]),
+                ("rms_norm_grad_ws_size", z, [i, i]),
+                ("rms_norm_grad", i, [i, i, i, p, i, p, i, p, f, p, i, p, i, p, p, z, p]),
+                ("quantize", i, [i, i, i, i, p, i, p, i, p, p]),
+                ("int8", i, [i, i, i, i, p, i, p, p, i, p, p, p, i, p]),
+                ("gated", i, [i, i, i, i, i, i, p, p, i, i, p, i, p, i, l, p, i, p, i, p]),
+                ("gate_grad", i, [i, i, i, i, p, i, p, i, p, i, p])):
             fn = getattr(lib, "gemm_f32_" + name)
             fn.argtypes, fn.restype = args, res
         lib.gemm_f32_status_string.argtypes = [i]
@@ -256,6 +268,59 @@ def gemm_f32_adapters(type, T, N, K, R, n, X, ldx, W, ldw, A, lda, stride_a, B, 
     _ints(T=T, N=N, K=K, R=R, n=n, ldx=ldx, ldw=ldw, lda=lda, ldb=ldb, ldy=ldy)
     return load().gemm_f32_adapters(type, T, N, K, R, n, X, ldx, W, ldw, A, lda, stride_a, B, ldb, stride_b, adapter,
                                     scale, Y, ldy, workspace, workspace_bytes, stream)
+
+
+# --- include/gemm_f32_ffn.h ---------------------------------------------------
+def gemm_f32_rms_norm(type, T, N, X, ldx, residual, ldr, weight, eps, sum, lds, Y, ldy, stream=0) -> int:
+    """Y = S / rms(S) * weight, S = X + residual."""
+    _ints(T=T, N=N, ldx=ldx, ldr=ldr, lds=lds, ldy=ldy)
+    return load().gemm_f32_rms_norm(type, T, N, X, ldx, residual, ldr, weight, eps, sum, lds, Y, ldy, stream)
+
+
+def gemm_f32_rms_norm_int8(type, T, N, X, ldx, residual, ldr, weight, eps, sum, lds, Q, ldq, scale, stream=0) -> int:
+    """The same with each row in 8 bits and a scale."""
+    _ints(T=T, N=N, ldx=ldx, ldr=ldr, lds=lds, ldq=ldq)
+    return load().gemm_f32_rms_norm_int8(type, T, N, X, ldx, residual, ldr, weight, eps, sum, lds, Q, ldq, scale, stream)
+
+
+def gemm_f32_rms_norm_grad_ws_size(T, N) -> int:
+    """Workspace bytes of gemm_f32_rms_norm_grad's dweight."""
+    _ints(T=T, N=N)
+    return load().gemm_f32_rms_norm_grad_ws_size(T, N)
+
+
+def gemm_f32_rms_norm_grad(type, T, N, dY, lddy, S, lds, weight, eps, dsum, ldds, dX, lddx, dweight, workspace,
+                           workspace_bytes, stream=0) -> int:
+    """Gradients of gemm_f32_rms_norm: of S, and of the weight."""
+    _ints(T=T, N=N, lddy=lddy, lds=lds, ldds=ldds, lddx=lddx)
+    return load().gemm_f32_rms_norm_grad(type, T, N, dY, lddy, S, lds, weight, eps, dsum, ldds, dX, lddx, dweight,
+                                         workspace, workspace_bytes, stream)
+
+
+def gemm_f32_quantize(type, gate, T, N, X, ldx, Q, ldq, scale, stream=0) -> int:
+    """Rows of X, or of a gated pair, in 8 bits and a scale each."""
+    _ints(gate=gate, T=T, N=N, ldx=ldx, ldq=ldq)
+    return load().gemm_f32_quantize(type, gate, T, N, X, ldx, Q, ldq, scale, stream)
+
+
+def gemm_f32_int8(type, T, N, K, Q, ldq, scale, W, ldw, w_scale, bias, Y, ldy, stream=0) -> int:
+    """Y = Q . W^T with a scale for each row of both, plus bias."""
+    _ints(T=T, N=N, K=K, ldq=ldq, ldw=ldw, ldy=ldy)
+    return load().gemm_f32_int8(type, T, N, K, Q, ldq, scale, W, ldw, w_scale, bias, Y, ldy, stream)
+
+
+def gemm_f32_gated(type, gate, G, P, N, K, offsets, order, per_row, rows, X, ldx, W, ldw, stride_w, H, ldh, pre, ldp,
+                   stream=0) -> int:
+    """H(p,:) = act(g) u, [g u] = X(r(p),:) . W_g for every place p of group g."""
+    _ints(gate=gate, G=G, P=P, N=N, K=K, per_row=per_row, rows=rows, ldx=ldx, ldw=ldw, ldh=ldh, ldp=ldp)
+    return load().gemm_f32_gated(type, gate, G, P, N, K, offsets, order, per_row, rows, X, ldx, W, ldw, stride_w, H, ldh,
+                                 pre, ldp, stream)
+
+
+def gemm_f32_gate_grad(type, gate, P, N, pre, ldp, dH, lddh, dpre, lddp, stream=0) -> int:
+    """Gradient of [g u] from that of act(g) u."""
+    _ints(gate=gate, P=P, N=N, ldp=ldp, lddh=lddh, lddp=lddp)
+    return load().gemm_f32_gate_grad(type, gate, P, N, pre, ldp, dH, lddh, dpre, lddp, stream)
 
 
 def gemm_f32_status_string(status: int) -> str:
@@ -504,6 +569,9 @@ def expert_map(index, experts: int, *, stream=None):
 def _grouped_args(X, offsets, order):
     """What forward and weight gradient have in common: places, rows, addresses."""
     import torch
+    if offsets is None:
+        P = X.shape[0] if order is None else order.numel()
+        return 1, P, 0, 0 if order is None else _vector(order, "order", torch.int32, X.device, (P,))
     G = offsets.numel() - 1
     if G < 0:
         raise ValueError("offsets must have one number more than there are groups")
@@ -513,11 +581,11 @@ def _grouped_args(X, offsets, order):
     return G, order.numel(), o, _vector(order, "order", torch.int32, X.device, (order.numel(),))
 
 
-def grouped_matmul(X, W, offsets, *, order=None, per_row: int = 1, out=None, stream=None):
+def grouped_matmul(X, W, offsets=None, *, order=None, per_row: int = 1, out=None, stream=None):
     """Y [P, N]: rows of X times the matrix W[g] ([G, K, N]) of the group their place is in.
 
-    Place p is in group g when offsets[g] <= p < offsets[g + 1].  Its row of
-    X is p, or order[p] // per_row (expert_map's order, and k choices per
+    Place p is in group g when offsets[g] <= p < offsets[g + 1]; offsets None: all
+    places are in the one group of W [1, K, N].  Its row of X is p, or order[p] // per_row (expert_map's order, and k choices per
     row).  Rows of `out` in no group are left as they were.
     """
     import torch
@@ -541,7 +609,7 @@ def grouped_matmul(X, W, offsets, *, order=None, per_row: int = 1, out=None, str
     return out
 
 
-def grouped_grad_x(dY, W, offsets, *, out=None, stream=None):
+def grouped_grad_x(dY, W, offsets=None, *, out=None, stream=None):
     """dX [P, K] of grouped_matmul's places: rows of dY [P, N] times W[g]^T.
 
     With an order, the gradient of X is combine(dX, position) over a row's places.
@@ -566,7 +634,7 @@ def grouped_grad_x(dY, W, offsets, *, out=None, stream=None):
     return out
 
 
-def grouped_grad_w(X, dY, offsets, *, order=None, per_row: int = 1, out=None, stream=None):
+def grouped_grad_w(X, dY, offsets=None, *, order=None, per_row: int = 1, out=None, stream=None):
     """dW [G, K, N] of grouped_matmul from the gradient dY [P, N] of its places."""
     import torch
     if X.dim() != 2 or dY.dim() != 2:
@@ -673,4 +741,235 @@ def adapter_matmul(X, W, A, B, adapter, scale=None, *, out=None, workspace=None,
     _check(_lib.gemm_f32_adapters(type_, T, N, K, R, n, X.data_ptr(), ldx, W.data_ptr(), ldw, A.data_ptr(), lda, sa,
                                   B.data_ptr(), ldb, sb, a, c, out.data_ptr(), ldy, workspace.data_ptr(),
                                   workspace.numel(), _here(device)), "gemm_f32_adapters")
+    return out
+
+
+# --- torch convenience: a feed-forward block -----------------------------------
+# As above.  Weights of the norm, scales and biases are contiguous float32 vectors;
+# 8-bit rows are int8 matrices.
+def _gate(gate: str) -> int:
+    try:
+        return {"silu": GEMM_F32_GATE_SILU, "gelu": GEMM_F32_GATE_GELU, "gelu_tanh": GEMM_F32_GATE_GELU_TANH}[gate]
+    except (KeyError, TypeError):
+        raise ValueError(f"gate {gate!r} is none of 'silu', 'gelu' and 'gelu_tanh'") from None
+
+
+def _int8(t, name: str, device, shape) -> int:
+    """Leading dimension of a matrix of 8-bit numbers."""
+    import torch
+    if t.dtype != torch.int8 or t.device != device:
+        raise TypeError(f"{name} is {t.dtype} on {t.device}, expected {torch.int8} on {device}")
+    return _matrix(t, name, None, shape)
+
+
+def _norm_args(X, weight, residual, out_sum):
+    """What both norms have in common: type, sizes, addresses and leading dimensions."""
+    import torch
+    T, N = X.shape
+    ldx = _matrix(X, "X")
+    w = 0 if weight is None else _vector(weight, "weight", torch.float32, X.device, (N,))
+    if residual is None:
+        if out_sum is not None:
+            raise ValueError("out_sum is the sum with a residual, and there is none")
+        return T, N, ldx, w, 0, 0, None, 0
+    ldr = _matrix(residual, "residual", X, (T, N))
+    if out_sum is None:
+        out_sum = X.new_empty((T, N))
+    return T, N, ldx, w, residual.data_ptr(), ldr, out_sum, _matrix(out_sum, "out_sum", X, (T, N))
+
+
+def rms_norm(X, weight=None, *, eps: float = 1e-6, residual=None, out=None, out_sum=None, stream=None):
+    """Y [T, N]: rows of S = X + residual over their root mean square, times weight [N].
+
+    Returns Y, or (Y, S) with a residual.  S is rounded to the type and Y is the
+    norm of that S.  out and out_sum may be X or the residual themselves.
+    """
+    if X.dim() != 2:
+        raise ValueError("X must be [T, N]")
+    type_ = _type(X)
+    device = X.device
+    if not X.is_cuda:
+        raise TypeError("X must be on a GPU")
+    if _elsewhere(device, stream):
+        return _call_on(device, stream, rms_norm, X, weight, eps=eps, residual=residual, out=out, out_sum=out_sum)
+    T, N, ldx, w, r, ldr, S, lds = _norm_args(X, weight, residual, out_sum)
+    if out is None:
+        out = X.new_empty((T, N))
+    ldy = _matrix(out, "out", X, (T, N))
+    _fit(T, N, ldx, ldr, lds, ldy)
+    _check(_lib.gemm_f32_rms_norm(type_, T, N, X.data_ptr(), ldx, r, ldr, w, eps, 0 if S is None else S.data_ptr(), lds,
+                                  out.data_ptr(), ldy, _here(device)), "gemm_f32_rms_norm")
+    return out if residual is None else (out, S)
+
+
+def rms_norm_int8(X, weight=None, *, eps: float = 1e-6, residual=None, out_sum=None, stream=None):
+    """(Q [T, N] int8, scale [T] float32), or (Q, scale, S) with a residual: rms_norm's rows in 8 bits.
+
+    scale is a row's largest magnitude / 127; Q * scale is the row to within half
+    a scale.  A row with NaN or infinities has scale NaN.
+    """
+    import torch
+    if X.dim() != 2:
+        raise ValueError("X must be [T, N]")
+    type_ = _type(X)
+    device = X.device
+    if not X.is_cuda:
+        raise TypeError("X must be on a GPU")
+    if _elsewhere(device, stream):
+        return _call_on(device, stream, rms_norm_int8, X, weight, eps=eps, residual=residual, out_sum=out_sum)
+    T, N, ldx, w, r, ldr, S, lds = _norm_args(X, weight, residual, out_sum)
+    Q = X.new_empty((T, N), dtype=torch.int8)
+    scale = X.new_empty(T, dtype=torch.float32)
+    ldq = max(N, 1)
+    _fit(T, N, ldx, ldr, lds, ldq)
+    _check(_lib.gemm_f32_rms_norm_int8(type_, T, N, X.data_ptr(), ldx, r, ldr, w, eps, 0 if S is None else S.data_ptr(),
+                                       lds, Q.data_ptr(), ldq, scale.data_ptr(), _here(device)),
+           "gemm_f32_rms_norm_int8")
+    return (Q, scale) if residual is None else (Q, scale, S)
+
+
+def rms_norm_grad(dY, S, weight=None, *, eps: float = 1e-6, dsum=None, out=None, stream=None):
+    """(dX [T, N], dweight [N] float32) of rms_norm() from dY, at its S (X without a residual).
+
+    dsum [T, N] is the gradient that reaches S by other ways; dX is that of X and of the
+    residual.  out may be dY, S or dsum itself.
+    """
+    import torch
+    if dY.dim() != 2:
+        raise ValueError("dY must be [T, N]")
+    type_, lddy = _type(dY), _matrix(dY, "dY")
+    device = dY.device
+    if _elsewhere(device, stream):
+        return _call_on(device, stream, rms_norm_grad, dY, S, weight, eps=eps, dsum=dsum, out=out)
+    T, N = dY.shape
+    lds = _matrix(S, "S", dY, (T, N))
+    w = 0 if weight is None else _vector(weight, "weight", torch.float32, device, (N,))
+    ds, ldds = (0, 0) if dsum is None else (dsum.data_ptr(), _matrix(dsum, "dsum", dY, (T, N)))
+    if out is None:
+        out = dY.new_empty((T, N))
+    lddx = _matrix(out, "out", dY, (T, N))
+    dweight = dY.new_empty(N, dtype=torch.float32)
+    _fit(T, N, lddy, lds, ldds, lddx)
+    ws = dY.new_empty(_lib.gemm_f32_rms_norm_grad_ws_size(T, N), dtype=torch.uint8)
+    _check(_lib.gemm_f32_rms_norm_grad(type_, T, N, dY.data_ptr(), lddy, S.data_ptr(), lds, w, eps, ds, ldds,
+                                       out.data_ptr(), lddx, dweight.data_ptr(), ws.data_ptr(), ws.numel(),
+                                       _here(device)), "gemm_f32_rms_norm_grad")
+    return out, dweight
+
+
+def quantize(X, *, gate=None, stream=None):
+    """(Q [T, N] int8, scale [T] float32): rows of X in 8 bits, as rms_norm_int8's.
+
+    With a gate ('silu', 'gelu' or 'gelu_tanh') X is [T, 2 N] and the rows are
+    act(X[:, :N]) * X[:, N:].  A weight [N, K] becomes int8_matmul's W and w_scale.
+    """
+    import torch
+    if X.dim() != 2:
+        raise ValueError("X must be [T, N]")
+    type_, ldx = _type(X), _matrix(X, "X")
+    kind = GEMM_F32_GATE_NONE if gate is None else _gate(gate)
+    device = X.device
+    T, N = X.shape
+    if gate is not None:
+        if N % 2:
+            raise ValueError(f"X has {N} columns, a gated pair has an even number")
+        N //= 2
+    if _elsewhere(device, stream):
+        return _call_on(device, stream, quantize, X, gate=gate)
+    Q = X.new_empty((T, N), dtype=torch.int8)
+    scale = X.new_empty(T, dtype=torch.float32)
+    _fit(T, N, ldx)
+    _check(_lib.gemm_f32_quantize(type_, kind, T, N, X.data_ptr(), ldx, Q.data_ptr(), max(N, 1), scale.data_ptr(),
+                                  _here(device)), "gemm_f32_quantize")
+    return Q, scale
+
+
+def int8_matmul(Q, scale, W, w_scale, *, bias=None, dtype=None, out=None, stream=None):
+    """Y [T, N] = (Q [T, K] . W [N, K]^T) * scale[:, None] * w_scale + bias, of `dtype` (bfloat16).
+
+    Q and W are int8 with a scale (float32) for each row of theirs, as quantize() makes
+    them; the sums are exact.
+    """
+    import torch
+    if Q.dim() != 2 or W.dim() != 2:
+        raise ValueError("Q must be [T, K] and W [N, K]")
+    device = Q.device
+    if not Q.is_cuda:
+        raise TypeError("Q must be on a GPU")
+    if _elsewhere(device, stream):
+        return _call_on(device, stream, int8_matmul, Q, scale, W, w_scale, bias=bias, dtype=dtype, out=out)
+    T, K = Q.shape
+    N = W.shape[0]
+    ldq, ldw = _int8(Q, "Q", device, (T, K)), _int8(W, "W", device, (N, K))
+    s = _vector(scale, "scale", torch.float32, device, (T,))
+    ws = _vector(w_scale, "w_scale", torch.float32, device, (N,))
+    b = 0 if bias is None else _vector(bias, "bias", torch.float32, device, (N,))
+    if out is None:
+        out = Q.new_empty((T, N), dtype=torch.bfloat16 if dtype is None else dtype)
+    elif dtype is not None and out.dtype != dtype:
+        raise TypeError(f"out is {out.dtype}, expected {dtype}")
+    type_ = _type(out)
+    if out.device != device:
+        raise TypeError(f"out is on {out.device}, expected {device}")
+    ldy = _matrix(out, "out", None, (T, N))
+    _fit(T, N, K, ldq, ldw, ldy)
+    _check(_lib.gemm_f32_int8(type_, T, N, K, Q.data_ptr(), ldq, s, W.data_ptr(), ldw, ws, b, out.data_ptr(), ldy,
+                              _here(device)), "gemm_f32_int8")
+    return out
+
+
+def gated_matmul(X, W, offsets=None, *, order=None, per_row: int = 1, gate: str = "silu", save: bool = False, out=None,
+                 stream=None):
+    """H [P, N] = act(g) * u with [g u] = rows of X times W[g] ([G, K, 2 N]: the gate's columns, then the others).
+
+    Places, offsets, order and per_row as in grouped_matmul(); offsets None: a dense
+    block, all places in the one group of W [1, K, 2 N].  With `save` returns (H, pre),
+    pre [P, 2 N] = [g u] for gate_grad().  Rows of no group are left as they were in
+    `out` (undefined if it is None, and in pre).
+    """
+    if X.dim() != 2 or W.dim() != 3:
+        raise ValueError("X must be [rows, K] and W [G, K, 2 N]")
+    type_, ldx, kind = _type(X), _matrix(X, "X"), _gate(gate)
+    device = X.device
+    if W.shape[2] % 2:
+        raise ValueError(f"W has {W.shape[2]} columns, a gated pair has an even number")
+    if _elsewhere(device, stream):
+        return _call_on(device, stream, gated_matmul, X, W, offsets, order=order, per_row=per_row, gate=gate, save=save,
+                        out=out)
+    G, P, o, r = _grouped_args(X, offsets, order)
+    rows, K = X.shape
+    N = W.shape[2] // 2
+    ldw = _matrix(W, "W", X, (G, K, 2 * N))
+    stride = _stack(W, "W", ldw)
+    if out is None:
+        out = X.new_empty((P, N))
+    ldh = _matrix(out, "out", X, (P, N))
+    pre = X.new_empty((P, 2 * N)) if save else None
+    _fit(G, P, 2 * N, K, per_row, rows, ldx, ldw, ldh)
+    _check(_lib.gemm_f32_gated(type_, kind, G, P, N, K, o, r, per_row, rows, X.data_ptr(), ldx, W.data_ptr(), ldw, stride,
+                               out.data_ptr(), ldh, pre.data_ptr() if save else 0, max(2 * N, 1), _here(device)),
+           "gemm_f32_gated")
+    return (out, pre) if save else out
+
+
+def gate_grad(dH, pre, *, gate: str = "silu", out=None, stream=None):
+    """dpre [P, 2 N] of gated_matmul() from dH [P, N], at the pre that it kept.
+
+    grouped_grad_x(dpre, W, offsets) and grouped_grad_w(X, dpre, offsets, ...) take it
+    on.  out may be pre itself.
+    """
+    if dH.dim() != 2 or pre.dim() != 2:
+        raise ValueError("dH must be [P, N] and pre [P, 2 N]")
+    type_, lddh, kind = _type(dH), _matrix(dH, "dH"), _gate(gate)
+    device = dH.device
+    if _elsewhere(device, stream):
+        return _call_on(device, stream, gate_grad, dH, pre, gate=gate, out=out)
+    P, N = dH.shape
+    ldp = _matrix(pre, "pre", dH, (P, 2 * N))
+    if out is None:
+        out = dH.new_empty((P, 2 * N))
+    ldo = _matrix(out, "out", dH, (P, 2 * N))
+    _fit(P, 2 * N, lddh, ldp, ldo)
+    _check(_lib.gemm_f32_gate_grad(type_, kind, P, N, pre.data_ptr(), ldp, dH.data_ptr(), lddh, out.data_ptr(), ldo,
+                                   _here(device)), "gemm_f32_gate_grad")
     return out

@@ -15,7 +15,8 @@ import sys
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 SOURCES = [os.path.join(PKG, "csrc", f) for f in
-           ("gemm_f32.hip", "host.hip", "rows_route.hip", "rows_grouped.hip", "rows_adapters.hip")]
+           ("gemm_f32.hip", "host.hip", "rows_route.hip", "rows_grouped.hip", "rows_adapters.hip", "ffn_norm.hip",
+            "ffn_quantize.hip", "ffn_int8.hip", "ffn_gated.hip")]
 INCLUDE = os.path.join(ROOT, "include")
 LIBRARY = os.path.join(PKG, "libgemm_f32.so")
 ARCH = "gfx950"

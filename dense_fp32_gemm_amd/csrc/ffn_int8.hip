@@ -1,0 +1,235 @@
+// The product of 8-bit rows and 8-bit weights with a scale for each token and channel
+// (include/gemm_f32_ffn.h).
+//
+//  * few rows: int8_few_kernel.  16 channels a workgroup, K over its waves,
+//    operands straight into registers.  Bound by the weights' bytes.
+//  * else int8_kernel: tiles as in rows_tile.h, both operands' k contiguous.
+
+#include "ffn_gate.h"
+#include "rows_groups.h"
+
+namespace ffn {
+namespace {
+
+struct Int8Args {
+    const int8_t *Q, *W;
+    const float *scale, *w_scale, *bias;
+    void *Y;
+    int64_t ldq, ldw, ldy;
+    int T, N, K;
+    int tiles_m, tiles_n, slots, xcds;
+    bool vector_y;
+};
+
+// Four neighbouring channels' sums of row t, scaled, to Y.
+template <class Out>
+__device__ inline void int8_store(const Int8Args &g, int64_t t, int n, i32x4 v)
+{
+    const float s = g.scale[t];
+    f32x4 y;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int c = n + i < g.N ? n + i : g.N - 1;
+        y[i] = (float)v[i] * (s * g.w_scale[c]);
+        if (g.bias != nullptr)
+            y[i] += g.bias[c];
+    }
+    typename Out::T *p = (typename Out::T *)g.Y + t * g.ldy + n;
+    if (g.vector_y)
+        store4<Out, true>(p, y, g.N - n);
+    else
+        store4<Out, false>(p, y, g.N - n);
+}
+
+template <class Out, int BM, int BN, int WM, int WN, int S, bool DMA>
+__device__ inline void int8_tile(const Int8Args &g, int m0, int n0, int8_t *lds)
+{
+    using Ti = Tile<I8, true, true, BM, BN, WM, WN>;
+    constexpr int NT = Ti::kThreads;
+    if (m0 >= g.T || n0 >= g.N)
+        return;                                      // the whole workgroup
+    const int tid = threadIdx.x, lane = tid % kWave, wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+    const int wm = wave / WN, wn = wave % WN;
+    Ti tile;
+    tile.clear();
+    const Along<I8, BM, NT> a(g.Q + m0 * g.ldq, tid, g.K, g.ldq, g.T - m0,
+                              [&](int, int r) { return m0 + r < g.T ? r * g.ldq : -1; });
+    const Along<I8, BN, NT> b(g.W + n0 * g.ldw, tid, g.K, g.ldw, g.N - n0,
+                              [&](int, int r) { return n0 + r < g.N ? r * g.ldw : -1; });
+    sum_panels<I8, DMA, S>(tile, g.K, a, b, lds, tid, wm, wn);
+    tile.each(wm, wn, lane, [&](int r, int c, i32x4 v) {
+        if (m0 + r < g.T && n0 + c < g.N)
+            int8_store<Out>(g, m0 + r, n0 + c, v);
+    });
+}
+
+// Tiles are numbered column by column: those of a die share W's panels.
+template <class Out, int BM, int BN, int WM, int WN, int S, bool CUT, bool DMA>
+__global__ __launch_bounds__(WM *WN *kWave, 2) void int8_kernel(Int8Args g)
+{
+    constexpr int kPanel = (BM + BN) * kDeep16 * I8::kChunk;
+    // (S = 2) two panels of the whole tile, three of a half, four of a quarter
+    __shared__ __attribute__((aligned(16))) int8_t lds[CUT && DMA ? 9 * kPanel / 4 : (DMA ? S : 2) * kPanel];
+    static_assert(!CUT || (S == 2 && BM == BN), "panels of cut tiles");
+    const int total = g.tiles_m * g.tiles_n;
+    Part part{-1, 1, 0};
+    if constexpr (CUT)
+        part = part_of(blockIdx.x, total, g.slots, g.xcds);
+    else if ((int)blockIdx.x < total)
+        part.tile = die_contiguous(blockIdx.x, total, g.xcds);
+    if (part.tile < 0)
+        return;                                      // the whole workgroup
+    const int m0 = part.tile % g.tiles_m * BM, n0 = part.tile / g.tiles_m * BN;
+    if (!CUT || part.cut == 1)
+        int8_tile<Out, BM, BN, WM, WN, S, DMA>(g, m0, n0, lds);
+    if constexpr (CUT) {
+        if (part.cut == 2)
+            int8_tile<Out, BM / 2, BN, WM, WN, 3, DMA>(g, m0 + part.piece * (BM / 2), n0, lds);
+        else if (part.cut == 4)
+            int8_tile<Out, BM / 2, BN / 2, WM, WN, 4, DMA>(g, m0 + part.piece % 2 * (BM / 2), n0 + part.piece / 2 * (BN / 2), lds);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Few rows
+// ---------------------------------------------------------------------------
+constexpr int kFewWaves = 8, kFewSteps = 4;          // waves of a workgroup; 64 k's a wave takes at once
+
+// 16 channels and up to 16 MT rows a workgroup.  Wave w takes every kFewWaves-th block of
+// 256 k: 16 bytes a lane, 256 bytes of a row side by side.  The waves' sums meet in LDS.
+template <class Out, bool VEC, int MT>
+__global__ __launch_bounds__(kFewWaves *kWave) void int8_few_kernel(Int8Args g)
+{
+    constexpr int kBlock = kFewSteps * 64;
+    __shared__ i32x4 part[kFewWaves][MT][kWave];
+    const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave, i = lane % 16, h = lane / 16;
+    const int n0 = blockIdx.x * 16;
+    const bool channel = n0 + i < g.N;
+    const int8_t *w = g.W + (channel ? n0 + i : 0) * g.ldw + 16 * h;
+    i32x4 acc[MT] = {};
+    for (int k0 = wave * kBlock; k0 < g.K; k0 += kFewWaves * kBlock) {
+        u32x4 b[kFewSteps], a[MT][kFewSteps];
+#pragma unroll
+        for (int s = 0; s < kFewSteps; ++s) {
+            const int k = k0 + 64 * s, left = g.K - k - 16 * h;
+            b[s] = load_chunk<I8, VEC>(w + k, channel ? left : 0);
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+                const int t = 16 * m + i;
+                a[m][s] = load_chunk<I8, VEC>(g.Q + (t < g.T ? t : 0) * g.ldq + 16 * h + k, t < g.T ? left : 0);
+            }
+        }
+#pragma unroll
+        for (int s = 0; s < kFewSteps; ++s)
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+                acc[m] = mfma<I8>(b[s], a[m][s], acc[m], 0);
+    }
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+        part[wave][m][lane] = acc[m];
+    __syncthreads();
+    for (int m = wave; m < MT; m += kFewWaves) {
+        i32x4 sum = part[0][m][lane];
+#pragma unroll
+        for (int v = 1; v < kFewWaves; ++v)
+            sum += part[v][m][lane];
+        const int t = 16 * m + i, n = n0 + 4 * h;
+        if (t < g.T && n < g.N)
+            int8_store<Out>(g, t, n, sum);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Host side
+// ---------------------------------------------------------------------------
+template <class Out, int BM, int BN, int WM, int WN, int S, int PER_CU>
+int launch_int8(Int8Args g, bool dma, hipStream_t stream, bool go)
+{
+    const int64_t tiles_m = ceil_div(g.T, BM), tiles_n = ceil_div(g.N, BN);
+    g.slots = (int)gemm_f32_internal::current_device().cus * PER_CU;
+    // cutting the last round adds at most three pieces for a quarter of the slots
+    const int64_t grid = tiles_m * tiles_n + g.slots;
+    if (grid > kMaxTiles)
+        return GEMM_F32_ERR_DIM;
+    if (!go || tiles_m * tiles_n == 0)
+        return GEMM_F32_OK;
+    g.tiles_m = (int)tiles_m;
+    g.tiles_n = (int)tiles_n;
+    constexpr bool kCut = PER_CU > 0;
+    if (dma)
+        int8_kernel<Out, BM, BN, WM, WN, S, kCut, true><<<(int)grid, WM * WN * kWave, 0, stream>>>(g);
+    else
+        int8_kernel<Out, BM, BN, WM, WN, S, kCut, false><<<(int)grid, WM * WN * kWave, 0, stream>>>(g);
+    return launched();
+}
+
+constexpr int kFewRows = 64;
+
+int launch_int8(int type, const Int8Args &g, bool dma, bool vec, hipStream_t stream, bool go)
+{
+    int rc = GEMM_F32_OK;
+    with_type(type, [&](auto e) {
+        using Out = decltype(e);
+        if (g.T <= kFewRows) {
+            const int64_t grid = ceil_div(g.N, 16);  // under kMaxTiles * 512 / 16: g.N < 2^31
+            if (grid * kFewWaves * kWave > UINT32_MAX) {
+                rc = GEMM_F32_ERR_DIM;
+                return;
+            }
+            if (!go || g.T == 0 || grid == 0)
+                return;
+            auto few = [&](auto mt) {
+                if (vec)
+                    int8_few_kernel<Out, true, decltype(mt)::value><<<(int)grid, kFewWaves * kWave, 0, stream>>>(g);
+                else
+                    int8_few_kernel<Out, false, decltype(mt)::value><<<(int)grid, kFewWaves * kWave, 0, stream>>>(g);
+            };
+            if (g.T <= 16)
+                few(std::integral_constant<int, 1>{});
+            else if (g.T <= 32)
+                few(std::integral_constant<int, 2>{});
+            else
+                few(std::integral_constant<int, 4>{});
+            rc = launched();
+        } else if (ceil_div(g.T, 256) * ceil_div(g.N, 256) * 5 >= 3 * gemm_f32_internal::current_device().cus) {
+            rc = launch_int8<Out, 256, 256, 2, 4, 2, 1>(g, dma, stream, go);
+        } else {
+            rc = launch_int8<Out, 64, 128, 2, 2, 3, 0>(g, dma, stream, go);
+        }
+    });
+    return rc;
+}
+
+// Rows of 8-bit elements that the direct loads can address (see dma_rows()).
+bool dma_bytes(const void *p, int64_t ld) { return aligned_to(p, 4) && ld % 4 == 0 && kPanelRows * ld < (int64_t)kNowhere - 16; }
+bool chunk_bytes(const void *p, int64_t ld, int K) { return aligned_to(p, 16) && ld % 16 == 0 && K % 16 == 0; }
+
+}  // namespace
+}  // namespace ffn
+
+using namespace ffn;
+
+extern "C" int gemm_f32_int8(int type, int T, int N, int K, const int8_t *Q, int ldq, const float *scale, const int8_t *W,
+                             int ldw, const float *w_scale, const float *bias, void *Y, int ldy, hipStream_t stream)
+{
+    if (!known_type(type))
+        return GEMM_F32_ERR_TYPE;
+    if (bad_size(T) || bad_size(N) || K < 0 || K > GEMM_F32_MAX_INT8_DEPTH)
+        return GEMM_F32_ERR_DIM;
+    const Int8Args g{Q, W, scale, w_scale, bias, Y, ldq, ldw, ldy, T, N, K, 0, 0, 0, gemm_f32_internal::current_device().xcds,
+                     vector_rows(type, Y, ldy, 0, N)};
+    const int rc = launch_int8(type, g, false, false, nullptr, false);
+    if (rc != GEMM_F32_OK)
+        return rc;
+    if (short_ld(ldq, K) || short_ld(ldw, K) || short_ld(ldy, N))
+        return GEMM_F32_ERR_LD;
+    if (T == 0 || N == 0)
+        return GEMM_F32_OK;
+    if ((K > 0 && (Q == nullptr || W == nullptr)) || scale == nullptr || w_scale == nullptr || Y == nullptr)
+        return GEMM_F32_ERR_NULL;
+    if (!aligned_to(scale, 4) || !aligned_to(w_scale, 4) || !aligned_to(bias, 4) || !aligned_to(Y, type_bytes(type)))
+        return GEMM_F32_ERR_ALIGN;
+    return launch_int8(type, g, dma_bytes(Q, ldq) && dma_bytes(W, ldw), chunk_bytes(Q, ldq, K) && chunk_bytes(W, ldw, K),
+                       stream, true);
+}

@@ -1,0 +1,403 @@
+// Root-mean-square norm with the residual's addition, and its gradient (include/gemm_f32_ffn.h).
+//
+// A row belongs to TPR threads (a wave, or a workgroup), C chunks of 16 bytes each in
+// registers: one pass over the data.  Rows that do not fit (C = 0) are read again
+// where they are needed, chunk by chunk.  All kernels are bound by HBM.
+
+#include "ffn_rows.h"
+
+namespace ffn {
+namespace {
+
+// ---------------------------------------------------------------------------
+// Norm
+// ---------------------------------------------------------------------------
+struct NormArgs {
+    const void *X, *R;       // R: the residual, or NULL
+    const float *weight;     // NULL: 1
+    void *S;                 // NULL: not written
+    void *Y;                 // of E, or 8 bits
+    float *scale;            // 8 bits: of each row
+    int64_t ldx, ldr, lds, ldy;
+    double eps;
+    int T, N;
+};
+
+template <class E, bool VEC, bool INT8, int TPR, int C>
+__global__ __launch_bounds__(kRowThreads<TPR>) void norm_kernel(NormArgs g)
+{
+    using T = typename E::T;
+    constexpr int kRows = kRowsAtOnce<TPR>, K = E::kChunk;
+    __shared__ uint64_t slots[2][TPR / kWave];
+    const int j = threadIdx.x % TPR;
+    RowSums<TPR> over{slots};
+    auto weights = [&](float (&w)[K], int n0) {
+        if (g.weight != nullptr)
+            load_floats<E>(w, g.weight + n0, g.N - n0);
+        else
+#pragma unroll
+            for (int e = 0; e < K; ++e)
+                w[e] = 1.f;
+    };
+    float w[C > 0 ? C : 1][K];
+    if constexpr (C > 0)
+        each_chunk<TPR, C, E>(g.N, j, [&](int i, int n0) { weights(w[i], n0); });
+    for (int64_t t0 = (int64_t)blockIdx.x * kRows; t0 < g.T; t0 += (int64_t)gridDim.x * kRows) {
+        const int64_t t = t0 + threadIdx.x / TPR;
+        const bool there = t < g.T;
+        const T *x = (const T *)g.X + (there ? t : 0) * g.ldx, *r = (const T *)g.R + (there && g.R != nullptr ? t : 0) * g.ldr;
+        T *s = (T *)g.S + (there ? t : 0) * g.lds;
+        // S as it is computed, before it is written over X or R
+        auto summed = [&](Chunk<E> &z, int n0) {
+            const int left = there ? g.N - n0 : 0;
+            z.raw = load_chunk<E, VEC>(x + n0, left);
+            if (g.R != nullptr) {
+                Chunk<E> b;
+                b.raw = load_chunk<E, VEC>(r + n0, left);
+#pragma unroll
+                for (int e = 0; e < K; ++e)
+                    z.e[e] = (T)((float)z.e[e] + (float)b.e[e]);
+            }
+        };
+        // ... and read again afterwards
+        const bool kept = g.R != nullptr && g.S != nullptr;
+        auto again = [&](Chunk<E> &z, int n0) {
+            if (kept)
+                z.raw = load_chunk<E, VEC>(s + n0, there ? g.N - n0 : 0);
+            else
+                summed(z, n0);
+        };
+        Chunk<E> z[C > 0 ? C : 1];
+        double squares = 0.0;
+        if constexpr (C > 0)                         // all loads, then their use
+            each_chunk<TPR, C, E>(g.N, j, [&](int i, int n0) { summed(z[i], n0); });
+        each_chunk<TPR, C, E>(g.N, j, [&](int i, int n0) {
+            if constexpr (C == 0)
+                summed(z[i], n0);
+            if (kept && there)
+                store_chunk<E, VEC>(s + n0, z[i], g.N - n0);
+#pragma unroll
+            for (int e = 0; e < K; ++e)
+                squares = fma((double)(float)z[i].e[e], (double)(float)z[i].e[e], squares);
+        });
+        const double scale = 1.0 / sqrt(over.sum(squares) / g.N + g.eps);
+        const float scale32 = (float)scale;
+        if constexpr (!INT8) {
+            each_chunk<TPR, C, E>(g.N, j, [&](int i, int n0) {
+                if constexpr (C == 0) {
+                    again(z[i], n0);
+                    weights(w[i], n0);
+                }
+                Chunk<E> o;
+#pragma unroll
+                for (int e = 0; e < K; ++e)
+                    o.e[e] = (T)((float)z[i].e[e] * scale32 * w[i][e]);
+                if (there)
+                    store_chunk<E, VEC>((T *)g.Y + t * g.ldy + n0, o, g.N - n0);
+            });
+        } else {
+            Int8Row<TPR, C, E> row{g.N, j, there, (int8_t *)g.Y + (there ? t : 0) * g.ldy};
+            int loaded = -1;                         // C = 0: the column whose chunk z and w hold
+            row.write(over, g.scale + t, 0x1p-21f,
+                      [&](int i, int e, int n) {
+                          if constexpr (C == 0) {
+                              if (loaded != n - e) {
+                                  loaded = n - e;
+                                  again(z[i], loaded);
+                                  weights(w[i], loaded);
+                              }
+                          }
+                          return (float)z[i].e[e] * scale32 * w[i][e];
+                      },
+                      [&](int n) {
+                          float v;
+                          if (kept)
+                              v = (float)s[n];
+                          else if (g.R != nullptr)
+                              v = (float)(T)((float)x[n] + (float)r[n]);
+                          else
+                              v = (float)x[n];
+                          return (double)v * (g.weight != nullptr ? (double)g.weight[n] : 1.0) * scale;
+                      },
+                      [](int, int, int) { return false; });
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Gradient of the norm
+// ---------------------------------------------------------------------------
+struct NormGradArgs {
+    const void *dY, *S, *dS;     // dS: NULL: none
+    const float *weight;
+    void *dX;                    // NULL: not computed
+    float *partial;              // [workgroups][N] of dweight, NULL: not computed
+    int64_t lddy, lds, ldds, lddx;
+    double eps;
+    int T, N;
+};
+
+// A thread keeps its columns over all rows of its workgroup, and their part of dweight in
+// registers; the workgroup's parts go to the workspace, which sum_kernel adds up.
+// (C = 0: the parts are added in the workspace, by the thread whose columns they are.)
+template <class E, bool VEC, int TPR, int C>
+__global__ __launch_bounds__(kRowThreads<TPR>) void norm_grad_kernel(NormGradArgs g)
+{
+    using T = typename E::T;
+    constexpr int kRows = kRowsAtOnce<TPR>, K = E::kChunk, kC = C > 0 ? C : 1;
+    __shared__ uint64_t slots[2][TPR / kWave];
+    const int j = threadIdx.x % TPR;
+    RowSums<TPR> over{slots};
+    float w[kC][K], sum[kC][K] = {};
+    auto weights = [&](float (&v)[K], int n0) {
+        if (g.weight != nullptr)
+            load_floats<E>(v, g.weight + n0, g.N - n0);
+        else
+#pragma unroll
+            for (int e = 0; e < K; ++e)
+                v[e] = 1.f;
+    };
+    if constexpr (C > 0)
+        each_chunk<TPR, C, E>(g.N, j, [&](int i, int n0) { weights(w[i], n0); });
+    float *mine = g.partial + ((int64_t)blockIdx.x * kRows + threadIdx.x / TPR) * g.N;
+    bool first = true;
+    for (int64_t t0 = (int64_t)blockIdx.x * kRows; t0 < g.T; t0 += (int64_t)gridDim.x * kRows) {
+        const int64_t t = t0 + threadIdx.x / TPR;
+        const bool there = t < g.T;
+        const int64_t at = there ? t : 0;
+        const T *dy = (const T *)g.dY + at * g.lddy, *s = (const T *)g.S + at * g.lds;
+        const T *ds = (const T *)g.dS + (g.dS != nullptr ? at * g.ldds : 0);
+        Chunk<E> d[kC], z[kC], more[kC];
+        auto load = [&](int i, int n0) {
+            const int left = there ? g.N - n0 : 0;
+            d[i].raw = load_chunk<E, VEC>(dy + n0, left);
+            z[i].raw = load_chunk<E, VEC>(s + n0, left);
+        };
+        if constexpr (C > 0)
+            each_chunk<TPR, C, E>(g.N, j, [&](int i, int n0) {
+                load(i, n0);
+                more[i].raw = load_chunk<E, VEC>(ds + n0, there && g.dS != nullptr ? g.N - n0 : 0);
+            });
+        double squares = 0.0, along = 0.0;
+        each_chunk<TPR, C, E>(g.N, j, [&](int i, int n0) {
+            if constexpr (C == 0) {
+                load(i, n0);
+                weights(w[i], n0);
+            }
+#pragma unroll
+            for (int e = 0; e < K; ++e) {
+                const double v = (double)(float)z[i].e[e];
+                squares = fma(v, v, squares);
+                along = fma((double)((float)d[i].e[e] * w[i][e]), v, along);
+            }
+        });
+        const double r = 1.0 / sqrt(over.sum(squares) / g.N + g.eps);
+        const float r32 = (float)r, k = (float)(over.sum(along) / g.N * r * r);
+        each_chunk<TPR, C, E>(g.N, j, [&](int i, int n0) {
+            if constexpr (C == 0) {
+                load(i, n0);
+                weights(w[i], n0);
+                more[i].raw = load_chunk<E, VEC>(ds + n0, there && g.dS != nullptr ? g.N - n0 : 0);
+            }
+            Chunk<E> o;
+#pragma unroll
+            for (int e = 0; e < K; ++e) {
+                const float v = (float)z[i].e[e], u = (float)d[i].e[e];
+                float x = r32 * fmaf(-v, k, u * w[i][e]);
+                if (g.dS != nullptr)
+                    x += (float)more[i].e[e];
+                o.e[e] = (T)x;
+                sum[i][e] = C == 0 ? u * (v * r32) : fmaf(u, v * r32, sum[i][e]);
+            }
+            if constexpr (C == 0) {
+                if (g.partial != nullptr)
+#pragma unroll
+                    for (int e = 0; e < K; ++e)
+                        if (n0 + e < g.N)
+                            mine[n0 + e] = first ? sum[i][e] : mine[n0 + e] + sum[i][e];
+            }
+            if (there && g.dX != nullptr)
+                store_chunk<E, VEC>((T *)g.dX + t * g.lddx + n0, o, g.N - n0);
+        });
+        first = false;
+    }
+    if constexpr (C > 0) {
+        if (g.partial != nullptr)
+            each_chunk<TPR, C, E>(g.N, j, [&](int i, int n0) {
+#pragma unroll
+                for (int e = 0; e < K; ++e)
+                    if (n0 + e < g.N)
+                        mine[n0 + e] = sum[i][e];
+            });
+    }
+}
+
+// dweight[n] = sum of `parts` rows of partial: 16 columns a workgroup, 16 threads a column.
+constexpr int kSumColumns = 16, kSumThreads = 256;
+__global__ __launch_bounds__(kSumThreads) void sum_kernel(const float *partial, int parts, int N, float *dweight)
+{
+    constexpr int kRows = kSumThreads / kSumColumns;
+    __shared__ double part[kRows][kSumColumns];
+    const int c = threadIdx.x % kSumColumns, r = threadIdx.x / kSumColumns;
+    for (int64_t n0 = (int64_t)blockIdx.x * kSumColumns; n0 < N; n0 += (int64_t)gridDim.x * kSumColumns) {
+        double sum = 0.0;
+        if (n0 + c < N) {
+#pragma unroll 8
+            for (int p = r; p < parts; p += kRows)
+                sum += (double)partial[(int64_t)p * N + n0 + c];
+        }
+        part[r][c] = sum;
+        __syncthreads();
+        if (r == 0 && n0 + c < N) {
+            double all = 0.0;
+#pragma unroll
+            for (int q = 0; q < kRows; ++q)
+                all += part[q][c];
+            dweight[n0 + c] = (float)all;
+        }
+        __syncthreads();
+    }
+}
+
+__global__ __launch_bounds__(kSumThreads) void zero_kernel(float *p, int N)
+{
+    for (int64_t n = (int64_t)blockIdx.x * kSumThreads + threadIdx.x; n < N; n += (int64_t)gridDim.x * kSumThreads)
+        p[n] = 0.f;
+}
+
+// ---------------------------------------------------------------------------
+// Host side
+// ---------------------------------------------------------------------------
+// Workgroups of the gradient: at most this many rows of parts.
+constexpr int kGradParts = 1024;
+int grad_grid(int T, int rows, int threads)
+{
+    const int64_t need = ceil_div(T, rows), most = kGradParts / rows;
+    const int64_t fit = gemm_f32_internal::current_device().cus * 4 * 256 / threads;
+    const int64_t limit = most < fit ? most : fit;
+    return (int)(need < limit ? need : limit);
+}
+// More than the workgroups that any type and row length take.
+int grad_parts(int T) { return (int)(ceil_div(T, 4) * 4 < kGradParts ? ceil_div(T, 4) * 4 : kGradParts); }
+
+bool bad_eps(float eps) { return !(eps > 0.f && eps < INFINITY); }
+
+int norm_call(int type, int T, int N, const void *X, int ldx, const void *R, int ldr, const float *weight, float eps,
+              void *S, int lds, void *Y, int ldy, float *scale, bool int8, hipStream_t stream)
+{
+    if (!known_type(type))
+        return GEMM_F32_ERR_TYPE;
+    if (bad_size(T) || bad_size(N))
+        return GEMM_F32_ERR_DIM;
+    if (short_ld(ldx, N) || (R != nullptr && short_ld(ldr, N)) || (R != nullptr && S != nullptr && short_ld(lds, N)) || short_ld(ldy, N))
+        return GEMM_F32_ERR_LD;
+    if (bad_eps(eps))
+        return GEMM_F32_ERR_OPTION;
+    if (T == 0 || (N == 0 && !int8))
+        return GEMM_F32_OK;
+    if ((N > 0 && (X == nullptr || Y == nullptr)) || (int8 && scale == nullptr))
+        return GEMM_F32_ERR_NULL;
+    const int b = type_bytes(type);
+    if (!aligned_to(X, b) || !aligned_to(R, b) || !aligned_to(weight, 4) || !aligned_to(S, b) || (!int8 && !aligned_to(Y, b)) ||
+        !aligned_to(scale, 4))
+        return GEMM_F32_ERR_ALIGN;
+    const NormArgs g{X, R, weight, S, Y, scale, ldx, ldr, lds, ldy, (double)eps, T, N};
+    const bool vec = chunk_rows(type, X, ldx, N) && (R == nullptr || chunk_rows(type, R, ldr, N)) &&
+                     (R == nullptr || S == nullptr || chunk_rows(type, S, lds, N)) && (int8 || chunk_rows(type, Y, ldy, N));
+    with_type(type, [&](auto e) {
+        using E = decltype(e);
+        with_row<E>(N, [&](auto tpr, auto c) {
+            constexpr int TPR = decltype(tpr)::value, C = decltype(c)::value, NT = kRowThreads<TPR>;
+            const int grid = row_grid(T, kRowsAtOnce<TPR>, NT);
+            auto launch = [&](auto v, auto q) {
+                norm_kernel<E, decltype(v)::value, decltype(q)::value, TPR, C><<<grid, NT, 0, stream>>>(g);
+            };
+            if (vec)
+                int8 ? launch(std::true_type{}, std::true_type{}) : launch(std::true_type{}, std::false_type{});
+            else
+                int8 ? launch(std::false_type{}, std::true_type{}) : launch(std::false_type{}, std::false_type{});
+        });
+    });
+    return launched();
+}
+
+}  // namespace
+}  // namespace ffn
+
+using namespace ffn;
+
+extern "C" {
+
+int gemm_f32_rms_norm(int type, int T, int N, const void *X, int ldx, const void *residual, int ldr, const float *weight,
+                      float eps, void *sum, int lds, void *Y, int ldy, hipStream_t stream)
+{
+    return norm_call(type, T, N, X, ldx, residual, ldr, weight, eps, sum, lds, Y, ldy, nullptr, false, stream);
+}
+
+int gemm_f32_rms_norm_int8(int type, int T, int N, const void *X, int ldx, const void *residual, int ldr,
+                           const float *weight, float eps, void *sum, int lds, int8_t *Q, int ldq, float *scale,
+                           hipStream_t stream)
+{
+    return norm_call(type, T, N, X, ldx, residual, ldr, weight, eps, sum, lds, Q, ldq, scale, true, stream);
+}
+
+size_t gemm_f32_rms_norm_grad_ws_size(int T, int N)
+{
+    if (T <= 0 || N <= 0 || bad_size(T) || bad_size(N))
+        return 0;
+    return (size_t)ceil_div((int64_t)grad_parts(T) * N * 4, 16) * 16;
+}
+
+int gemm_f32_rms_norm_grad(int type, int T, int N, const void *dY, int lddy, const void *S, int lds, const float *weight,
+                           float eps, const void *dsum, int ldds, void *dX, int lddx, float *dweight, void *workspace,
+                           size_t workspace_bytes, hipStream_t stream)
+{
+    if (!known_type(type))
+        return GEMM_F32_ERR_TYPE;
+    if (bad_size(T) || bad_size(N))
+        return GEMM_F32_ERR_DIM;
+    if (short_ld(lddy, N) || short_ld(lds, N) || (dsum != nullptr && short_ld(ldds, N)) || (dX != nullptr && short_ld(lddx, N)))
+        return GEMM_F32_ERR_LD;
+    if (bad_eps(eps))
+        return GEMM_F32_ERR_OPTION;
+    if (N == 0 || (dX == nullptr && dweight == nullptr) || (T == 0 && dweight == nullptr))
+        return GEMM_F32_OK;
+    if (T > 0 && (dY == nullptr || S == nullptr))
+        return GEMM_F32_ERR_NULL;
+    const int b = type_bytes(type);
+    if (!aligned_to(dY, b) || !aligned_to(S, b) || !aligned_to(weight, 4) || !aligned_to(dsum, b) || !aligned_to(dX, b) ||
+        !aligned_to(dweight, 4))
+        return GEMM_F32_ERR_ALIGN;
+    if (T > 0 && dweight != nullptr &&
+        (workspace == nullptr || !aligned_to(workspace, 16) || workspace_bytes < gemm_f32_rms_norm_grad_ws_size(T, N)))
+        return GEMM_F32_ERR_WORKSPACE;
+    const int sum_grid = (int)(ceil_div(N, kSumColumns) < 65536 ? ceil_div(N, kSumColumns) : 65536);
+    if (T == 0) {
+        zero_kernel<<<sum_grid, kSumThreads, 0, stream>>>(dweight, N);
+        return launched();
+    }
+    float *partial = dweight != nullptr ? (float *)workspace : nullptr;
+    const NormGradArgs g{dY, S, dsum, weight, dX, partial, lddy, lds, ldds, lddx, (double)eps, T, N};
+    const bool vec = chunk_rows(type, dY, lddy, N) && chunk_rows(type, S, lds, N) && (dsum == nullptr || chunk_rows(type, dsum, ldds, N)) &&
+                     (dX == nullptr || chunk_rows(type, dX, lddx, N));
+    int parts = 0;
+    with_type(type, [&](auto e) {
+        using E = decltype(e);
+        with_row<E>(N, [&](auto tpr, auto c) {
+            constexpr int TPR = decltype(tpr)::value, C = decltype(c)::value, NT = kRowThreads<TPR>;
+            const int grid = grad_grid(T, kRowsAtOnce<TPR>, NT);
+            parts = grid * kRowsAtOnce<TPR>;
+            if (vec)
+                norm_grad_kernel<E, true, TPR, C><<<grid, NT, 0, stream>>>(g);
+            else
+                norm_grad_kernel<E, false, TPR, C><<<grid, NT, 0, stream>>>(g);
+        });
+    });
+    const int rc = launched();
+    if (rc != GEMM_F32_OK || dweight == nullptr)
+        return rc;
+    sum_kernel<<<sum_grid, kSumThreads, 0, stream>>>(partial, parts, N, dweight);
+    return launched();
+}
+
+}  // extern "C"

@@ -1,0 +1,124 @@
+// Rows in 8 bits, as they are or gated (include/gemm_f32_ffn.h).  A row belongs to the
+// threads of a wave or a workgroup, in registers (see ffn_rows.h).  Bound by HBM.
+
+#include "ffn_rows.h"
+
+namespace ffn {
+namespace {
+
+struct QuantizeArgs {
+    const void *X;
+    int8_t *Q;
+    float *scale;
+    int64_t ldx, ldq;
+    int T, N;
+};
+
+// From where on to the left a gate's sigmoid is no normal binary32 number (as a factor of y it may
+// still count).
+template <int GATE>
+constexpr float gate_left()
+{
+    return GATE == GEMM_F32_GATE_SILU ? -80.f : GATE == GEMM_F32_GATE_GELU ? -12.f : -9.5f;
+}
+
+template <class E, bool VEC, int GATE, int TPR, int C>
+__global__ __launch_bounds__(kRowThreads<TPR>) void quantize_kernel(QuantizeArgs g)
+{
+    using T = typename E::T;
+    constexpr int kRows = kRowsAtOnce<TPR>, K = E::kChunk, kC = C > 0 ? C : 1;
+    constexpr bool kGated = GATE != GEMM_F32_GATE_NONE;
+    __shared__ uint64_t slots[2][TPR / kWave];
+    const int j = threadIdx.x % TPR;
+    RowSums<TPR> over{slots};
+    for (int64_t t0 = (int64_t)blockIdx.x * kRows; t0 < g.T; t0 += (int64_t)gridDim.x * kRows) {
+        const int64_t t = t0 + threadIdx.x / TPR;
+        const bool there = t < g.T;
+        const T *x = (const T *)g.X + (there ? t : 0) * g.ldx;
+        Chunk<E> a[kC], b[kGated ? kC : 1];
+        float y[kC][kGated ? K : 1];
+        auto load = [&](int i, int n0) {
+            const int left = there ? g.N - n0 : 0;
+            a[i].raw = load_chunk<E, VEC>(x + n0, left);
+            if constexpr (kGated)
+                b[i].raw = load_chunk<E, VEC>(x + g.N + n0, left);
+        };
+        auto open = [&](int i) {                     // the chunk's values
+            if constexpr (kGated)
+#pragma unroll
+                for (int e = 0; e < K; ++e)
+                    y[i][e] = gate<GATE>((float)a[i].e[e]) * (float)b[i].e[e];
+        };
+        if constexpr (C > 0) {
+            each_chunk<TPR, C, E>(g.N, j, load);
+            each_chunk<TPR, C, E>(g.N, j, [&](int i, int) { open(i); });
+        }
+        int loaded = -1;                             // C = 0: the column whose chunk a, b and y hold
+        Int8Row<TPR, C, E> row{g.N, j, there, g.Q + (there ? t : 0) * g.ldq};
+        row.write(over, g.scale + t, kGated ? gate_error<GATE>() : 0x1p-23f,
+                  [&](int i, int e, int n) {
+                      if constexpr (C == 0) {
+                          if (loaded != n - e) {
+                              loaded = n - e;
+                              load(i, loaded);
+                              open(i);
+                          }
+                      }
+                      if constexpr (kGated)
+                          return y[i][e];
+                      else
+                          return (float)a[i].e[e];
+                  },
+                  [&](int n) {
+                      if constexpr (kGated)
+                          return gate64<GATE>((double)(float)x[n]) * (double)(float)x[g.N + n];
+                      else
+                          return (double)(float)x[n];
+                  },
+                  [&](int i, int e, int) { return kGated && (float)a[i].e[e] < gate_left<GATE>(); });
+    }
+}
+
+}  // namespace
+}  // namespace ffn
+
+using namespace ffn;
+
+extern "C" {
+
+int gemm_f32_quantize(int type, int gate, int T, int N, const void *X, int ldx, int8_t *Q, int ldq, float *scale,
+                      hipStream_t stream)
+{
+    if (!known_type(type))
+        return GEMM_F32_ERR_TYPE;
+    if (bad_size(T) || bad_size(N) || (gate != GEMM_F32_GATE_NONE && N > kMaxSize / 2))
+        return GEMM_F32_ERR_DIM;
+    if (short_ld(ldx, gate != GEMM_F32_GATE_NONE ? 2 * N : N) || short_ld(ldq, N))
+        return GEMM_F32_ERR_LD;
+    if (gate != GEMM_F32_GATE_NONE && !known_gate(gate))
+        return GEMM_F32_ERR_OPTION;
+    if (T == 0)
+        return GEMM_F32_OK;
+    if ((N > 0 && (X == nullptr || Q == nullptr)) || scale == nullptr)
+        return GEMM_F32_ERR_NULL;
+    if (!aligned_to(X, type_bytes(type)) || !aligned_to(scale, 4))
+        return GEMM_F32_ERR_ALIGN;
+    const QuantizeArgs g{X, Q, scale, ldx, ldq, T, N};
+    const bool vec = chunk_rows(type, X, ldx, N);
+    with_type(type, [&](auto e) {
+        using E = decltype(e);
+        with_gate(gate, [&](auto kind) {
+            with_row<E>(N, [&](auto tpr, auto c) {
+                constexpr int TPR = decltype(tpr)::value, C = decltype(c)::value, NT = kRowThreads<TPR>;
+                const int grid = row_grid(T, kRowsAtOnce<TPR>, NT);
+                if (vec)
+                    quantize_kernel<E, true, decltype(kind)::value, TPR, C><<<grid, NT, 0, stream>>>(g);
+                else
+                    quantize_kernel<E, false, decltype(kind)::value, TPR, C><<<grid, NT, 0, stream>>>(g);
+            });
+        });
+    });
+    return launched();
+}
+
+}  // extern "C"

@@ -565,7 +565,6 @@ constexpr int kMaxTokens = 1 << 25;
 // Most rows of an operand that one panel's offsets span (a tile's, or a panel's depth).
 constexpr int kPanelRows = 256;
 
-bool short_ld(int64_t ld, int cols) { return ld < at_least_one(cols); }
 
 template <class E, int RN>
 int64_t down_blocks(const AdapterArgs &g)

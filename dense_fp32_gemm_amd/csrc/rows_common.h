@@ -16,6 +16,7 @@ namespace rows {
 constexpr int kWave = 64;
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
@@ -33,6 +34,12 @@ struct Bf16 {
 struct F16 {
     using T = _Float16;
     static constexpr int kBytes = 2, kChunk = 8;
+};
+
+// 8-bit operands, whose sums are whole numbers.
+struct I8 {
+    using T = int8_t;
+    static constexpr int kBytes = 1, kChunk = 16;
 };
 
 // 16 bytes of elements.
@@ -63,6 +70,13 @@ inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 constexpr int kMaxSize = INT32_MAX - 4095;
 inline bool bad_size(int n) { return n < 0 || n > kMaxSize; }
 inline int at_least_one(int n) { return n > 1 ? n : 1; }
+inline bool short_ld(int64_t ld, int cols) { return ld < at_least_one(cols); }
+// Rows whose chunks are whole and aligned.
+inline bool chunk_rows(int type, const void *p, int64_t ld, int64_t cols)
+{
+    const int chunk = 16 / type_bytes(type);
+    return aligned_to(p, 16) && ld % chunk == 0 && cols % chunk == 0;
+}
 
 inline int launched() { return hipGetLastError() == hipSuccess ? GEMM_F32_OK : GEMM_F32_ERR_LAUNCH; }
 

@@ -5,95 +5,12 @@
 //    workgroup's tile belongs to is found on the device, from the offsets.
 //  * combine_kernel, combine_grad_kernel: one workgroup per token.
 
-#include "rows_tile.h"
+#include "rows_groups.h"
 
 namespace rows {
 namespace {
 
 enum Op { kForward, kGradX, kGradW };
-
-struct GroupedArgs {
-    const int *offsets;
-    const int *order;        // forward, grad_w: rows of A; NULL: the place itself
-    const void *A;           // X (forward, grad_w), dY (grad_x)
-    const void *B;           // W (forward, grad_x), dY (grad_w)
-    void *C;                 // Y, dX, dW
-    int64_t lda, ldb, ldc;
-    int64_t stride;          // of W (of dW for grad_w)
-    int G, P, rows;          // rows: of X
-    Divisor per_row;
-    int M, N, K;             // grad_w: M x N of dW; else columns N of C, summed K
-    int xcds;
-    bool vector_c;           // C's rows take stores of four elements
-    int tiles_n;
-    int most_m;              // row tiles there can be
-    int slots;               // workgroups the device holds at once
-};
-
-// Group g's range of places, clamped to 0..P.
-__device__ inline void group_range(const int *offsets, int g, int P, int &lo, int &hi)
-{
-    lo = min(max(offsets[g], 0), P);
-    hi = min(max(offsets[g + 1], lo), P);
-}
-
-struct Place {
-    int group, lo, hi;       // the group's places
-    int tm, tn;              // row tile within the group, column tile
-};
-
-// Row tiles of all groups (64 groups at a time, a lane each), the same in every lane.
-__device__ inline int row_tiles(const GroupedArgs &g, int bm)
-{
-    const int lane = threadIdx.x % kWave;
-    int total = 0;
-    for (int g0 = 0; g0 < g.G; g0 += kWave) {
-        int a = 0, b = 0;
-        if (g0 + lane < g.G)
-            group_range(g.offsets, g0 + lane, g.P, a, b);
-        int n = (b - a + bm - 1) / bm;
-#pragma unroll
-        for (int d = kWave / 2; d > 0; d /= 2)
-            n += __shfl_xor(n, d);
-        total += n;
-    }
-    return __builtin_amdgcn_readfirstlane(total);
-}
-
-// Tile t, counted group by group and column by column within a group (W's
-// panels are shared).  Every wave of the workgroup computes it for itself.
-__device__ inline Place locate(const GroupedArgs &g, int bm, int t)
-{
-    const int lane = threadIdx.x % kWave;
-    int before = 0;                                  // row tiles of the groups before
-    Place p{0, 0, 0, 0, 0};
-    for (int g0 = 0; g0 < g.G; g0 += kWave) {
-        int a = 0, b = 0;
-        if (g0 + lane < g.G)
-            group_range(g.offsets, g0 + lane, g.P, a, b);
-        const int n = (b - a + bm - 1) / bm;
-        int scan = n;
-#pragma unroll
-        for (int d = 1; d < kWave; d *= 2) {
-            const int x = __shfl_up(scan, d);
-            scan += lane >= d ? x : 0;
-        }
-        const uint64_t past = __ballot(before + scan > t / g.tiles_n);
-        if (past) {
-            const int at = (int)__builtin_ctzll(past);
-            const int mine = __builtin_amdgcn_readlane(n, at);
-            const int first = before + __builtin_amdgcn_readlane(scan, at) - mine;
-            const int r = t - first * g.tiles_n;
-            p = Place{g0 + at, __builtin_amdgcn_readlane(a, at), __builtin_amdgcn_readlane(b, at), r % mine, r / mine};
-            break;
-        }
-        before += __builtin_amdgcn_readlane(scan, kWave - 1);
-    }
-    // scalars, whatever the compiler makes of the loop
-    return Place{__builtin_amdgcn_readfirstlane(p.group), __builtin_amdgcn_readfirstlane(p.lo),
-                 __builtin_amdgcn_readfirstlane(p.hi), __builtin_amdgcn_readfirstlane(p.tm),
-                 __builtin_amdgcn_readfirstlane(p.tn)};
-}
 
 // Tile t of dW.  A group's tiles cost its number of places, so each die's range of t has a
 // slice of every group (both gradients, 4096 x 4 slots over 16 experts of unlike
@@ -331,18 +248,6 @@ __global__ __launch_bounds__(kCombineThreads) void combine_grad_kernel(CombineAr
 // ---------------------------------------------------------------------------
 // Host side
 // ---------------------------------------------------------------------------
-// Rows whose chunks are whole and aligned.
-bool chunk_rows(int type, const void *p, int64_t ld, int64_t cols)
-{
-    const int chunk = 16 / type_bytes(type);
-    return aligned_to(p, 16) && ld % chunk == 0 && cols % chunk == 0;
-}
-
-// Most rows of an operand that one panel's offsets span (BM, BN or a panel's depth).
-constexpr int kPanelRows = 256;
-
-// Workgroups of a launch: a grid has fewer than 2^32 threads.
-constexpr int64_t kMaxTiles = UINT32_MAX / 512;
 static_assert(kCombineThreads <= 512, "grid limit");
 int token_grid(int T) { return T < kMaxTiles ? T : (int)kMaxTiles; }
 
@@ -423,9 +328,6 @@ int check_grouped(int type, int G, int P, int N, int K)
     return launch_grouped<OP>(type, g, false, nullptr, false);
 }
 
-bool short_ld(int64_t ld, int cols) { return ld < at_least_one(cols); }
-// K * ldw elements between groups at least (the last row may end at N).
-bool short_stride(int64_t stride, int G, int K, int64_t ldw) { return G > 1 && stride < K * ldw; }
 
 }  // namespace
 }  // namespace rows
@@ -449,7 +351,7 @@ int gemm_f32_grouped(int type, int G, int P, int N, int K, const int *offsets, c
         return GEMM_F32_ERR_OPTION;
     if (G == 0 || P == 0 || N == 0)
         return GEMM_F32_OK;
-    if (offsets == nullptr || Y == nullptr || (K > 0 && ((X == nullptr && rows > 0) || W == nullptr)))
+    if (no_offsets(offsets, G) || Y == nullptr || (K > 0 && ((X == nullptr && rows > 0) || W == nullptr)))
         return GEMM_F32_ERR_NULL;
     const int b = type_bytes(type);
     if (!aligned_to(offsets, 4) || !aligned_to(order, 4) || !aligned_to(X, b) || !aligned_to(W, b) || !aligned_to(Y, b))
@@ -470,7 +372,7 @@ int gemm_f32_grouped_grad_x(int type, int G, int P, int N, int K, const int *off
         return GEMM_F32_ERR_LD;
     if (G == 0 || P == 0 || K == 0)
         return GEMM_F32_OK;
-    if (offsets == nullptr || dX == nullptr || (N > 0 && (dY == nullptr || W == nullptr)))
+    if (no_offsets(offsets, G) || dX == nullptr || (N > 0 && (dY == nullptr || W == nullptr)))
         return GEMM_F32_ERR_NULL;
     const int b = type_bytes(type);
     if (!aligned_to(offsets, 4) || !aligned_to(dY, b) || !aligned_to(W, b) || !aligned_to(dX, b))
@@ -496,7 +398,7 @@ int gemm_f32_grouped_grad_w(int type, int G, int P, int N, int K, const int *off
         return GEMM_F32_ERR_OPTION;
     if (G == 0 || K == 0 || N == 0)
         return GEMM_F32_OK;
-    if (offsets == nullptr || dW == nullptr || (P > 0 && ((X == nullptr && rows > 0) || dY == nullptr)))
+    if (no_offsets(offsets, G) || dW == nullptr || (P > 0 && ((X == nullptr && rows > 0) || dY == nullptr)))
         return GEMM_F32_ERR_NULL;
     const int b = type_bytes(type);
     if (!aligned_to(offsets, 4) || !aligned_to(order, 4) || !aligned_to(X, b) || !aligned_to(dY, b) || !aligned_to(dW, b))

@@ -13,8 +13,8 @@
 //    reads up to 4 neighbouring rows' values per lane at once and gives them to
 //    as many fragments: fragment v of a group of V covers rows V*i + v.
 //
-// Matrix instruction: v_mfma_f32_16x16x32_{bf16,f16} (lane l: row l%16, k =
-// 8*(l/16) + 0..7) and v_mfma_f32_16x16x4_f32 (row l%16, k = l/16; the s-th of four
+// Matrix instruction: v_mfma_i32_16x16x64_i8 (lane l: row l%16, k = 16*(l/16) + 0..15),
+// v_mfma_f32_16x16x32_{bf16,f16} (k = 8*(l/16) + 0..7) and v_mfma_f32_16x16x4_f32 (row l%16, k = l/16; the s-th of four
 // instructions takes k = 4*(l/16) + s).  The second operand's fragment is passed first, so
 // that a lane's four results of a 16 x 16 block are four neighbouring columns of
 // one row: D(m = l%16, n = 4*(l/16) + r), and stores are 8 or 16 bytes wide.
@@ -69,14 +69,14 @@ template <class T>
 using lds_ptr = __attribute__((address_space(3))) T *;
 
 // Fragments of F consecutive 16-row blocks from row `row0` of a panel, one
-// k step (32 k of a 16-bit type, 16 of binary32: four chunks).
+// k step (64 k of 8 bits, 32 of a 16-bit type, 16 of binary32: four chunks).
 template <class E, bool ALONG, int RN, int F>
 struct Fragments {
     using T = typename E::T;
     // rows a group of fragments read together covers, /16
     static constexpr int kV = E::kBytes == 2 || ALONG ? 1 : F % 4 == 0 ? 4 : F % 2 == 0 ? 2 : 1;
     static constexpr int kReads = ALONG ? F : E::kBytes == 2 ? 2 * F : 4 * F / kV;   // LDS instructions
-    u32x4 q[F];      // 8 16-bit values, or 4 binary32 (k = 4*(l/16) + 0..3)
+    u32x4 q[F];      // 16 8-bit values, 8 16-bit ones, or 4 binary32 (k = 4*(l/16) + 0..3)
 
     __device__ inline void read(const T *panel, int row0, int step, int lane)
     {
@@ -116,14 +116,20 @@ struct Fragments {
     static __device__ inline int row_of(int f, int i) { return (f / kV) * 16 * kV + kV * i + f % kV; }
 };
 
+// Four sums of a lane: binary32, or whole numbers of the 8-bit products.
+template <class E>
+using Sum4 = std::conditional_t<E::kBytes == 1, i32x4, f32x4>;
+
 // d += a . b of one 16 x 16 block and the s-th instruction of a k step (kPerStep
 // of them); see the top for the order.
 template <class E>
 constexpr int kPerStep = E::kBytes == 4 ? 4 : 1;
 template <class E>
-__device__ inline f32x4 mfma(u32x4 b, u32x4 a, f32x4 d, int s)
+__device__ inline Sum4<E> mfma(u32x4 b, u32x4 a, Sum4<E> d, int s)
 {
-    if constexpr (E::kBytes == 4)
+    if constexpr (E::kBytes == 1)
+        return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, b), __builtin_bit_cast(i32x4, a), d, 0, 0, 0);
+    else if constexpr (E::kBytes == 4)
         return __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(b[s]), __uint_as_float(a[s]), d, 0, 0, 0);
     else if constexpr (std::is_same<E, Bf16>::value)
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, b), __builtin_bit_cast(bf16x8, a), d, 0, 0, 0);
@@ -147,7 +153,7 @@ struct Tile {
     static_assert((A_ALONG || (BM & (BM - 1)) == 0) && (B_ALONG || (BN & (BN - 1)) == 0),
                   "the chunk permutations across rows are made for powers of two");
 
-    f32x4 acc[kFm][kFn];
+    Sum4<E> acc[kFm][kFn];
 
     __device__ inline void clear()
     {
@@ -155,7 +161,7 @@ struct Tile {
         for (int m = 0; m < kFm; ++m)
 #pragma unroll
             for (int n = 0; n < kFn; ++n)
-                acc[m][n] = f32x4{0.f, 0.f, 0.f, 0.f};
+                acc[m][n] = Sum4<E>{0, 0, 0, 0};
     }
 
     // One step's fragments of a panel.

@@ -110,27 +110,29 @@ __device__ inline void gated_tile(const GatedArgs &args, int group, int m0, int 
                 [&](int i, int r) { return m0 + r < m_end && row[i] < g.rows ? row[i] * g.lda * E::kBytes : -1; });
     const AcrossPair<E, BN, NT, WN> b((const T *)g.B + group * g.stride, tid, g.K, g.ldb, n0, g.N);
     sum_panels<E, DMA, S>(tile, g.K, a, b, lds, tid, wm, wn);
-    auto store = [&](void *C, int64_t ld, bool vector, int m, int n, int first, f32x4 v) {
-        T *p = (T *)C + (int64_t)m * ld + first + n;
-        if (vector)
-            store4<E, true>(p, v, g.N - n);
-        else
-            store4<E, false>(p, v, g.N - n);
-    };
-    each_pair<E>(tile, wm, wn, lane, [&](int r, int c, f32x4 x, f32x4 u) {
-        const int m = m0 + r, n = n0 + c;
-        if (m >= m_end || n >= g.N)
-            return;
-        f32x4 y;
+    // (the three ways apart: merged, the compiler makes pieces of the wide stores)
+    auto store = [&](auto vec, auto keep) {
+        constexpr bool V = decltype(vec)::value;
+        each_pair<E>(tile, wm, wn, lane, [&](int r, int c, f32x4 x, f32x4 u) {
+            const int m = m0 + r, n = n0 + c;
+            if (m >= m_end || n >= g.N)
+                return;
+            f32x4 y;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            y[i] = gate<GATE>(x[i]) * u[i];
-        store(g.C, g.ldc, g.vector_c, m, n, 0, y);
-        if (args.pre != nullptr) {
-            store(args.pre, args.ldp, args.vector_p, m, n, 0, x);
-            store(args.pre, args.ldp, args.vector_p, m, n, g.N, u);
-        }
-    });
+            for (int i = 0; i < 4; ++i)
+                y[i] = gate<GATE>(x[i]) * u[i];
+            store4<E, V>((T *)g.C + (int64_t)m * g.ldc + n, y, g.N - n);
+            if constexpr (decltype(keep)::value) {
+                T *p = (T *)args.pre + (int64_t)m * args.ldp + n;
+                store4<E, V>(p, x, g.N - n);
+                store4<E, V>(p + g.N, u, g.N - n);
+            }
+        });
+    };
+    if (args.pre == nullptr)
+        g.vector_c ? store(std::true_type{}, std::false_type{}) : store(std::false_type{}, std::false_type{});
+    else
+        g.vector_c && args.vector_p ? store(std::true_type{}, std::true_type{}) : store(std::false_type{}, std::true_type{});
 }
 
 template <class E, int GATE, int BM, int BN, int WM, int WN, int S, bool CUT, bool DMA>

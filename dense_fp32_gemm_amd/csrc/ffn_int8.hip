@@ -21,24 +21,33 @@ struct Int8Args {
     bool vector_y;
 };
 
-// Four neighbouring channels' sums of row t, scaled, to Y.
-template <class Out>
-__device__ inline void int8_store(const Int8Args &g, int64_t t, int n, i32x4 v)
-{
-    const float s = g.scale[t];
-    f32x4 y;
+// Scales (and biases) of four neighbouring channels from n on.
+struct Channels {
+    f32x4 scale, bias;
+    __device__ inline void load(const Int8Args &g, int n)
+    {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int c = n + i < g.N ? n + i : g.N - 1;
-        y[i] = (float)v[i] * (s * g.w_scale[c]);
-        if (g.bias != nullptr)
-            y[i] += g.bias[c];
+        for (int i = 0; i < 4; ++i) {
+            const int c = n + i < g.N ? n + i : g.N - 1;
+            scale[i] = g.w_scale[c];
+            bias[i] = g.bias != nullptr ? g.bias[c] : 0.f;
+        }
     }
-    typename Out::T *p = (typename Out::T *)g.Y + t * g.ldy + n;
-    if (g.vector_y)
-        store4<Out, true>(p, y, g.N - n);
-    else
-        store4<Out, false>(p, y, g.N - n);
+    // Their sums of a row whose scale is s.
+    __device__ inline f32x4 scaled(i32x4 v, float s) const
+    {
+        f32x4 y;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            y[i] = (float)v[i] * (s * scale[i]) + bias[i];
+        return y;
+    }
+};
+
+template <class Out, bool VEC>
+__device__ inline void int8_store(const Int8Args &g, int64_t t, int n, f32x4 y)
+{
+    store4<Out, VEC>((typename Out::T *)g.Y + t * g.ldy + n, y, g.N - n);
 }
 
 template <class Out, int BM, int BN, int WM, int WN, int S, bool DMA>
@@ -57,13 +66,31 @@ __device__ inline void int8_tile(const Int8Args &g, int m0, int n0, int8_t *lds)
     const Along<I8, BN, NT> b(g.W + n0 * g.ldw, tid, g.K, g.ldw, g.N - n0,
                               [&](int, int r) { return n0 + r < g.N ? r * g.ldw : -1; });
     sum_panels<I8, DMA, S>(tile, g.K, a, b, lds, tid, wm, wn);
-    tile.each(wm, wn, lane, [&](int r, int c, i32x4 v) {
-        if (m0 + r < g.T && n0 + c < g.N)
-            int8_store<Out>(g, m0 + r, n0 + c, v);
-    });
+    // all scales, then their use: loaded one by one between the stores they cost a tile of 4096 k a fourth of its time
+    const int i = lane % 16, h = lane / 16, row = m0 + wm * (BM / WM) + i, col = n0 + wn * (BN / WN) + 4 * h;
+    float scale[Ti::kFm];
+    Channels channels[Ti::kFn];
+#pragma unroll
+    for (int m = 0; m < Ti::kFm; ++m)
+        scale[m] = g.scale[min(row + 16 * m, g.T - 1)];
+#pragma unroll
+    for (int n = 0; n < Ti::kFn; ++n)
+        channels[n].load(g, col + 16 * n);
+    auto store = [&](auto vec) {
+#pragma unroll
+        for (int m = 0; m < Ti::kFm; ++m)
+#pragma unroll
+            for (int n = 0; n < Ti::kFn; ++n)
+                if (row + 16 * m < g.T && col + 16 * n < g.N)
+                    int8_store<Out, decltype(vec)::value>(g, row + 16 * m, col + 16 * n, channels[n].scaled(tile.acc[m][n], scale[m]));
+    };
+    if (g.vector_y)
+        store(std::true_type{});
+    else
+        store(std::false_type{});
 }
 
-// Tiles are numbered column by column: those of a die share W's panels.
+// Tiles are numbered in bands as those of a group (see kBand; 8192 x 4096, K = 4096: 165 us, whole columns 171).
 template <class Out, int BM, int BN, int WM, int WN, int S, bool CUT, bool DMA>
 __global__ __launch_bounds__(WM *WN *kWave, 2) void int8_kernel(Int8Args g)
 {
@@ -79,7 +106,8 @@ __global__ __launch_bounds__(WM *WN *kWave, 2) void int8_kernel(Int8Args g)
         part.tile = die_contiguous(blockIdx.x, total, g.xcds);
     if (part.tile < 0)
         return;                                      // the whole workgroup
-    const int m0 = part.tile % g.tiles_m * BM, n0 = part.tile / g.tiles_m * BN;
+    const int from = part.tile / (kBand * g.tiles_n) * kBand, q = part.tile - from * g.tiles_n, high = min(kBand, g.tiles_m - from);
+    const int m0 = (from + q % high) * BM, n0 = q / high * BN;
     if (!CUT || part.cut == 1)
         int8_tile<Out, BM, BN, WM, WN, S, DMA>(g, m0, n0, lds);
     if constexpr (CUT) {
@@ -130,13 +158,16 @@ __global__ __launch_bounds__(kFewWaves *kWave) void int8_few_kernel(Int8Args g)
         part[wave][m][lane] = acc[m];
     __syncthreads();
     for (int m = wave; m < MT; m += kFewWaves) {
+        Channels channels;
+        channels.load(g, n0 + 4 * h);
+        const float s = g.scale[min(16 * m + i, g.T - 1)];
         i32x4 sum = part[0][m][lane];
 #pragma unroll
         for (int v = 1; v < kFewWaves; ++v)
             sum += part[v][m][lane];
         const int t = 16 * m + i, n = n0 + 4 * h;
         if (t < g.T && n < g.N)
-            int8_store<Out>(g, t, n, sum);
+            int8_store<Out, false>(g, t, n, channels.scaled(sum, s));
     }
 }
 

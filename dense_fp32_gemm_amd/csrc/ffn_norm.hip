@@ -96,30 +96,21 @@ __global__ __launch_bounds__(kRowThreads<TPR>) void norm_kernel(NormArgs g)
                     store_chunk<E, VEC>((T *)g.Y + t * g.ldy + n0, o, g.N - n0);
             });
         } else {
-            Int8Row<TPR, C, E> row{g.N, j, there, (int8_t *)g.Y + (there ? t : 0) * g.ldy};
+            Int8Row<TPR, C, E, false> row{g.N, j, there, (int8_t *)g.Y + (there ? t : 0) * g.ldy};
             int loaded = -1;                         // C = 0: the column whose chunk z and w hold
             row.write(over, g.scale + t, 0x1p-21f,
-                      [&](int i, int e, int n) {
+                      [&](int i, int e, int n0) {
                           if constexpr (C == 0) {
-                              if (loaded != n - e) {
-                                  loaded = n - e;
+                              if (loaded != n0) {
+                                  loaded = n0;
                                   again(z[i], loaded);
                                   weights(w[i], loaded);
                               }
                           }
                           return (float)z[i].e[e] * scale32 * w[i][e];
                       },
-                      [&](int n) {
-                          float v;
-                          if (kept)
-                              v = (float)s[n];
-                          else if (g.R != nullptr)
-                              v = (float)(T)((float)x[n] + (float)r[n]);
-                          else
-                              v = (float)x[n];
-                          return (double)v * (g.weight != nullptr ? (double)g.weight[n] : 1.0) * scale;
-                      },
-                      [](int, int, int) { return false; });
+                      [&](int i, int e, int) { return (double)pick(z[i], e) * (double)pick(w[i], e) * scale; },
+                      [](int, int) { return 0x1p-21f; }, [](int, int, int) { return false; });
         }
     }
 }

@@ -54,12 +54,12 @@ __global__ __launch_bounds__(kRowThreads<TPR>) void quantize_kernel(QuantizeArgs
             each_chunk<TPR, C, E>(g.N, j, [&](int i, int) { open(i); });
         }
         int loaded = -1;                             // C = 0: the column whose chunk a, b and y hold
-        Int8Row<TPR, C, E> row{g.N, j, there, g.Q + (there ? t : 0) * g.ldq};
-        row.write(over, g.scale + t, kGated ? gate_error<GATE>() : 0x1p-23f,
-                  [&](int i, int e, int n) {
+        Int8Row<TPR, C, E, !kGated> row{g.N, j, there, g.Q + (there ? t : 0) * g.ldq};
+        row.write(over, g.scale + t, kGated ? kGateFar : 0x1p-23f,
+                  [&](int i, int e, int n0) {
                       if constexpr (C == 0) {
-                          if (loaded != n - e) {
-                              loaded = n - e;
+                          if (loaded != n0) {
+                              loaded = n0;
                               load(i, loaded);
                               open(i);
                           }
@@ -69,12 +69,13 @@ __global__ __launch_bounds__(kRowThreads<TPR>) void quantize_kernel(QuantizeArgs
                       else
                           return (float)a[i].e[e];
                   },
-                  [&](int n) {
+                  [&](int i, int e, int) {
                       if constexpr (kGated)
-                          return gate64<GATE>((double)(float)x[n]) * (double)(float)x[g.N + n];
+                          return gate64<GATE>((double)pick(a[i], e)) * (double)pick(b[i], e);
                       else
-                          return (double)(float)x[n];
+                          return (double)pick(a[i], e);
                   },
+                  [&](int i, int e) { return kGated ? gate_error<GATE>((float)a[i].e[e]) : 0x1p-23f; },
                   [&](int i, int e, int) { return kGated && (float)a[i].e[e] < gate_left<GATE>(); });
     }
 }

@@ -115,6 +115,26 @@ __device__ inline void each_chunk(int N, int j, Fn &&f)
     }
 }
 
+// Element e of 16 bytes, or of K floats, in registers, where e is no constant.  (Whole vectors, then
+// selections: selections between elements of an array become loads from one in memory.)
+__device__ inline uint32_t pick(u32x4 v, int e) { return e < 2 ? (e == 0 ? v[0] : v[1]) : e == 2 ? v[2] : v[3]; }
+template <class E>
+__device__ inline float pick(const Chunk<E> &c, int e)
+{
+    if constexpr (E::kBytes == 4)
+        return __uint_as_float(pick(c.raw, e));
+    else
+        return (float)__builtin_bit_cast(typename E::T, (uint16_t)(pick(c.raw, e / 2) >> (e % 2 * 16)));
+}
+template <int K>
+__device__ inline float pick(const float (&c)[K], int e)
+{
+    u32x4 v[K / 4];
+    __builtin_memcpy(v, c, sizeof v);
+    const uint32_t low = pick(v[0], e % 4), high = pick(v[K / 4 - 1], e % 4);
+    return __uint_as_float(e < 4 ? low : high);
+}
+
 // ---------------------------------------------------------------------------
 // A row in 8 bits
 // ---------------------------------------------------------------------------
@@ -122,45 +142,56 @@ __device__ inline void each_chunk(int N, int j, Fn &&f)
 // relative error, and only those whose rounding that leaves open are computed in
 // binary64: the elements that may be the row's largest, and those next to a
 // rounding border (of 127 steps' binary32 error, one in ten thousand or fewer).  So the
-// results are the definition's at a binary32 pass's cost.
+// results are the definition's at a binary32 pass's cost.  SURE: approx is exact.
 //
-//   approx(i, e, n)  the i-th chunk's element e (column n), to within ERROR
-//   exact(n)         column n in binary64
-//   unsure(i, e, n)  whether approx may be off by more
-template <int TPR, int C, class E>
+//   approx(i, e, n0)  the i-th chunk's element e (column n0 + e); 0 past the row's end
+//   error(i, e)       how far that may be off, relative, at most most_error
+//   exact(i, e, n0)   the same in binary64; e is no constant (see pick())
+//   unsure(i, e, n0)  whether approx may be off by more
+template <int TPR, int C, class E, bool SURE>
 struct Int8Row {
     int N, j;
     bool there;                                      // the row
     int8_t *q;                                       // its start
 
-    template <class Approx, class Exact, class Unsure>
-    __device__ inline void write(RowSums<TPR> &over, float *scale, float error, Approx &&approx, Exact &&exact, Unsure &&unsure)
+    template <class Approx, class Exact, class Error, class Unsure>
+    __device__ inline void write(RowSums<TPR> &over, float *scale, float most_error, Approx &&approx, Exact &&exact, Error &&error,
+                                 Unsure &&unsure)
     {
+        constexpr int K = E::kChunk;
+        constexpr uint32_t kInf = 0x7f800000u;
         // NaN above infinity above every number, as whole numbers
-        uint32_t top = 0;
+        uint32_t mine = 0;
+        bool loose = false;
         each_chunk<TPR, C, E>(N, j, [&](int i, int n0) {
 #pragma unroll
-            for (int e = 0; e < E::kChunk; ++e)
-                if (n0 + e < N)
-                    top = max(top, __float_as_uint(approx(i, e, n0 + e)) & 0x7fffffffu);
-        });
-        top = over.max32(top);
-        // (rows up to 2^-120 get the smallest scale in any case)
-        const float near = top > 0x7f800000u ? INFINITY : fmaxf(__uint_as_float(top) * (1.f - 4.f * error), 0x1p-120f);
-        uint64_t most = 0;
-        each_chunk<TPR, C, E>(N, j, [&](int i, int n0) {
-            uint32_t check = 0;
-#pragma unroll
-            for (int e = 0; e < E::kChunk; ++e)
-                if (n0 + e < N && (!(fabsf(approx(i, e, n0 + e)) < near) || unsure(i, e, n0 + e)))
-                    check |= 1u << e;
-#pragma unroll 1
-            for (; check != 0; check &= check - 1) {
-                const uint64_t y = __builtin_bit_cast(uint64_t, fabs(exact(n0 + (int)__builtin_ctz(check))));
-                most = y > most ? y : most;
+            for (int e = 0; e < K; ++e) {
+                mine = max(mine, __float_as_uint(approx(i, e, n0)) & 0x7fffffffu);
+                loose |= unsure(i, e, n0);
             }
         });
-        most = over.max64(most);
+        const uint32_t top = over.max32(mine);
+        uint64_t most = 0;
+        if constexpr (SURE) {
+            most = __builtin_bit_cast(uint64_t, (double)__uint_as_float(top));
+        } else {
+            // Below `near` nothing is the row's largest.  (Rows up to 2^-120 get the smallest scale in any case.)
+            const float near = top > kInf ? INFINITY : fmaxf(__uint_as_float(top) * (1.f - 4.f * most_error), 0x1p-120f);
+            if (!(__uint_as_float(mine) < near) || loose)
+                each_chunk<TPR, C, E>(N, j, [&](int i, int n0) {
+                    uint32_t check = 0;
+#pragma unroll
+                    for (int e = 0; e < K; ++e)
+                        if (n0 + e < N && (!(fabsf(approx(i, e, n0)) < near) || unsure(i, e, n0)))
+                            check |= 1u << e;
+#pragma unroll 1
+                    for (; check != 0; check &= check - 1) {
+                        const uint64_t y = __builtin_bit_cast(uint64_t, fabs(exact(i, (int)__builtin_ctz(check), n0)));
+                        most = y > most ? y : most;
+                    }
+                });
+            most = over.max64(most);
+        }
         float s = fmaxf((float)(__builtin_bit_cast(double, most) / 127.0), 0x1p-126f);
         const bool bad = most >= 0x7ff0000000000000u || !(s < INFINITY);
         if (bad)
@@ -170,34 +201,49 @@ struct Int8Row {
         if (j == 0)
             *scale = s;
         const float per = 1.f / s;
-        // errors next to binary32's smallest numbers (of y, and of 1 / s) are not relative
-        const bool edge = !(s > 0x1p-100f && s < 0x1p100f);
+        // Next to binary32's ends (of y, of s and of 1 / s) errors are not relative.
+        const bool edge = top >= kInf || !(s > 0x1p-100f && s < 0x1p100f);
+        constexpr float kMagic = 0x1.8p23f;          // t + kMagic has t's nearest whole number in its low bits
         each_chunk<TPR, C, E>(N, j, [&](int i, int n0) {
-            struct {
-                int8_t v[E::kChunk];
+            float worst = 0.f;
+            union {
+                uint32_t word[K / 4];
+                int8_t v[K];
             } o;
-            uint32_t check = 0;
 #pragma unroll
-            for (int e = 0; e < E::kChunk; ++e) {
-                const float t = approx(i, e, n0 + e) * per, r = __builtin_rintf(t);
-                if (!(fabsf(t - r) < 0.5f - fabsf(t) * (2.f * error)) || unsure(i, e, n0 + e) || (edge && t != 0.f))
-                    check |= n0 + e < N ? 1u << e : 0u;
-                o.v[e] = bad ? 0 : (int8_t)(int)fminf(fmaxf(r, -127.f), 127.f);
+            for (int e = 0; e < K; e += 4) {
+                uint32_t b[4];
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const float t = approx(i, e + u, n0) * per, r = t + kMagic;
+                    worst = fmaxf(worst, fmaf(fabsf(t), 2.f * error(i, e + u), fabsf(t - (r - kMagic))));
+                    b[u] = __float_as_uint(r);
+                }
+                const uint32_t low = __builtin_amdgcn_perm(b[1], b[0], 0x0c0c0400u), high = __builtin_amdgcn_perm(b[3], b[2], 0x0c0c0400u);
+                o.word[e / 4] = bad ? 0u : __builtin_amdgcn_perm(high, low, 0x05040100u);
             }
-            if (n0 + E::kChunk <= N) {
+            if (n0 + K <= N) {
                 __builtin_memcpy(q + n0, &o, sizeof o);
             } else {
 #pragma unroll
-                for (int e = 0; e < E::kChunk; ++e)
+                for (int e = 0; e < K; ++e)
                     if (n0 + e < N)
                         q[n0 + e] = o.v[e];
             }
-            if (bad)
-                check = 0;
+            if (!bad && (worst >= 0.5f || loose || edge)) {
+                uint32_t check = 0;
+#pragma unroll
+                for (int e = 0; e < K; ++e) {
+                    const float t = approx(i, e, n0) * per;
+                    if (n0 + e < N && (!(fmaf(fabsf(t), 2.f * error(i, e), fabsf(t - __builtin_rintf(t))) < 0.5f) || unsure(i, e, n0) ||
+                                       (edge && t != 0.f)))
+                        check |= 1u << e;
+                }
 #pragma unroll 1
-            for (; check != 0; check &= check - 1) {
-                const int n = n0 + (int)__builtin_ctz(check);
-                q[n] = (int8_t)(int)fmin(fmax(__builtin_rint(exact(n) / (double)s), -127.0), 127.0);
+                for (; check != 0; check &= check - 1) {
+                    const int e = (int)__builtin_ctz(check);
+                    q[n0 + e] = (int8_t)(int)fmin(fmax(__builtin_rint(exact(i, e, n0) / (double)s), -127.0), 127.0);
+                }
             }
         });
     }
@@ -224,11 +270,11 @@ void with_row(int N, Fn &&f)
     else if (chunks <= 128)
         call(std::integral_constant<int, 64>{}, std::integral_constant<int, 2>{});
     else if (chunks <= 256)
-        call(std::integral_constant<int, 256>{}, std::integral_constant<int, 1>{});
+        call(std::integral_constant<int, 128>{}, std::integral_constant<int, 2>{});
     else if (chunks <= 512)
         call(std::integral_constant<int, 256>{}, std::integral_constant<int, 2>{});
     else if (chunks <= 1024)
-        call(std::integral_constant<int, 1024>{}, std::integral_constant<int, 1>{});
+        call(std::integral_constant<int, 256>{}, std::integral_constant<int, 4>{});
     else if (chunks <= 2048)
         call(std::integral_constant<int, 1024>{}, std::integral_constant<int, 2>{});
     else

@@ -58,8 +58,13 @@ __device__ inline int row_tiles(const GroupedArgs &g, int bm)
     return __builtin_amdgcn_readfirstlane(total);
 }
 
-// Tile t, counted group by group and column by column within a group (W's
-// panels are shared).  Every wave of the workgroup computes it for itself.
+// Row tiles of a band: a die's 32 tiles that run side by side are then 4 x 8 and share rows and columns in
+// its L2 (bf16, 8192 rows, 8192 columns, K = 2048: 231 us; 8: 233, whole columns: 247; the gradient of X
+// 197, 199, 211; 65536 slots over 64 experts, 2048 -> 1024: 293, 299, 296).
+constexpr int kBand = 4;
+
+// Tile t, counted group by group, band by band within a group and column by column within a
+// band.  Every wave of the workgroup computes it for itself.
 __device__ inline Place locate(const GroupedArgs &g, int bm, int t)
 {
     const int lane = threadIdx.x % kWave;
@@ -82,7 +87,8 @@ __device__ inline Place locate(const GroupedArgs &g, int bm, int t)
             const int mine = __builtin_amdgcn_readlane(n, at);
             const int first = before + __builtin_amdgcn_readlane(scan, at) - mine;
             const int r = t - first * g.tiles_n;
-            p = Place{g0 + at, __builtin_amdgcn_readlane(a, at), __builtin_amdgcn_readlane(b, at), r % mine, r / mine};
+            const int from = r / (kBand * g.tiles_n) * kBand, q = r - from * g.tiles_n, high = min(kBand, mine - from);
+            p = Place{g0 + at, __builtin_amdgcn_readlane(a, at), __builtin_amdgcn_readlane(b, at), from + q % high, q / high};
             break;
         }
         before += __builtin_amdgcn_readlane(scan, kWave - 1);

@@ -441,7 +441,7 @@ def _here(device) -> int:
     global _current_device, _current_raw_stream
     if _current_raw_stream is None:                  # the last one set: other threads may be here too
         import torch
-        _current_device = torch.cuda.current_device
+        _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
         # the raw address, without the Stream object around it where torch offers it
         _current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
                                       lambda index: torch.cuda.current_stream(index).cuda_stream)
@@ -754,28 +754,35 @@ def _gate(gate: str) -> int:
         raise ValueError(f"gate {gate!r} is none of 'silu', 'gelu' and 'gelu_tanh'") from None
 
 
+def _lead(t, name: str, like, rows: int, cols: int) -> int:
+    """_matrix() of a [rows, cols] matrix beside `like`; contiguous ones, most of them, in half the time."""
+    if t.dtype is like.dtype and t.shape == (rows, cols) and t.is_contiguous() and t.device == like.device and t.is_cuda:
+        return cols if cols > 1 else 1
+    return _matrix(t, name, like, (rows, cols))
+
+
 def _int8(t, name: str, device, shape) -> int:
     """Leading dimension of a matrix of 8-bit numbers."""
     import torch
     if t.dtype != torch.int8 or t.device != device:
         raise TypeError(f"{name} is {t.dtype} on {t.device}, expected {torch.int8} on {device}")
-    return _matrix(t, name, None, shape)
+    return _lead(t, name, t, *shape)
 
 
 def _norm_args(X, weight, residual, out_sum):
     """What both norms have in common: type, sizes, addresses and leading dimensions."""
     import torch
     T, N = X.shape
-    ldx = _matrix(X, "X")
+    ldx = _lead(X, "X", X, T, N)
     w = 0 if weight is None else _vector(weight, "weight", torch.float32, X.device, (N,))
     if residual is None:
         if out_sum is not None:
             raise ValueError("out_sum is the sum with a residual, and there is none")
         return T, N, ldx, w, 0, 0, None, 0
-    ldr = _matrix(residual, "residual", X, (T, N))
+    ldr = _lead(residual, "residual", X, T, N)
     if out_sum is None:
-        out_sum = X.new_empty((T, N))
-    return T, N, ldx, w, residual.data_ptr(), ldr, out_sum, _matrix(out_sum, "out_sum", X, (T, N))
+        return T, N, ldx, w, residual.data_ptr(), ldr, X.new_empty((T, N)), max(N, 1)
+    return T, N, ldx, w, residual.data_ptr(), ldr, out_sum, _lead(out_sum, "out_sum", X, T, N)
 
 
 def rms_norm(X, weight=None, *, eps: float = 1e-6, residual=None, out=None, out_sum=None, stream=None):
@@ -794,8 +801,9 @@ def rms_norm(X, weight=None, *, eps: float = 1e-6, residual=None, out=None, out_
         return _call_on(device, stream, rms_norm, X, weight, eps=eps, residual=residual, out=out, out_sum=out_sum)
     T, N, ldx, w, r, ldr, S, lds = _norm_args(X, weight, residual, out_sum)
     if out is None:
-        out = X.new_empty((T, N))
-    ldy = _matrix(out, "out", X, (T, N))
+        out, ldy = X.new_empty((T, N)), max(N, 1)
+    else:
+        ldy = _lead(out, "out", X, T, N)
     _fit(T, N, ldx, ldr, lds, ldy)
     _check(_lib.gemm_f32_rms_norm(type_, T, N, X.data_ptr(), ldx, r, ldr, w, eps, 0 if S is None else S.data_ptr(), lds,
                                   out.data_ptr(), ldy, _here(device)), "gemm_f32_rms_norm")
@@ -837,17 +845,20 @@ def rms_norm_grad(dY, S, weight=None, *, eps: float = 1e-6, dsum=None, out=None,
     import torch
     if dY.dim() != 2:
         raise ValueError("dY must be [T, N]")
-    type_, lddy = _type(dY), _matrix(dY, "dY")
+    type_ = _type(dY)
     device = dY.device
+    if not dY.is_cuda:
+        raise TypeError("dY must be on a GPU")
     if _elsewhere(device, stream):
         return _call_on(device, stream, rms_norm_grad, dY, S, weight, eps=eps, dsum=dsum, out=out)
     T, N = dY.shape
-    lds = _matrix(S, "S", dY, (T, N))
+    lddy, lds = _lead(dY, "dY", dY, T, N), _lead(S, "S", dY, T, N)
     w = 0 if weight is None else _vector(weight, "weight", torch.float32, device, (N,))
-    ds, ldds = (0, 0) if dsum is None else (dsum.data_ptr(), _matrix(dsum, "dsum", dY, (T, N)))
+    ds, ldds = (0, 0) if dsum is None else (dsum.data_ptr(), _lead(dsum, "dsum", dY, T, N))
     if out is None:
-        out = dY.new_empty((T, N))
-    lddx = _matrix(out, "out", dY, (T, N))
+        out, lddx = dY.new_empty((T, N)), max(N, 1)
+    else:
+        lddx = _lead(out, "out", dY, T, N)
     dweight = dY.new_empty(N, dtype=torch.float32)
     _fit(T, N, lddy, lds, ldds, lddx)
     ws = dY.new_empty(_lib.gemm_f32_rms_norm_grad_ws_size(T, N), dtype=torch.uint8)
@@ -866,10 +877,11 @@ def quantize(X, *, gate=None, stream=None):
     import torch
     if X.dim() != 2:
         raise ValueError("X must be [T, N]")
-    type_, ldx = _type(X), _matrix(X, "X")
+    type_ = _type(X)
     kind = GEMM_F32_GATE_NONE if gate is None else _gate(gate)
     device = X.device
     T, N = X.shape
+    ldx = _lead(X, "X", X, T, N)
     if gate is not None:
         if N % 2:
             raise ValueError(f"X has {N} columns, a gated pair has an even number")
@@ -905,13 +917,14 @@ def int8_matmul(Q, scale, W, w_scale, *, bias=None, dtype=None, out=None, stream
     ws = _vector(w_scale, "w_scale", torch.float32, device, (N,))
     b = 0 if bias is None else _vector(bias, "bias", torch.float32, device, (N,))
     if out is None:
-        out = Q.new_empty((T, N), dtype=torch.bfloat16 if dtype is None else dtype)
-    elif dtype is not None and out.dtype != dtype:
-        raise TypeError(f"out is {out.dtype}, expected {dtype}")
+        out, ldy = Q.new_empty((T, N), dtype=torch.bfloat16 if dtype is None else dtype), max(N, 1)
+    else:
+        if dtype is not None and out.dtype != dtype:
+            raise TypeError(f"out is {out.dtype}, expected {dtype}")
+        if out.device != device:
+            raise TypeError(f"out is on {out.device}, expected {device}")
+        ldy = _lead(out, "out", out, T, N)
     type_ = _type(out)
-    if out.device != device:
-        raise TypeError(f"out is on {out.device}, expected {device}")
-    ldy = _matrix(out, "out", None, (T, N))
     _fit(T, N, K, ldq, ldw, ldy)
     _check(_lib.gemm_f32_int8(type_, T, N, K, Q.data_ptr(), ldq, s, W.data_ptr(), ldw, ws, b, out.data_ptr(), ldy,
                               _here(device)), "gemm_f32_int8")
@@ -929,7 +942,7 @@ def gated_matmul(X, W, offsets=None, *, order=None, per_row: int = 1, gate: str 
     """
     if X.dim() != 2 or W.dim() != 3:
         raise ValueError("X must be [rows, K] and W [G, K, 2 N]")
-    type_, ldx, kind = _type(X), _matrix(X, "X"), _gate(gate)
+    type_, ldx, kind = _type(X), _lead(X, "X", X, *X.shape), _gate(gate)
     device = X.device
     if W.shape[2] % 2:
         raise ValueError(f"W has {W.shape[2]} columns, a gated pair has an even number")
@@ -942,8 +955,9 @@ def gated_matmul(X, W, offsets=None, *, order=None, per_row: int = 1, gate: str 
     ldw = _matrix(W, "W", X, (G, K, 2 * N))
     stride = _stack(W, "W", ldw)
     if out is None:
-        out = X.new_empty((P, N))
-    ldh = _matrix(out, "out", X, (P, N))
+        out, ldh = X.new_empty((P, N)), max(N, 1)
+    else:
+        ldh = _lead(out, "out", X, P, N)
     pre = X.new_empty((P, 2 * N)) if save else None
     _fit(G, P, 2 * N, K, per_row, rows, ldx, ldw, ldh)
     _check(_lib.gemm_f32_gated(type_, kind, G, P, N, K, o, r, per_row, rows, X.data_ptr(), ldx, W.data_ptr(), ldw, stride,
@@ -960,15 +974,16 @@ def gate_grad(dH, pre, *, gate: str = "silu", out=None, stream=None):
     """
     if dH.dim() != 2 or pre.dim() != 2:
         raise ValueError("dH must be [P, N] and pre [P, 2 N]")
-    type_, lddh, kind = _type(dH), _matrix(dH, "dH"), _gate(gate)
+    type_, lddh, kind = _type(dH), _lead(dH, "dH", dH, *dH.shape), _gate(gate)
     device = dH.device
     if _elsewhere(device, stream):
         return _call_on(device, stream, gate_grad, dH, pre, gate=gate, out=out)
     P, N = dH.shape
-    ldp = _matrix(pre, "pre", dH, (P, 2 * N))
+    ldp = _lead(pre, "pre", dH, P, 2 * N)
     if out is None:
-        out = dH.new_empty((P, 2 * N))
-    ldo = _matrix(out, "out", dH, (P, 2 * N))
+        out, ldo = dH.new_empty((P, 2 * N)), max(2 * N, 1)
+    else:
+        ldo = _lead(out, "out", dH, P, 2 * N)
     _fit(P, 2 * N, lddh, ldp, ldo)
     _check(_lib.gemm_f32_gate_grad(type_, kind, P, N, pre.data_ptr(), ldp, dH.data_ptr(), lddh, out.data_ptr(), ldo,
                                    _here(device)), "gemm_f32_gate_grad")

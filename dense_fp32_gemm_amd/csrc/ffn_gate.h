@@ -71,12 +71,16 @@ constexpr double kA = 1.59576912160573071176, kB = kA * 0.044715;     // sqrt(8 
 // power: e^(-g^2 / 2).
 __device__ inline float gelu_part(float g, float &power)
 {
-    constexpr float kFit[] = {0.0202376172f, -0.068247743f, 0.0379958786f, 0.0486143343f, 0.0366340727f, 0.098099038f, 0.100579329f, 0.113273494f, 0.112814017f};
     const float t = __builtin_amdgcn_rcpf(fmaf(fabsf(g), 0.28284271247f, 1.f));
-    float q = kFit[0];
-#pragma unroll
-    for (int i = 1; i < 9; ++i)
-        q = fmaf(q, t, kFit[i]);
+    float q = 0.0202376172f;
+    q = fmaf(q, t, -0.068247743f);
+    q = fmaf(q, t, 0.0379958786f);
+    q = fmaf(q, t, 0.0486143343f);
+    q = fmaf(q, t, 0.0366340727f);
+    q = fmaf(q, t, 0.098099038f);
+    q = fmaf(q, t, 0.100579329f);
+    q = fmaf(q, t, 0.113273494f);
+    q = fmaf(q, t, 0.112814017f);
     power = exp_minus(fminf(0.5f * g * g, 200.f));
     const float tail = q * t * power;
     return g < 0.f ? tail : 1.f - tail;

@@ -78,6 +78,27 @@ __device__ inline void each_pair(const Ti &tile, int wm, int wn, int lane, Fn &&
     }
 }
 
+// act(gate) * what it gates in the gate's place (see each_pair()).
+template <class E, int GATE, class Ti>
+__device__ inline void gate_pairs(Ti &tile)
+{
+#pragma unroll
+    for (int m = 0; m < Ti::kFm; ++m)
+#pragma unroll
+        for (int n = 0; n < Ti::kFn; ++n) {
+            constexpr int V = Ti::Fb::kV, kUp = E::kBytes == 2 ? Ti::kFn / 2 : 0;
+            if (E::kBytes == 2 && n >= kUp)
+                continue;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                if (E::kBytes == 4 && r & (V == 4 ? 1 : 2))
+                    continue;                        // binary32: the others stand one (V = 4) or two registers on
+                const int up = E::kBytes == 2 ? r : r + (V == 4 ? 1 : 2);
+                tile.acc[m][n][r] = gate<GATE>(tile.acc[m][n][r]) * tile.acc[m][n + kUp][up];
+            }
+        }
+}
+
 // One tile: places m0 .. m_end - 1, columns n0 .. n0 + BN / 2 of H.
 template <class E, int GATE, int BM, int BN, int WM, int WN, int S, bool DMA>
 __device__ inline void gated_tile(const GatedArgs &args, int group, int m0, int m_end, int n0, typename E::T *lds)
@@ -110,29 +131,29 @@ __device__ inline void gated_tile(const GatedArgs &args, int group, int m0, int 
                 [&](int i, int r) { return m0 + r < m_end && row[i] < g.rows ? row[i] * g.lda * E::kBytes : -1; });
     const AcrossPair<E, BN, NT, WN> b((const T *)g.B + group * g.stride, tid, g.K, g.ldb, n0, g.N);
     sum_panels<E, DMA, S>(tile, g.K, a, b, lds, tid, wm, wn);
-    // (the three ways apart: merged, the compiler makes pieces of the wide stores)
-    auto store = [&](auto vec, auto keep) {
-        constexpr bool V = decltype(vec)::value;
+    auto each = [&](auto &&f) {                      // of the pairs that are inside
         each_pair<E>(tile, wm, wn, lane, [&](int r, int c, f32x4 x, f32x4 u) {
-            const int m = m0 + r, n = n0 + c;
-            if (m >= m_end || n >= g.N)
-                return;
-            f32x4 y;
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                y[i] = gate<GATE>(x[i]) * u[i];
-            store4<E, V>((T *)g.C + (int64_t)m * g.ldc + n, y, g.N - n);
-            if constexpr (decltype(keep)::value) {
-                T *p = (T *)args.pre + (int64_t)m * args.ldp + n;
-                store4<E, V>(p, x, g.N - n);
-                store4<E, V>(p + g.N, u, g.N - n);
-            }
+            if (m0 + r < m_end && n0 + c < g.N)
+                f((int64_t)(m0 + r), n0 + c, x, u);
         });
     };
-    if (args.pre == nullptr)
-        g.vector_c ? store(std::true_type{}, std::false_type{}) : store(std::false_type{}, std::false_type{});
-    else
-        g.vector_c && args.vector_p ? store(std::true_type{}, std::true_type{}) : store(std::false_type{}, std::true_type{});
+    // (wide and narrow stores apart: merged, the compiler makes pieces of the wide ones, which doubled the
+    // time of the stores)
+    if (args.pre != nullptr) {
+        auto write = [&](auto vec) {
+            each([&](int64_t m, int n, f32x4 x, f32x4 u) {
+                T *p = (T *)args.pre + m * args.ldp + n;
+                store4<E, decltype(vec)::value>(p, x, g.N - n);
+                store4<E, decltype(vec)::value>(p + g.N, u, g.N - n);
+            });
+        };
+        args.vector_p ? write(std::true_type{}) : write(std::false_type{});
+    }
+    gate_pairs<E, GATE>(tile);
+    auto write = [&](auto vec) {
+        each([&](int64_t m, int n, f32x4 y, f32x4) { store4<E, decltype(vec)::value>((T *)g.C + m * g.ldc + n, y, g.N - n); });
+    };
+    g.vector_c ? write(std::true_type{}) : write(std::false_type{});
 }
 
 template <class E, int GATE, int BM, int BN, int WM, int WN, int S, bool CUT, bool DMA>

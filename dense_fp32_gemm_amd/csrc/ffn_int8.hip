@@ -121,34 +121,35 @@ __global__ __launch_bounds__(WM *WN *kWave, 2) void int8_kernel(Int8Args g)
 // ---------------------------------------------------------------------------
 // Few rows
 // ---------------------------------------------------------------------------
-constexpr int kFewWaves = 8, kFewSteps = 4;          // waves of a workgroup; 64 k's a wave takes at once
+constexpr int kFewWaves = 8;                         // of a workgroup
 
-// 16 channels and up to 16 MT rows a workgroup.  Wave w takes every kFewWaves-th block of
-// 256 k: 16 bytes a lane, 256 bytes of a row side by side.  The waves' sums meet in LDS.
-template <class Out, bool VEC, int MT>
+// 16 channels and up to 16 MT rows a workgroup.  Wave w takes every kFewWaves-th block of 64 STEPS
+// k: 16 bytes a lane, 64 bytes of a row side by side a step, all steps' loads before the first product.  The waves'
+// sums meet in LDS.
+template <class Out, bool VEC, int MT, int STEPS>
 __global__ __launch_bounds__(kFewWaves *kWave) void int8_few_kernel(Int8Args g)
 {
-    constexpr int kBlock = kFewSteps * 64;
+    constexpr int kBlock = STEPS * 64;
     __shared__ i32x4 part[kFewWaves][MT][kWave];
     const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave, i = lane % 16, h = lane / 16;
     const int n0 = blockIdx.x * 16;
     const bool channel = n0 + i < g.N;
-    const int8_t *w = g.W + (channel ? n0 + i : 0) * g.ldw + 16 * h;
+    const int8_t *w = g.W + (channel ? n0 + i : 0) * g.ldw;
     i32x4 acc[MT] = {};
     for (int k0 = wave * kBlock; k0 < g.K; k0 += kFewWaves * kBlock) {
-        u32x4 b[kFewSteps], a[MT][kFewSteps];
+        u32x4 b[STEPS], a[MT][STEPS];
 #pragma unroll
-        for (int s = 0; s < kFewSteps; ++s) {
-            const int k = k0 + 64 * s, left = g.K - k - 16 * h;
+        for (int s = 0; s < STEPS; ++s) {
+            const int k = k0 + 64 * s + 16 * h, left = g.K - k;
             b[s] = load_chunk<I8, VEC>(w + k, channel ? left : 0);
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
                 const int t = 16 * m + i;
-                a[m][s] = load_chunk<I8, VEC>(g.Q + (t < g.T ? t : 0) * g.ldq + 16 * h + k, t < g.T ? left : 0);
+                a[m][s] = load_chunk<I8, VEC>(g.Q + (t < g.T ? t : 0) * g.ldq + k, t < g.T ? left : 0);
             }
         }
 #pragma unroll
-        for (int s = 0; s < kFewSteps; ++s)
+        for (int s = 0; s < STEPS; ++s)
 #pragma unroll
             for (int m = 0; m < MT; ++m)
                 acc[m] = mfma<I8>(b[s], a[m][s], acc[m], 0);
@@ -158,14 +159,14 @@ __global__ __launch_bounds__(kFewWaves *kWave) void int8_few_kernel(Int8Args g)
         part[wave][m][lane] = acc[m];
     __syncthreads();
     for (int m = wave; m < MT; m += kFewWaves) {
+        const int t = 16 * m + i, n = n0 + 4 * h;
         Channels channels;
-        channels.load(g, n0 + 4 * h);
-        const float s = g.scale[min(16 * m + i, g.T - 1)];
+        channels.load(g, n);
+        const float s = g.scale[min(t, g.T - 1)];
         i32x4 sum = part[0][m][lane];
 #pragma unroll
         for (int v = 1; v < kFewWaves; ++v)
             sum += part[v][m][lane];
-        const int t = 16 * m + i, n = n0 + 4 * h;
         if (t < g.T && n < g.N)
             int8_store<Out, false>(g, t, n, channels.scaled(sum, s));
     }
@@ -195,38 +196,54 @@ int launch_int8(Int8Args g, bool dma, hipStream_t stream, bool go)
     return launched();
 }
 
-constexpr int kFewRows = 64;
+// Rows of the few-row kernel.  Every workgroup reads all rows, which the caches bear up to one workgroup a
+// compute unit (us in a graph, weights from HBM, against 32 x 64 tiles: 4096 channels, K = 4096: 16 rows 7.4 and 11.8, 32
+// rows 10.0 and 12.0, 48 rows 12.0 and 11.9; 2048 channels, K = 8192: 32 rows 15.1 and 20.0, 48 rows 19.4 and 19.7;
+// 8192 channels, K = 8192: 16 rows 19.6 and 21.2, 32 rows 28.0 and 21.7).
+int few_rows(int N) { return ceil_div(N, 16) <= gemm_f32_internal::current_device().cus ? 48 : 16; }
 
+// The largest tile of which there is one for every compute unit (us, 4096 channels, K = 4096: 128 rows 11.7 with
+// 32 x 64, 13.0 with 64 x 64, 15.6 with 64 x 128; 256 rows 14.0, 13.7, 15.9; 512 rows 26.0, 18.5, 17.0).
+// 256 x 256 tiles from a quarter of the units on, because they are cut there (1024 rows 26.2 against 25.9 for
+// 64 x 128, 1536 rows 34.4 against 43.1, 2048 rows 37.8 against 49.9).
 int launch_int8(int type, const Int8Args &g, bool dma, bool vec, hipStream_t stream, bool go)
 {
     int rc = GEMM_F32_OK;
+    const int64_t cus = gemm_f32_internal::current_device().cus;
+    auto tiles = [&](int bm, int bn) { return ceil_div(g.T, bm) * ceil_div(g.N, bn); };
     with_type(type, [&](auto e) {
         using Out = decltype(e);
-        if (g.T <= kFewRows) {
-            const int64_t grid = ceil_div(g.N, 16);  // under kMaxTiles * 512 / 16: g.N < 2^31
-            if (grid * kFewWaves * kWave > UINT32_MAX) {
+        if (g.T <= few_rows(g.N)) {
+            const int64_t grid = ceil_div(g.N, 16);
+            if (grid > kMaxTiles) {
                 rc = GEMM_F32_ERR_DIM;
                 return;
             }
             if (!go || g.T == 0 || grid == 0)
                 return;
-            auto few = [&](auto mt) {
+            auto few = [&](auto mt, auto steps) {
+                constexpr int MT = decltype(mt)::value, STEPS = decltype(steps)::value;
                 if (vec)
-                    int8_few_kernel<Out, true, decltype(mt)::value><<<(int)grid, kFewWaves * kWave, 0, stream>>>(g);
+                    int8_few_kernel<Out, true, MT, STEPS><<<(int)grid, kFewWaves * kWave, 0, stream>>>(g);
                 else
-                    int8_few_kernel<Out, false, decltype(mt)::value><<<(int)grid, kFewWaves * kWave, 0, stream>>>(g);
+                    int8_few_kernel<Out, false, MT, STEPS><<<(int)grid, kFewWaves * kWave, 0, stream>>>(g);
             };
+            using std::integral_constant;
             if (g.T <= 16)
-                few(std::integral_constant<int, 1>{});
+                few(integral_constant<int, 1>{}, integral_constant<int, 8>{});
             else if (g.T <= 32)
-                few(std::integral_constant<int, 2>{});
+                few(integral_constant<int, 2>{}, integral_constant<int, 4>{});
             else
-                few(std::integral_constant<int, 4>{});
+                few(integral_constant<int, 3>{}, integral_constant<int, 4>{});
             rc = launched();
-        } else if (ceil_div(g.T, 256) * ceil_div(g.N, 256) * 5 >= 3 * gemm_f32_internal::current_device().cus) {
+        } else if (4 * tiles(256, 256) > cus) {
             rc = launch_int8<Out, 256, 256, 2, 4, 2, 1>(g, dma, stream, go);
-        } else {
+        } else if (tiles(64, 128) >= cus) {
             rc = launch_int8<Out, 64, 128, 2, 2, 3, 0>(g, dma, stream, go);
+        } else if (tiles(64, 64) >= cus) {
+            rc = launch_int8<Out, 64, 64, 2, 2, 4, 0>(g, dma, stream, go);
+        } else {
+            rc = launch_int8<Out, 32, 64, 1, 4, 4, 0>(g, dma, stream, go);
         }
     });
     return rc;

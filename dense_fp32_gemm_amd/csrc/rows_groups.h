@@ -43,6 +43,8 @@ struct Place {
 // Row tiles of all groups (64 groups at a time, a lane each), the same in every lane.
 __device__ inline int row_tiles(const GroupedArgs &g, int bm)
 {
+    if (g.offsets == nullptr)
+        return (g.P + bm - 1) / bm;
     const int lane = threadIdx.x % kWave;
     int total = 0;
     for (int g0 = 0; g0 < g.G; g0 += kWave) {
@@ -63,10 +65,21 @@ __device__ inline int row_tiles(const GroupedArgs &g, int bm)
 // 197, 199, 211; 65536 slots over 64 experts, 2048 -> 1024: 293, 299, 296).
 constexpr int kBand = 4;
 
+// The r-th tile of a group that has `rows` row tiles.
+__device__ inline Place banded(const GroupedArgs &g, Place p, int r, int rows)
+{
+    const int from = r / (kBand * g.tiles_n) * kBand, q = r - from * g.tiles_n, high = min(kBand, rows - from);
+    p.tn = high == kBand ? q / kBand : q / high;     // (the usual case without a division)
+    p.tm = from + q - p.tn * high;
+    return p;
+}
+
 // Tile t, counted group by group, band by band within a group and column by column within a
 // band.  Every wave of the workgroup computes it for itself.
 __device__ inline Place locate(const GroupedArgs &g, int bm, int t)
 {
+    if (g.offsets == nullptr)
+        return banded(g, Place{0, 0, g.P, 0, 0}, t, (g.P + bm - 1) / bm);
     const int lane = threadIdx.x % kWave;
     int before = 0;                                  // row tiles of the groups before
     Place p{0, 0, 0, 0, 0};
@@ -86,9 +99,8 @@ __device__ inline Place locate(const GroupedArgs &g, int bm, int t)
             const int at = (int)__builtin_ctzll(past);
             const int mine = __builtin_amdgcn_readlane(n, at);
             const int first = before + __builtin_amdgcn_readlane(scan, at) - mine;
-            const int r = t - first * g.tiles_n;
-            const int from = r / (kBand * g.tiles_n) * kBand, q = r - from * g.tiles_n, high = min(kBand, mine - from);
-            p = Place{g0 + at, __builtin_amdgcn_readlane(a, at), __builtin_amdgcn_readlane(b, at), from + q % high, q / high};
+            p = banded(g, Place{g0 + at, __builtin_amdgcn_readlane(a, at), __builtin_amdgcn_readlane(b, at), 0, 0},
+                       t - first * g.tiles_n, mine);
             break;
         }
         before += __builtin_amdgcn_readlane(scan, kWave - 1);

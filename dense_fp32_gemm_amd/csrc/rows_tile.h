@@ -849,6 +849,8 @@ __device__ inline void sum_panels(Ti &tile, int K, const SrcA &a, const SrcB &b,
 // gets a contiguous range of tiles, whose operands its L2 then shares.
 __device__ inline int die_contiguous(int w, int total, int xcds)
 {
+    if (xcds == 8)                                   // a whole MI355X: without divisions
+        return (w & 7) * (total >> 3) + min(w & 7, total & 7) + (w >> 3);
     const int per = total / xcds, rem = total % xcds, xcd = w % xcds;
     return xcd * per + (xcd < rem ? xcd : rem) + w / xcds;
 }

@@ -255,9 +255,9 @@ def eight(g, T, K):
     return torch.randint(-128, 128, (T, K), generator=g, dtype=torch.int8)
 
 
-# few rows (1 to 64), tiles of 64 x 128, and of 256 x 256 whole and cut
-INT8 = [(1, 1, 1), (1, 16, 16), (2, 17, 15), (7, 65, 100), (16, 300, 256), (17, 33, 257), (32, 64, 2048), (33, 40, 1000), (64, 130, 4100),
-        (65, 1, 1), (65, 64, 128), (100, 129, 130), (129, 200, 1000), (300, 513, 77), (70, 300, 0), (3, 20, 0), (2000, 130, 64)]
+# few rows (1 to 48), tiles of 32 x 64, 64 x 64 and 64 x 128, and of 256 x 256 whole and cut
+INT8 = [(1, 1, 1), (1, 16, 16), (2, 17, 15), (7, 65, 100), (16, 300, 256), (16, 4200, 513), (17, 4200, 70), (17, 33, 257), (48, 40, 90), (49, 40, 90), (32, 64, 2048), (33, 40, 1000), (64, 130, 4100),
+        (520, 2050, 70), (1100, 2100, 96), (65, 1, 1), (65, 64, 128), (100, 129, 130), (129, 200, 1000), (300, 513, 77), (70, 300, 0), (3, 20, 0), (2000, 130, 64)]
 
 
 def check_int8(dev, g, T, N, K, pad, dtype, with_bias):
@@ -280,7 +280,7 @@ def test_int8_matmul(dev, dtype, pad, T, N, K):
 
 
 @pytest.mark.parametrize("pad", [0, 1], ids=["direct loads", "staged loads"])
-@pytest.mark.parametrize("T,N,K", [(4096, 4096, 128), (4200, 4100, 200), (2600, 5200, 300), (4096, 4864, 96), (8200, 2100, 144)])
+@pytest.mark.parametrize("T,N,K", [(4096, 4096, 128), (4200, 4100, 200), (2600, 5200, 300), (4096, 4864, 96), (8200, 2100, 144), (2600, 2600, 130)])
 def test_int8_large_tiles_whole_and_cut(dev, pad, T, N, K):
     say("int8 large", T, N, K, pad)
     check_int8(dev, seeded("int8 large", T, N, K), T, N, K, pad, torch.bfloat16, False)

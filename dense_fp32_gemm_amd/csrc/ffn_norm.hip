@@ -28,9 +28,9 @@ __global__ __launch_bounds__(kRowThreads<TPR>) void norm_kernel(NormArgs g)
 {
     using T = typename E::T;
     constexpr int kRows = kRowsAtOnce<TPR>, K = E::kChunk;
-    __shared__ uint64_t slots[2][TPR / kWave];
+    __shared__ typename RowJoin<TPR>::Pair slots[2][TPR / kWave];
     const int j = threadIdx.x % TPR;
-    RowSums<TPR> over{slots};
+    RowJoin<TPR> over{slots};
     auto weights = [&](float (&w)[K], int n0) {
         if (g.weight != nullptr)
             load_floats<E>(w, g.weight + n0, g.N - n0);
@@ -80,9 +80,8 @@ __global__ __launch_bounds__(kRowThreads<TPR>) void norm_kernel(NormArgs g)
             for (int e = 0; e < K; ++e)
                 squares = fma((double)(float)z[i].e[e], (double)(float)z[i].e[e], squares);
         });
-        const double scale = 1.0 / sqrt(over.sum(squares) / g.N + g.eps);
-        const float scale32 = (float)scale;
         if constexpr (!INT8) {
+            const float scale = (float)(1.0 / sqrt(over.sum(squares) / g.N + g.eps));
             each_chunk<TPR, C, E>(g.N, j, [&](int i, int n0) {
                 if constexpr (C == 0) {
                     again(z[i], n0);
@@ -91,26 +90,46 @@ __global__ __launch_bounds__(kRowThreads<TPR>) void norm_kernel(NormArgs g)
                 Chunk<E> o;
 #pragma unroll
                 for (int e = 0; e < K; ++e)
-                    o.e[e] = (T)((float)z[i].e[e] * scale32 * w[i][e]);
+                    o.e[e] = (T)((float)z[i].e[e] * scale * w[i][e]);
                 if (there)
                     store_chunk<E, VEC>((T *)g.Y + t * g.ldy + n0, o, g.N - n0);
             });
         } else {
-            Int8Row<TPR, C, E, false> row{g.N, j, there, (int8_t *)g.Y + (there ? t : 0) * g.ldy};
             int loaded = -1;                         // C = 0: the column whose chunk z and w hold
-            row.write(over, g.scale + t, 0x1p-21f,
-                      [&](int i, int e, int n0) {
-                          if constexpr (C == 0) {
-                              if (loaded != n0) {
-                                  loaded = n0;
-                                  again(z[i], loaded);
-                                  weights(w[i], loaded);
-                              }
-                          }
-                          return (float)z[i].e[e] * scale32 * w[i][e];
-                      },
-                      [&](int i, int e, int) { return (double)pick(z[i], e) * (double)pick(w[i], e) * scale; },
-                      [](int, int) { return 0x1p-21f; }, [](int, int, int) { return false; });
+            auto open = [&](int i, int n0) {
+                if constexpr (C == 0) {
+                    if (loaded != n0) {
+                        loaded = n0;
+                        again(z[i], n0);
+                        weights(w[i], n0);
+                    }
+                }
+            };
+            auto sure = [](int, int, int) { return false; };
+            auto some = [&](int i, int e) { return (float)z[i].e[e] != 0.f; };
+            // The largest S weight: a row's factor does not change which it is, so its approximation shares the
+            // squares' exchange.
+            auto product = [&](int i, int e, int n0) {
+                open(i, n0);
+                return (float)z[i].e[e] * w[i][e];
+            };
+            RowMost<TPR, C, E> most{g.N, j};
+            uint64_t top = most.approximate(product, sure);
+            const double sum = over.sum_and_most(squares, top), scale = 1.0 / sqrt(sum / max(g.N, 1) + g.eps);
+            const double largest = scale * most.exactly(over, top, 0x1p-23f, product,
+                                                        [&](int i, int e, int) { return (double)pick(z[i], e) * (double)pick(w[i], e); },
+                                                        sure, some);
+            const float scale32 = (float)scale;
+            if (there) {
+                Int8Row<TPR, C, E> row{g.N, j, (int8_t *)g.Y + t * g.ldy, false};
+                row.write(largest, g.scale + t,
+                          [&](int i, int e, int n0) {
+                              open(i, n0);
+                              return (float)z[i].e[e] * scale32 * w[i][e];
+                          },
+                          [&](int i, int e, int) { return (double)pick(z[i], e) * (double)pick(w[i], e) * scale; },
+                          [](int, int) { return 0x1p-21f; }, sure, some);
+            }
         }
     }
 }
@@ -136,9 +155,9 @@ __global__ __launch_bounds__(kRowThreads<TPR>) void norm_grad_kernel(NormGradArg
 {
     using T = typename E::T;
     constexpr int kRows = kRowsAtOnce<TPR>, K = E::kChunk, kC = C > 0 ? C : 1;
-    __shared__ uint64_t slots[2][TPR / kWave];
+    __shared__ typename RowJoin<TPR>::Pair slots[2][TPR / kWave];
     const int j = threadIdx.x % TPR;
-    RowSums<TPR> over{slots};
+    RowJoin<TPR> over{slots};
     float w[kC][K], sum[kC][K] = {};
     auto weights = [&](float (&v)[K], int n0) {
         if (g.weight != nullptr)
@@ -182,8 +201,9 @@ __global__ __launch_bounds__(kRowThreads<TPR>) void norm_grad_kernel(NormGradArg
                 along = fma((double)((float)d[i].e[e] * w[i][e]), v, along);
             }
         });
-        const double r = 1.0 / sqrt(over.sum(squares) / g.N + g.eps);
-        const float r32 = (float)r, k = (float)(over.sum(along) / g.N * r * r);
+        over.sums(squares, along);
+        const double r = 1.0 / sqrt(squares / g.N + g.eps);
+        const float r32 = (float)r, k = (float)(along / g.N * r * r);
         each_chunk<TPR, C, E>(g.N, j, [&](int i, int n0) {
             if constexpr (C == 0) {
                 load(i, n0);

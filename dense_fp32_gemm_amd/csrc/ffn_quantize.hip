@@ -28,9 +28,9 @@ __global__ __launch_bounds__(kRowThreads<TPR>) void quantize_kernel(QuantizeArgs
     using T = typename E::T;
     constexpr int kRows = kRowsAtOnce<TPR>, K = E::kChunk, kC = C > 0 ? C : 1;
     constexpr bool kGated = GATE != GEMM_F32_GATE_NONE;
-    __shared__ uint64_t slots[2][TPR / kWave];
+    __shared__ typename RowJoin<TPR>::Pair slots[2][TPR / kWave];
     const int j = threadIdx.x % TPR;
-    RowSums<TPR> over{slots};
+    RowJoin<TPR> over{slots};
     for (int64_t t0 = (int64_t)blockIdx.x * kRows; t0 < g.T; t0 += (int64_t)gridDim.x * kRows) {
         const int64_t t = t0 + threadIdx.x / TPR;
         const bool there = t < g.T;
@@ -54,29 +54,38 @@ __global__ __launch_bounds__(kRowThreads<TPR>) void quantize_kernel(QuantizeArgs
             each_chunk<TPR, C, E>(g.N, j, [&](int i, int) { open(i); });
         }
         int loaded = -1;                             // C = 0: the column whose chunk a, b and y hold
-        Int8Row<TPR, C, E, !kGated> row{g.N, j, there, g.Q + (there ? t : 0) * g.ldq};
-        row.write(over, g.scale + t, kGated ? kGateFar : 0x1p-23f,
-                  [&](int i, int e, int n0) {
-                      if constexpr (C == 0) {
-                          if (loaded != n0) {
-                              loaded = n0;
-                              load(i, loaded);
-                              open(i);
-                          }
-                      }
-                      if constexpr (kGated)
-                          return y[i][e];
-                      else
-                          return (float)a[i].e[e];
-                  },
-                  [&](int i, int e, int) {
-                      if constexpr (kGated)
-                          return gate64<GATE>((double)pick(a[i], e)) * (double)pick(b[i], e);
-                      else
-                          return (double)pick(a[i], e);
-                  },
-                  [&](int i, int e) { return kGated ? gate_error<GATE>((float)a[i].e[e]) : 0x1p-23f; },
-                  [&](int i, int e, int) { return kGated && (float)a[i].e[e] < gate_left<GATE>(); });
+        auto approx = [&](int i, int e, int n0) {
+            if constexpr (C == 0) {
+                if (loaded != n0) {
+                    loaded = n0;
+                    load(i, loaded);
+                    open(i);
+                }
+            }
+            if constexpr (kGated)
+                return y[i][e];
+            else
+                return (float)a[i].e[e];
+        };
+        auto exact = [&](int i, int e, int) {
+            if constexpr (kGated)
+                return gate64<GATE>((double)pick(a[i], e)) * (double)pick(b[i], e);
+            else
+                return (double)pick(a[i], e);
+        };
+        auto unsure = [&](int i, int e, int) { return kGated && (float)a[i].e[e] < gate_left<GATE>(); };
+        auto some = [&](int i, int e) { return (float)a[i].e[e] != 0.f; };
+        RowMost<TPR, C, E> most{g.N, j};
+        uint64_t top = most.approximate(approx, unsure);
+        over.most(top);
+        double largest = (double)__uint_as_float((uint32_t)top);
+        if constexpr (kGated)
+            largest = most.exactly(over, top, kGateFar, approx, exact, unsure, some);
+        if (there) {
+            Int8Row<TPR, C, E> row{g.N, j, g.Q + t * g.ldq, most.loose};
+            row.write(largest, g.scale + t, approx, exact,
+                      [&](int i, int e) { return kGated ? gate_error<GATE>((float)a[i].e[e]) : 0x1p-23f; }, unsure, some);
+        }
     }
 }
 

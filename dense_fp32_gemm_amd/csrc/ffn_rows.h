@@ -18,73 +18,83 @@ constexpr int kRowsAtOnce = TPR == kWave ? 4 : 1;
 template <int TPR>
 constexpr int kRowThreads = TPR * kRowsAtOnce<TPR>;
 
-__device__ inline double wave_sum(double v)
+// Rotations within rows of 16 lanes, then the four rows' first lanes, in scalars.
+template <int CTRL>
+__device__ inline uint64_t dpp64(uint64_t x)
 {
-#pragma unroll
-    for (int d = kWave / 2; d > 0; d /= 2)
-        v += __shfl_xor(v, d);
-    return v;
+    return (uint64_t)dpp<CTRL>((uint32_t)(x >> 32)) << 32 | dpp<CTRL>((uint32_t)x);
 }
-
-__device__ inline uint64_t wave_max64(uint64_t v)
+__device__ inline uint64_t lane64(uint64_t x, int lane)
 {
-#pragma unroll
-    for (int d = kWave / 2; d > 0; d /= 2) {
-        const uint64_t o = __shfl_xor((unsigned long long)v, d);
-        v = o > v ? o : v;
-    }
-    return v;
+    return (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(x >> 32), lane) << 32 |
+           (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)x, lane);
 }
+template <class Join>
+__device__ inline uint64_t wave_join(uint64_t v, Join &&join)
+{
+    v = join(v, dpp64<0x128>(v));   // row_ror:8
+    v = join(v, dpp64<0x124>(v));
+    v = join(v, dpp64<0x122>(v));
+    v = join(v, dpp64<0x121>(v));
+    return join(join(lane64(v, 0), lane64(v, 16)), join(lane64(v, 32), lane64(v, 48)));
+}
+__device__ inline uint64_t add64(uint64_t a, uint64_t b)
+{
+    return __builtin_bit_cast(uint64_t, __builtin_bit_cast(double, a) + __builtin_bit_cast(double, b));
+}
+__device__ inline uint64_t max64(uint64_t a, uint64_t b) { return a > b ? a : b; }
 
-// Reductions over a row's threads, the same in each.  Two slots in turn: a slot is
-// written again after the barrier that its readers pass next.
+// Reductions over a row's threads, the same in each: of a sum in binary64 and of something else,
+// with one barrier.  Two slots in turn: a slot is written again after the barrier that its readers pass next.
 template <int TPR>
-struct RowSums {
+struct RowJoin {
     static constexpr int kWaves = TPR / kWave;
-    uint64_t (*slots)[kWaves];                       // LDS [2][kWaves]
+    struct Pair {
+        uint64_t a, b;
+    };
+    Pair (*slots)[kWaves];                           // LDS [2][kWaves]
     int at = 0;
 
-    __device__ inline const uint64_t *exchange(uint64_t mine)
+    // a and b are the same in a wave
+    template <class JoinA, class JoinB>
+    __device__ inline void join(uint64_t &a, uint64_t &b, JoinA &&join_a, JoinB &&join_b)
     {
-        at ^= 1;
-        if (threadIdx.x % kWave == 0)
-            slots[at][threadIdx.x / kWave] = mine;
-        __syncthreads();
-        return slots[at];
-    }
-    __device__ inline double sum(double v)
-    {
-        v = wave_sum(v);
         if constexpr (kWaves > 1) {
-            const uint64_t *all = exchange(__builtin_bit_cast(uint64_t, v));
-            v = 0.0;
+            at ^= 1;
+            if (threadIdx.x % kWave == 0)
+                slots[at][threadIdx.x / kWave] = Pair{a, b};
+            __syncthreads();
+            a = slots[at][0].a, b = slots[at][0].b;
 #pragma unroll
-            for (int w = 0; w < kWaves; ++w)
-                v += __builtin_bit_cast(double, all[w]);
+            for (int w = 1; w < kWaves; ++w) {
+                a = join_a(a, slots[at][w].a);
+                b = join_b(b, slots[at][w].b);
+            }
         }
-        return v;
     }
-    __device__ inline uint32_t max32(uint32_t v)
+    __device__ inline void sums(double &x, double &y)
     {
-        v = wave_max(v);
-        if constexpr (kWaves > 1) {
-            const uint64_t *all = exchange(v);
-#pragma unroll
-            for (int w = 0; w < kWaves; ++w)
-                v = max(v, (uint32_t)all[w]);
-        }
-        return v;
+        uint64_t a = wave_join(__builtin_bit_cast(uint64_t, x), add64), b = wave_join(__builtin_bit_cast(uint64_t, y), add64);
+        join(a, b, add64, add64);
+        x = __builtin_bit_cast(double, a), y = __builtin_bit_cast(double, b);
     }
-    __device__ inline uint64_t max64(uint64_t v)
+    __device__ inline double sum(double x)
     {
-        v = wave_max64(v);
-        if constexpr (kWaves > 1) {
-            const uint64_t *all = exchange(v);
-#pragma unroll
-            for (int w = 0; w < kWaves; ++w)
-                v = all[w] > v ? all[w] : v;
-        }
-        return v;
+        uint64_t a = wave_join(__builtin_bit_cast(uint64_t, x), add64), b = 0;
+        join(a, b, add64, add64);
+        return __builtin_bit_cast(double, a);
+    }
+    // the row's largest b beside; b is the same in a wave
+    __device__ inline double sum_and_most(double x, uint64_t &b)
+    {
+        uint64_t a = wave_join(__builtin_bit_cast(uint64_t, x), add64);
+        join(a, b, add64, max64);
+        return __builtin_bit_cast(double, a);
+    }
+    __device__ inline void most(uint64_t &b)
+    {
+        uint64_t a = 0;
+        join(a, b, add64, max64);
     }
 };
 
@@ -142,67 +152,86 @@ __device__ inline float pick(const float (&c)[K], int e)
 // relative error, and only those whose rounding that leaves open are computed in
 // binary64: the elements that may be the row's largest, and those next to a
 // rounding border (of 127 steps' binary32 error, one in ten thousand or fewer).  So the
-// results are the definition's at a binary32 pass's cost.  SURE: approx is exact.
+// results are the definition's at a binary32 pass's cost.
 //
 //   approx(i, e, n0)  the i-th chunk's element e (column n0 + e); 0 past the row's end
 //   error(i, e)       how far that may be off, relative, at most most_error
 //   exact(i, e, n0)   the same in binary64; e is no constant (see pick())
 //   unsure(i, e, n0)  whether approx may be off by more
-template <int TPR, int C, class E, bool SURE>
-struct Int8Row {
-    int N, j;
-    bool there;                                      // the row
-    int8_t *q;                                       // its start
+//   some(i, e)        whether exact() may be other than 0
 
-    template <class Approx, class Exact, class Error, class Unsure>
-    __device__ inline void write(RowSums<TPR> &over, float *scale, float most_error, Approx &&approx, Exact &&exact, Error &&error,
-                                 Unsure &&unsure)
+// A row's largest magnitude in two steps, as whole numbers (NaN above infinity above every number):
+// that of approx() among the thread's elements, of which the caller makes the row's, and from
+// that the largest of exact().
+template <int TPR, int C, class E>
+struct RowMost {
+    int N, j;
+    uint32_t mine = 0;
+    bool loose = false;
+
+    // The wave's.
+    template <class Approx, class Unsure>
+    __device__ inline uint64_t approximate(Approx &&approx, Unsure &&unsure)
     {
-        constexpr int K = E::kChunk;
-        constexpr uint32_t kInf = 0x7f800000u;
-        // NaN above infinity above every number, as whole numbers
-        uint32_t mine = 0;
-        bool loose = false;
         each_chunk<TPR, C, E>(N, j, [&](int i, int n0) {
 #pragma unroll
-            for (int e = 0; e < K; ++e) {
+            for (int e = 0; e < E::kChunk; ++e) {
                 mine = max(mine, __float_as_uint(approx(i, e, n0)) & 0x7fffffffu);
                 loose |= unsure(i, e, n0);
             }
         });
-        const uint32_t top = over.max32(mine);
+        return wave_max(mine);
+    }
+    // The row's.
+    template <class Approx, class Exact, class Unsure, class Some>
+    __device__ inline double exactly(RowJoin<TPR> &over, uint64_t row_top, float most_error, Approx &&approx, Exact &&exact, Unsure &&unsure,
+                                     Some &&some) const
+    {
+        // Below `near` nothing is the largest.  Next to binary32's smallest numbers errors are not relative.
+        const uint32_t top = (uint32_t)row_top;
+        const float near = top > 0x7f800000u ? INFINITY : __uint_as_float(top) * (1.f - 4.f * most_error);
+        const bool small = near < 0x1p-100f;
         uint64_t most = 0;
-        if constexpr (SURE) {
-            most = __builtin_bit_cast(uint64_t, (double)__uint_as_float(top));
-        } else {
-            // Below `near` nothing is the row's largest.  (Rows up to 2^-120 get the smallest scale in any case.)
-            const float near = top > kInf ? INFINITY : fmaxf(__uint_as_float(top) * (1.f - 4.f * most_error), 0x1p-120f);
-            if (!(__uint_as_float(mine) < near) || loose)
-                each_chunk<TPR, C, E>(N, j, [&](int i, int n0) {
-                    uint32_t check = 0;
+        if (!(__uint_as_float(mine) < near) || loose || small)
+            each_chunk<TPR, C, E>(N, j, [&](int i, int n0) {
+                uint32_t check = 0;
 #pragma unroll
-                    for (int e = 0; e < K; ++e)
-                        if (n0 + e < N && (!(fabsf(approx(i, e, n0)) < near) || unsure(i, e, n0)))
-                            check |= 1u << e;
+                for (int e = 0; e < E::kChunk; ++e) {
+                    const bool large = !(fabsf(approx(i, e, n0)) < near);
+                    if (n0 + e < N && (small ? some(i, e) : large || unsure(i, e, n0)))
+                        check |= 1u << e;
+                }
 #pragma unroll 1
-                    for (; check != 0; check &= check - 1) {
-                        const uint64_t y = __builtin_bit_cast(uint64_t, fabs(exact(i, (int)__builtin_ctz(check), n0)));
-                        most = y > most ? y : most;
-                    }
-                });
-            most = over.max64(most);
-        }
-        float s = fmaxf((float)(__builtin_bit_cast(double, most) / 127.0), 0x1p-126f);
-        const bool bad = most >= 0x7ff0000000000000u || !(s < INFINITY);
+                for (; check != 0; check &= check - 1)
+                    most = max64(most, __builtin_bit_cast(uint64_t, fabs(exact(i, (int)__builtin_ctz(check), n0))));
+            });
+        if (__ballot(most != 0) != 0)                // few waves have any
+            most = wave_join(most, max64);
+        over.most(most);
+        return __builtin_bit_cast(double, most);
+    }
+};
+
+// A row's scale from the largest magnitude of its exact values, and its 8-bit numbers.
+template <int TPR, int C, class E>
+struct Int8Row {
+    int N, j;
+    int8_t *q;                                       // the row's start
+    bool loose;                                      // whether any of the thread's elements is unsure
+
+    template <class Approx, class Exact, class Error, class Unsure, class Some>
+    __device__ inline void write(double most, float *scale, Approx &&approx, Exact &&exact, Error &&error, Unsure &&unsure, Some &&some)
+    {
+        constexpr int K = E::kChunk;
+        float s = fmaxf((float)(most / 127.0), 0x1p-126f);
+        const bool bad = !(most < INFINITY) || !(s < INFINITY);
         if (bad)
             s = __uint_as_float(0x7fc00000u);
-        if (!there)
-            return;
         if (j == 0)
             *scale = s;
         const float per = 1.f / s;
         // Next to binary32's ends (of y, of s and of 1 / s) errors are not relative.
-        const bool edge = top >= kInf || !(s > 0x1p-100f && s < 0x1p100f);
+        const bool edge = !(s > 0x1p-100f && s < 0x1p100f);
         constexpr float kMagic = 0x1.8p23f;          // t + kMagic has t's nearest whole number in its low bits
         each_chunk<TPR, C, E>(N, j, [&](int i, int n0) {
             float worst = 0.f;
@@ -236,7 +265,7 @@ struct Int8Row {
                 for (int e = 0; e < K; ++e) {
                     const float t = approx(i, e, n0) * per;
                     if (n0 + e < N && (!(fmaf(fabsf(t), 2.f * error(i, e), fabsf(t - __builtin_rintf(t))) < 0.5f) || unsure(i, e, n0) ||
-                                       (edge && t != 0.f)))
+                                       (edge && some(i, e))))
                         check |= 1u << e;
                 }
 #pragma unroll 1
@@ -274,7 +303,7 @@ void with_row(int N, Fn &&f)
     else if (chunks <= 512)
         call(std::integral_constant<int, 256>{}, std::integral_constant<int, 2>{});
     else if (chunks <= 1024)
-        call(std::integral_constant<int, 256>{}, std::integral_constant<int, 4>{});
+        call(std::integral_constant<int, 512>{}, std::integral_constant<int, 2>{});
     else if (chunks <= 2048)
         call(std::integral_constant<int, 1024>{}, std::integral_constant<int, 2>{});
     else

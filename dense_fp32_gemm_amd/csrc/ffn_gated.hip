@@ -251,7 +251,11 @@ int launch_tile(GatedArgs a, bool dma, hipStream_t stream, bool go)
     return launched();
 }
 
-// Tiles as for the plain product of 2N columns (see launch_grouped()).
+// Tiles as for the plain product of 2N columns (see launch_grouped()), but the 16-bit types take 256 x 256
+// tiles, which are cut, as soon as there are more 64 x 128 ones than compute units and they do not pad most groups by
+// half (us for 64 x 128 and 256 x 256 tiles: one group, 2 x 4096 columns, K = 2048: 256 rows 17.9 and
+// 21.4, 512 rows 27.4 and 23.9, 2048 rows 85 and 57; 2 x 1024 columns: 1024 rows 17.4 and 20.6, 1536 rows 25.2 and 21.2;
+// 16 groups: 2048 rows 30.6 and 32.4, 4096 rows 48.6 and 37.2).
 template <int GATE>
 int launch_gated(int type, const GatedArgs &a, bool dma, hipStream_t stream, bool go)
 {
@@ -264,9 +268,7 @@ int launch_gated(int type, const GatedArgs &a, bool dma, hipStream_t stream, boo
         } else if constexpr (E::kBytes == 4) {
             rc = launch_tile<E, GATE, 64, 64, 2, 2, 2, 0>(a, dma, stream, go);
         } else {
-            // Half a tile a group is lost on average.
-            const int64_t rows = 2 * (g.P / 256) + (g.G < g.P ? g.G : g.P);
-            if ((rows < kMaxTiles ? rows : kMaxTiles) * ceil_div(g.N, 128) * 5 >= 6 * gemm_f32_internal::current_device().cus)
+            if (g.P > 128 * (int64_t)g.G && ceil_div(g.P, 64) * ceil_div(g.N, 64) > gemm_f32_internal::current_device().cus)
                 rc = launch_tile<E, GATE, 256, 256, 2, 4, 2, 1>(a, dma, stream, go);
             else
                 rc = launch_tile<E, GATE, 64, 128, 2, 2, 3, 0>(a, dma, stream, go);

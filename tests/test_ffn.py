@@ -372,7 +372,8 @@ def test_gated_dense(dev, dtype, kind, T, K, N):
 
 @pytest.mark.parametrize("dtype", TYPES[1:], ids=IDS[1:])
 @pytest.mark.parametrize("pad", [0, 1], ids=["direct loads", "staged loads"])
-@pytest.mark.parametrize("T,E,k,K,N", [(4096, 1, 1, 96, 2048), (4200, 1, 1, 70, 2100), (2000, 2, 2, 64, 2200), (2300, 4, 2, 72, 1300), (4100, 1, 1, 64, 2300)])
+@pytest.mark.parametrize("T,E,k,K,N", [(4096, 1, 1, 96, 2048), (4200, 1, 1, 70, 2100), (2000, 2, 2, 64, 2200), (2300, 4, 2, 72, 1300), (4100, 1, 1, 64, 2300),
+                                       (520, 1, 1, 200, 2200), (300, 2, 2, 64, 2200)])
 def test_gated_large_tiles_whole_and_cut(dev, dtype, pad, T, E, k, K, N):
     g = seeded("gated large", T, E, k, K, N)
     offsets, order, _ = places(g, T, k, E) if E > 1 else (None, None, None)

@@ -11,4 +11,10 @@ row (binary32, bfloat16, half): routing to experts, the experts' products, their
 gradients and weighted sums, and low-rank adapters; ``binding`` has them as
 functions of torch tensors (``route``, ``expert_map``, ``grouped_matmul``,
 ``combine``, ``adapter_matmul`` and the ``*_grad`` ones).
+
+``include/gemm_f32_ffn.h`` adds the operators around a feed-forward block's products:
+the root-mean-square norm with the residual's addition and its gradient, rows in 8
+bits and their product with 8-bit weights, and the gated pair of projections, dense
+or by expert, with its gradient (``rms_norm``, ``rms_norm_int8``, ``rms_norm_grad``,
+``quantize``, ``int8_matmul``, ``gated_matmul``, ``gate_grad``).
 """

@@ -2,8 +2,11 @@
 // (include/gemm_f32_ffn.h).
 //
 //  * few rows: int8_few_kernel.  16 channels a workgroup, K over its waves,
-//    operands straight into registers.  Bound by the weights' bytes.
-//  * else int8_kernel: tiles as in rows_tile.h, both operands' k contiguous.
+//    operands straight into registers.  Bound by the weights' bytes and one load's way: 4096 x 4096, weights from
+//    memory, in a graph: one row 5.9 us, 16 rows 7.4; 8192 x 8192, one row 15.2 us, 4.4 TB/s.
+//  * else int8_kernel: tiles as in rows_tile.h, both operands' k contiguous.  8192 x 4096, K = 4096: 117 us, 2350 TOP/s;
+//    8192 x 8192, K = 8192: 431 us, 2550 TOP/s (the library's 8-bit product without scales 127 and 517).  Bound by the card's
+//    power and the sums' loop: 11 us a round of tiles and 1024 k; 14 us a round for its start and its stores.
 
 #include "ffn_gate.h"
 #include "rows_groups.h"

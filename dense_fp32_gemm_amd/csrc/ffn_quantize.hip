@@ -22,6 +22,9 @@ constexpr float gate_left()
     return GATE == GEMM_F32_GATE_SILU ? -80.f : GATE == GEMM_F32_GATE_GELU ? -12.f : -9.5f;
 }
 
+// 8192 x 4096 as they are, bf16, 101 MB: 24 us, 4.1 TB/s.  silu, 4096 x 8192 fp16, 168 MB: 47-50 us with warm caches, 55
+// from memory, 3.0-3.6 TB/s: a wave's chain (gates, the row's largest in binary64, division, borders) with 16 waves
+// a compute unit; gelu_tanh 53, gelu 85, whose binary32 error sends more elements through binary64.
 template <class E, bool VEC, int GATE, int TPR, int C>
 __global__ __launch_bounds__(kRowThreads<TPR>) void quantize_kernel(QuantizeArgs g)
 {

@@ -128,7 +128,7 @@ GEMM_F32_API int gemm_f32_expert_map(int S, int E, const int *index,
 /*
  * One product per group of rows.  Place p belongs to group g when
  * offsets[g] <= p < offsets[g+1] (offsets: G + 1 rising numbers within
- * 0..P).  Row r(p) of X is order[p] / per_row, or p when order is NULL; a
+ * 0..P; NULL with G = 1: all P places are in the one group).  Row r(p) of X is order[p] / per_row, or p when order is NULL; a
  * negative order[p] or a row outside 0..rows-1 reads as zeros.
  *
  *   gemm_f32_grouped:         Y(p,:)  = X(r(p),:) . W_g           [K] x [K x N]

@@ -69,7 +69,8 @@ __device__ inline void int8_tile(const Int8Args &g, int m0, int n0, int8_t *lds)
     const Along<I8, BN, NT> b(g.W + n0 * g.ldw, tid, g.K, g.ldw, g.N - n0,
                               [&](int, int r) { return n0 + r < g.N ? r * g.ldw : -1; });
     sum_panels<I8, DMA, S>(tile, g.K, a, b, lds, tid, wm, wn);
-    // all scales, then their use: loaded one by one between the stores they cost a tile of 4096 k a fourth of its time
+    // All scales, then their use (8192 x 4096, K = 4096: loaded one by one between the stores 171 us against 154); wide and
+    // narrow stores apart (merged, the compiler makes 2- and 4-byte pieces of the wide ones: 154 against 117).
     const int i = lane % 16, h = lane / 16, row = m0 + wm * (BM / WM) + i, col = n0 + wn * (BN / WN) + 4 * h;
     float scale[Ti::kFm];
     Channels channels[Ti::kFn];

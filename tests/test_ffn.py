@@ -631,6 +631,64 @@ def test_two_streams_at_once(dev):
         assert all(torch.equal(x, y) for x, y in zip(g, w))
 
 
+@pytest.mark.parametrize("dtype", TYPES, ids=IDS)
+def test_operands_that_start_on_odd_elements(dev, dtype):
+    """Bases one element past an aligned address, and operands of unlike strides, give what aligned ones give."""
+    g = seeded("odd base")
+    T, N = 70, 96
+
+    def shifted(t):
+        wide = torch.empty(t.numel() + 1, dtype=t.dtype, device=dev)[1:]
+        return wide.view(t.shape).copy_(t)
+
+    X, R, D = (normal(g, T, N, dtype=dtype).to(dev) for _ in range(3))
+    P = normal(g, T, 2 * N, dtype=dtype).to(dev)
+    w = shifted(1 + normal(g, N, scale=0.1).to(dev))
+    far = strided(R.cpu(), 8, dev)
+    for got, want in ((gb.rms_norm(shifted(X), w, residual=far), gb.rms_norm(X, w.clone(), residual=R)),
+                      (gb.rms_norm_int8(X, w, residual=shifted(R)), gb.rms_norm_int8(X, w.clone(), residual=R)),
+                      (gb.rms_norm_grad(shifted(D), X, w, dsum=far), gb.rms_norm_grad(D, X, w, dsum=R)),
+                      (gb.quantize(shifted(P), gate="silu"), gb.quantize(P, gate="silu")), (gb.quantize(shifted(X)), gb.quantize(X))):
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    # (a product may be rounded to the type from binary32, or, by a mixed instruction, from its exact value: equal
+    # only to within the bound, which counts both roundings)
+    oracle.close(gb.gate_grad(shifted(D), P), *oracle.gate_grad(D.cpu(), P.cpu(), "silu"), "dpre")
+    q, k = eight(g, T, N).to(dev), eight(g, 40, N).to(dev)
+    s, ks = torch.rand(T, device=dev), torch.rand(40, device=dev)
+    for rows in (5, T):
+        want = gb.int8_matmul(q[:rows], s[:rows], k, ks, dtype=dtype)
+        assert torch.equal(gb.int8_matmul(shifted(q[:rows]), s[:rows], shifted(k), shifted(ks), dtype=dtype), want)
+        out = torch.empty(rows * 40 + 1, dtype=dtype, device=dev)[1:].view(rows, 40)
+        assert torch.equal(gb.int8_matmul(q[:rows], s[:rows], k, ks, out=out), want)
+    W = normal(g, 1, N, 80, dtype=dtype, scale=0.1).to(dev)
+    want, bound, _, _ = oracle.gated(X.cpu().double(), W[0].cpu(), "silu", dtype)
+    oracle.close(gb.gated_matmul(shifted(X), shifted(W)), want, bound, "H")
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=IDS)
+def test_many_short_rows(dev, dtype):
+    """More rows than workgroups take at once, against the formulas in 64 bits on the GPU."""
+    T, N = 100003, 24
+    g = torch.Generator(device=dev).manual_seed(9)
+    X = torch.randn(T, 2 * N, generator=g, device=dev).to(dtype)
+    D = torch.randn(T, N, generator=g, device=dev).to(dtype)
+    x = X[:, :N].contiguous()
+    say("many rows", dtype)
+    s = x.double()
+    r = (s.square().mean(1, keepdim=True) + 1e-6).rsqrt()
+    oracle.close(gb.rms_norm(x), (s * r).cpu(), (s * r).cpu().abs() * (4 * oracle.U + oracle.STEP[dtype]) + oracle.TINY[dtype], "Y")
+    dX, dw, bound, size = oracle.norm_grad(D.cpu(), x.cpu(), None, 1e-6, None)
+    got, got_w = gb.rms_norm_grad(D, x)
+    oracle.close(got, dX, bound, "dX")
+    oracle.close(got_w, dw, (T // 256 + 5) * oracle.U * size, "dweight")
+    for (Q, scale), y in ((gb.quantize(x), s), (gb.rms_norm_int8(x), s * r),
+                          (gb.quantize(X, gate="gelu"), oracle.gate(s, "gelu") * X[:, N:].double())):
+        want = (y.abs().amax(1) / 127).float().clamp_min(2.0 ** -126)
+        assert torch.equal(scale, want) and torch.equal(Q, torch.round(y / want.double()[:, None]).to(torch.int8))
+    want, bound = oracle.gate_grad(D.cpu(), X.cpu(), "silu")
+    oracle.close(gb.gate_grad(D, X), want, bound, "dpre")
+
+
 def test_far_rows(dev):
     """Rows whose offsets pass 2^31 elements."""
     ld = (1 << 30) + 64

@@ -113,15 +113,17 @@ __device__ inline void load_floats(float (&w)[E::kChunk], const float *p, int le
 // Chunks of a row: f(i, column) for each of this thread's, C of them in registers (the
 // index is a constant) or as many as the row has.
 template <int TPR, int C, class E, class Fn>
-__device__ inline void each_chunk(int N, int j, Fn &&f)
+__host__ __device__ inline void each_chunk(int N, int j, Fn &&f)
 {
     if constexpr (C > 0) {
 #pragma unroll
         for (int i = 0; i < C; ++i)
             f(i, (i * TPR + j) * E::kChunk);
     } else {
-        for (int n = j * E::kChunk; n < N; n += TPR * E::kChunk)
-            f(0, n);
+        // unsigned: the last step goes past a row by up to 8192, more than sizes leave under 2^31
+        static_assert((uint32_t)kMaxSize + TPR * E::kChunk > (uint32_t)kMaxSize, "the last step stays in 32 bits");
+        for (uint32_t n = j * E::kChunk; n < (uint32_t)N; n += TPR * E::kChunk)
+            f(0, (int)n);
     }
 }
 

@@ -66,7 +66,8 @@ inline bool known_type(int type) { return type >= GEMM_F32_TYPE_F32 && type <= G
 inline bool aligned_to(const void *p, int bytes) { return ((uintptr_t)p & (uintptr_t)(bytes - 1)) == 0; }
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // The largest of the sizes that kernels count along: loops step past a size by up to a ring of
-// panels, a block of row offsets or a workgroup's columns, all under 4096, in 32 bits.
+// panels, a block of row offsets or a workgroup's columns, all at most 4096, in 32 bits.  (A longer
+// step counts in unsigned numbers: see each_chunk() in ffn_rows.h.)
 constexpr int kMaxSize = INT32_MAX - 4095;
 inline bool bad_size(int n) { return n < 0 || n > kMaxSize; }
 inline int at_least_one(int n) { return n > 1 ? n : 1; }

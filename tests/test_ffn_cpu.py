@@ -2,6 +2,7 @@
 sizes, the declared ABI, and the oracle's own gradients against differences."""
 import os
 import re
+import subprocess
 
 import pytest
 
@@ -182,6 +183,56 @@ def test_the_direct_loads_stand_in_one_file():
     for name in os.listdir(folder):
         if name.startswith("ffn_"):
             assert "load_lds" not in open(os.path.join(folder, name)).read(), name
+
+
+EACH_CHUNK = r"""
+#include <stdio.h>
+#include <stdlib.h>
+#include "ffn_rows.h"
+
+// Whether a thread's columns are those of its chunks, one after the other, and end with the row.
+template <int TPR, class E>
+static void walk(int N)
+{
+    const int step = TPR * E::kChunk, js[] = {0, 1, TPR / 2 - 1, TPR / 2, TPR - 1};
+    for (int j : js) {
+        int64_t next = j * E::kChunk;
+        ffn::each_chunk<TPR, 0, E>(N, j, [&](int, int n0) {
+            if (n0 != next || n0 >= N) {
+                printf("%d threads of %d elements, N = %d, thread %d: column %d after %lld\n", TPR, (int)E::kChunk, N, j, n0,
+                       (long long)(next - step));
+                exit(1);
+            }
+            next += step;
+        });
+        if (next < N)
+            exit(2);
+    }
+}
+
+int main()
+{
+    const int most = rows::kMaxSize;
+    for (int N : {0, 1, 20000, most - 8192, most - 4096, most - 4095, most - 1, most}) {
+        walk<1024, rows::F32>(N);
+        walk<1024, rows::Bf16>(N);
+        walk<1024, rows::F16>(N);
+    }
+    return 0;
+}
+"""
+
+
+def test_rows_of_the_largest_sizes_end(tmp_path):
+    """The loop over a row that does not fit the registers, on the host, up to the largest size that is taken
+    (-fwrapv: an index that passes 2^31 comes out negative, as on the GPU)."""
+    src, exe = tmp_path / "each_chunk.hip", tmp_path / "each_chunk"
+    src.write_text(EACH_CHUNK)
+    csrc = os.path.join(ROOT, "dense_fp32_gemm_amd", "csrc")
+    subprocess.run(["hipcc", "-O1", "-fwrapv", "-std=c++17", "--offload-host-only", "-I", csrc, "-I", os.path.join(ROOT, "include"), str(src),
+                    "-o", str(exe)], check=True, capture_output=True, timeout=300)
+    done = subprocess.run([str(exe)], capture_output=True, text=True, timeout=60)
+    assert done.returncode == 0, done.stdout
 
 
 # --- the oracle against itself --------------------------------------------------------

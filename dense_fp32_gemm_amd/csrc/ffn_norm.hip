@@ -116,14 +116,14 @@ __global__ __launch_bounds__(kRowThreads<TPR>) void norm_kernel(NormArgs g)
                 return (float)z[i].e[e] * w[i][e];
             };
             RowMost<TPR, C, E> most{g.N, j};
-            uint64_t top = most.approximate(product, sure);
+            uint64_t top = most.approximate(product);
             const double sum = over.sum_and_most(squares, top), scale = 1.0 / sqrt(sum / max(g.N, 1) + g.eps);
             const double largest = scale * most.exactly(over, top, 0x1p-23f, product,
                                                         [&](int i, int e, int) { return (double)pick(z[i], e) * (double)pick(w[i], e); },
                                                         sure, some);
             const float scale32 = (float)scale;
             if (there) {
-                Int8Row<TPR, C, E> row{g.N, j, (int8_t *)g.Y + t * g.ldy, false};
+                Int8Row<TPR, C, E> row{g.N, j, (int8_t *)g.Y + t * g.ldy, false, false};
                 row.write(largest, g.scale + t,
                           [&](int i, int e, int n0) {
                               open(i, n0);

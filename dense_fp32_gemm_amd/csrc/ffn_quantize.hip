@@ -25,12 +25,14 @@ constexpr float gate_left()
 // 8192 x 4096 as they are, bf16, 101 MB: 24 us, 4.1 TB/s.  silu, 4096 x 8192 fp16, 168 MB: 47-50 us with warm caches, 55
 // from memory, 3.0-3.6 TB/s: a wave's chain (gates, the row's largest in binary64, division, borders) with 16 waves
 // a compute unit; gelu_tanh 53, gelu 85, whose binary32 error sends more elements through binary64.
+// 16-bit types: registers for three waves a SIMD, which gelu's two chunks otherwise just miss in some variants (169 of
+// 168; 8192 x 4096 bf16 with one too many: 79 us, 64 without).  binary32 fits four by itself.
 template <class E, bool VEC, int GATE, int TPR, int C>
-__global__ __launch_bounds__(kRowThreads<TPR>) void quantize_kernel(QuantizeArgs g)
+__global__ __launch_bounds__(kRowThreads<TPR>, E::kBytes == 2 && TPR < 1024 ? 3 : 1) void quantize_kernel(QuantizeArgs g)
 {
     using T = typename E::T;
     constexpr int kRows = kRowsAtOnce<TPR>, K = E::kChunk, kC = C > 0 ? C : 1;
-    constexpr bool kGated = GATE != GEMM_F32_GATE_NONE;
+    constexpr bool kGated = GATE != GEMM_F32_GATE_NONE, kSmallGates = !std::is_same<E, F16>::value;   // half has none under kSmall
     __shared__ typename RowJoin<TPR>::Pair slots[2][TPR / kWave];
     const int j = threadIdx.x % TPR;
     RowJoin<TPR> over{slots};
@@ -46,11 +48,18 @@ __global__ __launch_bounds__(kRowThreads<TPR>) void quantize_kernel(QuantizeArgs
             if constexpr (kGated)
                 b[i].raw = load_chunk<E, VEC>(x + g.N + n0, left);
         };
+        float lowest = 0.f, heavy = 0.f;             // the smallest gate, the largest of what they gate
         auto open = [&](int i) {                     // the chunk's values
             if constexpr (kGated)
 #pragma unroll
-                for (int e = 0; e < K; ++e)
-                    y[i][e] = gate<GATE>((float)a[i].e[e]) * (float)b[i].e[e];
+                for (int e = 0; e < K; e += 2) {
+                    const float p = (float)a[i].e[e], q = (float)a[i].e[e + 1], u = (float)b[i].e[e], v = (float)b[i].e[e + 1];
+                    y[i][e] = gate<GATE>(p) * u;
+                    y[i][e + 1] = gate<GATE>(q) * v;
+                    lowest = min3(lowest, p, q);
+                    if (kSmallGates)
+                        heavy = max3(heavy, fabsf(u), fabsf(v));
+                }
         };
         if constexpr (C > 0) {
             each_chunk<TPR, C, E>(g.N, j, load);
@@ -79,13 +88,31 @@ __global__ __launch_bounds__(kRowThreads<TPR>) void quantize_kernel(QuantizeArgs
         auto unsure = [&](int i, int e, int) { return kGated && (float)a[i].e[e] < gate_left<GATE>(); };
         auto some = [&](int i, int e) { return (float)a[i].e[e] != 0.f; };
         RowMost<TPR, C, E> most{g.N, j};
-        uint64_t top = most.approximate(approx, unsure);
+        uint64_t top = most.approximate(approx);
+        if constexpr (kGated && kSmallGates) {
+            // (the row's largest is that of a wave at least)
+            bool small = false;
+            if (__ballot(heavy * kHeavy > __uint_as_float((uint32_t)top)) != 0) {
+                each_chunk<TPR, C, E>(g.N, j, [&](int i, int n0) {
+#pragma unroll
+                    for (int e = 0; e < K; ++e) {
+                        approx(i, e, n0);
+                        const float x = fabsf((float)a[i].e[e]);         // act(x) is about x / 2
+                        small |= x != 0.f && x < kSmall;
+                    }
+                });
+                if (__ballot(small) != 0)
+                    top |= 1ull << 32;               // above every magnitude; exactly() then needs none
+            }
+        }
         over.most(top);
+        most.every = top >> 32 != 0;
         double largest = (double)__uint_as_float((uint32_t)top);
+        most.loose = kGated && lowest < gate_left<GATE>();
         if constexpr (kGated)
             largest = most.exactly(over, top, kGateFar, approx, exact, unsure, some);
         if (there) {
-            Int8Row<TPR, C, E> row{g.N, j, g.Q + t * g.ldq, most.loose};
+            Int8Row<TPR, C, E> row{g.N, j, g.Q + t * g.ldq, most.loose, most.every};
             row.write(largest, g.scale + t, approx, exact,
                       [&](int i, int e) { return kGated ? gate_error<GATE>((float)a[i].e[e]) : 0x1p-23f; }, unsure, some);
         }

@@ -159,8 +159,29 @@ __device__ inline float pick(const float (&c)[K], int e)
 //   approx(i, e, n0)  the i-th chunk's element e (column n0 + e); 0 past the row's end
 //   error(i, e)       how far that may be off, relative, at most most_error
 //   exact(i, e, n0)   the same in binary64; e is no constant (see pick())
-//   unsure(i, e, n0)  whether approx may be off by more
+//   unsure(i, e, n0)  whether approx may be off by more; asked where `loose` says that one of the thread's may be
 //   some(i, e)        whether exact() may be other than 0
+//
+// A factor of approx under binary32's normal numbers is off by up to 2^-150 instead, and the value by that times the
+// other factor.  In steps of the scale, 2^-7 of the row's largest, that is under 2^-25, beside errors of twice
+// error() (a value is looked at from half a step on), unless the other factor is beyond 2^118 of the row's largest.
+// There `every` element that may be other than 0 is computed in binary64.
+constexpr float kHeavy = 0x1p-118f, kSmall = 0x1p-120f;
+// The largest and the smallest of three numbers in one instruction (fmaxf() first quiets NaN); NaN if one is.
+__device__ inline float max3(float a, float b, float c) { return __builtin_elementwise_maximum(__builtin_elementwise_maximum(a, b), c); }
+__device__ inline float min3(float a, float b, float c) { return __builtin_elementwise_minimum(__builtin_elementwise_minimum(a, b), c); }
+
+// Which of a chunk's first `left` elements are so.
+template <class E, class Is>
+__device__ inline uint32_t ones(int left, Is &&is)
+{
+    uint32_t all = 0;
+#pragma unroll
+    for (int e = 0; e < E::kChunk; ++e)
+        if (e < left && is(e))
+            all |= 1u << e;
+    return all;
+}
 
 // A row's largest magnitude in two steps, as whole numbers (NaN above infinity above every number):
 // that of approx() among the thread's elements, of which the caller makes the row's, and from
@@ -169,18 +190,17 @@ template <int TPR, int C, class E>
 struct RowMost {
     int N, j;
     uint32_t mine = 0;
-    bool loose = false;
+    bool loose = false;                              // whether any of the thread's elements is unsure
+    bool every = false;                              // the same in all of the row's threads
 
     // The wave's.
-    template <class Approx, class Unsure>
-    __device__ inline uint64_t approximate(Approx &&approx, Unsure &&unsure)
+    template <class Approx>
+    __device__ inline uint64_t approximate(Approx &&approx)
     {
         each_chunk<TPR, C, E>(N, j, [&](int i, int n0) {
 #pragma unroll
-            for (int e = 0; e < E::kChunk; ++e) {
+            for (int e = 0; e < E::kChunk; ++e)
                 mine = max(mine, __float_as_uint(approx(i, e, n0)) & 0x7fffffffu);
-                loose |= unsure(i, e, n0);
-            }
         });
         return wave_max(mine);
     }
@@ -192,7 +212,7 @@ struct RowMost {
         // Below `near` nothing is the largest.  Next to binary32's smallest numbers errors are not relative.
         const uint32_t top = (uint32_t)row_top;
         const float near = top > 0x7f800000u ? INFINITY : __uint_as_float(top) * (1.f - 4.f * most_error);
-        const bool small = near < 0x1p-100f;
+        const bool small = near < 0x1p-100f || every;
         uint64_t most = 0;
         if (!(__uint_as_float(mine) < near) || loose || small)
             each_chunk<TPR, C, E>(N, j, [&](int i, int n0) {
@@ -200,9 +220,11 @@ struct RowMost {
 #pragma unroll
                 for (int e = 0; e < E::kChunk; ++e) {
                     const bool large = !(fabsf(approx(i, e, n0)) < near);
-                    if (n0 + e < N && (small ? some(i, e) : large || unsure(i, e, n0)))
+                    if (n0 + e < N && (small ? some(i, e) : large))
                         check |= 1u << e;
                 }
+                if (loose)                           // few waves have any
+                    check |= ones<E>(N - n0, [&](int e) { return unsure(i, e, n0); });
 #pragma unroll 1
                 for (; check != 0; check &= check - 1)
                     most = max64(most, __builtin_bit_cast(uint64_t, fabs(exact(i, (int)__builtin_ctz(check), n0))));
@@ -219,7 +241,7 @@ template <int TPR, int C, class E>
 struct Int8Row {
     int N, j;
     int8_t *q;                                       // the row's start
-    bool loose;                                      // whether any of the thread's elements is unsure
+    bool loose, every;                               // as RowMost's (every: of this thread)
 
     template <class Approx, class Exact, class Error, class Unsure, class Some>
     __device__ inline void write(double most, float *scale, Approx &&approx, Exact &&exact, Error &&error, Unsure &&unsure, Some &&some)
@@ -233,7 +255,7 @@ struct Int8Row {
             *scale = s;
         const float per = 1.f / s;
         // Next to binary32's ends (of y, of s and of 1 / s) errors are not relative.
-        const bool edge = !(s > 0x1p-100f && s < 0x1p100f);
+        const bool edge = !(s > 0x1p-100f && s < 0x1p100f) || every;
         constexpr float kMagic = 0x1.8p23f;          // t + kMagic has t's nearest whole number in its low bits
         each_chunk<TPR, C, E>(N, j, [&](int i, int n0) {
             float worst = 0.f;
@@ -266,10 +288,11 @@ struct Int8Row {
 #pragma unroll
                 for (int e = 0; e < K; ++e) {
                     const float t = approx(i, e, n0) * per;
-                    if (n0 + e < N && (!(fmaf(fabsf(t), 2.f * error(i, e), fabsf(t - __builtin_rintf(t))) < 0.5f) || unsure(i, e, n0) ||
-                                       (edge && some(i, e))))
+                    if (n0 + e < N && (!(fmaf(fabsf(t), 2.f * error(i, e), fabsf(t - __builtin_rintf(t))) < 0.5f) || (edge && some(i, e))))
                         check |= 1u << e;
                 }
+                if (loose)
+                    check |= ones<E>(N - n0, [&](int e) { return unsure(i, e, n0); });
 #pragma unroll 1
                 for (; check != 0; check &= check - 1) {
                     const int e = (int)__builtin_ctz(check);

@@ -250,6 +250,28 @@ def test_quantize_rows_of_every_kind(dev, kind, N):
     assert torch.equal(Q.cpu(), want_q)
 
 
+# Factors that are no normal binary32 numbers (and keep few of their digits there) times large ones: the product's
+# rounding shows every digit that was lost.
+@pytest.mark.parametrize("dtype", TYPES[:2], ids=IDS[:2])
+@pytest.mark.parametrize("kind", GATES)
+@pytest.mark.parametrize("N", [24, 1500, 4096, 40000])
+def test_quantize_small_gates_of_large_numbers(dev, dtype, kind, N):
+    g = seeded("small gates", N)
+    X = normal(g, 9, 2 * N)
+    for t, (gate, other) in enumerate([(-140, 60), (-134, 60), (-138, 60), (-141, 60), (-130, 60), (-128, 50), (-124, 40), (-145, 120)]):
+        X[t, :N] *= 2.0 ** gate
+        X[t, N:] *= 2.0 ** other
+    X[1, :N:3] = 0.0
+    # 1.5 of the smallest number (2 if rounded) times 2^100, beside 1.7 of an ordinary gate: the row's largest is the other
+    X[8] = 0.0
+    X[8, 1], X[8, N + 1], X[8, N - 2], X[8, 2 * N - 2] = 3 * 2.0 ** -149, 2.0 ** 100, 20.0, 1.7 * 2.0 ** -49 / 20
+    X = X.to(dtype)
+    say("small gates", kind, N, dtype)
+    Q, scale = gb.quantize(X.to(dev), gate=kind)
+    want_q, want_scale = oracle.int8_rows(oracle.gate(X[:, :N].double(), kind) * X[:, N:].double())
+    assert torch.equal(scale.cpu(), want_scale) and torch.equal(Q.cpu(), want_q)
+
+
 # --- 8-bit product -----------------------------------------------------------------------
 def eight(g, T, K):
     return torch.randint(-128, 128, (T, K), generator=g, dtype=torch.int8)

@@ -121,14 +121,12 @@ __global__ __launch_bounds__(kRowThreads<TPR>) void norm_kernel(NormArgs g)
             const double largest = scale * most.exactly(over, top, 0x1p-23f, product,
                                                         [&](int i, int e, int) { return (double)pick(z[i], e) * (double)pick(w[i], e); },
                                                         sure, some);
-            const float scale32 = (float)scale;
+            const float scale32 = (float)scale, most_product = __uint_as_float((uint32_t)top);
             if (there) {
-                Int8Row<TPR, C, E> row{g.N, j, (int8_t *)g.Y + t * g.ldy, false, false};
-                row.write(largest, g.scale + t,
-                          [&](int i, int e, int n0) {
-                              open(i, n0);
-                              return (float)z[i].e[e] * scale32 * w[i][e];
-                          },
+                // S weight first: where the row's largest is an ordinary number, none of the products is infinite, and one that is
+                // no normal number is nothing beside a step.  (S r may be none where a large weight makes it count.)
+                Int8Row<TPR, C, E> row{g.N, j, (int8_t *)g.Y + t * g.ldy, false, !(most_product > 0x1p-99f && most_product < INFINITY)};
+                row.write(largest, g.scale + t, [&](int i, int e, int n0) { return product(i, e, n0) * scale32; },
                           [&](int i, int e, int) { return (double)pick(z[i], e) * (double)pick(w[i], e) * scale; },
                           [](int, int) { return 0x1p-21f; }, sure, some);
             }

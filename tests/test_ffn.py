@@ -272,6 +272,39 @@ def test_quantize_small_gates_of_large_numbers(dev, dtype, kind, N):
     assert torch.equal(scale.cpu(), want_scale) and torch.equal(Q.cpu(), want_q)
 
 
+@pytest.mark.parametrize("dtype", TYPES[:2], ids=IDS[:2])
+@pytest.mark.parametrize("N", [24, 1500, 4096, 40000])
+def test_rms_norm_int8_small_elements_of_large_weights(dev, dtype, N):
+    """One element of each row sets its root mean square; the others, under binary32's normal numbers after it, set its scale."""
+    g = seeded("large weights", N)
+    X, w = normal(g, 5, N), (1 + normal(g, N, scale=0.2)) * 2.0 ** 60
+    for t, small in enumerate((-36, -40, -42, -44, -30)):
+        X[t] *= 2.0 ** small
+    X[:, N // 2] = 2.0 ** 100
+    w[N // 2] = 2.0 ** -88
+    X = X.to(dtype)
+    say("large weights", N, dtype)
+    Q, scale = gb.rms_norm_int8(X.to(dev), w.to(dev))
+    want_q, want_scale = oracle.int8_rows(oracle.normed(X, w, 1e-6))
+    assert torch.equal(scale.cpu(), want_scale) and torch.equal(Q.cpu(), want_q)
+
+
+@pytest.mark.parametrize("dtype", TYPES[:2], ids=IDS[:2])
+@pytest.mark.parametrize("by", [60, -60])
+@pytest.mark.parametrize("N", [24, 4096, 40000])
+def test_rms_norm_int8_products_beyond_binary32(dev, dtype, by, N):
+    """S times its weight passes binary32's ends on either side, and the row's factor brings it back."""
+    g = seeded("far products", N, by)
+    X, w = normal(g, 6, N), (1 + normal(g, N, scale=0.2)) * 2.0 ** by
+    for t, size in enumerate((80, 100, 66, -60, -70, -80)):
+        X[t] *= 2.0 ** size
+    X = X.to(dtype)
+    say("far products", by, N, dtype)
+    Q, scale = gb.rms_norm_int8(X.to(dev), w.to(dev), eps=2.0 ** -120)
+    want_q, want_scale = oracle.int8_rows(oracle.normed(X, w, 2.0 ** -120))
+    assert torch.equal(scale.cpu(), want_scale) and torch.equal(Q.cpu(), want_q)
+
+
 # --- 8-bit product -----------------------------------------------------------------------
 def eight(g, T, K):
     return torch.randint(-128, 128, (T, K), generator=g, dtype=torch.int8)

@@ -341,6 +341,23 @@ def test_int8_large_tiles_whole_and_cut(dev, pad, T, N, K):
     check_int8(dev, seeded("int8 large", T, N, K), T, N, K, pad, torch.bfloat16, False)
 
 
+# More panels of 128 k than twice a ring has, the last one partial: 32 x 64 (four in the ring), 64 x 64 (four), 64 x 128
+# (three), 256 x 256 whole (two) with a last round cut in four (four), and cut in two (three).
+DEEP_INT8 = [(100, 130, 2100), (520, 2050, 1400), (1100, 2100, 1100), (4200, 4100, 1300), (2600, 2600, 1300)]
+
+
+@pytest.mark.parametrize("pad", [0, 1, 4], ids=["rows as long as they are", "staged loads", "direct loads"])
+@pytest.mark.parametrize("T,N,K", DEEP_INT8)
+def test_int8_panels_in_turn(dev, pad, T, N, K):
+    """Sums of many panels, exact: whole numbers under 2^24, every k a part of each (no element is 0)."""
+    g = seeded("int8 deep", T, N, K)
+    Q, W = (torch.where(x < 0, x, x + 1) for x in (torch.randint(-64, 64, s, generator=g, dtype=torch.int8) for s in ((T, K), (N, K))))
+    say("int8 panels", T, N, K, pad)
+    got = gb.int8_matmul(strided(Q, pad, dev, 99), torch.ones(T, device=dev), strided(W, pad, dev, -77), torch.ones(N, device=dev),
+                         dtype=torch.float32)
+    assert torch.equal(got.cpu(), (Q.double() @ W.double().t()).float())
+
+
 @pytest.mark.parametrize("T", [3, 40, 100])
 def test_int8_sums_are_exact_at_the_largest_depth(dev, T):
     """-128 times -128, 131071 of them: just inside 32 bits; one less in one place."""
@@ -437,6 +454,32 @@ def test_gated_large_tiles_whole_and_cut(dev, dtype, pad, T, E, k, K, N):
     check_gated(dev, dtype, pad, X, W, offsets, order, k, "silu")
 
 
+# More panels than twice a ring has, the last one partial.  16-bit types (64 k a panel): 32 x 64 (a ring of four), 64 x 128
+# (three), 256 x 256 cut in four (four), in two (three), whole (two); binary32 (32 k): 32 x 64 and 64 x 64, whose sums
+# are folded every 512 k.
+DEEP_GATED = [(20, 40, 1100), (200, 200, 900), (520, 2200, 700), (1000, 2200, 650), (4200, 2100, 650)]
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=IDS)
+@pytest.mark.parametrize("pad", [0, 1], ids=["direct loads", "staged loads"])
+@pytest.mark.parametrize("T,N,K", DEEP_GATED + [(300, 100, 1700)])
+def test_gated_panels_in_turn(dev, dtype, pad, T, N, K):
+    """Sums of many panels, exact: whole numbers, every k a part of each (no element is 0)."""
+    if dtype == torch.float32:
+        T, N = min(T, 500), min(N, 300)
+    g = seeded("gated deep", T, N, K)
+    X, W = (torch.tensor([-2.0, -1.0, 1.0, 2.0])[torch.randint(4, s, generator=g)].to(dtype) for s in ((T, K), (1, K, 2 * N)))
+    say("gated panels", T, N, K, pad, dtype)
+    H, pre = gb.gated_matmul(strided(X, pad, dev), strided(W, pad, dev), save=True)
+    sums = X.double() @ W[0].double()
+    assert torch.equal(pre.cpu(), sums.to(dtype))
+    want = oracle.gate(sums[:, :N], "silu") * sums[:, N:]
+    # (half: from 65520 on, half a step past its largest number, infinities)
+    want = torch.where(want.to(dtype).isinf(), want.to(dtype).double(), want)
+    err = (oracle.GATE_ERROR["silu"] + 2 * oracle.U) * want.abs() + oracle.LOST_VALUE * (1 + sums[:, N:].abs())
+    oracle.close(H, want, err + oracle.STEP[dtype] * (want.abs() + err) + oracle.TINY[dtype], "H")
+
+
 @pytest.mark.parametrize("dtype", TYPES, ids=IDS)
 @pytest.mark.parametrize("rows", [3, 40, 300])
 def test_gated_infinities_stay_in_their_places(dev, dtype, rows):
@@ -474,6 +517,31 @@ def test_gate_grad(dev, dtype, kind, pad, P, N):
     assert (full[:, 2 * N:] == 7.0).all()
     gb.gate_grad(dH.to(dev), p, gate=kind, out=p)
     assert torch.equal(p, full[:, :2 * N])
+
+
+@pytest.mark.parametrize("kind", GATES)
+def test_gates_and_slopes_to_a_few_steps(dev, kind):
+    """act(g) and act'(g) in binary32, where nothing underflows, to the half steps that their steps leave.
+
+    The exponential: its argument's part under binary32 is made up for; 2^x as the hardware gives it 2 half steps, the
+    factor, their product 1 each: 4.  The reciprocal 2.
+      silu       exponential, 1 + e, reciprocal, g s: 8.  Slope s (1 + g (1 - s)): s 7, 1 - s 7, sum and product 2: 16
+      gelu       g^2 / 2 is off by a half step of itself, the exponential by g^2 / 2 half steps for that; t = 1 / (1 + 0.4 z):
+                 constant, sum, reciprocal 4, which counts up to 1.6 times; the polynomial 6 (whose fit is 1); three products:
+                 under 24 with the exponential's 4, and g^2 / 2.  Slope p + g e^(-g^2 / 2) / sqrt(2 pi): the same
+      gelu_tanh  v = g (kA + kB g^2): two constants and three steps, 5 |v| half steps of the exponential; else as silu, 10.
+                 Slope s + g s (1 - s) v': s and 1 - s each so, and six steps: 24 + 10 |v|
+    """
+    g = torch.linspace(-9, 12, 400001)
+    n = g.numel()
+    pre = torch.cat([g, torch.ones(n)])[None]
+    got = gb.gate_grad(torch.ones(1, n, device=dev), pre.to(dev), gate=kind).cpu().double()[0]
+    x = g.double()
+    p, q = oracle.gate_parts(x, kind)
+    v = math.sqrt(8 / math.pi) * (x + 0.044715 * x ** 3)
+    value, slope = {"silu": (8.0, 16.0), "gelu": (24 + x * x, 24 + x * x), "gelu_tanh": (10 + 5 * v.abs(), 24 + 10 * v.abs())}[kind]
+    oracle.close(got[n:], x * p, oracle.U * value * (x * p).abs(), "value")
+    oracle.close(got[:n], p + q, oracle.U * (slope + 1) * (p.abs() + q.abs()), "slope")
 
 
 @pytest.mark.parametrize("kind", GATES)
@@ -742,6 +810,34 @@ def test_many_short_rows(dev, dtype):
         assert torch.equal(scale, want) and torch.equal(Q, torch.round(y / want.double()[:, None]).to(torch.int8))
     want, bound = oracle.gate_grad(D.cpu(), X.cpu(), "silu")
     oracle.close(gb.gate_grad(D, X), want, bound, "dpre")
+
+
+# Rows of several waves, more of them than the device's workgroups take at once (eight of 256 threads a compute unit): a
+# workgroup's second row meets the LDS slots that its first one used.
+@pytest.mark.parametrize("dtype", TYPES, ids=IDS)
+@pytest.mark.parametrize("chunks,threads", [(138, 128), (263, 256), (520, 512), (1030, 1024), (2060, 1024)])
+def test_second_rows_of_several_waves(dev, dtype, chunks, threads):
+    N = chunks * 16 // torch.finfo(dtype).bits * 8
+    T = torch.cuda.get_device_properties(dev).multi_processor_count * 8 * 256 // threads * 9 // 8 + 3
+    g = torch.Generator(device=dev).manual_seed(chunks)
+    X = torch.randn(T, 2 * N, generator=g, device=dev)
+    X *= 2.0 ** (torch.arange(T, device=dev) % 7 - 3)[:, None]           # unlike rows side by side
+    X = X.to(dtype)
+    x, R = X[:, :N].contiguous(), X[:, N:].contiguous()
+    w = 1 + torch.randn(N, generator=g, device=dev) * 0.2
+    say("second rows", T, N, dtype)
+    S = (x.double() + R.double()).to(dtype)
+    s = S.double()
+    want = s * (s.square().mean(1, keepdim=True) + 1e-5).rsqrt() * w.double()
+    got, sum_ = gb.rms_norm(x, w, eps=1e-5, residual=R)
+    assert torch.equal(sum_, S)
+    room = want.abs() * (4 * oracle.U + oracle.STEP[dtype]) + oracle.TINY[dtype]
+    assert ((got.double() - want).abs() <= room).all()
+    for (Q, scale), y in ((gb.rms_norm_int8(x, w, eps=1e-5, residual=R)[:2], want), (gb.quantize(x), x.double()),
+                          (gb.quantize(X, gate="silu"), oracle.gate(x.double(), "silu") * R.double()),
+                          (gb.quantize(X, gate="gelu_tanh"), oracle.gate(x.double(), "gelu_tanh") * R.double())):
+        top = (y.abs().amax(1) / 127).float()
+        assert torch.equal(scale, top) and torch.equal(Q, torch.round(y / top.double()[:, None]).to(torch.int8))
 
 
 def test_far_rows(dev):

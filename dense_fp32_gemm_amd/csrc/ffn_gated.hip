@@ -180,7 +180,7 @@ __global__ __launch_bounds__(WM *WN *kWave, 2) void gated_kernel(GatedArgs args)
         part.tile = die_contiguous(blockIdx.x, total, g.xcds);
     if (part.tile < 0)
         return;                                      // the whole workgroup
-    const Place p = locate(g, BM, part.tile);
+    const Place p = locate(g, BM, BM == 256, part.tile);
     const int m0 = p.lo + p.tm * BM, n0 = p.tn * (BN / 2);
     if (!CUT || part.cut == 1)
         gated_tile<E, GATE, BM, BN, WM, WN, S, DMA>(args, p.group, m0, p.hi, n0, lds);

@@ -123,7 +123,7 @@ __global__ __launch_bounds__(WM *WN *kWave, 2) void grouped_kernel(GroupedArgs g
         p.lo = __builtin_amdgcn_readfirstlane(p.lo);
         p.hi = __builtin_amdgcn_readfirstlane(p.hi);
     } else {
-        p = locate(g, BM, part.tile);
+        p = locate(g, BM, BM == 256 && (OP == kForward || g.G == 1), part.tile);
     }
     const int m0 = (OP == kGradW ? 0 : p.lo) + p.tm * BM, m_end = OP == kGradW ? g.M : p.hi, n0 = p.tn * BN;
     if (!CUT || part.cut == 1)

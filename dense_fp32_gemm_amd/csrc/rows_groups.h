@@ -60,26 +60,33 @@ __device__ inline int row_tiles(const GroupedArgs &g, int bm)
     return __builtin_amdgcn_readfirstlane(total);
 }
 
-// Row tiles of a band: a die's 32 tiles that run side by side are then 4 x 8 and share rows and columns in
-// its L2 (bf16, 8192 rows, 8192 columns, K = 2048: 231 us; 8: 233, whole columns: 247; the gradient of X
-// 197, 199, 211; 65536 slots over 64 experts, 2048 -> 1024: 293, 299, 296).
+// Row tiles of a band of 256 x 256 tiles: a die's 32 tiles that run side by side are then 4 x 8 and share rows and
+// columns in its L2 (bf16, 8192 rows, 8192 columns, K = 2048: 232 us; bands of 8: 233, whole columns: 242; the gradient
+// of X 195 and 204; 32768 rows over 8 groups, 2048 x 2048: 262 and 272).  Whole columns, one after the other, are as
+// good or better up to two bands of rows, in the gradient of X of several groups (32768 over 8: 250 us, banded 260;
+// 65536 over 64, 2048 -> 1024: 320 and 335), and with 64 x 128 tiles (1500 rows over 8, 2048 x 2048: 24.7 and 28.2).
 constexpr int kBand = 4;
 
 // The r-th tile of a group that has `rows` row tiles.
-__device__ inline Place banded(const GroupedArgs &g, Place p, int r, int rows)
+__device__ inline Place tile_of(const GroupedArgs &g, bool banded, Place p, int r, int rows)
 {
+    if (!banded || rows <= 2 * kBand) {
+        p.tn = r / rows;
+        p.tm = r - p.tn * rows;
+        return p;
+    }
     const int from = r / (kBand * g.tiles_n) * kBand, q = r - from * g.tiles_n, high = min(kBand, rows - from);
     p.tn = high == kBand ? q / kBand : q / high;     // (the usual case without a division)
     p.tm = from + q - p.tn * high;
     return p;
 }
 
-// Tile t, counted group by group, band by band within a group and column by column within a
+// Tile t, counted group by group, band by band within a group if they are banded, and column by column within a
 // band.  Every wave of the workgroup computes it for itself.
-__device__ inline Place locate(const GroupedArgs &g, int bm, int t)
+__device__ inline Place locate(const GroupedArgs &g, int bm, bool banded, int t)
 {
     if (g.offsets == nullptr)
-        return banded(g, Place{0, 0, g.P, 0, 0}, t, (g.P + bm - 1) / bm);
+        return tile_of(g, banded, Place{0, 0, g.P, 0, 0}, t, (g.P + bm - 1) / bm);
     const int lane = threadIdx.x % kWave;
     int before = 0;                                  // row tiles of the groups before
     Place p{0, 0, 0, 0, 0};
@@ -99,7 +106,7 @@ __device__ inline Place locate(const GroupedArgs &g, int bm, int t)
             const int at = (int)__builtin_ctzll(past);
             const int mine = __builtin_amdgcn_readlane(n, at);
             const int first = before + __builtin_amdgcn_readlane(scan, at) - mine;
-            p = banded(g, Place{g0 + at, __builtin_amdgcn_readlane(a, at), __builtin_amdgcn_readlane(b, at), 0, 0},
+            p = tile_of(g, banded, Place{g0 + at, __builtin_amdgcn_readlane(a, at), __builtin_amdgcn_readlane(b, at), 0, 0},
                        t - first * g.tiles_n, mine);
             break;
         }

@@ -480,6 +480,29 @@ def test_gated_panels_in_turn(dev, dtype, pad, T, N, K):
     oracle.close(H, want, err + oracle.STEP[dtype] * (want.abs() + err) + oracle.TINY[dtype], "H")
 
 
+@pytest.mark.parametrize("dtype", TYPES[1:], ids=IDS[1:])
+@pytest.mark.parametrize("bounds", [[0, 6100], [0, 2500, 6100], [5, 2000, 2000, 5900], [0, 700, 6100]])
+def test_tiles_of_long_and_short_groups(dev, dtype, bounds):
+    """256 x 256 tiles of groups of up to 24 row tiles, in bands and in whole columns, each once: whole numbers, exact."""
+    G, P, K, N = len(bounds) - 1, 6100, 70, 1800
+    g = seeded("bands", bounds)
+    few = torch.tensor([-2.0, -1.0, 1.0, 2.0])
+    X, W = (few[torch.randint(4, s, generator=g)].to(dtype) for s in ((P, K), (G, K, N)))
+    off = None if bounds == [0, P] else torch.tensor(bounds, dtype=torch.int32, device=dev)
+    say("bands", bounds, dtype)
+    x, w = X.to(dev), W.to(dev)
+    Y = gb.grouped_matmul(x, w, off, out=torch.full((P, N), 7.0, dtype=dtype, device=dev))
+    pre = gb.gated_matmul(x, w, off, save=True)[1]
+    # the gradient of X has K columns: the products' roles changed about
+    dX = gb.grouped_grad_x(x, w.transpose(1, 2).contiguous(), off, out=torch.full((P, N), 7.0, dtype=dtype, device=dev))
+    for e in range(G):
+        lo, hi = bounds[e], bounds[e + 1]
+        want = (X[lo:hi].double() @ W[e].double()).to(dtype)
+        assert torch.equal(Y[lo:hi].cpu(), want) and torch.equal(pre[lo:hi].cpu(), want) and torch.equal(dX[lo:hi].cpu(), want)
+    for out in (Y, dX):
+        assert (out[:bounds[0]] == 7.0).all() and (out[bounds[-1]:] == 7.0).all()
+
+
 @pytest.mark.parametrize("dtype", TYPES, ids=IDS)
 @pytest.mark.parametrize("rows", [3, 40, 300])
 def test_gated_infinities_stay_in_their_places(dev, dtype, rows):

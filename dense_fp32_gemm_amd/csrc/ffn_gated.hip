@@ -27,8 +27,8 @@ struct GatedArgs {
 };
 
 // Columns of a panel: each wave's BN / WN are half the gate's, half the others'.  16-bit types:
-// the first blocks of 16 and the rest.  binary32: four and four in turn, as a lane holds four
-// neighbouring ones of the V blocks that are read together.
+// the first blocks of 16 and the rest.  binary32: four and four in turn, as a lane holds eight
+// neighbouring ones of the two blocks that are read together (no tile here reads four).
 template <class E, int BN, int NT, int WN>
 struct AcrossPair : Across<E, BN, NT> {
     using Base = Across<E, BN, NT>;
@@ -68,13 +68,6 @@ __device__ inline void each_pair(const Ti &tile, int wm, int wn, int lane, Fn &&
 #pragma unroll
             for (int n = 0; n < Ti::kFn / 2; ++n)
                 f(row, col + 16 * n + 4 * h, a[n], a[n + Ti::kFn / 2]);
-        } else if constexpr (Ti::Fb::kV == 4) {
-#pragma unroll
-            for (int n = 0; n < Ti::kFn; n += 4)
-#pragma unroll
-                for (int r = 0; r < 4; r += 2)
-                    f(row, col + 8 * n + 8 * h + 2 * r, f32x4{a[n][r], a[n + 1][r], a[n + 2][r], a[n + 3][r]},
-                      f32x4{a[n][r + 1], a[n + 1][r + 1], a[n + 2][r + 1], a[n + 3][r + 1]});
         } else {
             static_assert(Ti::Fb::kV == 2, "columns of a pair in one lane");
 #pragma unroll
@@ -93,14 +86,14 @@ __device__ inline void gate_pairs(Ti &tile)
     for (int m = 0; m < Ti::kFm; ++m)
 #pragma unroll
         for (int n = 0; n < Ti::kFn; ++n) {
-            constexpr int V = Ti::Fb::kV, kUp = E::kBytes == 2 ? Ti::kFn / 2 : 0;
+            constexpr int kUp = E::kBytes == 2 ? Ti::kFn / 2 : 0;
             if (E::kBytes == 2 && n >= kUp)
                 continue;
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                if (E::kBytes == 4 && r & (V == 4 ? 1 : 2))
-                    continue;                        // binary32: the others stand one (V = 4) or two registers on
-                const int up = E::kBytes == 2 ? r : r + (V == 4 ? 1 : 2);
+                if (E::kBytes == 4 && r >= 2)
+                    continue;                        // binary32: the others stand two registers on
+                const int up = E::kBytes == 2 ? r : r + 2;
                 tile.acc[m][n][r] = gate<GATE>(tile.acc[m][n][r]) * tile.acc[m][n + kUp][up];
             }
         }

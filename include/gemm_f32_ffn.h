@@ -115,7 +115,9 @@ GEMM_F32_API int gemm_f32_quantize(int type, int gate, int T, int N, const void 
  * rounded to the type; Q [T x K], W [N x K], both with k contiguous (W as
  * gemm_f32_quantize() makes it from a weight's rows, one per output channel);
  * bias NULL: 0.  The sums are exact (K over GEMM_F32_MAX_INT8_DEPTH is
- * GEMM_F32_ERR_DIM); they are rounded to binary32 once and scaled there.
+ * GEMM_F32_ERR_DIM).  Binary32 results are computed in binary64 and rounded once.
+ * For the 16-bit types the sums are rounded to binary32 and scaled there, so that
+ * scales whose product is no binary32 number give infinities (NaN for a sum of 0) or lose digits.
  */
 GEMM_F32_API int gemm_f32_int8(int type, int T, int N, int K,
                                const int8_t *Q, int ldq, const float *scale,

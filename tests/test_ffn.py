@@ -372,6 +372,30 @@ def test_int8_sums_are_exact_at_the_largest_depth(dev, T):
     assert torch.equal(got, want)
 
 
+@pytest.mark.parametrize("T", [5, 80, 300])
+@pytest.mark.parametrize("with_bias", [False, True])
+def test_int8_results_in_binary32_are_rounded_once(dev, T, with_bias):
+    """Scales from 2^-126 to 2^100, whose products no binary32 number may hold: sums of 0 stay 0, the others half a step off."""
+    K, N = 200, 130
+    g = seeded("int8 once", T)
+    Q, W = eight(g, T, K), eight(g, N, K)
+    Q[1] = 0
+    s, ws = torch.rand(T, generator=g) + 0.5, torch.rand(N, generator=g) + 0.5
+    for t, by in enumerate((0, 100, -126, -100, 100)):
+        s[t::5] *= 2.0 ** by
+    for n, by in enumerate((0, 100, -126, -40, -10, -30, 20)):
+        ws[n::7] *= 2.0 ** by
+    bias = normal(g, N) if with_bias else None
+    say("int8 once", T, with_bias)
+    got = gb.int8_matmul(Q.to(dev), s.to(dev), W.to(dev), ws.to(dev), bias=put(bias, dev), dtype=torch.float32)
+    want = (Q.double() @ W.double().t()) * (s.double()[:, None] * ws.double())
+    if with_bias:
+        want = want + bias.double()
+    want = torch.where(want.float().isinf(), want.float().double(), want)
+    # half a step of binary32, and of binary64 before
+    oracle.close(got, want, want.abs().nan_to_num(posinf=0) * (oracle.U + 2.0 ** -52) + 2.0 ** -150, "Y")
+
+
 @pytest.mark.parametrize("T", [5, 80])
 def test_int8_scales_that_are_not_finite_stay_in_their_row(dev, T):
     g = seeded("int8 nan", T)

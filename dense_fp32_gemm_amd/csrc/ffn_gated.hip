@@ -11,7 +11,8 @@
 //
 // pre is rounded to the type where it is kept: the gradient is that of the rounded sums (off by half a step of
 // each), and costs half of what binary32 would move.  dpre is rounded once more, as an operand of the
-// products that follow.
+// products that follow, whose matrix instructions take no other (dX and dW: the root of two roundings' squares, 2.3e-3
+// against 1.7e-3 in the 2-norm for bf16).
 
 #include "ffn_gate.h"
 #include "rows_groups.h"

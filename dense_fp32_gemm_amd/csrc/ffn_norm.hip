@@ -24,7 +24,7 @@ struct NormArgs {
 };
 
 // Bound by HBM: 8192 x 4096 fp16 with a residual, 268 MB, 43.2 us, 6.2 TB/s.  To 8 bits the rows' chains of steps show
-// (sum, largest, factor, division): bf16, 235 MB, 50 us with warm caches, 56-59 from memory, 4.0-4.7 TB/s.
+// (sum, largest, factor, division): bf16, 235 MB, 50 us with warm caches, 56-57 from memory, 4.1-4.7 TB/s.
 template <class E, bool VEC, bool INT8, int TPR, int C>
 __global__ __launch_bounds__(kRowThreads<TPR>) void norm_kernel(NormArgs g)
 {
@@ -147,7 +147,8 @@ struct NormGradArgs {
     int T, N;
 };
 
-// Bound by HBM: 16383 x 2048 bf16, 268 MB, 52.5 us, 5.1 TB/s, and 5.8 us for the parts.
+// 16383 x 2048 bf16, 268 MB: 50.6 us, 5.3 TB/s (the norm above moves as much in 43.2: bound by the loads that eight
+// waves a compute unit have in flight), and 5.4 us for the parts.
 // A thread keeps its columns over all rows of its workgroup, and their part of dweight in
 // registers; the workgroup's parts go to the workspace, which sum_kernel adds up.
 // (C = 0: the parts are added in the workspace, by the thread whose columns they are.)
@@ -298,7 +299,8 @@ __global__ __launch_bounds__(kSumThreads) void zero_kernel(float *p, int N)
 // ---------------------------------------------------------------------------
 // Host side
 // ---------------------------------------------------------------------------
-// Workgroups of the gradient, each with its part of dweight: four of 256 threads on a compute unit of a whole MI355X
+// Workgroups of the gradient at most, each with its part of dweight: on a whole MI355X four a compute unit up to 256
+// threads a row (with 128 threads that is eight waves, half of what 256 have), two of 512, one of 1024
 // (16384 x 512 fp16, four rows a workgroup, whose parts are joined in LDS: 18.5 us; 24.5 with a part in the workspace
 // for each, which allows a quarter of the workgroups).
 constexpr int kGradParts = 1024;

@@ -22,9 +22,11 @@ constexpr float gate_left()
     return GATE == GEMM_F32_GATE_SILU ? -80.f : GATE == GEMM_F32_GATE_GELU ? -12.f : -9.5f;
 }
 
-// 8192 x 4096 as they are, bf16, 101 MB: 24 us, 4.1 TB/s.  silu, 4096 x 8192 fp16, 168 MB: 47-50 us with warm caches, 55
-// from memory, 3.0-3.6 TB/s: a wave's chain (gates, the row's largest in binary64, division, borders) with 16 waves
-// a compute unit; gelu_tanh 53, gelu 85, whose binary32 error sends more elements through binary64.
+// 8192 x 4096 as they are, bf16, 101 MB: 23 us, 4.4 TB/s.  silu, 4096 x 8192 fp16, 168 MB: 44 us with warm caches, 52
+// from memory, 3.2-3.8 TB/s: a wave's chain (gates, the row's largest in binary64, division, borders) with 16 waves
+// a compute unit; gelu_tanh 49.  gelu 87: as many elements go through binary64 (gate_error() is the same), but erfc()
+// there costs several times an exponential, once a row at least and behind a barrier, the binary32 polynomial is longer,
+// and of 1024 threads a row the variants spill (25 registers in bf16, 14 in half).
 // 16-bit types: registers for three waves a SIMD, which gelu's two chunks otherwise just miss in some variants (169 of
 // 168; 8192 x 4096 bf16 with one too many: 79 us, 64 without).  binary32 fits four by itself.
 template <class E, bool VEC, int GATE, int TPR, int C>

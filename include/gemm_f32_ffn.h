@@ -18,6 +18,10 @@
  * of the norms, of their gradient or of gemm_f32_gate_grad() goes in and one of the same shape
  * comes out, both may be the same (address and leading dimension).
  *
+ * Factors of a result are binary32 and round as such: where S r (of the norm), act(g)
+ * or act'(g) is under 2^-126, it is off by up to 2^-149, 2^-119 or 2^-117, and the
+ * result by that times its other factors.  (8-bit rows have no such error.)
+ *
  * Validation order: the element type (GEMM_F32_ERR_TYPE), sizes
  * (GEMM_F32_ERR_DIM: negative, over 2^31 - 4096, or more tiles than a grid
  * has), leading dimensions and strides (GEMM_F32_ERR_LD), options
@@ -139,7 +143,8 @@ GEMM_F32_API int gemm_f32_int8(int type, int T, int N, int K,
  *
  *   dpre(p,n)   = dH(p,n) * u * act'(g),   dpre(p,N+n) = dH(p,n) * act(g)
  *
- * rounded once; row by row for all P rows (those of no group give what stands in them).
+ * rounded once (the products' results then have the errors of two roundings); row by
+ * row for all P rows (those of no group give what stands in them).
  * gemm_f32_grouped_grad_x() and _grad_w() take offsets NULL with G = 1 too.
  */
 GEMM_F32_API int gemm_f32_gated(int type, int gate, int G, int P, int N, int K,

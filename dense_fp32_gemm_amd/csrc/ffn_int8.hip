@@ -213,12 +213,12 @@ int launch_int8(Int8Args g, bool dma, hipStream_t stream, bool go)
 // 8192 channels, K = 8192: 16 rows 19.6 and 21.2, 32 rows 28.0 and 21.7).
 int few_rows(int N) { return ceil_div(N, 16) <= gemm_f32_internal::current_device().cus ? 48 : 16; }
 
-// The largest tile of which there is one for every compute unit (all measured at 4096 channels; us, 4096 channels, K = 4096: 128 rows 11.7 with
+// The largest tile of which there is one for every compute unit (us, all at 4096 channels, K = 4096: 128 rows 11.7 with
 // 32 x 64, 13.0 with 64 x 64, 15.6 with 64 x 128; 256 rows 14.0, 13.7, 15.9; 512 rows 26.0, 18.5, 17.0).
 // 256 x 256 tiles from a quarter of the units on, because they are cut there (1024 rows 26.2 against 25.9 for
 // 64 x 128, 1536 rows 34.4 against 43.1, 2048 rows 37.8 against 49.9).  That branch does not look at the rows: with
 // 16640 channels or more it takes 17 to 255 rows too, mostly padding (28672 channels, K = 4096: 17 rows 34.4 us, 64 37.2,
-// 128 41.2, whose weights alone are 25 at a copy's rate; the smaller tiles there: not measured).
+// 128 41.2, whose weights alone are 25 at a copy's rate).
 int launch_int8(int type, const Int8Args &g, bool dma, bool vec, hipStream_t stream, bool go)
 {
     int rc = GEMM_F32_OK;

@@ -123,8 +123,8 @@ __global__ __launch_bounds__(kRowThreads<TPR>) void norm_kernel(NormArgs g)
                                                         sure, some);
             const float scale32 = (float)scale, most_product = __uint_as_float((uint32_t)top);
             if (there) {
-                // S weight first: where the row's largest is an ordinary number, none of the products is infinite, and one that is
-                // no normal number is nothing beside a step.  (S r may be none where a large weight makes it count.)
+                // S weight first: where the row's largest is an ordinary number, no product is infinite, and one under the normal
+                // numbers is nothing beside a step.  (S r may be under them where a large weight makes it count.)
                 Int8Row<TPR, C, E> row{g.N, j, (int8_t *)g.Y + t * g.ldy, false, !(most_product > 0x1p-99f && most_product < INFINITY)};
                 row.write(largest, g.scale + t, [&](int i, int e, int n0) { return product(i, e, n0) * scale32; },
                           [&](int i, int e, int) { return (double)pick(z[i], e) * (double)pick(w[i], e) * scale; },
